@@ -465,6 +465,133 @@ size_t q4_attn_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim, int 
 int q4_kv_append(const float *k, const float *v, uint16_t *k_cache, uint16_t *v_cache, const int *pos,
                  int capacity, int kv_dim, void *stream);
 
+/* ------------------------------------------------------- paged KV cache */
+
+/*
+ * Keys and values of many sequences in pages, for batches of sequences of
+ * different lengths, prompt chunks and several new tokens at once (the pages
+ * this library follows cache per sequence and layer; pages of positions are
+ * the common way to give that memory out in pieces).  One layer's cache:
+ *   k_pages, v_pages    device, [n_pages][n_kv_heads][page_size][head_dim], 16-byte aligned:
+ *                       Q4_KV_F16 binary16 values; Q4_KV_Q8 signed 8-bit codes
+ *   k_scales, v_scales  device, Q4_KV_Q8 only, 16-byte aligned: binary16
+ *                       [n_pages][n_kv_heads][page_size][head_dim / 32], the
+ *                       scale d of each block of 32 values (GGUF Q8_0's block
+ *                       arithmetic with codes and scales apart)
+ *   page_size           positions per page: 16, 32, 64, 128 or 256
+ *   head_dim            64, 128, 192 or 256
+ *   n_pages * n_kv_heads * page_size must stay below 2^31
+ * A Q8 block holds d = f16(max|x| / 127) and codes rint(x / d) within -127..127
+ * (all 0 when d is 0); an element stands for f16(code * d).  A block with a NaN
+ * or an infinity, or whose d overflows binary16, holds d = NaN and codes 0: it
+ * stands for NaN throughout.
+ */
+#define Q4_KV_F16 0
+#define Q4_KV_Q8 1
+
+typedef struct q4_paged_kv {
+  void *k_pages;
+  void *v_pages;
+  uint16_t *k_scales;
+  uint16_t *v_scales;
+  int n_pages;
+  int page_size;
+  int n_kv_heads;
+  int head_dim;
+  int type;            /* Q4_KV_F16 or Q4_KV_Q8 */
+} q4_paged_kv;
+
+/*
+ * The new tokens of a batch of sequences, the same for the three calls below.
+ * Token rows token_starts[s] .. token_starts[s + 1] - 1 of the caller's
+ * buffers belong to sequence s; row token_starts[s] + i stands at position
+ * kv_lens[s] - (token_starts[s + 1] - token_starts[s]) + i, so kv_lens counts
+ * the new tokens too.  Position p of sequence s is slot p % page_size of page
+ * page_table[s][p / page_size]; an entry outside 0..n_pages-1 is a hole (a
+ * page not given out, or given back): nothing is read or written there.
+ *   token_starts   device int [n_seqs + 1], not decreasing, within 0..n_tokens
+ *   kv_lens        device int [n_seqs], taken within 0..table_width * page_size
+ *   page_table     device int [n_seqs][table_width]
+ *   n_tokens       rows of the caller's buffers; rows that belong to no
+ *                  sequence are neither read nor written
+ *   max_new        the most new tokens of one sequence, as far as the caller
+ *                  knows: it chooses the kernel, results do not depend on it
+ *                  beyond the error bound
+ * The arrays are read by the kernels, so one captured graph serves every
+ * content of them.  A sequence may have no new token.  A row at a negative
+ * position (kv_lens below the new tokens) is in no page: it is not written,
+ * reads back as zeros, and sees nothing as a query.  n_seqs <= 65535; with no
+ * sequence or no token a call does nothing.  Sequences may share pages that are only read; a page that
+ * receives tokens in a call must belong to one sequence of that call only.
+ */
+typedef struct q4_paged_batch {
+  const int *token_starts;
+  const int *kv_lens;
+  const int *page_table;
+  int n_seqs;
+  int n_tokens;
+  int table_width;
+  int max_new;
+} q4_paged_batch;
+
+/* Element types of the caller's rows. */
+#define Q4_TYPE_F32 0
+#define Q4_TYPE_F16 1
+
+/*
+ * Write the new tokens' keys and values into their pages (as binary16, or
+ * quantised to Q8).
+ *   k, v   device, [n_tokens] rows of n_kv_heads * head_dim values of `type`
+ *          (Q4_TYPE_*), `ld` values from row to row (ld >= the row, a row of a
+ *          q|k|v product's output for instance), each row 16-byte aligned
+ * Errors: Q4_ERR_ARG, Q4_ERR_ALIGN, Q4_ERR_CUDA.
+ */
+int q4_paged_write(const q4_paged_kv *kv, const q4_paged_batch *batch, const void *k, const void *v, int type,
+                   int64_t ld, void *stream);
+
+/*
+ * Read the batch's positions back out of their pages into rows laid out as
+ * q4_paged_write's: with kv_lens new tokens per sequence, whole caches (into
+ * the contiguous binary16 bucket that q4_attn_decode and
+ * q4_decoder_create_kv take, for instance).  Q8 elements become what they
+ * stand for, f16(code * d), in either type; positions in no page read as zeros.
+ * Errors: Q4_ERR_ARG, Q4_ERR_ALIGN, Q4_ERR_CUDA.
+ */
+int q4_paged_read(const q4_paged_kv *kv, const q4_paged_batch *batch, void *k, void *v, int type, int64_t ld,
+                  void *stream);
+
+/*
+ * Attention of every new token over its sequence's pages.  For a query head h
+ * of the token at position p, with value head g = h / (n_q_heads/n_kv_heads):
+ *   s_t = q[h] . k[t][g] / sqrt(head_dim) over the positions t it sees,
+ *   out[h] = f16(sum_t softmax(s)_t v[t][g]).
+ * It sees t <= p and, with window > 0, only t > p - window or t < sinks (the
+ * first tokens that stay visible); never a position in a hole, so pages that
+ * left the window may be given back.  A token that sees nothing gets zeros.
+ * Values outside what a query sees (stale slots, NaN, infinities) do not
+ * reach its output.  The new tokens' own keys and values must be in the pages
+ * (q4_paged_write).
+ *   q      device, [n_tokens] rows of n_q_heads * head_dim values of q_type
+ *          (Q4_TYPE_*), q_ld values from row to row, rows 16-byte aligned
+ *   out    device, binary16 [n_tokens] rows of n_q_heads * head_dim, out_ld
+ *          values from row to row, rows 16-byte aligned, written
+ *   n_q_heads   a multiple of n_kv_heads, at most 64 query heads per value head
+ *   window      0 (none) or the positions a query sees back, its own included
+ *   sinks       first positions visible beside the window (0 without one)
+ *   workspace   device, >= q4_attn_paged_workspace_bytes() bytes, 16-byte
+ *               aligned; its content does not matter before or after.  Calls
+ *               that may run at the same time need one each
+ * Error bound, with S_t = sum |q k_t| / sqrt(head_dim) and w = softmax(s):
+ * |out - exact| <= (2^-10 + 2^-19 max S_t) sum w|v| + (positions) 2^-25 max|v| + 2^-24.
+ * Errors: Q4_ERR_ARG, Q4_ERR_ALIGN, Q4_ERR_OOM, Q4_ERR_CUDA.
+ */
+int q4_attn_paged(const q4_paged_kv *kv, const q4_paged_batch *batch, const void *q, int q_type, int64_t q_ld,
+                  int n_q_heads, int window, int sinks, uint16_t *out, int64_t out_ld, void *workspace,
+                  size_t workspace_bytes, void *stream);
+
+/* Bytes of the workspace of q4_attn_paged (0 for invalid sizes).  Host only. */
+size_t q4_attn_paged_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim);
+
 /* ------------------------------------------------------- streamed layers */
 
 typedef struct q4_stream q4_stream;

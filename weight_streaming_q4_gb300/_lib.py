@@ -41,6 +41,10 @@ Q4_DEC_TENSOR_CORE = 2
 Q4_DEC_BARRIER = 4
 Q4_DEC_CUDA_CORE = 8
 Q4_DEC_BATCH_ENGINE = 16
+Q4_KV_F16 = 0
+Q4_KV_Q8 = 1
+Q4_TYPE_F32 = 0
+Q4_TYPE_F16 = 1
 Q4_STREAM_POISON = 1
 Q4_STREAM_TENSOR_CORE = 2
 Q4_STREAM_CHUNKED = 4
@@ -79,6 +83,34 @@ class KVCache(ctypes.Structure):
                 ("pos", c_p), ("attn_workspace", c_p), ("attn_workspace_bytes", c_size)]
 
 
+class PagedKV(ctypes.Structure):
+    """q4_paged_kv.  Made once per layer cache; keeps its tensors alive."""
+    _fields_ = [("k_pages", c_p), ("v_pages", c_p), ("k_scales", c_p), ("v_scales", c_p), ("n_pages", c_int),
+                ("page_size", c_int), ("n_kv_heads", c_int), ("head_dim", c_int), ("type", c_int)]
+
+    @classmethod
+    def of(cls, k_pages, v_pages, n_pages, page_size, n_kv_heads, head_dim, cache_type=Q4_KV_F16, k_scales=None,
+           v_scales=None):
+        s = cls(_dev_ptr(k_pages), _dev_ptr(v_pages), _dev_ptr(k_scales), _dev_ptr(v_scales), n_pages, page_size,
+                n_kv_heads, head_dim, cache_type)
+        s._keep = (k_pages, v_pages, k_scales, v_scales)
+        return s
+
+
+class PagedBatch(ctypes.Structure):
+    """q4_paged_batch.  The kernels read the arrays, so one object serves every
+    content of them; keeps its tensors alive."""
+    _fields_ = [("token_starts", c_p), ("kv_lens", c_p), ("page_table", c_p), ("n_seqs", c_int), ("n_tokens", c_int),
+                ("table_width", c_int), ("max_new", c_int)]
+
+    @classmethod
+    def of(cls, token_starts, kv_lens, page_table, n_seqs, n_tokens, table_width, max_new):
+        s = cls(_dev_ptr(token_starts, 4), _dev_ptr(kv_lens, 4), _dev_ptr(page_table, 4), n_seqs, n_tokens,
+                table_width, max_new)
+        s._keep = (token_starts, kv_lens, page_table)
+        return s
+
+
 def _declare(lib):
     sig = {
         "q4_status_string": ([c_int], ctypes.c_char_p),
@@ -113,6 +145,11 @@ def _declare(lib):
         "q4_attn_decode": ([c_p, c_p, c_p, c_p, c_int, c_int, c_int, c_int, c_p, c_p, c_size, c_p], c_int),
         "q4_attn_workspace_bytes": ([c_int, c_int, c_int, c_int], c_size),
         "q4_kv_append": ([c_p, c_p, c_p, c_p, c_p, c_int, c_int, c_p], c_int),
+        "q4_paged_write": ([ctypes.POINTER(PagedKV), ctypes.POINTER(PagedBatch), c_p, c_p, c_int, c_i64, c_p], c_int),
+        "q4_paged_read": ([ctypes.POINTER(PagedKV), ctypes.POINTER(PagedBatch), c_p, c_p, c_int, c_i64, c_p], c_int),
+        "q4_attn_paged": ([ctypes.POINTER(PagedKV), ctypes.POINTER(PagedBatch), c_p, c_int, c_i64, c_int, c_int, c_int,
+                           c_p, c_i64, c_p, c_size, c_p], c_int),
+        "q4_attn_paged_workspace_bytes": ([c_int, c_int, c_int], c_size),
         "q4_stream_status": ([c_p, c_p, ctypes.POINTER(c_int)], c_int),
         "q4_stream_tagged": ([c_p, ctypes.POINTER(c_int)], c_int),
         "q4_stream_timeline": ([c_p, c_p, c_int, c_p], c_int),
@@ -158,6 +195,36 @@ def _ptr(t):
         return None
     if isinstance(t, int):
         return t
+    return t.data_ptr()
+
+
+def _dev_ptr(t, itemsize=None):
+    """_ptr of a tensor that the kernels can reach: contiguous, on the current
+    CUDA device, of the given element size (an integer is taken as an address)."""
+    if t is None or isinstance(t, int):
+        return t
+    import torch
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise Q4Error(Q4_ERR_ARG, f"a tensor on {t.device}, not the current CUDA device")
+    if not t.is_contiguous() or (itemsize and t.element_size() != itemsize):
+        raise Q4Error(Q4_ERR_ARG, f"a {t.dtype} tensor of strides {tuple(t.stride())}")
+    return t.data_ptr()
+
+
+def _rows_ptr(t, what, rows, row, ld, kind):
+    """_ptr of a buffer of ``rows`` rows of ``row`` values, ``ld`` apart: a
+    tensor has to be on the current device, of that type, and hold them (a view
+    that starts inside a wider row does: its storage counts)."""
+    if t is None or isinstance(t, int):
+        return t
+    import torch
+    size = 4 if kind == Q4_TYPE_F32 else 2
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise Q4Error(Q4_ERR_ARG, f"{what}: a tensor on {t.device}, not the current CUDA device")
+    if t.element_size() != size:
+        raise Q4Error(Q4_ERR_ARG, f"{what}: a {t.dtype} tensor for {size}-byte values")
+    if rows > 0 and t.storage_offset() + (rows - 1) * ld + row > t.untyped_storage().nbytes() // size:
+        raise Q4Error(Q4_ERR_ARG, f"{what}: {rows} rows of {row} values {ld} apart do not fit its storage")
     return t.data_ptr()
 
 
@@ -335,6 +402,36 @@ def q4_attn_workspace_bytes(n_q_heads: int, n_kv_heads: int, head_dim: int, capa
 def q4_kv_append(k, v, k_cache, v_cache, pos, capacity: int, kv_dim: int, stream=None):
     _check(lib().q4_kv_append(_ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(pos), capacity, kv_dim,
                               _stream(stream)), "q4_kv_append")
+
+
+def q4_paged_write(kv: PagedKV, batch: PagedBatch, k, v, kind: int, ld: int, stream=None):
+    """The new tokens' keys and values (rows of Q4_TYPE_F32 or Q4_TYPE_F16 values, ld apart) into their pages."""
+    row = kv.n_kv_heads * kv.head_dim
+    _check(lib().q4_paged_write(kv, batch, _rows_ptr(k, "q4_paged_write: k", batch.n_tokens, row, ld, kind),
+                                _rows_ptr(v, "q4_paged_write: v", batch.n_tokens, row, ld, kind), kind, ld,
+                                _stream(stream)), "q4_paged_write")
+
+
+def q4_paged_read(kv: PagedKV, batch: PagedBatch, k, v, kind: int, ld: int, stream=None):
+    """The batch's positions out of their pages into rows of Q4_TYPE_F32 or Q4_TYPE_F16 values, ld apart."""
+    row = kv.n_kv_heads * kv.head_dim
+    _check(lib().q4_paged_read(kv, batch, _rows_ptr(k, "q4_paged_read: k", batch.n_tokens, row, ld, kind),
+                               _rows_ptr(v, "q4_paged_read: v", batch.n_tokens, row, ld, kind), kind, ld,
+                               _stream(stream)), "q4_paged_read")
+
+
+def q4_attn_paged(kv: PagedKV, batch: PagedBatch, q, q_type: int, q_ld: int, n_q_heads: int, window: int, sinks: int,
+                  out, out_ld: int, workspace, workspace_bytes: int, stream=None):
+    """Attention of the new tokens over their sequences' pages, into binary16 rows out_ld apart."""
+    row = n_q_heads * kv.head_dim
+    _check(lib().q4_attn_paged(kv, batch, _rows_ptr(q, "q4_attn_paged: q", batch.n_tokens, row, q_ld, q_type), q_type,
+                               q_ld, n_q_heads, window, sinks,
+                               _rows_ptr(out, "q4_attn_paged: out", batch.n_tokens, row, out_ld, Q4_TYPE_F16), out_ld,
+                               _dev_ptr(workspace), workspace_bytes, _stream(stream)), "q4_attn_paged")
+
+
+def q4_attn_paged_workspace_bytes(n_q_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    return lib().q4_attn_paged_workspace_bytes(n_q_heads, n_kv_heads, head_dim)
 
 
 def q4_stream_layers(st, hidden, stream=None, timeout_us: int = 0):

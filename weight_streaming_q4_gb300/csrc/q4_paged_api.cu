@@ -1,0 +1,116 @@
+// C ABI of the paged KV cache (include/q4.h): argument checks and launches.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "q4.h"
+#include "q4_device.cuh"
+#include "q4_paged.cuh"
+
+namespace {
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+bool heads_ok(int n_kv, int hd) { return n_kv >= 1 && n_kv <= 1024 && hd >= 64 && hd <= 256 && hd % 64 == 0; }
+
+bool group_ok(int n_q, int n_kv) { return n_q >= n_kv && n_q % n_kv == 0 && n_q / n_kv <= 64; }
+
+// Checks and converts the cache and the batch.  *empty: nothing to do.
+int check_batch(const q4_paged_kv* kv, const q4_paged_batch* b, q4::PagedKv* k, q4::PagedBatch* pb, bool* empty) {
+  if (!kv || !b || !kv->k_pages || !kv->v_pages) return Q4_ERR_ARG;
+  if (kv->type != Q4_KV_F16 && kv->type != Q4_KV_Q8) return Q4_ERR_ARG;
+  if (!heads_ok(kv->n_kv_heads, kv->head_dim) || kv->n_pages < 1) return Q4_ERR_ARG;
+  int log2 = 4;
+  while (log2 < 8 && (1 << log2) != kv->page_size) ++log2;
+  if ((1 << log2) != kv->page_size) return Q4_ERR_ARG;
+  if ((static_cast<int64_t>(kv->n_pages) * kv->n_kv_heads << log2) > INT32_MAX) return Q4_ERR_ARG;
+  if (kv->type == Q4_KV_Q8 && (!kv->k_scales || !kv->v_scales)) return Q4_ERR_ARG;
+  if (b->n_seqs < 0 || b->n_seqs > 65535 || b->n_tokens < 0 || b->table_width < 1 || b->max_new < 0) return Q4_ERR_ARG;
+  if ((static_cast<int64_t>(b->table_width) << log2) > (1 << 30)) return Q4_ERR_ARG;
+  if (!aligned(kv->k_pages, 16) || !aligned(kv->v_pages, 16)) return Q4_ERR_ALIGN;
+  if (kv->type == Q4_KV_Q8 && (!aligned(kv->k_scales, 16) || !aligned(kv->v_scales, 16))) return Q4_ERR_ALIGN;
+  *empty = b->n_seqs == 0 || b->n_tokens == 0;
+  if (!*empty) {
+    if (!b->token_starts || !b->kv_lens || !b->page_table) return Q4_ERR_ARG;
+    if (!aligned(b->token_starts, 4) || !aligned(b->kv_lens, 4) || !aligned(b->page_table, 4)) return Q4_ERR_ALIGN;
+  }
+  *k = {kv->k_pages, kv->v_pages, reinterpret_cast<__half*>(kv->k_scales), reinterpret_cast<__half*>(kv->v_scales),
+        kv->n_pages, log2, kv->n_kv_heads, kv->head_dim};
+  *pb = {b->token_starts, b->kv_lens, b->page_table, b->n_seqs, b->n_tokens, b->table_width};
+  return Q4_OK;
+}
+
+// A buffer of rows of `row` values of a type, ld apart.
+int check_rows(const void* p, int type, int64_t ld, int64_t row) {
+  if (!p || (type != Q4_TYPE_F32 && type != Q4_TYPE_F16) || ld < row || ld > (int64_t{1} << 31)) return Q4_ERR_ARG;
+  if (!aligned(p, 16) || ld * (type == Q4_TYPE_F32 ? 4 : 2) % 16) return Q4_ERR_ALIGN;
+  return Q4_OK;
+}
+
+}  // namespace
+
+#define Q4_CUDA(call)                                           \
+  do {                                                          \
+    cudaError_t e_ = (call);                                    \
+    if (e_ != cudaSuccess) return q4::record_cuda_error(e_);    \
+  } while (0)
+
+extern "C" int q4_paged_write(const q4_paged_kv* kv, const q4_paged_batch* batch, const void* k, const void* v, int type,
+                              int64_t ld, void* stream) {
+  q4::PagedKv pk;
+  q4::PagedBatch pb;
+  bool empty = false;
+  int st = check_batch(kv, batch, &pk, &pb, &empty);
+  if (st != Q4_OK || empty) return st;
+  const int64_t row = static_cast<int64_t>(pk.n_kv) * pk.hd;
+  if ((st = check_rows(k, type, ld, row)) != Q4_OK || (st = check_rows(v, type, ld, row)) != Q4_OK) return st;
+  Q4_CUDA(q4::paged_write_launch(pk, pb, k, v, type == Q4_TYPE_F32, ld, kv->type == Q4_KV_Q8,
+                                 static_cast<cudaStream_t>(stream)));
+  return Q4_OK;
+}
+
+extern "C" int q4_paged_read(const q4_paged_kv* kv, const q4_paged_batch* batch, void* k, void* v, int type, int64_t ld,
+                             void* stream) {
+  q4::PagedKv pk;
+  q4::PagedBatch pb;
+  bool empty = false;
+  int st = check_batch(kv, batch, &pk, &pb, &empty);
+  if (st != Q4_OK || empty) return st;
+  const int64_t row = static_cast<int64_t>(pk.n_kv) * pk.hd;
+  if ((st = check_rows(k, type, ld, row)) != Q4_OK || (st = check_rows(v, type, ld, row)) != Q4_OK) return st;
+  Q4_CUDA(q4::paged_read_launch(pk, pb, k, v, type == Q4_TYPE_F32, ld, kv->type == Q4_KV_Q8,
+                                static_cast<cudaStream_t>(stream)));
+  return Q4_OK;
+}
+
+extern "C" size_t q4_attn_paged_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim) {
+  if (!heads_ok(n_kv_heads, head_dim) || !group_ok(n_q_heads, n_kv_heads)) return 0;
+  return 16;
+}
+
+extern "C" int q4_attn_paged(const q4_paged_kv* kv, const q4_paged_batch* batch, const void* q, int q_type, int64_t q_ld,
+                             int n_q_heads, int window, int sinks, uint16_t* out, int64_t out_ld, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  q4::PagedAttnArgs a;
+  bool empty = false;
+  int st = check_batch(kv, batch, &a.kv, &a.b, &empty);
+  if (st != Q4_OK) return st;
+  if (!group_ok(n_q_heads, a.kv.n_kv) || window < 0 || sinks < 0 || (sinks > 0 && window == 0)) return Q4_ERR_ARG;
+  if (empty) return Q4_OK;
+  const int64_t row = static_cast<int64_t>(n_q_heads) * a.kv.hd;
+  if ((st = check_rows(q, q_type, q_ld, row)) != Q4_OK) return st;
+  if ((st = check_rows(out, Q4_TYPE_F16, out_ld, row)) != Q4_OK) return st;
+  if (!workspace) return Q4_ERR_ARG;
+  if (!aligned(workspace, 16)) return Q4_ERR_ALIGN;
+  if (workspace_bytes < q4_attn_paged_workspace_bytes(n_q_heads, a.kv.n_kv, a.kv.hd)) return Q4_ERR_OOM;
+  a.q = q;
+  a.q_ld = q_ld;
+  a.out = reinterpret_cast<__half*>(out);
+  a.out_ld = out_ld;
+  a.group = n_q_heads / a.kv.n_kv;
+  a.window = window;
+  a.sinks = sinks;
+  a.scale = static_cast<float>(1.4426950408889634 / sqrt(static_cast<double>(a.kv.hd)));
+  Q4_CUDA(q4::paged_attn_launch(a, q_type == Q4_TYPE_F32, kv->type == Q4_KV_Q8, static_cast<cudaStream_t>(stream)));
+  return Q4_OK;
+}
