@@ -335,7 +335,9 @@ extern "C" int q4_device_status(void) {
   int tc = 0, os = 0;
   Q4_CUDA(q4::tc_engine_read_status(&tc));
   Q4_CUDA(q4::oneshot_read_status(&os));
-  return v | m | tc | os;
+  int pt = 0;
+  Q4_CUDA(q4::paged_read_status(&pt));
+  return v | m | tc | os | pt;
 }
 
 extern "C" int q4_dequant_debug(const void* w, float* w_out, int n, int k, void* stream) {

@@ -490,6 +490,8 @@ cudaError_t oneshot_prepare();
 cudaError_t oneshot_launch(const uint8_t* w, const uint16_t* x, float* y, int n, int k, uint32_t wait_limit,
                            bool chain, cudaStream_t stream);
 cudaError_t oneshot_read_status(int* out);
+// Status bits of the paged attention kernels (q4_paged_tile.cu).
+cudaError_t paged_read_status(int* out);
 // A product of another kernel was launched on `stream`: the next one-shot
 // product there does not start early.
 void oneshot_chain_break(cudaStream_t stream);

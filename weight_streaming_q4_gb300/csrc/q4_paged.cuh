@@ -88,7 +88,7 @@ __device__ __forceinline__ void q8_values4(uint32_t codes, __half2 d, __half2& l
   hi = __hmul2(q8_pair(b, 0x4342), d);
 }
 
-// Launchers (q4_paged_cache.cu, q4_paged_attn.cu).
+// Launchers (q4_paged_cache.cu).
 cudaError_t paged_write_launch(const PagedKv& kv, const PagedBatch& b, const void* k, const void* v, bool f32,
                                int64_t ld, bool q8, cudaStream_t s);
 cudaError_t paged_read_launch(const PagedKv& kv, const PagedBatch& b, void* k, void* v, bool f32, int64_t ld, bool q8,
@@ -105,6 +105,5 @@ struct PagedAttnArgs {
   int window, sinks;
   float scale;        // log2(e) / sqrt(hd): softmax in powers of two
 };
-cudaError_t paged_attn_launch(const PagedAttnArgs& a, bool q_f32, bool q8, cudaStream_t s);
 
 }  // namespace q4

@@ -3,9 +3,11 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "q4.h"
 #include "q4_device.cuh"
-#include "q4_paged.cuh"
+#include "q4_paged_sched.cuh"
 
 namespace {
 
@@ -47,13 +49,32 @@ int check_rows(const void* p, int type, int64_t ld, int64_t row) {
   return Q4_OK;
 }
 
-}  // namespace
-
 #define Q4_CUDA(call)                                           \
   do {                                                          \
     cudaError_t e_ = (call);                                    \
     if (e_ != cudaSuccess) return q4::record_cuda_error(e_);    \
   } while (0)
+
+// CTAs of the attention kernels on the current device (one per SM), which are
+// made ready on its first call.
+int attn_grid(int* grid) {
+  static std::mutex mutex;
+  static int sms[64];
+  int dev = 0;
+  Q4_CUDA(cudaGetDevice(&dev));
+  if (dev < 0 || dev >= 64) return Q4_ERR_ARG;
+  std::lock_guard<std::mutex> lock(mutex);
+  if (sms[dev] == 0) {
+    int n = 0;
+    Q4_CUDA(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev));
+    Q4_CUDA(q4::paged_tile_prepare());
+    sms[dev] = n < q4::kPagedMaxCtas ? n : q4::kPagedMaxCtas;
+  }
+  *grid = sms[dev];
+  return Q4_OK;
+}
+
+}  // namespace
 
 extern "C" int q4_paged_write(const q4_paged_kv* kv, const q4_paged_batch* batch, const void* k, const void* v, int type,
                               int64_t ld, void* stream) {
@@ -85,7 +106,9 @@ extern "C" int q4_paged_read(const q4_paged_kv* kv, const q4_paged_batch* batch,
 
 extern "C" size_t q4_attn_paged_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim) {
   if (!heads_ok(n_kv_heads, head_dim) || !group_ok(n_q_heads, n_kv_heads)) return 0;
-  return 16;
+  // two slots per CTA of up to 256 rows (head_dim above 128: 128): outputs, maximum and sum in fp32
+  const size_t rows = head_dim <= 128 ? 256 : 128;
+  return q4::kPagedRecordBytes + 2 * q4::kPagedMaxCtas * rows * (head_dim + 2) * sizeof(float);
 }
 
 extern "C" int q4_attn_paged(const q4_paged_kv* kv, const q4_paged_batch* batch, const void* q, int q_type, int64_t q_ld,
@@ -111,6 +134,9 @@ extern "C" int q4_attn_paged(const q4_paged_kv* kv, const q4_paged_batch* batch,
   a.window = window;
   a.sinks = sinks;
   a.scale = static_cast<float>(1.4426950408889634 / sqrt(static_cast<double>(a.kv.hd)));
-  Q4_CUDA(q4::paged_attn_launch(a, q_type == Q4_TYPE_F32, kv->type == Q4_KV_Q8, static_cast<cudaStream_t>(stream)));
+  int grid = 0;
+  if ((st = attn_grid(&grid)) != Q4_OK) return st;
+  Q4_CUDA(q4::paged_tile_launch(a, q_type == Q4_TYPE_F32, kv->type == Q4_KV_Q8, workspace, grid,
+                                static_cast<cudaStream_t>(stream)));
   return Q4_OK;
 }

@@ -1,0 +1,214 @@
+// How the attention over pages is split over the CTAs, on the device (sm_103a).
+//
+// An item is one tile of R query rows of one value head of one sequence: row r
+// of a head is query head r % group of new token r / group, so that the group's
+// queries share each key and value that is read.  An item walks the key tiles
+// (BN positions each) that its rows see: the sinks' tiles, then the tiles from
+// the first row's window to the last row's position.  All items' key tiles in
+// a row (sequence, row tile, head, key tile) are the units; every CTA takes the
+// same number of consecutive units, whatever the lengths, so a long sequence
+// spreads over many CTAs and short ones share one.  An item that a CTA does not
+// hold whole leaves partial results (maximum, sum, unnormalised output per row):
+//   slot 0 of a CTA: its first item, begun by an earlier CTA
+//   slot 1 of a CTA: its last item, begun there and not finished
+// so an item begun by CTA c is slot 1 of c, then slot 0 of c + 1, ...: joined in
+// that order by a second kernel, whose result depends on the lengths alone.
+// Everything is computed from the arrays in device memory by every CTA for
+// itself (one scan over the sequences, about a microsecond), so a captured
+// graph serves any content of them and there is no plan to keep.
+#pragma once
+
+#include <stdint.h>
+
+#include "q4_paged.cuh"
+
+namespace q4 {
+
+constexpr int kPagedMaxCtas = 160;      // CTAs a workspace has slots for
+
+// The key tiles of one item.
+struct ItemTiles {
+  int p0, p1;       // positions of its first and last row (p1 < 0: the rows see nothing)
+  int n_sink;       // tiles 0 .. n_sink - 1 come first
+  int lo;           // then tiles lo ..
+  int cnt;          // tiles in all, at least 1 (an item without work still writes its zeros)
+  __device__ __forceinline__ int tile(int i) const { return i < n_sink ? i : lo + i - n_sink; }
+};
+
+template <int R, int BN>
+__device__ __forceinline__ ItemTiles item_tiles(const PagedAttnArgs& a, const SeqSpan& sp, int j) {
+  ItemTiles t;
+  const int rows = sp.n_new * a.group;
+  const int first = sp.len - sp.n_new;
+  t.p0 = first + j * R / a.group;
+  t.p1 = first + (min(rows, j * R + R) - 1) / a.group;
+  t.n_sink = 0, t.lo = 0, t.cnt = 1;
+  if (t.p1 < 0) return t;
+  const int seen = a.window ? max(0, t.p0 - a.window + 1) : 0;     // first position inside the first row's window
+  t.lo = seen / BN;
+  t.n_sink = min((a.sinks + BN - 1) / BN, t.lo);
+  t.cnt = t.n_sink + t.p1 / BN - t.lo + 1;
+  return t;
+}
+
+template <int R, int BN>
+__device__ __forceinline__ long long seq_units(const PagedAttnArgs& a, const SeqSpan& sp) {
+  const int n = (sp.n_new * a.group + R - 1) / R;
+  long long u = 0;
+  for (int j = 0; j < n; ++j) u += item_tiles<R, BN>(a, sp, j).cnt;
+  return u * a.kv.n_kv;
+}
+
+// Where a CTA starts and how many units it takes.
+struct CtaWork {
+  long long per;            // units of every CTA but the last ones
+  int n;                    // units of this CTA (0: none)
+  int seq, j, head, tile;   // its first unit
+};
+
+// One scan over the sequences by the whole block of NT threads (a multiple of
+// 32); s_scan holds NT / 32 + 1 values.  Ends with the result in *out (shared
+// memory) and the block synchronised.
+template <int R, int BN, int NT>
+__device__ void cta_work(const PagedAttnArgs& a, long long* s_scan, CtaWork* out) {
+  constexpr int W = NT / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // inclusive scan of v over the block; *total its sum
+  auto scan = [&](long long v, long long* total) {
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(~0u, v, d);
+      if (lane >= d) v += o;
+    }
+    __syncthreads();
+    if (lane == 31) s_scan[warp] = v;
+    __syncthreads();
+    long long before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const long long x = s_scan[w];
+      before += w < warp ? x : 0;
+      all += x;
+    }
+    *total = all;
+    return v + before;
+  };
+  const int n_seqs = a.b.n_seqs;
+  long long total = 0, mine = 0, incl = 0;
+  SeqSpan sp = {};
+  if (n_seqs <= NT) {       // the common case: one sequence per thread, kept
+    if (tid < n_seqs) {
+      sp = paged_span(a.kv, a.b, tid);
+      mine = seq_units<R, BN>(a, sp);
+    }
+    incl = scan(mine, &total);
+  } else {
+    for (int s = tid; s < n_seqs; s += NT) mine += seq_units<R, BN>(a, paged_span(a.kv, a.b, s));
+    scan(mine, &total);
+  }
+  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  const long long u0 = per * blockIdx.x;
+  if (tid == 0) out->per = per, out->n = u0 < total ? static_cast<int>(min(per, total - u0)) : 0;
+  auto place = [&](int s, long long end) {     // the thread whose sequence holds u0 finds the unit in it
+    if (mine == 0 || u0 < end - mine || u0 >= end) return;
+    long long u = u0 - (end - mine);
+    for (int j = 0;; ++j) {
+      const int cnt = item_tiles<R, BN>(a, sp, j).cnt;
+      const long long of_j = static_cast<long long>(cnt) * a.kv.n_kv;
+      if (u < of_j) {
+        out->seq = s, out->j = j, out->head = static_cast<int>(u / cnt), out->tile = static_cast<int>(u % cnt);
+        return;
+      }
+      u -= of_j;
+    }
+  };
+  if (n_seqs <= NT) {
+    place(tid, incl);
+  } else if (u0 < total) {
+    long long carry = 0;
+    for (int base = 0; base < n_seqs && carry <= u0; base += NT) {
+      const int s = base + tid;
+      mine = 0;
+      if (s < n_seqs) {
+        sp = paged_span(a.kv, a.b, s);
+        mine = seq_units<R, BN>(a, sp);
+      }
+      long long sum;
+      incl = scan(mine, &sum);
+      place(s, carry + incl);
+      carry += sum;
+    }
+  }
+  __syncthreads();
+}
+
+// A CTA's units as segments: the tiles of one item that it holds.  Every role
+// of the kernel walks its own copy.
+template <int R, int BN>
+struct SegmentWalk {
+  int group;
+  int left;                 // units not yet walked
+  int seq, j, head;         // current item
+  SeqSpan sp;
+  ItemTiles it;
+  int i0, i1;               // its tiles [i0, i1) in this segment
+
+  __device__ __forceinline__ void begin(const PagedAttnArgs& a, const CtaWork& w) {
+    group = a.group, left = w.n, seq = w.seq, j = w.j, head = w.head, i0 = w.tile;
+    if (left > 0) {
+      sp = paged_span(a.kv, a.b, seq);
+      it = item_tiles<R, BN>(a, sp, j);
+      i1 = min(it.cnt, i0 + left);
+    }
+  }
+  __device__ __forceinline__ bool live() const { return left > 0; }
+  __device__ __forceinline__ void next(const PagedAttnArgs& a) {
+    left -= i1 - i0;
+    if (left <= 0) return;
+    i0 = 0;
+    if (++head == a.kv.n_kv) {
+      head = 0, ++j;
+      while (j * R >= sp.n_new * group) {       // the next sequence with rows: there is one, units are left
+        if (++seq >= a.b.n_seqs) {
+          left = 0;
+          return;
+        }
+        j = 0;
+        sp = paged_span(a.kv, a.b, seq);
+      }
+      it = item_tiles<R, BN>(a, sp, j);
+    }
+    i1 = min(it.cnt, left);
+  }
+  __device__ __forceinline__ int rows() const { return min(R, sp.n_new * group - j * R); }
+};
+
+// Workspace: a record per CTA, then the partial results of its two slots.
+struct JoinRecord {
+  int n;                    // CTAs that hold a part of the item that slot 1 begins (0: none)
+  int t0, row0, rows;       // the sequence's first token row; the item's first row and its rows
+  int head;
+};
+constexpr size_t kPagedRecordBytes = kPagedMaxCtas * 32;
+static_assert(sizeof(JoinRecord) <= 32, "records are 32 bytes apart");
+
+struct PartSlots {
+  char* base;
+  int rows, hd;             // R and head_dim
+  __host__ __device__ __forceinline__ size_t slot_floats() const { return static_cast<size_t>(rows) * (hd + 2); }
+  __device__ __forceinline__ JoinRecord* record(int cta) const { return reinterpret_cast<JoinRecord*>(base + cta * 32); }
+  // [rows][hd] outputs, then [rows] maxima, then [rows] sums
+  __device__ __forceinline__ float* out(int cta, int slot) const {
+    return reinterpret_cast<float*>(base + kPagedRecordBytes) + (2 * cta + slot) * slot_floats();
+  }
+  __device__ __forceinline__ float* max(int cta, int slot) const { return out(cta, slot) + static_cast<size_t>(rows) * hd; }
+  __device__ __forceinline__ float* sum(int cta, int slot) const { return max(cta, slot) + rows; }
+};
+
+// Launchers.  ws: the workspace; grid: CTAs, at most kPagedMaxCtas.
+cudaError_t paged_tile_prepare();
+cudaError_t paged_tile_launch(const PagedAttnArgs& a, bool q_f32, bool q8, void* ws, int grid, cudaStream_t s);
+// Joins the parts that a kernel of `grid` CTAs left (q4_paged_join.cu).
+cudaError_t paged_join_launch(const PagedAttnArgs& a, const PartSlots& parts, int grid, cudaStream_t s);
+
+}  // namespace q4

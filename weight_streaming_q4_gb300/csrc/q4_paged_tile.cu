@@ -1,0 +1,688 @@
+// Attention of chunks of new tokens over a paged KV cache on the fifth
+// generation's tensor cores (sm_103a).
+//
+// One persistent CTA per SM (q4_paged_sched.cuh splits the work), R = 256 query
+// rows of a value head per item (two tiles of 128; one at head_dim above 128 or
+// with fp32 queries), key tiles of BN positions.  Per query tile and key tile:
+//   S = Q K^T       tcgen05.mma, Q and K in shared memory, S [128][BN] in tensor memory
+//   P = 2^(S c - m) 128 threads, a row each: no exchange between threads
+//   O += P V        tcgen05.mma, P (binary16) in tensor memory over S's columns,
+//                   V in shared memory as it lies in the page ([position][head_dim])
+// with the running maximum m and sum l of a row in its thread.  m is only raised,
+// and O rescaled, when a tile's maximum exceeds it by more than 8 (a factor of
+// 256: P stays far inside binary16, sums are fp32), so O is seldom touched.
+// The two query tiles take turns: while the threads of one work on its scores,
+// the tensor cores work for the other.
+//
+// Warps 0-3 and 4-7: the softmax of query tile 0 and 1; warps 8-10 fill the ring
+// of key and value tiles; warp 11 issues the products.
+//
+// Keys and values go through the threads, not TMA: a tile is made of pages,
+// positions outside what the item's rows see must arrive as zeros (a stale or
+// later value may be NaN, and 0 * NaN is NaN in the product), and Q8 codes
+// become binary16 on the way.  Binary16 pages are copied with 16-byte cp.async
+// (zero-filling); Q8 codes are copied into a staging ring of which each thread
+// reads back its own pieces, so that it needs no barrier, and stored as
+// f16(code * d).  In a tile that some rows see only in part, values that are
+// not finite are taken out (zero) and noted; the rows that do see them get them
+// added at the end.
+//
+// Precision: binary16 queries enter as they are, fp32 queries as two binary16
+// parts (22 bits; two products into the same S); P is rounded to binary16
+// (2^-11 relative, the output's own rounding again), the sum l is taken of the
+// unrounded weights.
+#include <cuda_fp16.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "q4_paged_sched.cuh"
+
+namespace q4 {
+
+namespace {
+
+constexpr int kPtThreads = 384;
+constexpr int kPtLoaders = 96;
+constexpr uint32_t kPtWaitLimit = 1u << 21;
+__device__ int g_status_pt;
+
+// ------------------------------------------------------------------ tcgen05
+
+__device__ __forceinline__ void tm_alloc(uint32_t* at, int cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(at)), "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tm_free(uint32_t addr, int cols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tm_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tm_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// The barrier gets one arrival when the products issued before it are done.
+__device__ __forceinline__ void tm_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+// d[tensor memory] (+)= a b, binary16 operands, fp32 sums, K = 16.
+__device__ __forceinline__ void tm_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+      : "memory");
+}
+__device__ __forceinline__ void tm_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+      : "memory");
+}
+
+#define Q4_OUT8(x, o) "=r"(x[o]), "=r"(x[o + 1]), "=r"(x[o + 2]), "=r"(x[o + 3]), "=r"(x[o + 4]), "=r"(x[o + 5]), "=r"(x[o + 6]), "=r"(x[o + 7])
+#define Q4_IN8(x, o) "r"(x[o]), "r"(x[o + 1]), "r"(x[o + 2]), "r"(x[o + 3]), "r"(x[o + 4]), "r"(x[o + 5]), "r"(x[o + 6]), "r"(x[o + 7])
+#define Q4_IO8(x, o) "+r"(x[o]), "+r"(x[o + 1]), "+r"(x[o + 2]), "+r"(x[o + 3]), "+r"(x[o + 4]), "+r"(x[o + 5]), "+r"(x[o + 6]), "+r"(x[o + 7])
+
+// 32 columns of the warp's 32 lanes: x[i] = column i of this thread's row.
+__device__ __forceinline__ void tm_ld32(uint32_t addr, uint32_t* x) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : Q4_OUT8(x, 0), Q4_OUT8(x, 8), Q4_OUT8(x, 16), Q4_OUT8(x, 24)
+      : "r"(addr)
+      : "memory");
+}
+// The values of earlier loads are there after this: x passes through it.
+__device__ __forceinline__ void tm_ld_wait(uint32_t* x) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : Q4_IO8(x, 0), Q4_IO8(x, 8), Q4_IO8(x, 16), Q4_IO8(x, 24)::"memory");
+}
+__device__ __forceinline__ void tm_ld_waited(uint32_t* x) {
+  asm volatile("" : Q4_IO8(x, 0), Q4_IO8(x, 8), Q4_IO8(x, 16), Q4_IO8(x, 24)::"memory");
+}
+__device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t* x) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      Q4_IN8(x, 0), Q4_IN8(x, 8), Q4_IN8(x, 16), Q4_IN8(x, 24)
+      : "memory");
+}
+__device__ __forceinline__ void tm_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Instruction descriptor: fp32 sums of binary16 products, M = 128; b_mn: the
+// second operand lies with its N index contiguous.
+__host__ __device__ constexpr uint32_t mma_idesc(int n, bool b_mn) {
+  return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n / 8) << 17) | (8u << 24);
+}
+// Shared-memory operand in rows of 128 bytes, 16-byte pieces swizzled by row
+// mod 8 (the 128-byte swizzle), 8-row groups 1024 bytes apart; lead: bytes
+// between blocks of 64 contiguous elements (only where N is contiguous).
+__device__ __forceinline__ uint64_t mma_sdesc(uint32_t addr, uint32_t lead) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3fff) | (static_cast<uint64_t>(lead >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+__device__ __forceinline__ void cp16_zfill(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// What the threads stored in shared memory becomes visible to the tensor cores.
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Whether one of two binary16 values is infinite or NaN.
+__device__ __forceinline__ bool h2_bad(uint32_t u) {
+  return (u & 0x7c00u) == 0x7c00u || (u & 0x7c000000u) == 0x7c000000u;
+}
+
+// ------------------------------------------------------------------ geometry
+
+template <int HD, bool QF32, bool Q8>
+struct Pt {
+  static constexpr int BN = HD <= 128 ? 128 : 64;
+  static constexpr int NQ = HD <= 128 && !QF32 ? 2 : 1;
+  static constexpr int R = 128 * NQ;
+  static constexpr int QB = 128 * HD * 2;               // bytes of a query tile (one part)
+  static constexpr int KB = BN * HD * 2;                // bytes of a key or value tile
+  static constexpr int LIMIT = 232448 - 1024 - 1024;    // control data, and the alignment of the tiles
+  static constexpr int QALL = QB * (QF32 ? 2 : NQ);
+  static constexpr int FIT = (LIMIT - QALL) / KB;
+  static constexpr int NS = FIT > 8 ? 8 : FIT;          // ring of key and value tiles
+  static constexpr int SMEM = 2048 + QALL + NS * KB;
+  static constexpr int O_COL = NQ == 2 ? 256 : 128;     // tensor memory columns: S of tile q at q * 128, then O
+  static constexpr int CHUNKS = KB / 16;                // 16-byte pieces of a tile
+  static_assert(NS >= 3, "the ring holds a key and a value tile and the next key tile");
+};
+
+struct PtCtl {
+  uint64_t full[8], empty[8], q_full[2], s_full[2], p_full[2], o_full[2];
+  uint32_t tmem;
+  int dead;
+  int bad[8];              // segment number (+ 1) in whose values the loaders met infinities or NaN, by number mod 8
+  uint32_t there[8];       // per key tile, by number mod 8: bit g = rows 16 g .. of the tile are in a page
+                           // (the loaders are at most five key tiles and five segments ahead of the softmax)
+  CtaWork work;
+  long long scan[kPtThreads / 32 + 1];
+};
+static_assert(sizeof(PtCtl) <= 1024, "control data fits its place");
+
+// A wait that gives up at once when one has run out before: the roles walk on
+// and the kernel ends (its results do not count: the status word says so).
+__device__ __forceinline__ void pt_wait(PtCtl* c, uint64_t* bar, uint32_t parity) {
+  const uint32_t limit = *reinterpret_cast<volatile int*>(&c->dead) ? 0 : kPtWaitLimit;
+  if (!mbar_wait_bounded(bar, parity, limit)) {
+    *reinterpret_cast<volatile int*>(&c->dead) = 1;
+    atomicOr(&g_status_pt, ST_FULL_TIMEOUT);
+  }
+}
+
+// As pt_wait for a whole warp, which is together again afterwards.
+__device__ __forceinline__ void pt_wait_warp(PtCtl* c, uint64_t* bar, uint32_t parity) {
+  pt_wait(c, bar, parity);
+  __syncwarp();
+}
+
+// What of a key tile an item's rows see.
+struct TileView {
+  int base;             // first position of the tile
+  bool whole;           // every row sees every position of it (holes aside)
+};
+template <int BN>
+__device__ __forceinline__ TileView tile_view(const PagedAttnArgs& a, const ItemTiles& it, int i) {
+  TileView v;
+  v.base = it.tile(i) * BN;
+  v.whole = v.base + BN - 1 <= it.p0 && (!a.window || v.base > it.p1 - a.window || v.base + BN <= a.sinks);
+  return v;
+}
+
+// ------------------------------------------------------------------ kernel
+
+template <int HD, bool QF32, bool Q8>
+__global__ void __launch_bounds__(kPtThreads, 1) paged_tile_kernel(const __grid_constant__ PagedAttnArgs a, PartSlots parts) {
+  using G = Pt<HD, QF32, Q8>;
+  constexpr int BN = G::BN, NQ = G::NQ, R = G::R, NS = G::NS;
+  extern __shared__ char smem_raw[];
+  PtCtl* c = reinterpret_cast<PtCtl*>(smem_raw);
+  // tiles start on 1024-byte boundaries (the swizzle's period)
+  char* tiles = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1024 + 1023) & ~uintptr_t{1023});
+  const uint32_t s_q = smem_u32(tiles), s_ring = s_q + G::QALL;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) mbar_init(&c->full[i], 3), mbar_init(&c->empty[i], 1);
+    for (int q = 0; q < 2; ++q) {
+      mbar_init(&c->q_full[q], 128);
+      mbar_init(&c->s_full[q], 1);
+      mbar_init(&c->p_full[q], 128);
+      mbar_init(&c->o_full[q], 1);
+    }
+    c->dead = 0;
+    for (int i = 0; i < 8; ++i) c->bad[i] = 0;
+    fence_mbar_init();
+  }
+  if (warp == 11) tm_alloc(&c->tmem, 512);
+  cta_work<R, BN, kPtThreads>(a, c->scan, &c->work);     // ends synchronised
+  tm_before();
+  __syncthreads();
+  tm_after();
+  const uint32_t tmem = c->tmem;
+  const CtaWork work = c->work;
+  SegmentWalk<R, BN> w;
+  w.begin(a, work);
+
+  if (warp < 4 * NQ) {
+    // ---------------------------------------------------------------- softmax of query tile q
+    const int q = warp >> 2, wl = warp & 3;
+    const uint32_t t_s = tmem + q * 128 + (static_cast<uint32_t>(wl * 32) << 16);
+    const uint32_t t_o = tmem + G::O_COL + q * 128 + (static_cast<uint32_t>(wl * 32) << 16);
+    uint32_t n_s = 0;       // S tiles seen: parity of s_full, and of the product before it
+    int seg = 0;
+    uint32_t n_k = 0;       // key tiles of the CTA before the current one
+    for (; w.live(); w.next(a), ++seg) {
+      const int rows = w.rows(), row0 = w.j * R;
+      const int n_tiles = w.i1 - w.i0;
+      if (q * 128 >= rows) {        // no rows in this query tile
+        n_k += n_tiles;
+        continue;
+      }
+      // queries: the warp's 32 rows, 16-byte pieces of a row side by side
+      {
+        constexpr int PIECES = HD / 8;
+#pragma unroll 4
+        for (int x = lane; x < 32 * PIECES; x += 32) {
+          const int rr = wl * 32 + x / PIECES, pc = x % PIECES;
+          const int r = row0 + q * 128 + rr;
+          const bool there = q * 128 + rr < rows;
+          const int64_t at = (w.sp.t0 + (there ? r / a.group : 0)) * a.q_ld +
+                             (w.head * a.group + (there ? r % a.group : 0)) * HD + pc * 8;
+          const uint32_t off = (pc >> 3) * (128 * 128) + rr * 128 + (((pc & 7) ^ (rr & 7)) << 4);
+          uint4 hi = make_uint4(0, 0, 0, 0);
+          if (QF32) {
+            uint4 lo = make_uint4(0, 0, 0, 0);
+            if (there) {
+              const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at);
+              const float4 f0 = __ldg(p), f1 = __ldg(p + 1);
+              const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+              __half2* h = reinterpret_cast<__half2*>(&hi);
+              __half2* l = reinterpret_cast<__half2*>(&lo);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                h[e] = __floats2half2_rn(f[2 * e], f[2 * e + 1]);
+                const float2 b = __half22float2(h[e]);
+                l[e] = __floats2half2_rn(f[2 * e] - b.x, f[2 * e + 1] - b.y);
+              }
+            }
+            *reinterpret_cast<uint4*>(tiles + G::QB + off) = lo;
+          } else if (there) {
+            hi = __ldg(reinterpret_cast<const uint4*>(static_cast<const __half*>(a.q) + at));
+          }
+          *reinterpret_cast<uint4*>(tiles + q * G::QB + off) = hi;
+        }
+        fence_async();
+        mbar_arrive(&c->q_full[q]);
+      }
+      const int r = row0 + q * 128 + wl * 32 + lane;       // this thread's row
+      const bool mine = q * 128 + wl * 32 + lane < rows;
+      const int p = mine ? w.sp.len - w.sp.n_new + r / a.group : -1;
+      float m = -INFINITY, l = 0.f;
+      for (int i = w.i0; i < w.i1; ++i) {
+        const TileView tv = tile_view<BN>(a, w.it, i);
+        pt_wait_warp(c, &c->s_full[q], n_s & 1);
+        tm_after();
+        uint32_t x[BN];
+        float* f = reinterpret_cast<float*>(x);
+#pragma unroll
+        for (int b = 0; b < BN; b += 32) tm_ld32(t_s + b, x + b);
+        const uint32_t there = *reinterpret_cast<volatile uint32_t*>(&c->there[n_k & 7]);
+        ++n_k;
+        tm_ld_wait(x);
+#pragma unroll
+        for (int b = 32; b < BN; b += 32) tm_ld_waited(x + b);
+        if (!tv.whole || there != (1u << (BN / 16)) - 1) {
+          const int hi = p - tv.base;
+          const int lo = a.window ? hi - a.window + 1 : 0, sk = a.sinks - tv.base;
+#pragma unroll
+          for (int e = 0; e < BN; ++e)
+            if (!(e <= hi && (e >= lo || e < sk) && ((there >> (e >> 4)) & 1))) f[e] = -INFINITY;
+        }
+        float m4[4] = {f[0], f[1], f[2], f[3]};
+#pragma unroll
+        for (int e = 4; e < BN; ++e) m4[e & 3] = fmaxf(m4[e & 3], f[e]);
+        const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale;
+        const bool raise = top > m + 8.f || m == -INFINITY;
+        if (i == w.i0) {
+          m = top;
+        } else if (__any_sync(~0u, raise && top != m)) {
+          // raise m and rescale what O and l hold, after the product before this tile's
+          const float m2 = raise ? fmaxf(m, top) : m;
+          const float fac = m == m2 ? 1.f : exp2f(m - m2);
+          pt_wait_warp(c, &c->o_full[q], (n_s - 1) & 1);
+          tm_after();
+#pragma unroll 1
+          for (int b = 0; b < HD; b += 32) {
+            uint32_t o[32];
+            tm_ld32(t_o + b, o);
+            tm_ld_wait(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fac);
+            tm_st32(t_o + b, o);
+          }
+          l *= fac;
+          m = m2;
+        }
+        const float mm = m == -INFINITY ? 0.f : m;
+        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < BN; e += 2) {
+          float a0, a1;
+          asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a0) : "f"(fmaf(f[e], a.scale, -mm)));
+          asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a1) : "f"(fmaf(f[e + 1], a.scale, -mm)));
+          l4[e & 2] += a0;
+          l4[(e & 2) + 1] += a1;
+          x[e / 2] = pack_h2(a0, a1);
+        }
+        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+#pragma unroll
+        for (int b = 0; b < BN / 2; b += 32) tm_st32(t_s + b, x + b);
+        tm_st_wait();
+        tm_before();
+        mbar_arrive(&c->p_full[q]);
+        ++n_s;
+      }
+      // the item's (or the part's) end
+      pt_wait_warp(c, &c->o_full[q], (n_s - 1) & 1);
+      tm_after();
+      const bool whole_item = w.i0 == 0 && w.i1 == w.it.cnt;
+      const bool bad = *reinterpret_cast<volatile int*>(&c->bad[seg & 7]) == seg + 1;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const int slot = w.i0 == 0 ? 1 : 0;
+      const int rr = q * 128 + wl * 32 + lane;
+      __half* out = a.out + static_cast<int64_t>(w.sp.t0 + (mine ? r / a.group : 0)) * a.out_ld +
+                    (w.head * a.group + (mine ? r % a.group : 0)) * HD;
+      float* part = parts.out(blockIdx.x, slot) + static_cast<size_t>(rr) * HD;
+#pragma unroll 1
+      for (int b = 0; b < HD; b += 32) {
+        uint32_t o[32];
+        __syncwarp();
+        tm_ld32(t_o + b, o);
+        tm_ld_wait(o);
+        float* of = reinterpret_cast<float*>(o);
+        if (bad) {
+          // values that were taken out of tiles seen in part: back into the rows that see them
+          for (int i = w.i0; i < w.i1; ++i) {
+            const TileView tv = tile_view<BN>(a, w.it, i);
+            if (tv.whole) continue;
+            for (int t = tv.base; t < tv.base + BN && t <= p; ++t) {
+              if (a.window && t <= p - a.window && t >= a.sinks) continue;
+              const int vr = paged_row(a.kv, a.b, w.seq, t, w.head);
+              if (vr < 0) continue;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const size_t at = static_cast<size_t>(vr) * HD + b + e;
+                const __half h = Q8 ? __hmul(__int2half_rn(static_cast<const int8_t*>(a.kv.v)[at]), a.kv.vs[at / 32])
+                                    : static_cast<const __half*>(a.kv.v)[at];
+                if (__hisinf(h) || __hisnan(h)) of[e] += __half2float(h);
+              }
+            }
+          }
+        }
+        if (mine && whole_item) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            const uint4 u = make_uint4(pack_h2(of[e] * inv, of[e + 1] * inv), pack_h2(of[e + 2] * inv, of[e + 3] * inv),
+                                       pack_h2(of[e + 4] * inv, of[e + 5] * inv), pack_h2(of[e + 6] * inv, of[e + 7] * inv));
+            *reinterpret_cast<uint4*>(out + b + e) = u;
+          }
+        } else if (mine) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(part + b + e) = make_float4(of[e], of[e + 1], of[e + 2], of[e + 3]);
+        }
+      }
+      if (!whole_item && mine) {
+        parts.max(blockIdx.x, slot)[rr] = m;
+        parts.sum(blockIdx.x, slot)[rr] = l;
+      }
+    }
+  } else if (warp >= 8 && warp < 11) {
+    // ---------------------------------------------------------------- key and value tiles
+    const int lt = tid - 8 * 32;
+    constexpr int LAG = Q8 ? 0 : (NS > 4 ? 3 : NS - 2);       // copies in flight behind the one being issued
+    uint32_t n = 0;                                            // tiles issued (keys and values)
+    // binary16: tiles whose copies are under way, newest last
+    struct Pending {
+      bool check;
+      int seg;
+    } pend[LAG + 1];
+    auto finish = [&](uint32_t at, bool check, int seg) {      // tile number `at` has landed (this thread's pieces)
+      if (check) {
+        bool found = false;
+        for (int x = lt; x < G::CHUNKS; x += kPtLoaders) {
+          const int row = x / (HD / 8), pc = x % (HD / 8);
+          uint4* v = reinterpret_cast<uint4*>(tiles + G::QALL + (at % NS) * G::KB + (pc >> 3) * (BN * 128) + row * 128 +
+                                              (((pc & 7) ^ (row & 7)) << 4));
+          uint4 u = *v;
+          if (h2_bad(u.x) || h2_bad(u.y) || h2_bad(u.z) || h2_bad(u.w)) {
+            __half* h = reinterpret_cast<__half*>(&u);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (__hisinf(h[e]) || __hisnan(h[e])) h[e] = __ushort_as_half(0);
+            *v = u;
+            found = true;
+          }
+        }
+        if (found) *reinterpret_cast<volatile int*>(&c->bad[seg & 7]) = seg + 1;
+      }
+      fence_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c->full[at % NS]);
+    };
+    // The page-memory row of rows 16 * lane .. of key tile `base` of the walk's item (-1: not to be read)
+    auto lookup = [&](const SegmentWalk<R, BN>& g, int base) {
+      const int t = base + lane * 16;
+      return lane < BN / 16 && t <= g.it.p1 ? paged_row(a.kv, a.b, g.seq, t, g.head) : -1;
+    };
+    int seg = 0;
+    int row16 = w.live() ? lookup(w, w.it.tile(w.i0) * BN) : -1;
+    while (w.live()) {
+      for (int i = w.i0; i < w.i1; ++i) {
+        const TileView tv = tile_view<BN>(a, w.it, i);
+        const int my16 = row16;
+        // the next tile's page entries, while this one is copied
+        if (i + 1 < w.i1) row16 = lookup(w, w.it.tile(i + 1) * BN);
+        const uint32_t there = __ballot_sync(~0u, my16 >= 0) & ((1u << (BN / 16)) - 1);
+        // of the tile, positions that some row sees
+        const int last = w.it.p1 - tv.base, first = a.window ? max(w.it.p0, 0) - a.window + 1 - tv.base : 0, sk = a.sinks - tv.base;
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv, ++n) {
+          const uint32_t slot = n % NS;
+          pt_wait_warp(c, &c->empty[slot], ((n / NS) & 1) ^ 1);
+          if (kv == 0 && lt == 0) *reinterpret_cast<volatile uint32_t*>(&c->there[(n / 2) & 7]) = there;
+          const uint32_t dst = s_ring + slot * G::KB;
+          if (!Q8) {
+            const __half* src = static_cast<const __half*>(kv ? a.kv.v : a.kv.k);
+#pragma unroll 4
+            for (int x0 = 0; x0 < G::CHUNKS; x0 += kPtLoaders) {
+              const int x = x0 + lt;
+              const int row = x / (HD / 8), pc = x % (HD / 8);
+              const int r0 = __shfl_sync(~0u, my16, (row >> 4) & 31);
+              if (x < G::CHUNKS) {
+                const bool ok = r0 >= 0 && row <= last && (row >= first || row < sk);
+                cp16_zfill(dst + (pc >> 3) * (BN * 128) + row * 128 + (((pc & 7) ^ (row & 7)) << 4),
+                           src + (ok ? static_cast<size_t>(r0 + (row & 15)) * HD + pc * 8 : 0), ok);
+              }
+            }
+            cp_commit();
+#pragma unroll
+            for (int k = 0; k < LAG; ++k) pend[k] = pend[k + 1];
+            pend[LAG] = {kv == 1 && !tv.whole, seg};
+            if (static_cast<int>(n) >= LAG) {
+              cp_wait<LAG>();
+              finish(n - LAG, pend[0].check, pend[0].seg);
+            }
+          } else {
+            const int8_t* src = static_cast<const int8_t*>(kv ? a.kv.v : a.kv.k);
+            const __half* sc = kv ? a.kv.vs : a.kv.ks;
+            bool found = false;
+            const bool check = kv == 1 && !tv.whole;
+            constexpr int PIECES = BN * HD / 16;               // 16 codes each
+#pragma unroll 2
+            for (int x0 = 0; x0 < PIECES; x0 += kPtLoaders) {
+              const int x = x0 + lt;
+              const int row = x / (HD / 16), pc = x % (HD / 16);
+              const int r0 = __shfl_sync(~0u, my16, (row >> 4) & 31);
+              if (x >= PIECES) continue;
+              const bool ok = r0 >= 0 && row <= last && (row >= first || row < sk);
+              uint4 u[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+              if (ok) {
+                const size_t at = static_cast<size_t>(r0 + (row & 15)) * HD + pc * 16;
+                const uint4 codes = __ldg(reinterpret_cast<const uint4*>(src + at));
+                const __half2 d = __half2half2(sc[at / 32]);
+                __half2* h = reinterpret_cast<__half2*>(u);
+                q8_values4(codes.x, d, h[0], h[1]);
+                q8_values4(codes.y, d, h[2], h[3]);
+                q8_values4(codes.z, d, h[4], h[5]);
+                q8_values4(codes.w, d, h[6], h[7]);
+                if (check) {
+                  uint32_t* b = reinterpret_cast<uint32_t*>(u);
+                  bool any = false;
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) any |= h2_bad(b[e]);
+                  if (any) {
+                    __half* he = reinterpret_cast<__half*>(u);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                      if (__hisinf(he[e]) || __hisnan(he[e])) he[e] = __ushort_as_half(0);
+                    found = true;
+                  }
+                }
+              }
+              char* to = tiles + G::QALL + slot * G::KB + (pc >> 2) * (BN * 128) + row * 128;
+              const int p0 = (pc & 3) * 2;
+              *reinterpret_cast<uint4*>(to + ((p0 ^ (row & 7)) << 4)) = u[0];
+              *reinterpret_cast<uint4*>(to + (((p0 + 1) ^ (row & 7)) << 4)) = u[1];
+            }
+            if (found) *reinterpret_cast<volatile int*>(&c->bad[seg & 7]) = seg + 1;
+            fence_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c->full[slot]);
+          }
+        }
+      }
+      w.next(a);
+      ++seg;
+      if (w.live()) row16 = lookup(w, w.it.tile(w.i0) * BN);
+    }
+    if (!Q8) {
+      cp_wait<0>();
+      const uint32_t from = n > LAG ? n - LAG : 0;
+      // pend[k] belongs to tile n - 1 - LAG + k
+#pragma unroll
+      for (int k = 1; k <= LAG; ++k) {
+        const int at = static_cast<int>(n) - 1 - LAG + k;
+        if (at >= static_cast<int>(from)) finish(at, pend[k].check, pend[k].seg);
+      }
+    }
+  } else if (warp == 11 && lane == 0) {
+    // ---------------------------------------------------------------- products
+    constexpr uint32_t ID_S = mma_idesc(BN, false), ID_O = mma_idesc(HD, true);
+    constexpr uint64_t BLOCK = (BN * 128) >> 4;         // next 64 values of head_dim, in descriptor units
+    uint32_t n = 0;                                      // tiles taken (keys and values)
+    uint32_t n_seg[2] = {0, 0}, n_p[2] = {0, 0};         // segments and products of each query tile
+    for (; w.live(); w.next(a)) {
+      const int active = w.rows() > 128 ? NQ : 1;
+      const int cnt = w.i1 - w.i0;
+      auto scores = [&](int q, uint32_t tile) {          // S of query tile q with key tile number `tile`
+        const uint64_t k0 = mma_sdesc(s_ring + (tile % NS) * G::KB, 0);
+#pragma unroll
+        for (int part = 0; part < (QF32 ? 2 : 1); ++part) {
+          const uint64_t q0 = mma_sdesc(s_q + (QF32 ? part : q) * G::QB, 0);
+#pragma unroll
+          for (int k = 0; k < HD / 16; ++k)
+            tm_mma_ss(tmem + q * 128, q0 + (k >> 2) * ((128 * 128) >> 4) + (k & 3) * 2, k0 + (k >> 2) * BLOCK + (k & 3) * 2,
+                      ID_S, part > 0 || k > 0);
+        }
+        tm_commit(&c->s_full[q]);
+      };
+      pt_wait(c, &c->full[n % NS], (n / NS) & 1);
+      for (int q = 0; q < active; ++q) {
+        pt_wait(c, &c->q_full[q], n_seg[q] & 1);
+        ++n_seg[q];
+        tm_after();
+        scores(q, n);
+      }
+      tm_commit(&c->empty[n % NS]);
+      for (int i = 0; i < cnt; ++i, n += 2) {
+        const uint32_t v = n + 1, k_next = n + 2;
+        pt_wait(c, &c->full[v % NS], (v / NS) & 1);
+        for (int q = 0; q < active; ++q) {
+          pt_wait(c, &c->p_full[q], n_p[q] & 1);
+          ++n_p[q];
+          tm_after();
+          const uint64_t v0 = mma_sdesc(s_ring + (v % NS) * G::KB, BN * 128);
+#pragma unroll
+          for (int k = 0; k < BN / 16; ++k)
+            tm_mma_ts(tmem + G::O_COL + q * 128, tmem + q * 128 + k * 8, v0 + k * (2048 >> 4), ID_O, i > 0 || k > 0);
+          tm_commit(&c->o_full[q]);
+          if (i + 1 < cnt) {
+            if (q == 0) {
+              pt_wait(c, &c->full[k_next % NS], (k_next / NS) & 1);
+              tm_after();
+            }
+            scores(q, k_next);
+          }
+        }
+        tm_commit(&c->empty[v % NS]);
+        if (i + 1 < cnt) tm_commit(&c->empty[k_next % NS]);
+      }
+    }
+  }
+  // an item begun here and not finished: who holds the rest
+  if (tid == 0) {
+    SegmentWalk<R, BN> g;
+    g.begin(a, work);
+    JoinRecord rec = {};
+    while (g.live()) {
+      if (g.left == g.i1 - g.i0) {       // the last segment
+        if (g.i0 == 0 && g.i1 < g.it.cnt) {
+          rec.n = 1 + static_cast<int>((g.it.cnt - g.i1 + work.per - 1) / work.per);
+          rec.t0 = g.sp.t0, rec.row0 = g.j * R, rec.rows = g.rows(), rec.head = g.head;
+        }
+        break;
+      }
+      g.next(a);
+    }
+    *parts.record(blockIdx.x) = rec;
+  }
+  __syncwarp();
+  tm_before();
+  __syncthreads();
+  if (warp == 11) {
+    tm_after();
+    tm_free(tmem, 512);
+  }
+}
+
+template <int HD, bool QF32, bool Q8>
+cudaError_t prepare_tile() {
+  return cudaFuncSetAttribute(paged_tile_kernel<HD, QF32, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Pt<HD, QF32, Q8>::SMEM);
+}
+
+template <int HD>
+cudaError_t prepare_hd() {
+  const cudaError_t e[4] = {prepare_tile<HD, false, false>(), prepare_tile<HD, false, true>(),
+                            prepare_tile<HD, true, false>(), prepare_tile<HD, true, true>()};
+  for (cudaError_t x : e)
+    if (x != cudaSuccess) return x;
+  return cudaSuccess;
+}
+
+template <int HD, bool QF32, bool Q8>
+cudaError_t launch_tile(const PagedAttnArgs& a, void* ws, int grid, cudaStream_t s) {
+  using G = Pt<HD, QF32, Q8>;
+  PartSlots parts{static_cast<char*>(ws), G::R, HD};
+  paged_tile_kernel<HD, QF32, Q8><<<grid, kPtThreads, G::SMEM, s>>>(a, parts);
+  const cudaError_t e = cudaGetLastError();
+  return e != cudaSuccess ? e : paged_join_launch(a, parts, grid, s);
+}
+
+template <int HD>
+cudaError_t launch_hd(const PagedAttnArgs& a, bool f32, bool q8, void* ws, int grid, cudaStream_t s) {
+  if (f32) return q8 ? launch_tile<HD, true, true>(a, ws, grid, s) : launch_tile<HD, true, false>(a, ws, grid, s);
+  return q8 ? launch_tile<HD, false, true>(a, ws, grid, s) : launch_tile<HD, false, false>(a, ws, grid, s);
+}
+
+}  // namespace
+
+cudaError_t paged_tile_prepare() {
+  const cudaError_t e[4] = {prepare_hd<64>(), prepare_hd<128>(), prepare_hd<192>(), prepare_hd<256>()};
+  for (cudaError_t x : e)
+    if (x != cudaSuccess) return x;
+  return cudaSuccess;
+}
+
+cudaError_t paged_tile_launch(const PagedAttnArgs& a, bool q_f32, bool q8, void* ws, int grid, cudaStream_t s) {
+  switch (a.kv.hd) {
+    case 64: return launch_hd<64>(a, q_f32, q8, ws, grid, s);
+    case 128: return launch_hd<128>(a, q_f32, q8, ws, grid, s);
+    case 192: return launch_hd<192>(a, q_f32, q8, ws, grid, s);
+    default: return launch_hd<256>(a, q_f32, q8, ws, grid, s);
+  }
+}
+
+cudaError_t paged_read_status(int* out) {
+  int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_status_pt, sizeof(int));
+  if (e != cudaSuccess || *out == 0) return e;
+  return cudaMemcpyToSymbol(g_status_pt, &zero, sizeof(int));
+}
+
+}  // namespace q4
