@@ -68,6 +68,7 @@ int attn_grid(int* grid) {
     int n = 0;
     Q4_CUDA(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev));
     Q4_CUDA(q4::paged_tile_prepare());
+    Q4_CUDA(q4::paged_rows_prepare());
     sms[dev] = n < q4::kPagedMaxCtas ? n : q4::kPagedMaxCtas;
   }
   *grid = sms[dev];
@@ -136,7 +137,12 @@ extern "C" int q4_attn_paged(const q4_paged_kv* kv, const q4_paged_batch* batch,
   a.scale = static_cast<float>(1.4426950408889634 / sqrt(static_cast<double>(a.kv.hd)));
   int grid = 0;
   if ((st = attn_grid(&grid)) != Q4_OK) return st;
-  Q4_CUDA(q4::paged_tile_launch(a, q_type == Q4_TYPE_F32, kv->type == Q4_KV_Q8, workspace, grid,
-                                static_cast<cudaStream_t>(stream)));
+  const bool f32 = q_type == Q4_TYPE_F32, q8 = kv->type == Q4_KV_Q8;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int64_t rows = static_cast<int64_t>(batch->max_new) * a.group;
+  if (rows <= 32)
+    Q4_CUDA(q4::paged_rows_launch(a, f32, q8, static_cast<int>(rows), workspace, grid, s));
+  else
+    Q4_CUDA(q4::paged_tile_launch(a, f32, q8, workspace, grid, s));
   return Q4_OK;
 }

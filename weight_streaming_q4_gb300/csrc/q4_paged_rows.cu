@@ -1,0 +1,527 @@
+// Attention of few query rows over a paged KV cache (sm_103a): single tokens and
+// short drafts, where reading the keys and values is all there is to do.
+//
+// An item (q4_paged_sched.cuh) is R = 16 or 32 query rows of one value head, its
+// units are 32 positions.  Persistent, one CTA per SM.  Within a CTA every warp
+// works for itself: it takes every W-th group of 16 positions of the CTA's
+// units, copies their keys and values into its own ring with 16-byte cp.async
+// (several groups in flight per warp, no barrier between the warps), and keeps its own
+// maximum, sum and output of every row, so that nothing but the memory paces it.
+// The warps' results meet in shared memory once per item.  The ring runs across
+// items: the next item's keys are on their way while an item is finished.
+//
+// Both products are mma.sync m16n8k16 (binary16 in, fp32 sums): 16 rows are one
+// operand tile of it, an eighth of a tcgen05 one, and the scores' registers are
+// the weights' operand as they lie.  fp32 queries enter as two binary16 parts.
+// Q8 pages stay codes in shared memory: a lane's 16 codes of a key are its share
+// of four instructions (the order of head_dim in the product is free, the
+// queries follow it), a transposed matrix load of value codes holds two columns of one
+// position pair per register; f16(code * d) is formed in registers.
+#include <cuda_fp16.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "q4_paged_sched.cuh"
+
+namespace q4 {
+
+namespace {
+
+template <int HD, int MT, bool QF32, bool Q8>
+struct Pr {
+  static constexpr int W = HD <= 128 ? 8 : 4;               // warps
+  static constexpr int NT = W * 32;
+  static constexpr int R = 16 * MT;
+  static constexpr int KS = HD / 16;                        // products of a key group
+  static constexpr int ROW = Q8 ? HD : 2 * HD;              // bytes of a staged key
+  static constexpr int SC = Q8 ? HD / 32 * 2 * 16 : 0;      // bytes of a group's scales
+  static constexpr int STAGE = 2 * 16 * ROW + 2 * SC;       // keys, values, their scales
+  static constexpr int PITCH = HD + 8;                      // floats of a row of the warps' results
+  static constexpr int QB = MT * (QF32 ? 2 : 1) * KS * 512; // queries as operands
+  static constexpr int MERGE = W * 16 * PITCH * 4 + 2 * W * R * 4;
+  static constexpr int FIT = (231424 - 1024 - QB - MERGE) / (W * STAGE);
+  static constexpr int NS = FIT > 6 ? 6 : FIT;              // stages per warp
+  static constexpr int SMEM = 1024 + QB + MERGE + W * NS * STAGE;
+  static_assert(NS >= 2, "a group is copied while one is read");
+};
+
+struct PrCtl {
+  CtaWork work;
+  long long scan[9];
+  int bad;                 // segment number + 1 in whose partly seen values a warp met infinities or NaN
+  int row[8][8];           // per warp and stage: page-memory row of the group (-1: hole)
+};
+static_assert(sizeof(PrCtl) <= 1024, "control data fits its place");
+
+__device__ __forceinline__ void pr_cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void pr_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void pr_ldsm(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void pr_ldsm_t(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ uint4 pr_lds16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void pr_mma(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ float pr_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// u with infinities and NaN replaced by zero; *found is set if there were any.
+__device__ __forceinline__ uint32_t pr_finite(uint32_t u, bool* found) {
+  if ((u & 0x7c00u) == 0x7c00u) u &= 0xffff0000u, *found = true;
+  if ((u & 0x7c000000u) == 0x7c000000u) u &= 0x0000ffffu, *found = true;
+  return u;
+}
+
+// The place of 16-byte piece `c` in row `r` of a staged group.  Matrix loads
+// take the same piece of 8 consecutive rows: the pieces of 128 bytes' worth of banks
+// are exchanged by row so that these fall apart.  Keys as Q8 are read by lanes
+// of two rows and four pieces at a time instead.
+template <int ROW, bool KEY8>
+__device__ __forceinline__ int place(int r, int c) {
+  if (KEY8) return ROW % 128 == 0 ? r * ROW + ((c ^ ((r & 1) << 2)) << 4) : r * ROW + (c << 4);
+  if (ROW % 128 == 0) return r * ROW + ((c ^ (r & 7)) << 4);
+  return r * ROW + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+// A warp's groups, segment by segment: those of the copies run ahead of those
+// of the products.
+template <int R, int W>
+struct GroupWalk {
+  SegmentWalk<R, 32> w;
+  int g, n;             // the warp's current group of the segment, and the segment's groups
+  __device__ __forceinline__ void count() {
+    n = 2 * (w.i1 - w.i0);
+    if (w.i1 == w.it.cnt && (w.it.p1 & 31) < 16) --n;      // the last tile's second half holds no position seen
+    if (w.it.p1 < 0) n = 0;
+  }
+  __device__ __forceinline__ int base() const { return w.it.tile(w.i0 + (g >> 1)) * 32 + (g & 1) * 16; }
+};
+
+template <int HD, int MT, bool QF32, bool Q8>
+__global__ void __launch_bounds__(Pr<HD, MT, QF32, Q8>::NT, 1)
+    paged_rows_kernel(const __grid_constant__ PagedAttnArgs a, PartSlots parts) {
+  using G = Pr<HD, MT, QF32, Q8>;
+  constexpr int W = G::W, R = G::R, NS = G::NS, KS = G::KS, ROW = G::ROW, PIECES = ROW / 16;
+  extern __shared__ __align__(16) char smem_pr[];
+  PrCtl* c = reinterpret_cast<PrCtl*>(smem_pr);
+  uint4* s_q = reinterpret_cast<uint4*>(smem_pr + 1024);                  // [MT][part][KS][lane]
+  float* s_o = reinterpret_cast<float*>(smem_pr + 1024 + G::QB);          // [W][16][PITCH]
+  float* s_m = s_o + W * 16 * G::PITCH;                                   // [W][R]
+  float* s_l = s_m + W * R;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const uint32_t ring = smem_u32(smem_pr + 1024 + G::QB + G::MERGE) + warp * NS * G::STAGE;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid == 0) c->bad = 0;
+  cta_work<R, 32, G::NT>(a, c->scan, &c->work);
+  const CtaWork work = c->work;
+
+  // ------------------------------------------------------------------ copies
+  GroupWalk<R, W> cp;
+  cp.w.begin(a, work);
+  cp.g = warp;
+  if (cp.w.live()) cp.count();
+  // brings cp to the warp's next group; the page row of it, or -1 (no copy)
+  auto settle = [&]() -> int {
+    while (cp.w.live() && cp.g >= cp.n) {
+      cp.w.next(a);
+      cp.g = warp;
+      if (cp.w.live()) cp.count();
+    }
+    return cp.w.live() ? paged_row(a.kv, a.b, cp.w.seq, cp.base(), cp.w.head) : -1;
+  };
+  uint32_t n_cp = 0, n_use = 0;
+  int next_row = settle();
+  auto copy = [&]() {       // the group at cp into the next stage; always one commit
+    if (cp.w.live()) {
+      const int stage = n_cp % NS;
+      const uint32_t to = ring + stage * G::STAGE;
+      const int r0 = next_row;
+      if (lane == 0) c->row[warp][stage] = r0;
+      if (r0 >= 0) {
+        const char* k = static_cast<const char*>(a.kv.k) + static_cast<size_t>(r0) * ROW;
+        const char* v = static_cast<const char*>(a.kv.v) + static_cast<size_t>(r0) * ROW;
+#pragma unroll
+        for (int x = lane; x < 16 * PIECES; x += 32)
+          pr_cp16(to + place<ROW, Q8>(x / PIECES, x % PIECES), k + x * 16);
+        if (Q8) {
+          constexpr int SP = G::SC / 16;
+          const char* ks = reinterpret_cast<const char*>(a.kv.ks) + static_cast<size_t>(r0) * (HD / 16);
+          const char* vs = reinterpret_cast<const char*>(a.kv.vs) + static_cast<size_t>(r0) * (HD / 16);
+          if (lane < SP) pr_cp16(to + 32 * ROW + lane * 16, ks + lane * 16);
+          else if (lane < 2 * SP) pr_cp16(to + 32 * ROW + lane * 16, vs + (lane - SP) * 16);
+        }
+#pragma unroll
+        for (int x = lane; x < 16 * PIECES; x += 32)
+          pr_cp16(to + 16 * ROW + place<ROW, false>(x / PIECES, x % PIECES), v + x * 16);
+      }
+      ++n_cp;
+      cp.g += W;
+      next_row = settle();
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll 1
+  for (int i = 0; i < NS - 1; ++i) copy();
+
+  // ------------------------------------------------------------------ items
+  GroupWalk<R, W> u;
+  u.w.begin(a, work);
+  int seg = 0;
+  for (; u.w.live(); u.w.next(a), ++seg) {
+    const SegmentWalk<R, 32>& w = u.w;
+    const int rows = w.rows(), row0 = w.j * R, first = w.sp.len - w.sp.n_new;
+    // queries in operand order: lane (g, t) of product ks holds rows g and g + 8
+    for (int x = tid; x < MT * KS * 32; x += G::NT) {
+      const int mt = x / (KS * 32), ks = x / 32 % KS, xl = x & 31, xg = xl >> 2, xt = xl & 3;
+      const int e0 = Q8 ? (xt + 4 * (ks >> 2)) * 16 + 4 * (ks & 3) : ks * 16 + xt * 2, e1 = e0 + (Q8 ? 2 : 8);
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int rr = mt * 16 + xg + (i & 1) * 8, r = row0 + rr;
+        hi[i] = lo[i] = 0;
+        if (rr < rows) {
+          const int64_t at = (w.sp.t0 + r / a.group) * a.q_ld + (w.head * a.group + r % a.group) * HD + (i < 2 ? e0 : e1);
+          if (QF32) {
+            const float2 f = __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(a.q) + at));
+            const __half2 h = __floats2half2_rn(f.x, f.y);
+            const float2 b = __half22float2(h);
+            hi[i] = as_u32(h);
+            lo[i] = as_u32(__floats2half2_rn(f.x - b.x, f.y - b.y));
+          } else {
+            hi[i] = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const __half*>(a.q) + at));
+          }
+        }
+      }
+      s_q[(mt * (QF32 ? 2 : 1) * KS + ks) * 32 + xl] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      if (QF32) s_q[((mt * 2 + 1) * KS + ks) * 32 + xl] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    int p[MT][2];              // positions of this lane's rows
+    float m[MT][2], l[MT][2], o[MT][HD / 8][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int rr = mt * 16 + g + h * 8;
+        p[mt][h] = rr < rows ? first + (row0 + rr) / a.group : -1;
+        m[mt][h] = -INFINITY, l[mt][h] = 0.f;
+      }
+#pragma unroll
+      for (int n = 0; n < HD / 8; ++n) o[mt][n][0] = o[mt][n][1] = o[mt][n][2] = o[mt][n][3] = 0.f;
+    }
+    __syncthreads();           // queries are there
+    u.count();
+    bool found = false;
+    for (u.g = warp; u.g < u.n; u.g += W) {
+      copy();
+      pr_wait<NS - 1>();
+      __syncwarp();
+      const int stage = n_use % NS;
+      ++n_use;
+      const uint32_t at = ring + stage * G::STAGE;
+      const int base = u.base();
+      if (c->row[warp][stage] >= 0) {
+        // ---- scores
+        float s[MT][2][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.f;
+        auto product = [&](int ks, const uint32_t (&b)[2][2]) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int part = 0; part < (QF32 ? 2 : 1); ++part) {
+              const uint4 q = s_q[((mt * (QF32 ? 2 : 1) + part) * KS + ks) * 32 + lane];
+#pragma unroll
+              for (int nt = 0; nt < 2; ++nt) pr_mma(s[mt][nt], q, b[nt][0], b[nt][1]);
+            }
+        };
+        if (!Q8) {
+#pragma unroll
+          for (int k2 = 0; k2 < KS / 2; ++k2) {
+            uint32_t r[2][4];
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) pr_ldsm(r[nt], at + place<ROW, false>(nt * 8 + (lane & 7), k2 * 4 + (lane >> 3)));
+            const uint32_t b0[2][2] = {{r[0][0], r[0][1]}, {r[1][0], r[1][1]}};
+            const uint32_t b1[2][2] = {{r[0][2], r[0][3]}, {r[1][2], r[1][3]}};
+            product(2 * k2, b0);
+            product(2 * k2 + 1, b1);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < HD / 64; ++j) {
+            __half2 h[2][8];
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+              const uint4 q = pr_lds16(at + place<ROW, true>(nt * 8 + g, t + 4 * j));
+              uint16_t d;
+              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(d) : "r"(at + 32 * ROW + (nt * 8 + g) * (HD / 16) + ((t >> 1) + 2 * j) * 2) : "memory");
+              const __half2 d2 = __half2half2(__ushort_as_half(d));
+              q8_values4(q.x, d2, h[nt][0], h[nt][1]);
+              q8_values4(q.y, d2, h[nt][2], h[nt][3]);
+              q8_values4(q.z, d2, h[nt][4], h[nt][5]);
+              q8_values4(q.w, d2, h[nt][6], h[nt][7]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t b[2][2] = {{as_u32(h[0][2 * k]), as_u32(h[0][2 * k + 1])}, {as_u32(h[1][2 * k]), as_u32(h[1][2 * k + 1])}};
+              product(4 * j + k, b);
+            }
+          }
+        }
+        const bool whole = base + 15 <= w.it.p0 && (!a.window || base > w.it.p1 - a.window || base + 16 <= a.sinks);
+        if (!whole) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int pr = p[mt][(e >> 1) & 1], x = base + (e >> 2) * 8 + 2 * t + (e & 1);
+              if (x > pr || (a.window && x <= pr - a.window && x >= a.sinks)) s[mt][e >> 2][e & 3] = -INFINITY;
+            }
+        }
+        // ---- weights
+        uint4 pw[MT];
+        float top[MT][2];
+        bool raise = false;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float x = fmaxf(fmaxf(s[mt][0][2 * h], s[mt][0][2 * h + 1]), fmaxf(s[mt][1][2 * h], s[mt][1][2 * h + 1]));
+            x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
+            x = fmaxf(x, __shfl_xor_sync(~0u, x, 2)) * a.scale;
+            top[mt][h] = x;
+            raise |= x > m[mt][h] + 8.f || (m[mt][h] == -INFINITY && x > m[mt][h]);
+          }
+        if (__any_sync(~0u, raise)) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            float f[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float m2 = fmaxf(m[mt][h], top[mt][h]);
+              f[h] = m2 == m[mt][h] ? 1.f : pr_exp2(m[mt][h] - m2);
+              m[mt][h] = m2;
+              l[mt][h] *= f[h];
+            }
+#pragma unroll
+            for (int n = 0; n < HD / 8; ++n)
+              o[mt][n][0] *= f[0], o[mt][n][1] *= f[0], o[mt][n][2] *= f[1], o[mt][n][3] *= f[1];
+          }
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          uint32_t x[2][2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float mm = m[mt][h] == -INFINITY ? 0.f : m[mt][h];
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+              const float w0 = pr_exp2(fmaf(s[mt][nt][2 * h], a.scale, -mm)), w1 = pr_exp2(fmaf(s[mt][nt][2 * h + 1], a.scale, -mm));
+              l[mt][h] += w0 + w1;
+              x[nt][h] = as_u32(__floats2half2_rn(w0, w1));
+            }
+          }
+          pw[mt] = make_uint4(x[0][0], x[0][1], x[1][0], x[1][1]);
+        }
+        // ---- values
+        const int vr = (lane & 7) + (lane & 8);
+        __half2 d0[HD / 32], d1[HD / 32];       // Q8: scales of positions 2t, 2t + 1 and of 8 further on
+        if (Q8) {
+          const uint32_t sc = at + 32 * ROW + G::SC;
+#pragma unroll
+          for (int b = 0; b < HD / 32; ++b) {
+            uint16_t x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x[i]) : "r"(sc + (2 * t + (i & 1) + (i >> 1) * 8) * (HD / 16) + b * 2) : "memory");
+            d0[b] = __halves2half2(__ushort_as_half(x[0]), __ushort_as_half(x[1]));
+            d1[b] = __halves2half2(__ushort_as_half(x[2]), __ushort_as_half(x[3]));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < PIECES / 2; ++i) {
+          uint32_t r[4];
+          pr_ldsm_t(r, at + 16 * ROW + place<ROW, false>(vr, 2 * i + (lane >> 4)));
+          if (!Q8) {
+            if (!whole) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) r[e] = pr_finite(r[e], &found);
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              pr_mma(o[mt][2 * i], pw[mt], r[0], r[1]);
+              pr_mma(o[mt][2 * i + 1], pw[mt], r[2], r[3]);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {       // 16 codes' even and odd columns, of two pieces
+              const int pc = 2 * i + (e >> 1);
+              const uint32_t sel = (e & 1) ? 0x4341u : 0x4240u;
+              uint32_t b0 = as_u32(__hmul2(q8_pair(r[(e >> 1) * 2] ^ 0x80808080u, sel), d0[pc / 2]));
+              uint32_t b1 = as_u32(__hmul2(q8_pair(r[(e >> 1) * 2 + 1] ^ 0x80808080u, sel), d1[pc / 2]));
+              if (!whole) b0 = pr_finite(b0, &found), b1 = pr_finite(b1, &found);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) pr_mma(o[mt][2 * pc + (e & 1)], pw[mt], b0, b1);
+            }
+          }
+        }
+      }
+      __syncwarp();            // the stage may be written again
+    }
+    if (found) *reinterpret_cast<volatile int*>(&c->bad) = seg + 1;
+    // ---- the warps' results meet, 16 rows at a time
+    const bool whole_item = w.i0 == 0 && w.i1 == w.it.cnt;
+    const int slot = w.i0 == 0 ? 1 : 0;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      float* mine = s_o + warp * 16 * G::PITCH;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int rr = g + h * 8;
+        float sum = l[mt][h];
+        sum += __shfl_xor_sync(~0u, sum, 1);
+        sum += __shfl_xor_sync(~0u, sum, 2);
+        if (t == 0) s_m[warp * R + mt * 16 + rr] = m[mt][h], s_l[warp * R + mt * 16 + rr] = sum;
+        if (!Q8) {
+#pragma unroll
+          for (int n = 0; n < HD / 8; ++n)
+            *reinterpret_cast<float2*>(mine + rr * G::PITCH + n * 8 + 2 * t) = make_float2(o[mt][n][2 * h], o[mt][n][2 * h + 1]);
+        } else {
+#pragma unroll
+          for (int pc = 0; pc < HD / 16; ++pc)
+            *reinterpret_cast<float4*>(mine + rr * G::PITCH + pc * 16 + 4 * t) =
+                make_float4(o[mt][2 * pc][2 * h], o[mt][2 * pc + 1][2 * h], o[mt][2 * pc][2 * h + 1], o[mt][2 * pc + 1][2 * h + 1]);
+        }
+      }
+      __syncthreads();
+      const bool bad = c->bad == seg + 1;
+      const int n_rows = min(16, rows - mt * 16);
+      for (int x = tid; x < n_rows * (HD / 4); x += G::NT) {
+        const int rr = x / (HD / 4), e = x % (HD / 4) * 4, r = row0 + mt * 16 + rr;
+        float top = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < W; ++k) top = fmaxf(top, s_m[k * R + mt * 16 + rr]);
+        float sum = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+          const float mk = s_m[k * R + mt * 16 + rr], f = mk == -INFINITY ? 0.f : pr_exp2(mk - top);
+          const float4 y = *reinterpret_cast<const float4*>(s_o + (k * 16 + rr) * G::PITCH + e);
+          sum += s_l[k * R + mt * 16 + rr] * f;
+          v[0] += y.x * f, v[1] += y.y * f, v[2] += y.z * f, v[3] += y.w * f;
+        }
+        if (bad) {
+          // values that were taken out of groups seen in part: back into the rows that see them
+          const int pr = first + r / a.group;
+          for (int i = w.i0; i < w.i1; ++i)
+            for (int b = 0; b < 2; ++b) {
+              const int base = w.it.tile(i) * 32 + b * 16;
+              if (base + 15 <= w.it.p0 && (!a.window || base > w.it.p1 - a.window || base + 16 <= a.sinks)) continue;
+              for (int q = base; q < base + 16 && q <= pr; ++q) {
+                if (a.window && q <= pr - a.window && q >= a.sinks) continue;
+                const int vrow = paged_row(a.kv, a.b, w.seq, q, w.head);
+                if (vrow < 0) continue;
+                for (int k = 0; k < 4; ++k) {
+                  const size_t from = static_cast<size_t>(vrow) * HD + e + k;
+                  const __half h = Q8 ? __hmul(__int2half_rn(static_cast<const int8_t*>(a.kv.v)[from]), a.kv.vs[from / 32])
+                                      : static_cast<const __half*>(a.kv.v)[from];
+                  if (__hisinf(h) || __hisnan(h)) v[k] += __half2float(h);
+                }
+              }
+            }
+        }
+        if (whole_item) {
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          __half* out = a.out + static_cast<int64_t>(w.sp.t0 + r / a.group) * a.out_ld + (w.head * a.group + r % a.group) * HD + e;
+          const uint2 y = make_uint2(as_u32(__floats2half2_rn(v[0] * inv, v[1] * inv)), as_u32(__floats2half2_rn(v[2] * inv, v[3] * inv)));
+          *reinterpret_cast<uint2*>(out) = y;
+        } else {
+          *reinterpret_cast<float4*>(parts.out(blockIdx.x, slot) + static_cast<size_t>(mt * 16 + rr) * HD + e) =
+              make_float4(v[0], v[1], v[2], v[3]);
+          if (e == 0) {
+            parts.max(blockIdx.x, slot)[mt * 16 + rr] = top;
+            parts.sum(blockIdx.x, slot)[mt * 16 + rr] = sum;
+          }
+        }
+      }
+      if (mt + 1 < MT) __syncthreads();        // the next item's queries are waited for anyway
+    }
+  }
+  if (tid == 0) *parts.record(blockIdx.x) = join_record<R, 32>(a, work);
+}
+
+template <int HD, int MT, bool QF32, bool Q8>
+cudaError_t prepare_rows() {
+  return cudaFuncSetAttribute(paged_rows_kernel<HD, MT, QF32, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Pr<HD, MT, QF32, Q8>::SMEM);
+}
+
+template <int HD, int MT>
+cudaError_t prepare_mt() {
+  const cudaError_t e[4] = {prepare_rows<HD, MT, false, false>(), prepare_rows<HD, MT, false, true>(),
+                            prepare_rows<HD, MT, true, false>(), prepare_rows<HD, MT, true, true>()};
+  for (cudaError_t x : e)
+    if (x != cudaSuccess) return x;
+  return cudaSuccess;
+}
+
+template <int HD, int MT, bool QF32, bool Q8>
+cudaError_t launch_rows(const PagedAttnArgs& a, void* ws, int grid, cudaStream_t s) {
+  using G = Pr<HD, MT, QF32, Q8>;
+  PartSlots parts{static_cast<char*>(ws), G::R, HD};
+  paged_rows_kernel<HD, MT, QF32, Q8><<<grid, G::NT, G::SMEM, s>>>(a, parts);
+  const cudaError_t e = cudaGetLastError();
+  return e != cudaSuccess ? e : paged_join_launch(a, parts, grid, s);
+}
+
+template <int HD, int MT>
+cudaError_t launch_mt(const PagedAttnArgs& a, bool f32, bool q8, void* ws, int grid, cudaStream_t s) {
+  if (f32) return q8 ? launch_rows<HD, MT, true, true>(a, ws, grid, s) : launch_rows<HD, MT, true, false>(a, ws, grid, s);
+  return q8 ? launch_rows<HD, MT, false, true>(a, ws, grid, s) : launch_rows<HD, MT, false, false>(a, ws, grid, s);
+}
+
+}  // namespace
+
+cudaError_t paged_rows_prepare() {
+  const cudaError_t e[6] = {prepare_mt<64, 1>(), prepare_mt<64, 2>(), prepare_mt<128, 1>(), prepare_mt<128, 2>(),
+                            prepare_mt<192, 1>(), prepare_mt<256, 1>()};
+  for (cudaError_t x : e)
+    if (x != cudaSuccess) return x;
+  return cudaSuccess;
+}
+
+cudaError_t paged_rows_launch(const PagedAttnArgs& a, bool q_f32, bool q8, int rows, void* ws, int grid, cudaStream_t s) {
+  switch (a.kv.hd) {
+    case 64: return rows <= 16 ? launch_mt<64, 1>(a, q_f32, q8, ws, grid, s) : launch_mt<64, 2>(a, q_f32, q8, ws, grid, s);
+    case 128: return rows <= 16 ? launch_mt<128, 1>(a, q_f32, q8, ws, grid, s) : launch_mt<128, 2>(a, q_f32, q8, ws, grid, s);
+    case 192: return launch_mt<192, 1>(a, q_f32, q8, ws, grid, s);
+    default: return launch_mt<256, 1>(a, q_f32, q8, ws, grid, s);
+  }
+}
+
+}  // namespace q4

@@ -192,6 +192,21 @@ struct JoinRecord {
 constexpr size_t kPagedRecordBytes = kPagedMaxCtas * 32;
 static_assert(sizeof(JoinRecord) <= 32, "records are 32 bytes apart");
 
+// The record of a CTA that did `work`.
+template <int R, int BN>
+__device__ JoinRecord join_record(const PagedAttnArgs& a, const CtaWork& work) {
+  JoinRecord rec = {};
+  SegmentWalk<R, BN> g;
+  for (g.begin(a, work); g.live(); g.next(a)) {
+    if (g.left > g.i1 - g.i0) continue;
+    if (g.i0 == 0 && g.i1 < g.it.cnt) {       // the last segment begins an item and does not finish it
+      rec.n = 1 + static_cast<int>((g.it.cnt - g.i1 + work.per - 1) / work.per);
+      rec.t0 = g.sp.t0, rec.row0 = g.j * R, rec.rows = g.rows(), rec.head = g.head;
+    }
+  }
+  return rec;
+}
+
 struct PartSlots {
   char* base;
   int rows, hd;             // R and head_dim
@@ -208,6 +223,9 @@ struct PartSlots {
 // Launchers.  ws: the workspace; grid: CTAs, at most kPagedMaxCtas.
 cudaError_t paged_tile_prepare();
 cudaError_t paged_tile_launch(const PagedAttnArgs& a, bool q_f32, bool q8, void* ws, int grid, cudaStream_t s);
+// For items of few rows: `rows` query rows of a head at most, as far as is known.
+cudaError_t paged_rows_prepare();
+cudaError_t paged_rows_launch(const PagedAttnArgs& a, bool q_f32, bool q8, int rows, void* ws, int grid, cudaStream_t s);
 // Joins the parts that a kernel of `grid` CTAs left (q4_paged_join.cu).
 cudaError_t paged_join_launch(const PagedAttnArgs& a, const PartSlots& parts, int grid, cudaStream_t s);
 

@@ -604,23 +604,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_tile_kernel(const __grid_
       }
     }
   }
-  // an item begun here and not finished: who holds the rest
-  if (tid == 0) {
-    SegmentWalk<R, BN> g;
-    g.begin(a, work);
-    JoinRecord rec = {};
-    while (g.live()) {
-      if (g.left == g.i1 - g.i0) {       // the last segment
-        if (g.i0 == 0 && g.i1 < g.it.cnt) {
-          rec.n = 1 + static_cast<int>((g.it.cnt - g.i1 + work.per - 1) / work.per);
-          rec.t0 = g.sp.t0, rec.row0 = g.j * R, rec.rows = g.rows(), rec.head = g.head;
-        }
-        break;
-      }
-      g.next(a);
-    }
-    *parts.record(blockIdx.x) = rec;
-  }
+  if (tid == 0) *parts.record(blockIdx.x) = join_record<R, BN>(a, work);
   __syncwarp();
   tm_before();
   __syncthreads();
