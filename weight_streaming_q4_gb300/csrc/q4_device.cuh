@@ -532,6 +532,10 @@ cudaError_t mma_read_status(int* out);
 // elements, box tc_pitch(k) / 8 columns by box_rows rows); false if the
 // driver cannot encode it.
 bool encode_q4_rows(CUtensorMap* m, const uint8_t* w, int n_rows, int k, int box_rows);
+// Host: the TMA descriptor of rows of `cols` binary16 values (cols a multiple of
+// 64), box 64 columns by box_rows rows, stored with the 128-byte swizzle; false
+// if the driver cannot encode it.
+bool encode_f16_rows(CUtensorMap* m, const void* base, int64_t rows, int cols, int box_rows);
 // Glue launches; pdl as for mma_launch (each glue kernel waits for its inputs first).
 cudaError_t glue_norm(const uint16_t* src16, const float* src32, int batch, int dim, float eps, uint16_t* z,
                       cudaStream_t s, bool pdl = false);

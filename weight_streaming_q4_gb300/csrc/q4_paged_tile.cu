@@ -17,15 +17,17 @@
 // Warps 0-3 and 4-7: the softmax of query tile 0 and 1; warps 8-10 fill the ring
 // of key and value tiles; warp 11 issues the products.
 //
-// Keys and values go through the threads, not TMA: a tile is made of pages,
-// positions outside what the item's rows see must arrive as zeros (a stale or
-// later value may be NaN, and 0 * NaN is NaN in the product), and Q8 codes
-// become binary16 on the way.  Binary16 pages are copied with 16-byte cp.async
-// (zero-filling); Q8 codes are copied into a staging ring of which each thread
-// reads back its own pieces, so that it needs no barrier, and stored as
-// f16(code * d).  In a tile that some rows see only in part, values that are
-// not finite are taken out (zero) and noted; the rows that do see them get them
-// added at the end.
+// A tile is made of pieces of pages.  Binary16: a tensor copy (TMA, 128-byte
+// swizzle) per 64 columns and page or 16 .. BN rows of it, issued by the lanes of
+// warp 8 side by side; a copy through the threads (16-byte cp.async) took 6700
+// cycles a tile where the products take 2050.  Q8: bulk copies of codes and
+// scales into a staging ring, from which warps 8-10 store f16(code * d).
+// Positions that no row of the item sees must count as zeros in the product with
+// P = 0 (a stale or later value may be NaN, and 0 * NaN is NaN), and so must
+// values that are not finite in a tile that some rows see only in part: such
+// tiles (the last one or two of an item, a window's edge, holes) are cleaned in
+// shared memory, what was not finite is noted, and the rows that do see it get
+// it added at the end.  Keys need no cleaning: their scores are replaced.
 //
 // Precision: binary16 queries enter as they are, fp32 queries as two binary16
 // parts (22 bits; two products into the same S); P is rounded to binary16
@@ -121,14 +123,6 @@ __device__ __forceinline__ uint64_t mma_sdesc(uint32_t addr, uint32_t lead) {
          (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
-__device__ __forceinline__ void cp16_zfill(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 // What the threads stored in shared memory becomes visible to the tensor cores.
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -152,16 +146,30 @@ struct Pt {
   static constexpr int KB = BN * HD * 2;                // bytes of a key or value tile
   static constexpr int LIMIT = 232448 - 1024 - 1024;    // control data, and the alignment of the tiles
   static constexpr int QALL = QB * (QF32 ? 2 : NQ);
-  static constexpr int FIT = (LIMIT - QALL) / KB;
+  static constexpr int RAW = Q8 ? BN * HD + BN * HD / 16 : 0;   // a staged Q8 tile: codes, then scales
+  static constexpr int NRAW = !Q8 ? 0 : (LIMIT - QALL - 2 * RAW) / KB >= 2 ? 2 : 1;
+  static constexpr int FIT = (LIMIT - QALL - NRAW * RAW) / KB;
   static constexpr int NS = FIT > 8 ? 8 : FIT;          // ring of key and value tiles
-  static constexpr int SMEM = 2048 + QALL + NS * KB;
+  static constexpr int SMEM = 2048 + QALL + NS * KB + NRAW * RAW;
   static constexpr int O_COL = NQ == 2 ? 256 : 128;     // tensor memory columns: S of tile q at q * 128, then O
   static constexpr int CHUNKS = KB / 16;                // 16-byte pieces of a tile
-  static_assert(NS >= 3, "the ring holds a key and a value tile and the next key tile");
+  // registers per thread after the split: softmax warpgroups, the others
+  static constexpr int REG_S = NQ == 2 ? 208 : 232, REG_O = NQ == 2 ? 88 : 96;
+  static constexpr int REGS = (NQ * REG_S + (3 - NQ) * REG_O) * 128;
+  static_assert(NS >= 2, "the ring holds a key and a value tile");
+};
+
+// Tensor copies of binary16 pages: rows of HD values, boxes of 64 values by
+// 2^box_log2 rows.
+struct PtMaps {
+  CUtensorMap k, v;
+  int box_log2;
 };
 
 struct PtCtl {
   uint64_t full[8], empty[8], q_full[2], s_full[2], p_full[2], o_full[2];
+  uint64_t fixed[8];       // the value tile in a ring slot has been looked at, and cleaned if need be
+  uint64_t raw[2];         // a staged Q8 tile has landed
   uint32_t tmem;
   int dead;
   int bad[8];              // segment number (+ 1) in whose values the loaders met infinities or NaN, by number mod 8
@@ -204,7 +212,8 @@ __device__ __forceinline__ TileView tile_view(const PagedAttnArgs& a, const Item
 // ------------------------------------------------------------------ kernel
 
 template <int HD, bool QF32, bool Q8>
-__global__ void __launch_bounds__(kPtThreads, 1) paged_tile_kernel(const __grid_constant__ PagedAttnArgs a, PartSlots parts) {
+__global__ void __launch_bounds__(kPtThreads, 1)
+    paged_tile_kernel(const __grid_constant__ PagedAttnArgs a, PartSlots parts, const __grid_constant__ PtMaps maps) {
   using G = Pt<HD, QF32, Q8>;
   constexpr int BN = G::BN, NQ = G::NQ, R = G::R, NS = G::NS;
   extern __shared__ char smem_raw[];
@@ -216,13 +225,14 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_tile_kernel(const __grid_
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) {
-    for (int i = 0; i < NS; ++i) mbar_init(&c->full[i], 3), mbar_init(&c->empty[i], 1);
+    for (int i = 0; i < NS; ++i) mbar_init(&c->full[i], Q8 ? 3 : 1), mbar_init(&c->empty[i], 1), mbar_init(&c->fixed[i], 2);
     for (int q = 0; q < 2; ++q) {
       mbar_init(&c->q_full[q], 128);
       mbar_init(&c->s_full[q], 1);
       mbar_init(&c->p_full[q], 128);
       mbar_init(&c->o_full[q], 1);
     }
+    mbar_init(&c->raw[0], 1), mbar_init(&c->raw[1], 1);
     c->dead = 0;
     for (int i = 0; i < 8; ++i) c->bad[i] = 0;
     fence_mbar_init();
@@ -237,6 +247,10 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_tile_kernel(const __grid_
   SegmentWalk<R, BN> w;
   w.begin(a, work);
 
+  if (warp < 4 * NQ)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::REG_S));
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::REG_O));
   if (warp < 4 * NQ) {
     // ---------------------------------------------------------------- softmax of query tile q
     const int q = warp >> 2, wl = warp & 3;
@@ -413,105 +427,158 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_tile_kernel(const __grid_
     }
   } else if (warp >= 8 && warp < 11) {
     // ---------------------------------------------------------------- key and value tiles
-    const int lt = tid - 8 * 32;
-    constexpr int LAG = Q8 ? 0 : (NS > 4 ? 3 : NS - 2);       // copies in flight behind the one being issued
-    uint32_t n = 0;                                            // tiles issued (keys and values)
-    // binary16: tiles whose copies are under way, newest last
-    struct Pending {
-      bool check;
-      int seg;
-    } pend[LAG + 1];
-    auto finish = [&](uint32_t at, bool check, int seg) {      // tile number `at` has landed (this thread's pieces)
-      if (check) {
-        bool found = false;
-        for (int x = lt; x < G::CHUNKS; x += kPtLoaders) {
-          const int row = x / (HD / 8), pc = x % (HD / 8);
-          uint4* v = reinterpret_cast<uint4*>(tiles + G::QALL + (at % NS) * G::KB + (pc >> 3) * (BN * 128) + row * 128 +
-                                              (((pc & 7) ^ (row & 7)) << 4));
-          uint4 u = *v;
-          if (h2_bad(u.x) || h2_bad(u.y) || h2_bad(u.z) || h2_bad(u.w)) {
-            __half* h = reinterpret_cast<__half*>(&u);
+    constexpr uint32_t ALL = (1u << (BN / 16)) - 1;
+    const int bl = Q8 ? min(a.kv.page_log2, BN == 128 ? 7 : 6) : maps.box_log2;   // rows of a piece of a page: 2^bl
+    constexpr int COLS = Q8 ? 1 : HD / 64;                                       // copies per piece
+    // Piece `lane / COLS` of tile i of the walk's item: its page-memory row, or -1 (not there, or seen by no row)
+    auto lookup = [&](const SegmentWalk<R, BN>& g, int i) {
+      const int base = g.it.tile(i) * BN, t = base + ((lane / COLS) << bl);
+      if ((lane / COLS) << bl >= BN || t > g.it.p1) return -1;
+      if (a.window && t + (1 << bl) <= max(g.it.p0, 0) - a.window + 1 && t >= a.sinks) return -1;
+      return paged_row(a.kv, a.b, g.seq, t, g.head);
+    };
+    // bit r / 16: rows r .. of the tile are in a page (and seen)
+    auto there_of = [&](int row) {
+      const int at = __shfl_sync(~0u, row, (((lane & 7) << 4) >> bl) * COLS);
+      return __ballot_sync(~0u, at >= 0) & ALL;
+    };
+    if (!Q8 && warp == 8) {
+      uint32_t n = 0;                                            // tiles issued (keys and values)
+      int row = w.live() ? lookup(w, w.i0) : -1;
+      while (w.live()) {
+        for (int i = w.i0; i < w.i1; ++i) {
+          const int now = row;
+          if (i + 1 < w.i1) row = lookup(w, i + 1);              // the next tile's page entries on their way
+          const uint32_t there = there_of(now);
+          const uint32_t bytes = __popc(__ballot_sync(~0u, now >= 0)) << (bl + 7);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (__hisinf(h[e]) || __hisnan(h[e])) h[e] = __ushort_as_half(0);
-            *v = u;
-            found = true;
+          for (int kv = 0; kv < 2; ++kv, ++n) {
+            const uint32_t slot = n % NS;
+            pt_wait_warp(c, &c->empty[slot], ((n / NS) & 1) ^ 1);
+            if (lane == 0) {
+              if (kv == 0) *reinterpret_cast<volatile uint32_t*>(&c->there[(n / 2) & 7]) = there;
+              mbar_arrive_expect_tx(&c->full[slot], bytes);
+            }
+            __syncwarp();
+            if (now >= 0)
+              tma_load_2d(tiles + G::QALL + slot * G::KB + (lane % COLS) * (BN * 128) + ((lane / COLS) << (bl + 7)),
+                          kv ? &maps.v : &maps.k, (lane % COLS) * 64, now, &c->full[slot]);
           }
         }
-        if (found) *reinterpret_cast<volatile int*>(&c->bad[seg & 7]) = seg + 1;
+        w.next(a);
+        if (w.live()) row = lookup(w, w.i0);
       }
-      fence_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&c->full[at % NS]);
-    };
-    // The page-memory row of rows 16 * lane .. of key tile `base` of the walk's item (-1: not to be read)
-    auto lookup = [&](const SegmentWalk<R, BN>& g, int base) {
-      const int t = base + lane * 16;
-      return lane < BN / 16 && t <= g.it.p1 ? paged_row(a.kv, a.b, g.seq, t, g.head) : -1;
-    };
-    int seg = 0;
-    int row16 = w.live() ? lookup(w, w.it.tile(w.i0) * BN) : -1;
-    while (w.live()) {
-      for (int i = w.i0; i < w.i1; ++i) {
-        const TileView tv = tile_view<BN>(a, w.it, i);
-        const int my16 = row16;
-        // the next tile's page entries, while this one is copied
-        if (i + 1 < w.i1) row16 = lookup(w, w.it.tile(i + 1) * BN);
-        const uint32_t there = __ballot_sync(~0u, my16 >= 0) & ((1u << (BN / 16)) - 1);
-        // of the tile, positions that some row sees
-        const int last = w.it.p1 - tv.base, first = a.window ? max(w.it.p0, 0) - a.window + 1 - tv.base : 0, sk = a.sinks - tv.base;
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv, ++n) {
-          const uint32_t slot = n % NS;
-          pt_wait_warp(c, &c->empty[slot], ((n / NS) & 1) ^ 1);
-          if (kv == 0 && lt == 0) *reinterpret_cast<volatile uint32_t*>(&c->there[(n / 2) & 7]) = there;
-          const uint32_t dst = s_ring + slot * G::KB;
-          if (!Q8) {
-            const __half* src = static_cast<const __half*>(kv ? a.kv.v : a.kv.k);
+    } else if (!Q8) {
+      // value tiles to be cleaned, by warps 9 and 10
+      uint32_t n = 1;
+      int seg = 0;
+      for (; w.live(); w.next(a), ++seg) {
+        for (int i = w.i0; i < w.i1; ++i, n += 2) {
+          pt_wait_warp(c, &c->full[n % NS], (n / NS) & 1);
+          const TileView tv = tile_view<BN>(a, w.it, i);
+          const uint32_t there = *reinterpret_cast<volatile uint32_t*>(&c->there[(n / 2) & 7]);
+          if (tv.whole && there == ALL) {
+            if (lane == 0) mbar_arrive(&c->fixed[n % NS]);
+            continue;
+          }
+          const int last = w.it.p1 - tv.base, first = a.window ? max(w.it.p0, 0) - a.window + 1 - tv.base : 0, sk = a.sinks - tv.base;
+          bool found = false;
 #pragma unroll 4
-            for (int x0 = 0; x0 < G::CHUNKS; x0 += kPtLoaders) {
-              const int x = x0 + lt;
-              const int row = x / (HD / 8), pc = x % (HD / 8);
-              const int r0 = __shfl_sync(~0u, my16, (row >> 4) & 31);
-              if (x < G::CHUNKS) {
-                const bool ok = r0 >= 0 && row <= last && (row >= first || row < sk);
-                cp16_zfill(dst + (pc >> 3) * (BN * 128) + row * 128 + (((pc & 7) ^ (row & 7)) << 4),
-                           src + (ok ? static_cast<size_t>(r0 + (row & 15)) * HD + pc * 8 : 0), ok);
-              }
-            }
-            cp_commit();
+          for (int x = tid - 9 * 32; x < G::CHUNKS; x += 64) {
+            const int row = x / (HD / 8), pc = x % (HD / 8);
+            uint4* v = reinterpret_cast<uint4*>(tiles + G::QALL + (n % NS) * G::KB + (pc >> 3) * (BN * 128) + row * 128 +
+                                                (((pc & 7) ^ (row & 7)) << 4));
+            if (((there >> (row >> 4)) & 1) && row <= last && (row >= first || row < sk)) {
+              uint4 u = *v;
+              if (h2_bad(u.x) || h2_bad(u.y) || h2_bad(u.z) || h2_bad(u.w)) {
+                __half* h = reinterpret_cast<__half*>(&u);
 #pragma unroll
-            for (int k = 0; k < LAG; ++k) pend[k] = pend[k + 1];
-            pend[LAG] = {kv == 1 && !tv.whole, seg};
-            if (static_cast<int>(n) >= LAG) {
-              cp_wait<LAG>();
-              finish(n - LAG, pend[0].check, pend[0].seg);
+                for (int e = 0; e < 8; ++e)
+                  if (__hisinf(h[e]) || __hisnan(h[e])) h[e] = __ushort_as_half(0);
+                *v = u;
+                found = true;
+              }
+            } else {
+              *v = make_uint4(0, 0, 0, 0);
             }
-          } else {
-            const int8_t* src = static_cast<const int8_t*>(kv ? a.kv.v : a.kv.k);
-            const __half* sc = kv ? a.kv.vs : a.kv.ks;
+          }
+          if (found) *reinterpret_cast<volatile int*>(&c->bad[seg & 7]) = seg + 1;
+          fence_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&c->fixed[n % NS]);
+        }
+      }
+    } else {
+      // Q8: staged codes to binary16, by warps 8 to 10; warp 8 also issues the staging copies
+      const int lt = tid - 8 * 32;
+      constexpr int PIECES = BN * HD / 16;               // 16 codes each
+      char* const raw = tiles + G::QALL + NS * G::KB;
+      constexpr int NRAW = G::NRAW > 0 ? G::NRAW : 1;
+      // the staging copies' own walk, NRAW tiles ahead
+      SegmentWalk<R, BN> cp = w;
+      int ci = cp.live() ? cp.i0 : 0, row = -1, kv_next = 0;
+      uint32_t n_raw = 0;
+      if (warp == 8 && cp.live()) row = lookup(cp, ci);
+      auto stage = [&]() {                               // the next tile's codes and scales (warp 8)
+        if (!cp.live()) return;
+        char* to = raw + n_raw % NRAW * G::RAW;
+        uint64_t* bar = &c->raw[n_raw % NRAW];
+        const uint32_t got = __popc(__ballot_sync(~0u, row >= 0));
+        const uint32_t there = there_of(row);
+        if (lane == 0) {
+          if (kv_next == 0) *reinterpret_cast<volatile uint32_t*>(&c->there[(n_raw / 2) & 7]) = there;
+          mbar_arrive_expect_tx(bar, got * ((HD + HD / 16) << bl));
+        }
+        __syncwarp();
+        if (row >= 0) {
+          const size_t at = static_cast<size_t>(row) * HD;
+          bulk_g2s(to + (lane << bl) * HD, static_cast<const char*>(kv_next ? a.kv.v : a.kv.k) + at, HD << bl, bar);
+          bulk_g2s(to + BN * HD + (lane << bl) * (HD / 16), reinterpret_cast<const char*>(kv_next ? a.kv.vs : a.kv.ks) + at / 16,
+                   (HD / 16) << bl, bar);
+        }
+        ++n_raw;
+        if (kv_next++ == 0) return;
+        kv_next = 0;
+        if (++ci == cp.i1) {
+          cp.next(a);
+          if (cp.live()) ci = cp.i0;
+        }
+        if (cp.live()) row = lookup(cp, ci);
+      };
+      if (warp == 8) {
+#pragma unroll 1
+        for (int k = 0; k < NRAW; ++k) stage();
+      }
+      uint32_t n = 0;                                    // tiles stored (keys and values)
+      int seg = 0;
+      for (; w.live(); w.next(a), ++seg) {
+        for (int i = w.i0; i < w.i1; ++i) {
+          const TileView tv = tile_view<BN>(a, w.it, i);
+          const int last = w.it.p1 - tv.base, first = a.window ? max(w.it.p0, 0) - a.window + 1 - tv.base : 0, sk = a.sinks - tv.base;
+#pragma unroll 1
+          for (int kv = 0; kv < 2; ++kv, ++n) {
+            const uint32_t slot = n % NS;
+            pt_wait_warp(c, &c->raw[n % NRAW], (n / NRAW) & 1);
+            pt_wait_warp(c, &c->empty[slot], ((n / NS) & 1) ^ 1);
+            const uint32_t there = *reinterpret_cast<volatile uint32_t*>(&c->there[(n / 2) & 7]);
+            const bool clean = kv == 1 && !(tv.whole && there == ALL);
+            const char* from = raw + n % NRAW * G::RAW;
+            char* const dst = tiles + G::QALL + slot * G::KB;
             bool found = false;
-            const bool check = kv == 1 && !tv.whole;
-            constexpr int PIECES = BN * HD / 16;               // 16 codes each
 #pragma unroll 2
-            for (int x0 = 0; x0 < PIECES; x0 += kPtLoaders) {
-              const int x = x0 + lt;
+            for (int x = lt; x < PIECES; x += kPtLoaders) {
               const int row = x / (HD / 16), pc = x % (HD / 16);
-              const int r0 = __shfl_sync(~0u, my16, (row >> 4) & 31);
-              if (x >= PIECES) continue;
-              const bool ok = r0 >= 0 && row <= last && (row >= first || row < sk);
-              uint4 u[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-              if (ok) {
-                const size_t at = static_cast<size_t>(r0 + (row & 15)) * HD + pc * 16;
-                const uint4 codes = __ldg(reinterpret_cast<const uint4*>(src + at));
-                const __half2 d = __half2half2(sc[at / 32]);
-                __half2* h = reinterpret_cast<__half2*>(u);
-                q8_values4(codes.x, d, h[0], h[1]);
-                q8_values4(codes.y, d, h[2], h[3]);
-                q8_values4(codes.z, d, h[4], h[5]);
-                q8_values4(codes.w, d, h[6], h[7]);
-                if (check) {
-                  uint32_t* b = reinterpret_cast<uint32_t*>(u);
+              uint4 u[2];
+              const uint4 codes = *reinterpret_cast<const uint4*>(from + x * 16);
+              const __half2 d = __half2half2(*reinterpret_cast<const __half*>(from + BN * HD + (x >> 1) * 2));
+              __half2* h = reinterpret_cast<__half2*>(u);
+              q8_values4(codes.x, d, h[0], h[1]);
+              q8_values4(codes.y, d, h[2], h[3]);
+              q8_values4(codes.z, d, h[4], h[5]);
+              q8_values4(codes.w, d, h[6], h[7]);
+              if (clean) {
+                if (((there >> (row >> 4)) & 1) && row <= last && (row >= first || row < sk)) {
+                  const uint32_t* b = reinterpret_cast<const uint32_t*>(u);
                   bool any = false;
 #pragma unroll
                   for (int e = 0; e < 8; ++e) any |= h2_bad(b[e]);
@@ -522,32 +589,23 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_tile_kernel(const __grid_
                       if (__hisinf(he[e]) || __hisnan(he[e])) he[e] = __ushort_as_half(0);
                     found = true;
                   }
+                } else {
+                  u[0] = u[1] = make_uint4(0, 0, 0, 0);
                 }
               }
-              char* to = tiles + G::QALL + slot * G::KB + (pc >> 2) * (BN * 128) + row * 128;
-              const int p0 = (pc & 3) * 2;
-              *reinterpret_cast<uint4*>(to + ((p0 ^ (row & 7)) << 4)) = u[0];
-              *reinterpret_cast<uint4*>(to + (((p0 + 1) ^ (row & 7)) << 4)) = u[1];
+              // the two halves of a piece in an order that keeps 8 lanes' stores in different banks
+              char* to = dst + (pc >> 2) * (BN * 128) + row * 128;
+              const int odd = (pc >> 2) & 1, p0 = (pc & 3) * 2;
+              *reinterpret_cast<uint4*>(to + (((p0 + odd) ^ (row & 7)) << 4)) = odd ? u[1] : u[0];
+              *reinterpret_cast<uint4*>(to + (((p0 + 1 - odd) ^ (row & 7)) << 4)) = odd ? u[0] : u[1];
             }
             if (found) *reinterpret_cast<volatile int*>(&c->bad[seg & 7]) = seg + 1;
             fence_async();
-            __syncwarp();
+            asm volatile("bar.sync 1, %0;" ::"n"(kPtLoaders) : "memory");      // the staged tile is free again
             if (lane == 0) mbar_arrive(&c->full[slot]);
+            if (warp == 8) stage();
           }
         }
-      }
-      w.next(a);
-      ++seg;
-      if (w.live()) row16 = lookup(w, w.it.tile(w.i0) * BN);
-    }
-    if (!Q8) {
-      cp_wait<0>();
-      const uint32_t from = n > LAG ? n - LAG : 0;
-      // pend[k] belongs to tile n - 1 - LAG + k
-#pragma unroll
-      for (int k = 1; k <= LAG; ++k) {
-        const int at = static_cast<int>(n) - 1 - LAG + k;
-        if (at >= static_cast<int>(from)) finish(at, pend[k].check, pend[k].seg);
       }
     }
   } else if (warp == 11 && lane == 0) {
@@ -582,6 +640,8 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_tile_kernel(const __grid_
       for (int i = 0; i < cnt; ++i, n += 2) {
         const uint32_t v = n + 1, k_next = n + 2;
         pt_wait(c, &c->full[v % NS], (v / NS) & 1);
+        // (the turns of a slot that hold values: every one, or every other one of an odd ring)
+        if (!Q8) pt_wait(c, &c->fixed[v % NS], (NS & 1 ? v / (2 * NS) : v / NS) & 1);
         for (int q = 0; q < active; ++q) {
           pt_wait(c, &c->p_full[q], n_p[q] & 1);
           ++n_p[q];
@@ -616,6 +676,11 @@ __global__ void __launch_bounds__(kPtThreads, 1) paged_tile_kernel(const __grid_
 
 template <int HD, bool QF32, bool Q8>
 cudaError_t prepare_tile() {
+  // the warps' register split must fit what a block is launched with (it waits for registers otherwise)
+  cudaFuncAttributes at;
+  const cudaError_t e = cudaFuncGetAttributes(&at, paged_tile_kernel<HD, QF32, Q8>);
+  if (e != cudaSuccess) return e;
+  if ((at.numRegs + 7) / 8 * 8 * kPtThreads < Pt<HD, QF32, Q8>::REGS) return cudaErrorInvalidConfiguration;
   return cudaFuncSetAttribute(paged_tile_kernel<HD, QF32, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               Pt<HD, QF32, Q8>::SMEM);
 }
@@ -633,7 +698,15 @@ template <int HD, bool QF32, bool Q8>
 cudaError_t launch_tile(const PagedAttnArgs& a, void* ws, int grid, cudaStream_t s) {
   using G = Pt<HD, QF32, Q8>;
   PartSlots parts{static_cast<char*>(ws), G::R, HD};
-  paged_tile_kernel<HD, QF32, Q8><<<grid, kPtThreads, G::SMEM, s>>>(a, parts);
+  PtMaps maps = {};
+  if (!Q8) {
+    maps.box_log2 = a.kv.page_log2 < (G::BN == 128 ? 7 : 6) ? a.kv.page_log2 : (G::BN == 128 ? 7 : 6);
+    const int64_t rows = static_cast<int64_t>(a.kv.n_pages) * a.kv.n_kv << a.kv.page_log2;
+    if (!encode_f16_rows(&maps.k, a.kv.k, rows, HD, 1 << maps.box_log2) ||
+        !encode_f16_rows(&maps.v, a.kv.v, rows, HD, 1 << maps.box_log2))
+      return cudaErrorInvalidValue;
+  }
+  paged_tile_kernel<HD, QF32, Q8><<<grid, kPtThreads, G::SMEM, s>>>(a, parts, maps);
   const cudaError_t e = cudaGetLastError();
   return e != cudaSuccess ? e : paged_join_launch(a, parts, grid, s);
 }
