@@ -14,14 +14,14 @@
 // The two query tiles take turns: while the threads of one work on its scores,
 // the tensor cores work for the other.
 //
-// Warps 0-3 and 4-7: the softmax of query tile 0 and 1; warps 8-10 fill the ring
-// of key and value tiles; warp 11 issues the products.
+// Warps 0-3 and 4-7: the softmax of query tile 0 and 1; the warps behind them fill
+// the ring of key and value tiles, the last warp issues the products.
 //
 // A tile is made of pieces of pages.  Binary16: a tensor copy (TMA, 128-byte
 // swizzle) per 64 columns and page or 16 .. BN rows of it, issued by the lanes of
-// warp 8 side by side; a copy through the threads (16-byte cp.async) took 6700
+// one warp side by side; a copy through the threads (16-byte cp.async) took 6700
 // cycles a tile where the products take 2050.  Q8: bulk copies of codes and
-// scales into a staging ring, from which warps 8-10 store f16(code * d).
+// scales into a staging ring, from which four warps store f16(code * d).
 // Positions that no row of the item sees must count as zeros in the product with
 // P = 0 (a stale or later value may be NaN, and 0 * NaN is NaN), and so must
 // values that are not finite in a tile that some rows see only in part: such
@@ -43,8 +43,6 @@ namespace q4 {
 
 namespace {
 
-constexpr int kPtThreads = 384;
-constexpr int kPtLoaders = 96;
 constexpr uint32_t kPtWaitLimit = 1u << 21;
 __device__ int g_status_pt;
 
@@ -108,7 +106,20 @@ __device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t* x) {
       Q4_IN8(x, 0), Q4_IN8(x, 8), Q4_IN8(x, 16), Q4_IN8(x, 24)
       : "memory");
 }
+__device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t* x) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      Q4_IN8(x, 0), Q4_IN8(x, 8)
+      : "memory");
+}
 __device__ __forceinline__ void tm_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// True for one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
 
 // Instruction descriptor: fp32 sums of binary16 products, M = 128; b_mn: the
 // second operand lies with its N index contiguous.
@@ -151,11 +162,19 @@ struct Pt {
   static constexpr int FIT = (LIMIT - QALL - NRAW * RAW) / KB;
   static constexpr int NS = FIT > 8 ? 8 : FIT;          // ring of key and value tiles
   static constexpr int SMEM = 2048 + QALL + NS * KB + NRAW * RAW;
-  static constexpr int O_COL = NQ == 2 ? 256 : 128;     // tensor memory columns: S of tile q at q * 128, then O
+  // tensor memory columns: S of query tile q at q * 128, then O; with one query tile S has two places
+  // that take turns, so that the next scores are computed while the softmax works on these
+  static constexpr int O_COL = 256;
+  static constexpr int H = BN / 2;                      // positions of a half: P is handed over in halves
   static constexpr int CHUNKS = KB / 16;                // 16-byte pieces of a tile
+  // warpgroups: two of softmax, then binary16: copies (warp 8), cleaning (9, 10), products (11);
+  // Q8: conversion (8 to 11), copies (12), products (15)
+  static constexpr int GROUPS = Q8 ? 4 : 3, THREADS = 128 * GROUPS;
+  static constexpr int W_COPY = Q8 ? 12 : 8, W_MMA = 4 * GROUPS - 1, CONV = 4;
   // registers per thread after the split: softmax warpgroups, the others
-  static constexpr int REG_S = NQ == 2 ? 208 : 232, REG_O = NQ == 2 ? 88 : 96;
-  static constexpr int REGS = (NQ * REG_S + (3 - NQ) * REG_O) * 128;
+  static constexpr int REG_S = Q8 ? 160 : 184;
+  static constexpr int REG_O = Q8 ? (NQ == 2 ? 96 : 112) : (NQ == 2 ? 136 : 152);
+  static constexpr int REGS = (NQ * REG_S + (GROUPS - NQ) * REG_O) * 128;
   static_assert(NS >= 2, "the ring holds a key and a value tile");
 };
 
@@ -167,22 +186,27 @@ struct PtMaps {
 };
 
 struct PtCtl {
-  uint64_t full[8], empty[8], q_full[2], s_full[2], p_full[2], o_full[2];
+  uint64_t full[8], empty[8], q_full[2];
+  uint64_t s_full[2];      // scores of query tile q are there (one query tile: in place 0, 1)
+  uint64_t p_full[2][2];   // weights of query tile q (one query tile: in place 0, 1, since the softmax
+                           // may be a tile ahead of the products), half h
+  uint64_t o_full[2][2];   // the product with half h is done
   uint64_t fixed[8];       // the value tile in a ring slot has been looked at, and cleaned if need be
-  uint64_t raw[2];         // a staged Q8 tile has landed
+  uint64_t raw[2], raw_free[2];   // a staged Q8 tile has landed; its place is free again
   uint32_t tmem;
   int dead;
   int bad[8];              // segment number (+ 1) in whose values the loaders met infinities or NaN, by number mod 8
   uint32_t there[8];       // per key tile, by number mod 8: bit g = rows 16 g .. of the tile are in a page
                            // (the loaders are at most five key tiles and five segments ahead of the softmax)
   CtaWork work;
-  long long scan[kPtThreads / 32 + 1];
+  long long scan[17];
 };
 static_assert(sizeof(PtCtl) <= 1024, "control data fits its place");
 
 // A wait that gives up at once when one has run out before: the roles walk on
 // and the kernel ends (its results do not count: the status word says so).
 __device__ __forceinline__ void pt_wait(PtCtl* c, uint64_t* bar, uint32_t parity) {
+  if (mbar_test_wait(bar, parity)) return;
   const uint32_t limit = *reinterpret_cast<volatile int*>(&c->dead) ? 0 : kPtWaitLimit;
   if (!mbar_wait_bounded(bar, parity, limit)) {
     *reinterpret_cast<volatile int*>(&c->dead) = 1;
@@ -195,6 +219,18 @@ __device__ __forceinline__ void pt_wait_warp(PtCtl* c, uint64_t* bar, uint32_t p
   pt_wait(c, bar, parity);
   __syncwarp();
 }
+
+// A place in the ring and the parity of its current turn.
+template <int NS>
+struct RingAt {
+  uint32_t slot = 0, parity = 0;
+  __device__ __forceinline__ void step() {
+    if (++slot == NS) slot = 0, parity ^= 1;
+  }
+  // which value tile of its slot the n-th value tile of the ring is (an odd ring holds keys and values
+  // in turn in every slot, an even one values in its odd slots)
+  static __device__ __forceinline__ uint32_t turn(uint32_t n) { return NS & 1 ? n / NS : n / (NS / 2); }
+};
 
 // What of a key tile an item's rows see.
 struct TileView {
@@ -212,10 +248,10 @@ __device__ __forceinline__ TileView tile_view(const PagedAttnArgs& a, const Item
 // ------------------------------------------------------------------ kernel
 
 template <int HD, bool QF32, bool Q8>
-__global__ void __launch_bounds__(kPtThreads, 1)
+__global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
     paged_tile_kernel(const __grid_constant__ PagedAttnArgs a, PartSlots parts, const __grid_constant__ PtMaps maps) {
   using G = Pt<HD, QF32, Q8>;
-  constexpr int BN = G::BN, NQ = G::NQ, R = G::R, NS = G::NS;
+  constexpr int BN = G::BN, NQ = G::NQ, R = G::R, NS = G::NS, H = G::H;
   extern __shared__ char smem_raw[];
   PtCtl* c = reinterpret_cast<PtCtl*>(smem_raw);
   // tiles start on 1024-byte boundaries (the swizzle's period)
@@ -225,24 +261,23 @@ __global__ void __launch_bounds__(kPtThreads, 1)
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) {
-    for (int i = 0; i < NS; ++i) mbar_init(&c->full[i], Q8 ? 3 : 1), mbar_init(&c->empty[i], 1), mbar_init(&c->fixed[i], 2);
+    for (int i = 0; i < NS; ++i) mbar_init(&c->full[i], Q8 ? G::CONV : 1), mbar_init(&c->empty[i], 1), mbar_init(&c->fixed[i], 2);
     for (int q = 0; q < 2; ++q) {
       mbar_init(&c->q_full[q], 128);
       mbar_init(&c->s_full[q], 1);
-      mbar_init(&c->p_full[q], 128);
-      mbar_init(&c->o_full[q], 1);
+      for (int h = 0; h < 2; ++h) mbar_init(&c->p_full[q][h], 128), mbar_init(&c->o_full[q][h], 1);
     }
-    mbar_init(&c->raw[0], 1), mbar_init(&c->raw[1], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&c->raw[i], 1), mbar_init(&c->raw_free[i], G::CONV);
     c->dead = 0;
     for (int i = 0; i < 8; ++i) c->bad[i] = 0;
     fence_mbar_init();
   }
-  if (warp == 11) tm_alloc(&c->tmem, 512);
-  cta_work<R, BN, kPtThreads>(a, c->scan, &c->work);     // ends synchronised
+  if (warp == G::W_MMA) tm_alloc(&c->tmem, 512);
+  cta_work<R, BN, G::THREADS>(a, c->scan, &c->work);     // ends synchronised
   tm_before();
   __syncthreads();
   tm_after();
-  const uint32_t tmem = c->tmem;
+  const uint32_t tmem = __shfl_sync(~0u, c->tmem, 0);
   const CtaWork work = c->work;
   SegmentWalk<R, BN> w;
   w.begin(a, work);
@@ -259,119 +294,159 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     uint32_t n_s = 0;       // S tiles seen: parity of s_full, and of the product before it
     int seg = 0;
     uint32_t n_k = 0;       // key tiles of the CTA before the current one
-    for (; w.live(); w.next(a), ++seg) {
-      const int rows = w.rows(), row0 = w.j * R;
-      const int n_tiles = w.i1 - w.i0;
-      if (q * 128 >= rows) {        // no rows in this query tile
-        n_k += n_tiles;
-        continue;
-      }
-      // queries: the warp's 32 rows, 16-byte pieces of a row side by side
-      {
-        constexpr int PIECES = HD / 8;
-#pragma unroll 4
-        for (int x = lane; x < 32 * PIECES; x += 32) {
-          const int rr = wl * 32 + x / PIECES, pc = x % PIECES;
-          const int r = row0 + q * 128 + rr;
-          const bool there = q * 128 + rr < rows;
-          const int64_t at = (w.sp.t0 + (there ? r / a.group : 0)) * a.q_ld +
-                             (w.head * a.group + (there ? r % a.group : 0)) * HD + pc * 8;
-          const uint32_t off = (pc >> 3) * (128 * 128) + rr * 128 + (((pc & 7) ^ (rr & 7)) << 4);
-          uint4 hi = make_uint4(0, 0, 0, 0);
-          if (QF32) {
-            uint4 lo = make_uint4(0, 0, 0, 0);
-            if (there) {
-              const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at);
-              const float4 f0 = __ldg(p), f1 = __ldg(p + 1);
-              const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
-              __half2* h = reinterpret_cast<__half2*>(&hi);
-              __half2* l = reinterpret_cast<__half2*>(&lo);
+    // The queries of this tile of an item into shared memory: the warp's 32 rows,
+    // 16-byte pieces of a row side by side.  The products that read the last ones
+    // are done (their scores have been taken).
+    auto load_q = [&](const SegmentWalk<R, BN>& g) {
+      const int rows = g.rows();
+      if (q * 128 >= rows) return;
+      constexpr int PIECES = HD / 8;
+      const int own = q * 128 + wl * 32 + lane, r = g.j * R + own;
+      const int64_t own_at = own < rows ? (g.sp.t0 + r / a.group) * a.q_ld + (g.head * a.group + r % a.group) * HD : -1;
+#pragma unroll 8
+      for (int x = lane; x < 32 * PIECES; x += 32) {
+        const int rl = x / PIECES, rr = wl * 32 + rl, pc = x % PIECES;
+        const int64_t at = __shfl_sync(~0u, own_at, rl) + pc * 8;
+        const bool there = q * 128 + rr < rows;
+        const uint32_t off = (pc >> 3) * (128 * 128) + rr * 128 + (((pc & 7) ^ (rr & 7)) << 4);
+        uint4 hi = make_uint4(0, 0, 0, 0);
+        if (QF32) {
+          uint4 lo = make_uint4(0, 0, 0, 0);
+          if (there) {
+            const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at);
+            const float4 f0 = __ldg(p), f1 = __ldg(p + 1);
+            const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+            __half2* h = reinterpret_cast<__half2*>(&hi);
+            __half2* l = reinterpret_cast<__half2*>(&lo);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                h[e] = __floats2half2_rn(f[2 * e], f[2 * e + 1]);
-                const float2 b = __half22float2(h[e]);
-                l[e] = __floats2half2_rn(f[2 * e] - b.x, f[2 * e + 1] - b.y);
-              }
+            for (int e = 0; e < 4; ++e) {
+              h[e] = __floats2half2_rn(f[2 * e], f[2 * e + 1]);
+              const float2 b = __half22float2(h[e]);
+              l[e] = __floats2half2_rn(f[2 * e] - b.x, f[2 * e + 1] - b.y);
             }
-            *reinterpret_cast<uint4*>(tiles + G::QB + off) = lo;
-          } else if (there) {
-            hi = __ldg(reinterpret_cast<const uint4*>(static_cast<const __half*>(a.q) + at));
           }
-          *reinterpret_cast<uint4*>(tiles + q * G::QB + off) = hi;
+          *reinterpret_cast<uint4*>(tiles + G::QB + off) = lo;
+        } else if (there) {
+          hi = __ldg(reinterpret_cast<const uint4*>(static_cast<const __half*>(a.q) + at));
         }
-        fence_async();
-        mbar_arrive(&c->q_full[q]);
+        *reinterpret_cast<uint4*>(tiles + q * G::QB + off) = hi;
       }
+      fence_async();
+      mbar_arrive(&c->q_full[q]);
+    };
+    if (w.live()) load_q(w);
+    while (w.live()) {
+      const int rows = w.rows(), row0 = w.j * R;
+      const bool active = q * 128 < rows;
       const int r = row0 + q * 128 + wl * 32 + lane;       // this thread's row
       const bool mine = q * 128 + wl * 32 + lane < rows;
       const int p = mine ? w.sp.len - w.sp.n_new + r / a.group : -1;
       float m = -INFINITY, l = 0.f;
-      for (int i = w.i0; i < w.i1; ++i) {
+      if (!active) n_k += w.i1 - w.i0;
+      for (int i = active ? w.i0 : w.i1; i < w.i1; ++i, ++n_s, ++n_k) {
         const TileView tv = tile_view<BN>(a, w.it, i);
-        pt_wait_warp(c, &c->s_full[q], n_s & 1);
+        const uint32_t turn = NQ == 2 ? 0 : n_s & 1;
+        if (NQ == 2)
+          pt_wait_warp(c, &c->s_full[q], n_s & 1);
+        else
+          pt_wait_warp(c, &c->s_full[turn], (n_s >> 1) & 1);
         tm_after();
-        uint32_t x[BN];
-        float* f = reinterpret_cast<float*>(x);
-#pragma unroll
-        for (int b = 0; b < BN; b += 32) tm_ld32(t_s + b, x + b);
         const uint32_t there = *reinterpret_cast<volatile uint32_t*>(&c->there[n_k & 7]);
-        ++n_k;
-        tm_ld_wait(x);
-#pragma unroll
-        for (int b = 32; b < BN; b += 32) tm_ld_waited(x + b);
-        if (!tv.whole || there != (1u << (BN / 16)) - 1) {
-          const int hi = p - tv.base;
-          const int lo = a.window ? hi - a.window + 1 : 0, sk = a.sinks - tv.base;
-#pragma unroll
-          for (int e = 0; e < BN; ++e)
-            if (!(e <= hi && (e >= lo || e < sk) && ((there >> (e >> 4)) & 1))) f[e] = -INFINITY;
-        }
-        float m4[4] = {f[0], f[1], f[2], f[3]};
-#pragma unroll
-        for (int e = 4; e < BN; ++e) m4[e & 3] = fmaxf(m4[e & 3], f[e]);
-        const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale;
-        const bool raise = top > m + 8.f || m == -INFINITY;
-        if (i == w.i0) {
-          m = top;
-        } else if (__any_sync(~0u, raise && top != m)) {
-          // raise m and rescale what O and l hold, after the product before this tile's
-          const float m2 = raise ? fmaxf(m, top) : m;
-          const float fac = m == m2 ? 1.f : exp2f(m - m2);
-          pt_wait_warp(c, &c->o_full[q], (n_s - 1) & 1);
-          tm_after();
+        const bool part = !tv.whole || there != (1u << (BN / 16)) - 1;
+        const uint32_t t_x = t_s + turn * BN;
 #pragma unroll 1
-          for (int b = 0; b < HD; b += 32) {
-            uint32_t o[32];
-            tm_ld32(t_o + b, o);
-            tm_ld_wait(o);
+        for (int h = 0; h < 2; ++h) {
+          uint32_t x[H];
+          float* f = reinterpret_cast<float*>(x);
+          float2 sum;
+          // The weights with the maximum as it is; where that turns out to be too low, once
+          // more.  So the maximum of a half costs no time before its weights.
+#pragma unroll 1
+          for (;;) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fac);
-            tm_st32(t_o + b, o);
+            for (int b = 0; b < H; b += 32) tm_ld32(t_x + h * H + b, x + b);
+            tm_ld_wait(x);
+#pragma unroll
+            for (int b = 32; b < H; b += 32) tm_ld_waited(x + b);
+            if (part) {
+              const int hi = p - tv.base - h * H;
+              const int lo = a.window ? hi - a.window + 1 : 0, sk = a.sinks - tv.base - h * H;
+              const uint32_t in_page = there >> (h * (H / 16));
+#pragma unroll
+              for (int b = 0; b < H; b += 32) {
+                // bit e: this row sees column b + e
+                uint32_t see = hi - b >= 31 ? ~0u : hi < b ? 0u : (2u << (hi - b)) - 1;
+                const uint32_t in = lo <= b ? ~0u : lo - b > 31 ? 0u : ~0u << (lo - b);
+                const uint32_t sink = sk - b > 31 ? ~0u : sk <= b ? 0u : (1u << (sk - b)) - 1;
+                see &= (in | sink) &
+                       (((in_page >> (b >> 4)) & 1 ? 0xffffu : 0u) | ((in_page >> (b >> 4)) & 2 ? 0xffff0000u : 0u));
+#pragma unroll
+                for (int e = 0; e < 32; ++e) f[b + e] = (see >> e) & 1 ? f[b + e] : -INFINITY;
+              }
+            }
+            const float mm = m == -INFINITY ? 0.f : m;
+            const float2 sc2 = make_float2(a.scale, a.scale), mm2 = make_float2(-mm, -mm);
+            float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int e = 0; e < H; e += 2) {
+              top4[(e >> 1) & 3] = fmaxf(top4[(e >> 1) & 3], fmaxf(f[e], f[e + 1]));
+              const float2 t = f2_fma(make_float2(f[e], f[e + 1]), sc2, mm2);
+              float2 y;
+              asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(t.x));
+              asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(t.y));
+              sum2[(e >> 1) & 1] = f2_add(sum2[(e >> 1) & 1], y);
+              x[e / 2] = pack_h2(y.x, y.y);
+            }
+            sum = f2_add(sum2[0], sum2[1]);
+            const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * a.scale;
+            const bool raise = top > m + 8.f || (m == -INFINITY && top > m);
+            if (!__any_sync(~0u, raise)) break;
+            // raise the warp's maxima and rescale what O and l hold, after the product before this half's
+            const float m2 = fmaxf(m, top);
+            const float fac = m == m2 ? 1.f : exp2f(m - m2);
+            if (i > w.i0 || h > 0) {
+              pt_wait_warp(c, &c->o_full[q][h ^ 1], (h ? n_s : n_s - 1) & 1);
+              tm_after();
+#pragma unroll 1
+              for (int b = 0; b < HD; b += 32) {
+                uint32_t o[32];
+                tm_ld32(t_o + b, o);
+                tm_ld_wait(o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fac);
+                tm_st32(t_o + b, o);
+              }
+            }
+            l *= fac;
+            m = m2;
           }
-          l *= fac;
-          m = m2;
+          l += sum.x + sum.y;
+          // With one query tile these scores came ahead of the last tile's product.  Before P goes out that
+          // product is done (the next could not start earlier anyway): so a wait for a turn of o_full, here,
+          // above or below, only ever finds that turn open or just over, never the one after it.
+          if (NQ == 1 && h == 0 && n_s > 0) pt_wait_warp(c, &c->o_full[q][1], (n_s - 1) & 1);
+          // P over the scores' first columns (their half has been read)
+          if (H == 64)
+            tm_st32(t_x + h * (H / 2), x);
+          else
+            tm_st16(t_x + h * (H / 2), x);
+          tm_st_wait();
+          tm_before();
+          mbar_arrive(&c->p_full[NQ == 2 ? q : turn][h]);
         }
-        const float mm = m == -INFINITY ? 0.f : m;
-        float l4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int e = 0; e < BN; e += 2) {
-          float a0, a1;
-          asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a0) : "f"(fmaf(f[e], a.scale, -mm)));
-          asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a1) : "f"(fmaf(f[e + 1], a.scale, -mm)));
-          l4[e & 2] += a0;
-          l4[(e & 2) + 1] += a1;
-          x[e / 2] = pack_h2(a0, a1);
-        }
-        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-#pragma unroll
-        for (int b = 0; b < BN / 2; b += 32) tm_st32(t_s + b, x + b);
-        tm_st_wait();
-        tm_before();
-        mbar_arrive(&c->p_full[q]);
-        ++n_s;
+      }
+      // the next item's queries, so that its first scores are computed meanwhile
+      SegmentWalk<R, BN> next = w;
+      next.next(a);
+      if (next.live()) load_q(next);
+      if (!active) {
+        w = next;
+        ++seg;
+        continue;
       }
       // the item's (or the part's) end
-      pt_wait_warp(c, &c->o_full[q], (n_s - 1) & 1);
+      pt_wait_warp(c, &c->o_full[q][1], (n_s - 1) & 1);
       tm_after();
       const bool whole_item = w.i0 == 0 && w.i1 == w.it.cnt;
       const bool bad = *reinterpret_cast<volatile int*>(&c->bad[seg & 7]) == seg + 1;
@@ -424,8 +499,10 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         parts.max(blockIdx.x, slot)[rr] = m;
         parts.sum(blockIdx.x, slot)[rr] = l;
       }
+      w = next;
+      ++seg;
     }
-  } else if (warp >= 8 && warp < 11) {
+  } else if (warp >= 8 && warp < G::W_MMA) {
     // ---------------------------------------------------------------- key and value tiles
     constexpr uint32_t ALL = (1u << (BN / 16)) - 1;
     const int bl = Q8 ? min(a.kv.page_log2, BN == 128 ? 7 : 6) : maps.box_log2;   // rows of a piece of a page: 2^bl
@@ -442,7 +519,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       const int at = __shfl_sync(~0u, row, (((lane & 7) << 4) >> bl) * COLS);
       return __ballot_sync(~0u, at >= 0) & ALL;
     };
-    if (!Q8 && warp == 8) {
+    if (!Q8 && warp == G::W_COPY) {
       uint32_t n = 0;                                            // tiles issued (keys and values)
       int row = w.live() ? lookup(w, w.i0) : -1;
       while (w.live()) {
@@ -468,7 +545,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         w.next(a);
         if (w.live()) row = lookup(w, w.i0);
       }
-    } else if (!Q8) {
+    } else if (!Q8) {   // (warps 9 and 10)
       // value tiles to be cleaned, by warps 9 and 10
       uint32_t n = 1;
       int seg = 0;
@@ -508,47 +585,45 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           if (lane == 0) mbar_arrive(&c->fixed[n % NS]);
         }
       }
-    } else {
-      // Q8: staged codes to binary16, by warps 8 to 10; warp 8 also issues the staging copies
+    } else if (warp == G::W_COPY) {
+      // Q8: codes and scales into the staging ring
+      constexpr int NRAW = G::NRAW > 0 ? G::NRAW : 1;
+      char* const raw = tiles + G::QALL + NS * G::KB;
+      uint32_t n = 0;
+      int row = w.live() ? lookup(w, w.i0) : -1;
+      while (w.live()) {
+        for (int i = w.i0; i < w.i1; ++i) {
+          const int now = row;
+          if (i + 1 < w.i1) row = lookup(w, i + 1);              // the next tile's page entries on their way
+          const uint32_t there = there_of(now);
+          const uint32_t bytes = __popc(__ballot_sync(~0u, now >= 0)) * ((HD + HD / 16) << bl);
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv, ++n) {
+            char* const to = raw + n % NRAW * G::RAW;
+            uint64_t* bar = &c->raw[n % NRAW];
+            pt_wait_warp(c, &c->raw_free[n % NRAW], ((n / NRAW) & 1) ^ 1);
+            if (lane == 0) {
+              if (kv == 0) *reinterpret_cast<volatile uint32_t*>(&c->there[(n / 2) & 7]) = there;
+              mbar_arrive_expect_tx(bar, bytes);
+            }
+            __syncwarp();
+            if (now >= 0) {
+              const size_t at = static_cast<size_t>(now) * HD;
+              bulk_g2s(to + (lane << bl) * HD, static_cast<const char*>(kv ? a.kv.v : a.kv.k) + at, HD << bl, bar);
+              bulk_g2s(to + BN * HD + (lane << bl) * (HD / 16), reinterpret_cast<const char*>(kv ? a.kv.vs : a.kv.ks) + at / 16,
+                       (HD / 16) << bl, bar);
+            }
+          }
+        }
+        w.next(a);
+        if (w.live()) row = lookup(w, w.i0);
+      }
+    } else if (warp < 8 + G::CONV) {
+      // Q8: staged codes to binary16
       const int lt = tid - 8 * 32;
       constexpr int PIECES = BN * HD / 16;               // 16 codes each
-      char* const raw = tiles + G::QALL + NS * G::KB;
       constexpr int NRAW = G::NRAW > 0 ? G::NRAW : 1;
-      // the staging copies' own walk, NRAW tiles ahead
-      SegmentWalk<R, BN> cp = w;
-      int ci = cp.live() ? cp.i0 : 0, row = -1, kv_next = 0;
-      uint32_t n_raw = 0;
-      if (warp == 8 && cp.live()) row = lookup(cp, ci);
-      auto stage = [&]() {                               // the next tile's codes and scales (warp 8)
-        if (!cp.live()) return;
-        char* to = raw + n_raw % NRAW * G::RAW;
-        uint64_t* bar = &c->raw[n_raw % NRAW];
-        const uint32_t got = __popc(__ballot_sync(~0u, row >= 0));
-        const uint32_t there = there_of(row);
-        if (lane == 0) {
-          if (kv_next == 0) *reinterpret_cast<volatile uint32_t*>(&c->there[(n_raw / 2) & 7]) = there;
-          mbar_arrive_expect_tx(bar, got * ((HD + HD / 16) << bl));
-        }
-        __syncwarp();
-        if (row >= 0) {
-          const size_t at = static_cast<size_t>(row) * HD;
-          bulk_g2s(to + (lane << bl) * HD, static_cast<const char*>(kv_next ? a.kv.v : a.kv.k) + at, HD << bl, bar);
-          bulk_g2s(to + BN * HD + (lane << bl) * (HD / 16), reinterpret_cast<const char*>(kv_next ? a.kv.vs : a.kv.ks) + at / 16,
-                   (HD / 16) << bl, bar);
-        }
-        ++n_raw;
-        if (kv_next++ == 0) return;
-        kv_next = 0;
-        if (++ci == cp.i1) {
-          cp.next(a);
-          if (cp.live()) ci = cp.i0;
-        }
-        if (cp.live()) row = lookup(cp, ci);
-      };
-      if (warp == 8) {
-#pragma unroll 1
-        for (int k = 0; k < NRAW; ++k) stage();
-      }
+      const char* const raw = tiles + G::QALL + NS * G::KB;
       uint32_t n = 0;                                    // tiles stored (keys and values)
       int seg = 0;
       for (; w.live(); w.next(a), ++seg) {
@@ -565,102 +640,156 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             const char* from = raw + n % NRAW * G::RAW;
             char* const dst = tiles + G::QALL + slot * G::KB;
             bool found = false;
-#pragma unroll 2
-            for (int x = lt; x < PIECES; x += kPtLoaders) {
-              const int row = x / (HD / 16), pc = x % (HD / 16);
-              uint4 u[2];
-              const uint4 codes = *reinterpret_cast<const uint4*>(from + x * 16);
-              const __half2 d = __half2half2(*reinterpret_cast<const __half*>(from + BN * HD + (x >> 1) * 2));
-              __half2* h = reinterpret_cast<__half2*>(u);
-              q8_values4(codes.x, d, h[0], h[1]);
-              q8_values4(codes.y, d, h[2], h[3]);
-              q8_values4(codes.z, d, h[4], h[5]);
-              q8_values4(codes.w, d, h[6], h[7]);
-              if (clean) {
-                if (((there >> (row >> 4)) & 1) && row <= last && (row >= first || row < sk)) {
-                  const uint32_t* b = reinterpret_cast<const uint32_t*>(u);
-                  bool any = false;
+            constexpr int PER = PIECES / (G::CONV * 32), BATCH = PER % 4 == 0 ? 4 : PER % 3 == 0 ? 3 : 2;
+            static_assert(PIECES % (G::CONV * 32) == 0 && PER % BATCH == 0, "every thread has the same pieces");
+#pragma unroll 1
+            for (int y0 = 0; y0 < PER; y0 += BATCH) {
+              uint4 codes[BATCH];
+              __half sc[BATCH];
 #pragma unroll
-                  for (int e = 0; e < 8; ++e) any |= h2_bad(b[e]);
-                  if (any) {
-                    __half* he = reinterpret_cast<__half*>(u);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                      if (__hisinf(he[e]) || __hisnan(he[e])) he[e] = __ushort_as_half(0);
-                    found = true;
-                  }
-                } else {
-                  u[0] = u[1] = make_uint4(0, 0, 0, 0);
-                }
+              for (int y = 0; y < BATCH; ++y) {
+                const int x = lt + (y0 + y) * G::CONV * 32;
+                codes[y] = *reinterpret_cast<const uint4*>(from + x * 16);
+                sc[y] = *reinterpret_cast<const __half*>(from + BN * HD + (x >> 1) * 2);
               }
-              // the two halves of a piece in an order that keeps 8 lanes' stores in different banks
-              char* to = dst + (pc >> 2) * (BN * 128) + row * 128;
-              const int odd = (pc >> 2) & 1, p0 = (pc & 3) * 2;
-              *reinterpret_cast<uint4*>(to + (((p0 + odd) ^ (row & 7)) << 4)) = odd ? u[1] : u[0];
-              *reinterpret_cast<uint4*>(to + (((p0 + 1 - odd) ^ (row & 7)) << 4)) = odd ? u[0] : u[1];
+#pragma unroll
+              for (int y = 0; y < BATCH; ++y) {
+                const int x = lt + (y0 + y) * G::CONV * 32, row = x / (HD / 16), pc = x % (HD / 16);
+                uint4 u[2];
+                __half2* h = reinterpret_cast<__half2*>(u);
+                const __half2 d = __half2half2(sc[y]);
+                q8_values4(codes[y].x, d, h[0], h[1]);
+                q8_values4(codes[y].y, d, h[2], h[3]);
+                q8_values4(codes[y].z, d, h[4], h[5]);
+                q8_values4(codes[y].w, d, h[6], h[7]);
+                if (clean) {
+                  if (((there >> (row >> 4)) & 1) && row <= last && (row >= first || row < sk)) {
+                    uint32_t* b = reinterpret_cast<uint32_t*>(u);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                      if ((b[e] & 0x7c00u) == 0x7c00u) b[e] &= 0xffff0000u, found = true;
+                      if ((b[e] & 0x7c000000u) == 0x7c000000u) b[e] &= 0x0000ffffu, found = true;
+                    }
+                  } else {
+                    u[0] = u[1] = make_uint4(0, 0, 0, 0);
+                  }
+                }
+                // the two halves of a piece in an order that keeps 8 lanes' stores in different banks
+                char* to = dst + (pc >> 2) * (BN * 128) + row * 128;
+                const int odd = (pc >> 2) & 1, p0 = (pc & 3) * 2;
+                *reinterpret_cast<uint4*>(to + (((p0 + odd) ^ (row & 7)) << 4)) = odd ? u[1] : u[0];
+                *reinterpret_cast<uint4*>(to + (((p0 + 1 - odd) ^ (row & 7)) << 4)) = odd ? u[0] : u[1];
+              }
             }
             if (found) *reinterpret_cast<volatile int*>(&c->bad[seg & 7]) = seg + 1;
             fence_async();
-            asm volatile("bar.sync 1, %0;" ::"n"(kPtLoaders) : "memory");      // the staged tile is free again
-            if (lane == 0) mbar_arrive(&c->full[slot]);
-            if (warp == 8) stage();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&c->full[slot]);
+              mbar_arrive(&c->raw_free[n % NRAW]);
+            }
           }
         }
       }
     }
-  } else if (warp == 11 && lane == 0) {
+  } else if (warp == G::W_MMA) {
     // ---------------------------------------------------------------- products
+    // The whole warp walks; one elected lane issues.  Warp-uniform values let
+    // the descriptors live in uniform registers.
     constexpr uint32_t ID_S = mma_idesc(BN, false), ID_O = mma_idesc(HD, true);
     constexpr uint64_t BLOCK = (BN * 128) >> 4;         // next 64 values of head_dim, in descriptor units
-    uint32_t n = 0;                                      // tiles taken (keys and values)
-    uint32_t n_seg[2] = {0, 0}, n_p[2] = {0, 0};         // segments and products of each query tile
+    const bool one = elect_one();
+    RingAt<NS> at_k, at_v;                               // the next key and value tile
+    at_v.step();
+    uint32_t n_v = 0;                                    // value tiles: turns of their slots
+    uint32_t par_q[2] = {0, 0}, par_p[2] = {0, 0}, par_s = 0;
     for (; w.live(); w.next(a)) {
-      const int active = w.rows() > 128 ? NQ : 1;
-      const int cnt = w.i1 - w.i0;
-      auto scores = [&](int q, uint32_t tile) {          // S of query tile q with key tile number `tile`
-        const uint64_t k0 = mma_sdesc(s_ring + (tile % NS) * G::KB, 0);
+      const int active = __shfl_sync(~0u, w.rows() > 128 ? NQ : 1, 0);
+      const int cnt = __shfl_sync(~0u, w.i1 - w.i0, 0);
+      auto scores = [&](int q) {                         // S of query tile q with the key tile at_k
+        if (one) {
+          const uint64_t k0 = mma_sdesc(s_ring + at_k.slot * G::KB, 0);
+          const uint32_t d = NQ == 2 ? tmem + q * 128 : tmem + par_s * BN;
 #pragma unroll
-        for (int part = 0; part < (QF32 ? 2 : 1); ++part) {
-          const uint64_t q0 = mma_sdesc(s_q + (QF32 ? part : q) * G::QB, 0);
+          for (int part = 0; part < (QF32 ? 2 : 1); ++part) {
+            const uint64_t q0 = mma_sdesc(s_q + (QF32 ? part : q) * G::QB, 0);
 #pragma unroll
-          for (int k = 0; k < HD / 16; ++k)
-            tm_mma_ss(tmem + q * 128, q0 + (k >> 2) * ((128 * 128) >> 4) + (k & 3) * 2, k0 + (k >> 2) * BLOCK + (k & 3) * 2,
-                      ID_S, part > 0 || k > 0);
+            for (int k = 0; k < HD / 16; ++k)
+              tm_mma_ss(d, q0 + (k >> 2) * ((128 * 128) >> 4) + (k & 3) * 2, k0 + (k >> 2) * BLOCK + (k & 3) * 2, ID_S,
+                        part > 0 || k > 0);
+          }
+          tm_commit(&c->s_full[NQ == 2 ? q : par_s]);
         }
-        tm_commit(&c->s_full[q]);
       };
-      pt_wait(c, &c->full[n % NS], (n / NS) & 1);
-      for (int q = 0; q < active; ++q) {
-        pt_wait(c, &c->q_full[q], n_seg[q] & 1);
-        ++n_seg[q];
-        tm_after();
-        scores(q, n);
-      }
-      tm_commit(&c->empty[n % NS]);
-      for (int i = 0; i < cnt; ++i, n += 2) {
-        const uint32_t v = n + 1, k_next = n + 2;
-        pt_wait(c, &c->full[v % NS], (v / NS) & 1);
-        // (the turns of a slot that hold values: every one, or every other one of an odd ring)
-        if (!Q8) pt_wait(c, &c->fixed[v % NS], (NS & 1 ? v / (2 * NS) : v / NS) & 1);
-        for (int q = 0; q < active; ++q) {
-          pt_wait(c, &c->p_full[q], n_p[q] & 1);
-          ++n_p[q];
-          tm_after();
-          const uint64_t v0 = mma_sdesc(s_ring + (v % NS) * G::KB, BN * 128);
+      auto values = [&](int q, uint32_t p_at, int h, bool add) {     // O += P V, half h
+        if (one) {
+          const uint64_t v0 = mma_sdesc(s_ring + at_v.slot * G::KB, BN * 128) + h * (G::H / 16) * (2048 >> 4);
 #pragma unroll
-          for (int k = 0; k < BN / 16; ++k)
-            tm_mma_ts(tmem + G::O_COL + q * 128, tmem + q * 128 + k * 8, v0 + k * (2048 >> 4), ID_O, i > 0 || k > 0);
-          tm_commit(&c->o_full[q]);
-          if (i + 1 < cnt) {
-            if (q == 0) {
-              pt_wait(c, &c->full[k_next % NS], (k_next / NS) & 1);
+          for (int k = 0; k < G::H / 16; ++k)
+            tm_mma_ts(tmem + G::O_COL + q * 128, p_at + h * (G::H / 2) + k * 8, v0 + k * (2048 >> 4), ID_O, add || k > 0);
+          tm_commit(&c->o_full[q][h]);
+        }
+      };
+      pt_wait_warp(c, &c->full[at_k.slot], at_k.parity);
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        if (q >= active) break;
+        pt_wait_warp(c, &c->q_full[q], par_q[q]);
+        par_q[q] ^= 1;
+        tm_after();
+        scores(q);
+      }
+      if (one) tm_commit(&c->empty[at_k.slot]);
+      at_k.step(), at_k.step();
+      for (int i = 0; i < cnt; ++i) {
+        const bool more = i + 1 < cnt;
+        if (NQ == 1) {
+          // the next scores go ahead of this tile's weights, into the other place
+          const uint32_t now = par_s;
+          par_s ^= 1;
+          if (more) {
+            pt_wait_warp(c, &c->full[at_k.slot], at_k.parity);
+            tm_after();
+            scores(0);
+            if (one) tm_commit(&c->empty[at_k.slot]);
+            at_k.step(), at_k.step();
+          }
+          pt_wait_warp(c, &c->full[at_v.slot], at_v.parity);
+          if (!Q8) pt_wait_warp(c, &c->fixed[at_v.slot], at_v.turn(n_v) & 1);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            pt_wait_warp(c, &c->p_full[now][h], par_p[now]);
+            tm_after();
+            values(0, tmem + now * BN, h, i > 0 || h > 0);
+          }
+          par_p[now] ^= 1;
+        } else {
+          pt_wait_warp(c, &c->full[at_v.slot], at_v.parity);
+          if (!Q8) pt_wait_warp(c, &c->fixed[at_v.slot], at_v.turn(n_v) & 1);
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) {
+            if (q >= active) break;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              pt_wait_warp(c, &c->p_full[q][h], par_p[q]);
               tm_after();
+              values(q, tmem + q * 128, h, i > 0 || h > 0);
             }
-            scores(q, k_next);
+            par_p[q] ^= 1;
+            if (more) {
+              if (q == 0) pt_wait_warp(c, &c->full[at_k.slot], at_k.parity);
+              tm_after();
+              scores(q);
+            }
+          }
+          if (more) {
+            if (one) tm_commit(&c->empty[at_k.slot]);
+            at_k.step(), at_k.step();
           }
         }
-        tm_commit(&c->empty[v % NS]);
-        if (i + 1 < cnt) tm_commit(&c->empty[k_next % NS]);
+        if (one) tm_commit(&c->empty[at_v.slot]);
+        at_v.step(), at_v.step();
+        ++n_v;
       }
     }
   }
@@ -668,7 +797,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   __syncwarp();
   tm_before();
   __syncthreads();
-  if (warp == 11) {
+  if (warp == G::W_MMA) {
     tm_after();
     tm_free(tmem, 512);
   }
@@ -680,7 +809,7 @@ cudaError_t prepare_tile() {
   cudaFuncAttributes at;
   const cudaError_t e = cudaFuncGetAttributes(&at, paged_tile_kernel<HD, QF32, Q8>);
   if (e != cudaSuccess) return e;
-  if ((at.numRegs + 7) / 8 * 8 * kPtThreads < Pt<HD, QF32, Q8>::REGS) return cudaErrorInvalidConfiguration;
+  if ((at.numRegs + 7) / 8 * 8 * Pt<HD, QF32, Q8>::THREADS < Pt<HD, QF32, Q8>::REGS) return cudaErrorInvalidConfiguration;
   return cudaFuncSetAttribute(paged_tile_kernel<HD, QF32, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               Pt<HD, QF32, Q8>::SMEM);
 }
@@ -706,7 +835,7 @@ cudaError_t launch_tile(const PagedAttnArgs& a, void* ws, int grid, cudaStream_t
         !encode_f16_rows(&maps.v, a.kv.v, rows, HD, 1 << maps.box_log2))
       return cudaErrorInvalidValue;
   }
-  paged_tile_kernel<HD, QF32, Q8><<<grid, kPtThreads, G::SMEM, s>>>(a, parts, maps);
+  paged_tile_kernel<HD, QF32, Q8><<<grid, G::THREADS, G::SMEM, s>>>(a, parts, maps);
   const cudaError_t e = cudaGetLastError();
   return e != cudaSuccess ? e : paged_join_launch(a, parts, grid, s);
 }
