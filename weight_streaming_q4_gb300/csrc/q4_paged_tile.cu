@@ -21,7 +21,7 @@
 // swizzle) per 64 columns and page or 16 .. BN rows of it, issued by the lanes of
 // one warp side by side; a copy through the threads (16-byte cp.async) took 6700
 // cycles a tile where the products take 2050.  Q8: bulk copies of codes and
-// scales into a staging ring, from which four warps store f16(code * d).
+// scales into a staging ring, from which six warps store f16(code * d).
 // Positions that no row of the item sees must count as zeros in the product with
 // P = 0 (a stale or later value may be NaN, and 0 * NaN is NaN), and so must
 // values that are not finite in a tile that some rows see only in part: such
@@ -134,6 +134,9 @@ __device__ __forceinline__ uint64_t mma_sdesc(uint32_t addr, uint32_t lead) {
          (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
+__device__ __forceinline__ void cp16_zfill(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
 // What the threads stored in shared memory becomes visible to the tensor cores.
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -158,24 +161,25 @@ struct Pt {
   static constexpr int LIMIT = 232448 - 1024 - 1024;    // control data, and the alignment of the tiles
   static constexpr int QALL = QB * (QF32 ? 2 : NQ);
   static constexpr int RAW = Q8 ? BN * HD + BN * HD / 16 : 0;   // a staged Q8 tile: codes, then scales
-  static constexpr int NRAW = !Q8 ? 0 : (LIMIT - QALL - 2 * RAW) / KB >= 2 ? 2 : 1;
-  static constexpr int FIT = (LIMIT - QALL - NRAW * RAW) / KB;
+  static constexpr int NRAW = !Q8 ? 0 : (LIMIT - QALL - NQ * 8192 - 2 * RAW) / KB >= 2 ? 2 : 1;
+  static constexpr int OUT = NQ * 4 * 2048;             // per softmax warp: 32 rows of 64 bytes on their way out
+  static constexpr int FIT = (LIMIT - QALL - OUT - NRAW * RAW) / KB;
   static constexpr int NS = FIT > 8 ? 8 : FIT;          // ring of key and value tiles
-  static constexpr int SMEM = 2048 + QALL + NS * KB + NRAW * RAW;
+  static constexpr int SMEM = 2048 + QALL + NS * KB + NRAW * RAW + OUT;
   // tensor memory columns: S of query tile q at q * 128, then O; with one query tile S has two places
   // that take turns, so that the next scores are computed while the softmax works on these
   static constexpr int O_COL = 256;
   static constexpr int H = BN / 2;                      // positions of a half: P is handed over in halves
   static constexpr int CHUNKS = KB / 16;                // 16-byte pieces of a tile
   // warpgroups: two of softmax, then binary16: copies (warp 8), cleaning (9, 10), products (11);
-  // Q8: conversion (8 to 11), copies (12), products (15)
+  // Q8: conversion (8 to 13), copies (14), products (15)
   static constexpr int GROUPS = Q8 ? 4 : 3, THREADS = 128 * GROUPS;
-  static constexpr int W_COPY = Q8 ? 12 : 8, W_MMA = 4 * GROUPS - 1, CONV = 4;
+  static constexpr int W_COPY = Q8 ? 14 : 8, W_MMA = 4 * GROUPS - 1, CONV = 6;
   // registers per thread after the split: softmax warpgroups, the others
-  static constexpr int REG_S = Q8 ? 160 : 184;
-  static constexpr int REG_O = Q8 ? (NQ == 2 ? 96 : 112) : (NQ == 2 ? 136 : 152);
+  static constexpr int REG_S = Q8 ? 136 : 184;
+  static constexpr int REG_O = Q8 ? 120 : (NQ == 2 ? 136 : 152);
   static constexpr int REGS = (NQ * REG_S + (GROUPS - NQ) * REG_O) * 128;
-  static_assert(NS >= 2, "the ring holds a key and a value tile");
+  static_assert(NS >= (NQ == 2 ? 3 : 2), "a key and a value tile, and the next key tile beside two query tiles");
 };
 
 // Tensor copies of binary16 pages: rows of HD values, boxes of 64 values by
@@ -245,6 +249,27 @@ __device__ __forceinline__ TileView tile_view(const PagedAttnArgs& a, const Item
   return v;
 }
 
+// Values that were taken out of tiles seen in part, back into columns b .. of a
+// row at position p that sees them (rare, so out of the way of the registers).
+template <int R, int BN, int HD, bool Q8>
+__device__ __noinline__ void add_taken_out(const PagedAttnArgs& a, const SegmentWalk<R, BN>& w, int p, int b, float* of) {
+  for (int i = w.i0; i < w.i1; ++i) {
+    const TileView tv = tile_view<BN>(a, w.it, i);
+    if (tv.whole) continue;
+    for (int t = tv.base; t < tv.base + BN && t <= p; ++t) {
+      if (a.window && t <= p - a.window && t >= a.sinks) continue;
+      const int row = paged_row(a.kv, a.b, w.seq, t, w.head);
+      if (row < 0) continue;
+      for (int e = 0; e < 32; ++e) {
+        const size_t at = static_cast<size_t>(row) * HD + b + e;
+        const __half h = Q8 ? __hmul(__int2half_rn(static_cast<const int8_t*>(a.kv.v)[at]), a.kv.vs[at / 32])
+                            : static_cast<const __half*>(a.kv.v)[at];
+        if (__hisinf(h) || __hisnan(h)) of[e] += __half2float(h);
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------------------ kernel
 
 template <int HD, bool QF32, bool Q8>
@@ -303,17 +328,23 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
       constexpr int PIECES = HD / 8;
       const int own = q * 128 + wl * 32 + lane, r = g.j * R + own;
       const int64_t own_at = own < rows ? (g.sp.t0 + r / a.group) * a.q_ld + (g.head * a.group + r % a.group) * HD : -1;
+      if (!QF32) {
+#pragma unroll 4
+        for (int x = lane; x < 32 * PIECES; x += 32) {
+          const int rl = x / PIECES, rr = wl * 32 + rl, pc = x % PIECES;
+          const int64_t at = __shfl_sync(~0u, own_at, rl);
+          const uint32_t off = (pc >> 3) * (128 * 128) + rr * 128 + (((pc & 7) ^ (rr & 7)) << 4);
+          cp16_zfill(s_q + q * G::QB + off, static_cast<const __half*>(a.q) + (at < 0 ? 0 : at + pc * 8), at >= 0);
+        }
+      } else {
 #pragma unroll 8
-      for (int x = lane; x < 32 * PIECES; x += 32) {
-        const int rl = x / PIECES, rr = wl * 32 + rl, pc = x % PIECES;
-        const int64_t at = __shfl_sync(~0u, own_at, rl) + pc * 8;
-        const bool there = q * 128 + rr < rows;
-        const uint32_t off = (pc >> 3) * (128 * 128) + rr * 128 + (((pc & 7) ^ (rr & 7)) << 4);
-        uint4 hi = make_uint4(0, 0, 0, 0);
-        if (QF32) {
-          uint4 lo = make_uint4(0, 0, 0, 0);
-          if (there) {
-            const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at);
+        for (int x = lane; x < 32 * PIECES; x += 32) {
+          const int rl = x / PIECES, rr = wl * 32 + rl, pc = x % PIECES;
+          const int64_t at = __shfl_sync(~0u, own_at, rl);
+          const uint32_t off = (pc >> 3) * (128 * 128) + rr * 128 + (((pc & 7) ^ (rr & 7)) << 4);
+          uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
+          if (at >= 0) {
+            const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at + pc * 8);
             const float4 f0 = __ldg(p), f1 = __ldg(p + 1);
             const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
             __half2* h = reinterpret_cast<__half2*>(&hi);
@@ -326,15 +357,20 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
             }
           }
           *reinterpret_cast<uint4*>(tiles + G::QB + off) = lo;
-        } else if (there) {
-          hi = __ldg(reinterpret_cast<const uint4*>(static_cast<const __half*>(a.q) + at));
+          *reinterpret_cast<uint4*>(tiles + q * G::QB + off) = hi;
         }
-        *reinterpret_cast<uint4*>(tiles + q * G::QB + off) = hi;
       }
+    };
+    auto loaded_q = [&](const SegmentWalk<R, BN>& g) {       // ... are there
+      if (q * 128 >= g.rows()) return;
+      if (!QF32) asm volatile("cp.async.wait_all;" ::: "memory");
       fence_async();
       mbar_arrive(&c->q_full[q]);
     };
-    if (w.live()) load_q(w);
+    if (w.live()) {
+      load_q(w);
+      loaded_q(w);
+    }
     while (w.live()) {
       const int rows = w.rows(), row0 = w.j * R;
       const bool active = q * 128 < rows;
@@ -441,6 +477,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
       next.next(a);
       if (next.live()) load_q(next);
       if (!active) {
+        if (next.live()) loaded_q(next);
         w = next;
         ++seg;
         continue;
@@ -448,14 +485,20 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
       // the item's (or the part's) end
       pt_wait_warp(c, &c->o_full[q][1], (n_s - 1) & 1);
       tm_after();
+      if (next.live()) loaded_q(next);
       const bool whole_item = w.i0 == 0 && w.i1 == w.it.cnt;
       const bool bad = *reinterpret_cast<volatile int*>(&c->bad[seg & 7]) == seg + 1;
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const int slot = w.i0 == 0 ? 1 : 0;
-      const int rr = q * 128 + wl * 32 + lane;
-      __half* out = a.out + static_cast<int64_t>(w.sp.t0 + (mine ? r / a.group : 0)) * a.out_ld +
-                    (w.head * a.group + (mine ? r % a.group : 0)) * HD;
-      float* part = parts.out(blockIdx.x, slot) + static_cast<size_t>(rr) * HD;
+      // A thread holds a row, but stores go out with four lanes to a row, over shared memory: 64 bytes of
+      // each row at a time, the 16-byte pieces exchanged by row so that they fall into different banks.
+      // (A store of 16 bytes in each of 32 rows costs 32 passes.)
+      const int64_t out_at = static_cast<int64_t>(w.sp.t0 + (mine ? r / a.group : 0)) * a.out_ld +
+                             (w.head * a.group + (mine ? r % a.group : 0)) * HD;
+      char* const turn_at = tiles + G::QALL + NS * G::KB + G::NRAW * G::RAW + warp * 2048;
+      char* const turn_mine = turn_at + lane * 64;
+      float* const part0 = parts.out(blockIdx.x, slot) + static_cast<size_t>(q * 128 + wl * 32) * HD;
+      const int n_mine = rows - q * 128 - wl * 32;                // rows of this warp
 #pragma unroll 1
       for (int b = 0; b < HD; b += 32) {
         uint32_t o[32];
@@ -464,40 +507,49 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
         tm_ld_wait(o);
         float* of = reinterpret_cast<float*>(o);
         if (bad) {
-          // values that were taken out of tiles seen in part: back into the rows that see them
-          for (int i = w.i0; i < w.i1; ++i) {
-            const TileView tv = tile_view<BN>(a, w.it, i);
-            if (tv.whole) continue;
-            for (int t = tv.base; t < tv.base + BN && t <= p; ++t) {
-              if (a.window && t <= p - a.window && t >= a.sinks) continue;
-              const int vr = paged_row(a.kv, a.b, w.seq, t, w.head);
-              if (vr < 0) continue;
+          float back[32];
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const size_t at = static_cast<size_t>(vr) * HD + b + e;
-                const __half h = Q8 ? __hmul(__int2half_rn(static_cast<const int8_t*>(a.kv.v)[at]), a.kv.vs[at / 32])
-                                    : static_cast<const __half*>(a.kv.v)[at];
-                if (__hisinf(h) || __hisnan(h)) of[e] += __half2float(h);
-              }
-            }
-          }
+          for (int e = 0; e < 32; ++e) back[e] = of[e];
+          add_taken_out<R, BN, HD, Q8>(a, w, p, b, back);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) of[e] = back[e];
+          __syncwarp();
         }
-        if (mine && whole_item) {
+        if (whole_item) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            const uint4 u = make_uint4(pack_h2(of[e] * inv, of[e + 1] * inv), pack_h2(of[e + 2] * inv, of[e + 3] * inv),
-                                       pack_h2(of[e + 4] * inv, of[e + 5] * inv), pack_h2(of[e + 6] * inv, of[e + 7] * inv));
-            *reinterpret_cast<uint4*>(out + b + e) = u;
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4*>(turn_mine + ((k ^ ((lane >> 1) & 3)) << 4)) =
+                make_uint4(pack_h2(of[8 * k] * inv, of[8 * k + 1] * inv), pack_h2(of[8 * k + 2] * inv, of[8 * k + 3] * inv),
+                           pack_h2(of[8 * k + 4] * inv, of[8 * k + 5] * inv), pack_h2(of[8 * k + 6] * inv, of[8 * k + 7] * inv));
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int row = k * 8 + (lane >> 2), pc = lane & 3;
+            const int64_t at = __shfl_sync(~0u, out_at, row);
+            const uint4 u = *reinterpret_cast<const uint4*>(turn_at + row * 64 + ((pc ^ ((row >> 1) & 3)) << 4));
+            if (row < n_mine) *reinterpret_cast<uint4*>(a.out + at + b + pc * 8) = u;
           }
-        } else if (mine) {
+        } else {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4*>(part + b + e) = make_float4(of[e], of[e + 1], of[e + 2], of[e + 3]);
+          for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              *reinterpret_cast<float4*>(turn_mine + ((k ^ ((lane >> 1) & 3)) << 4)) =
+                  make_float4(of[half * 16 + 4 * k], of[half * 16 + 4 * k + 1], of[half * 16 + 4 * k + 2], of[half * 16 + 4 * k + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int row = k * 8 + (lane >> 2), pc = lane & 3;
+              const float4 u = *reinterpret_cast<const float4*>(turn_at + row * 64 + ((pc ^ ((row >> 1) & 3)) << 4));
+              if (row < n_mine) *reinterpret_cast<float4*>(part0 + static_cast<size_t>(row) * HD + b + half * 16 + pc * 4) = u;
+            }
+            __syncwarp();
+          }
         }
       }
       if (!whole_item && mine) {
-        parts.max(blockIdx.x, slot)[rr] = m;
-        parts.sum(blockIdx.x, slot)[rr] = l;
+        parts.max(blockIdx.x, slot)[q * 128 + wl * 32 + lane] = m;
+        parts.sum(blockIdx.x, slot)[q * 128 + wl * 32 + lane] = l;
       }
       w = next;
       ++seg;
@@ -620,7 +672,6 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
       }
     } else if (warp < 8 + G::CONV) {
       // Q8: staged codes to binary16
-      const int lt = tid - 8 * 32;
       constexpr int PIECES = BN * HD / 16;               // 16 codes each
       constexpr int NRAW = G::NRAW > 0 ? G::NRAW : 1;
       const char* const raw = tiles + G::QALL + NS * G::KB;
@@ -640,28 +691,32 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
             const char* from = raw + n % NRAW * G::RAW;
             char* const dst = tiles + G::QALL + slot * G::KB;
             bool found = false;
-            constexpr int PER = PIECES / (G::CONV * 32), BATCH = PER % 4 == 0 ? 4 : PER % 3 == 0 ? 3 : 2;
-            static_assert(PIECES % (G::CONV * 32) == 0 && PER % BATCH == 0, "every thread has the same pieces");
+            // groups of 32 pieces go round the warps from tile to tile
+            constexpr int PARTS = PIECES / 32, BATCH = 3;
+            const int j0 = (warp - 8 + G::CONV - static_cast<int>(n * PARTS % G::CONV)) % G::CONV;
 #pragma unroll 1
-            for (int y0 = 0; y0 < PER; y0 += BATCH) {
+            for (int jb = j0; jb < PARTS; jb += BATCH * G::CONV) {
               uint4 codes[BATCH];
               __half sc[BATCH];
 #pragma unroll
               for (int y = 0; y < BATCH; ++y) {
-                const int x = lt + (y0 + y) * G::CONV * 32;
+                const int x = min(jb + y * G::CONV, PARTS - 1) * 32 + lane;
                 codes[y] = *reinterpret_cast<const uint4*>(from + x * 16);
                 sc[y] = *reinterpret_cast<const __half*>(from + BN * HD + (x >> 1) * 2);
               }
 #pragma unroll
               for (int y = 0; y < BATCH; ++y) {
-                const int x = lt + (y0 + y) * G::CONV * 32, row = x / (HD / 16), pc = x % (HD / 16);
+                if (jb + y * G::CONV >= PARTS) break;
+                const int x = (jb + y * G::CONV) * 32 + lane, row = x / (HD / 16), pc = x % (HD / 16);
                 uint4 u[2];
                 __half2* h = reinterpret_cast<__half2*>(u);
                 const __half2 d = __half2half2(sc[y]);
-                q8_values4(codes[y].x, d, h[0], h[1]);
-                q8_values4(codes[y].y, d, h[2], h[3]);
-                q8_values4(codes[y].z, d, h[4], h[5]);
-                q8_values4(codes[y].w, d, h[6], h[7]);
+                // the two halves of a piece in an order that keeps 8 lanes' stores in different banks
+                const bool odd = (pc >> 2) & 1;
+                q8_values4(odd ? codes[y].z : codes[y].x, d, h[0], h[1]);
+                q8_values4(odd ? codes[y].w : codes[y].y, d, h[2], h[3]);
+                q8_values4(odd ? codes[y].x : codes[y].z, d, h[4], h[5]);
+                q8_values4(odd ? codes[y].y : codes[y].w, d, h[6], h[7]);
                 if (clean) {
                   if (((there >> (row >> 4)) & 1) && row <= last && (row >= first || row < sk)) {
                     uint32_t* b = reinterpret_cast<uint32_t*>(u);
@@ -674,11 +729,10 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
                     u[0] = u[1] = make_uint4(0, 0, 0, 0);
                   }
                 }
-                // the two halves of a piece in an order that keeps 8 lanes' stores in different banks
                 char* to = dst + (pc >> 2) * (BN * 128) + row * 128;
-                const int odd = (pc >> 2) & 1, p0 = (pc & 3) * 2;
-                *reinterpret_cast<uint4*>(to + (((p0 + odd) ^ (row & 7)) << 4)) = odd ? u[1] : u[0];
-                *reinterpret_cast<uint4*>(to + (((p0 + 1 - odd) ^ (row & 7)) << 4)) = odd ? u[0] : u[1];
+                const int p0 = (pc & 3) * 2 + odd;
+                *reinterpret_cast<uint4*>(to + ((p0 ^ (row & 7)) << 4)) = u[0];
+                *reinterpret_cast<uint4*>(to + (((p0 ^ 1) ^ (row & 7)) << 4)) = u[1];
               }
             }
             if (found) *reinterpret_cast<volatile int*>(&c->bad[seg & 7]) = seg + 1;
@@ -706,13 +760,19 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
     for (; w.live(); w.next(a)) {
       const int active = __shfl_sync(~0u, w.rows() > 128 ? NQ : 1, 0);
       const int cnt = __shfl_sync(~0u, w.i1 - w.i0, 0);
+      auto wait_v = [&](const RingAt<NS>& at, uint32_t n) {
+        pt_wait_warp(c, &c->full[at.slot], at.parity);
+        if (!Q8) pt_wait_warp(c, &c->fixed[at.slot], at.turn(n) & 1);
+      };
       auto scores = [&](int q) {                         // S of query tile q with the key tile at_k
         if (one) {
           const uint64_t k0 = mma_sdesc(s_ring + at_k.slot * G::KB, 0);
           const uint32_t d = NQ == 2 ? tmem + q * 128 : tmem + par_s * BN;
 #pragma unroll
           for (int part = 0; part < (QF32 ? 2 : 1); ++part) {
-            const uint64_t q0 = mma_sdesc(s_q + (QF32 ? part : q) * G::QB, 0);
+            uint32_t q_at = s_q + (QF32 ? part : q) * G::QB;
+            asm volatile("" : "+r"(q_at));               // (descriptors formed here, not kept in registers)
+            const uint64_t q0 = mma_sdesc(q_at, 0);
 #pragma unroll
             for (int k = 0; k < HD / 16; ++k)
               tm_mma_ss(d, q0 + (k >> 2) * ((128 * 128) >> 4) + (k & 3) * 2, k0 + (k >> 2) * BLOCK + (k & 3) * 2, ID_S,
@@ -754,8 +814,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
             if (one) tm_commit(&c->empty[at_k.slot]);
             at_k.step(), at_k.step();
           }
-          pt_wait_warp(c, &c->full[at_v.slot], at_v.parity);
-          if (!Q8) pt_wait_warp(c, &c->fixed[at_v.slot], at_v.turn(n_v) & 1);
+          wait_v(at_v, n_v);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             pt_wait_warp(c, &c->p_full[now][h], par_p[now]);
@@ -764,8 +823,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
           }
           par_p[now] ^= 1;
         } else {
-          pt_wait_warp(c, &c->full[at_v.slot], at_v.parity);
-          if (!Q8) pt_wait_warp(c, &c->fixed[at_v.slot], at_v.turn(n_v) & 1);
+          wait_v(at_v, n_v);
 #pragma unroll
           for (int q = 0; q < NQ; ++q) {
             if (q >= active) break;
@@ -790,6 +848,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
         if (one) tm_commit(&c->empty[at_v.slot]);
         at_v.step(), at_v.step();
         ++n_v;
+
       }
     }
   }
