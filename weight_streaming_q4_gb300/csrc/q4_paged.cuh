@@ -102,8 +102,28 @@ struct PagedAttnArgs {
   __half* out;
   int64_t out_ld;
   int group;          // query heads per value head
+  uint32_t div_mul;   // row / group as row * div_mul >> div_shift (rows below 2^31, paged_attn_divisor)
+  int div_shift;
   int window, sinks;
   float scale;        // log2(e) / sqrt(hd): softmax in powers of two
+
+  __device__ __forceinline__ int token_of(int row) const {
+    return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(row)) * div_mul >> div_shift);
+  }
+  // Offset of a row of an item in buffers whose token rows are ld values apart: row r of a value head is
+  // query head r % group of new token r / group.
+  __device__ __forceinline__ int64_t row_at(int t0, int head, int row, int64_t ld) const {
+    const int t = token_of(row);
+    return static_cast<int64_t>(t0 + t) * ld + (head * group + row - t * group) * kv.hd;
+  }
 };
+// With l = ceil(log2 group), ceil(2^(31 + l) / group) is below 2^32 and exceeds the quotient by less than 1, so row
+// times it exceeds row / group * 2^(31 + l) by less than 2^31 <= 2^(31 + l) / group: the whole part is exact.
+inline void paged_attn_divisor(PagedAttnArgs* a) {
+  int l = 0;
+  while ((1 << l) < a->group) ++l;
+  a->div_shift = 31 + l;
+  a->div_mul = static_cast<uint32_t>(((uint64_t{1} << a->div_shift) + a->group - 1) / a->group);
+}
 
 }  // namespace q4

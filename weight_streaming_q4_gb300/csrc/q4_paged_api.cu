@@ -132,6 +132,7 @@ extern "C" int q4_attn_paged(const q4_paged_kv* kv, const q4_paged_batch* batch,
   a.out = reinterpret_cast<__half*>(out);
   a.out_ld = out_ld;
   a.group = n_q_heads / a.kv.n_kv;
+  q4::paged_attn_divisor(&a);
   a.window = window;
   a.sinks = sinks;
   a.scale = static_cast<float>(1.4426950408889634 / sqrt(static_cast<double>(a.kv.hd)));

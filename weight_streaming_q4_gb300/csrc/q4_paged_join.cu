@@ -20,37 +20,56 @@ constexpr int kPjRows = 32;
 
 template <int HD>
 __global__ void __launch_bounds__(kPjThreads) paged_join_kernel(const __grid_constant__ PagedAttnArgs a, PartSlots parts) {
-  constexpr int E = HD / 32;
+  constexpr int E = HD / 32, B = 8;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int cta = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const JoinRecord rec = *parts.record(cta);
   const int end = min(rec.rows, static_cast<int>(blockIdx.y + 1) * kPjRows);
   if (rec.n <= 0) return;
   for (int r = blockIdx.y * kPjRows + warp; r < end; r += kPjThreads / 32) {
-    // part 0 is slot 1 of this CTA, part c > 0 slot 0 of CTA cta + c
-    float top = -INFINITY;
-    for (int c = lane; c < rec.n; c += 32) top = fmaxf(top, parts.max(cta + c, c == 0)[r]);
+    // Part 0 is slot 1 of this CTA, part c > 0 slot 0 of CTA cta + c.  Eight parts' loads at a time are
+    // under way together; the sums run in the order of the parts, rescaled when a later one raises the maximum.
+    float top = -INFINITY, sum = 0.f, o[E] = {};
+    for (int c0 = 0; c0 < rec.n; c0 += B) {
+      float m[B], l[B];
+      float2 v[B][E / 2];
 #pragma unroll
-    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-    float sum = 0.f, o[E] = {};
-#pragma unroll 4
-    for (int c = 0; c < rec.n; ++c) {
-      const float m = parts.max(cta + c, c == 0)[r], l = parts.sum(cta + c, c == 0)[r];
-      const float* src = parts.out(cta + c, c == 0) + static_cast<size_t>(r) * HD + lane * 2;
-      const float f = m == -INFINITY ? 0.f : exp2f(m - top);
-      sum += l * f;
+      for (int k = 0; k < B; ++k) {
+        const int c = min(c0 + k, rec.n - 1);
+        m[k] = c0 + k < rec.n ? parts.max(cta + c, c == 0)[r] : -INFINITY;
+        l[k] = parts.sum(cta + c, c == 0)[r];
+        const float* src = parts.out(cta + c, c == 0) + static_cast<size_t>(r) * HD + lane * 2;
 #pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const float2 v = *reinterpret_cast<const float2*>(src + e * 32);
-        o[e] += v.x * f;
-        o[e + 1] += v.y * f;
+        for (int e = 0; e < E / 2; ++e) v[k][e] = *reinterpret_cast<const float2*>(src + e * 64);
+      }
+      float most = top;
+#pragma unroll
+      for (int k = 0; k < B; ++k) most = fmaxf(most, m[k]);
+      const float back = top == most ? 1.f : exp2f(top - most);
+      top = most;
+      sum *= back;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= back;
+#pragma unroll
+      for (int k = 0; k < B; ++k) {
+        if (m[k] == -INFINITY) {
+          if (c0 + k < rec.n) sum += l[k] * 0.f;       // (a sum that is not a number stays one)
+          continue;
+        }
+        const float f = exp2f(m[k] - top);
+        sum += l[k] * f;
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+          o[2 * e] += v[k][e].x * f;
+          o[2 * e + 1] += v[k][e].y * f;
+        }
       }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int row = rec.row0 + r;
-    __half* out = a.out + static_cast<int64_t>(rec.t0 + row / a.group) * a.out_ld + (rec.head * a.group + row % a.group) * HD + lane * 2;
+    __half* out = a.out + a.row_at(rec.t0, rec.head, rec.row0 + r, a.out_ld) + lane * 2;
 #pragma unroll
-    for (int e = 0; e < E; e += 2) *reinterpret_cast<__half2*>(out + e * 32) = __floats2half2_rn(o[e] * inv, o[e + 1] * inv);
+    for (int e = 0; e < E / 2; ++e)
+      *reinterpret_cast<__half2*>(out + e * 64) = __floats2half2_rn(o[2 * e] * inv, o[2 * e + 1] * inv);
   }
 }
 

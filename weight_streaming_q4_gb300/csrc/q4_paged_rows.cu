@@ -27,7 +27,10 @@ namespace q4 {
 
 namespace {
 
-template <int HD, int MT, bool QF32, bool Q8>
+// CL: the CTAs of a cluster share every item (ClusterWalk).
+constexpr int kPrCluster = 8;
+
+template <int HD, int MT, bool QF32, bool Q8, bool CL>
 struct Pr {
   static constexpr int W = HD <= 128 ? 8 : 4;               // warps
   static constexpr int NT = W * 32;
@@ -39,9 +42,12 @@ struct Pr {
   static constexpr int PITCH = HD + 8;                      // floats of a row of the warps' results
   static constexpr int QB = MT * (QF32 ? 2 : 1) * KS * 512; // queries as operands
   static constexpr int MERGE = W * 16 * PITCH * 4 + 2 * W * R * 4;
-  static constexpr int FIT = (231424 - 1024 - QB - MERGE) / (W * STAGE);
+  // In a cluster the ring is empty when the results meet, and they take its place.
+  static constexpr int JOINED = CL ? R * (HD + 2) * 4 : 0;  // the CTA's result for the others of its cluster
+  static constexpr int FIT = (231424 - 1024 - QB - (CL ? 0 : MERGE)) / (W * STAGE);
   static constexpr int NS = FIT > 6 ? 6 : FIT;              // stages per warp
-  static constexpr int SMEM = 1024 + QB + MERGE + W * NS * STAGE;
+  static constexpr int RING = W * NS * STAGE;
+  static constexpr int SMEM = 1024 + QB + (CL ? (RING > MERGE + JOINED ? RING : MERGE + JOINED) : MERGE + RING);
   static_assert(NS >= 2, "a group is copied while one is read");
 };
 
@@ -83,6 +89,26 @@ __device__ __forceinline__ void pr_mma(float (&d)[4], const uint4& a, uint32_t b
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
+// All CTAs of the cluster, with what they wrote to shared memory.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Address of this CTA's shared-memory address `at` in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_at(uint32_t at, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float cluster_ld(uint32_t at) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 cluster_ld4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+  return v;
+}
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ float pr_exp2(float x) {
   float y;
@@ -107,24 +133,33 @@ __device__ __forceinline__ int place(int r, int c) {
   return r * ROW + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
+template <bool CL, int R>
+struct WalkOf {
+  using T = SegmentWalk<R, 32>;
+};
+template <int R>
+struct WalkOf<true, R> {
+  using T = ClusterWalk<R, 32>;
+};
+
 // A warp's groups, segment by segment: those of the copies run ahead of those
 // of the products.
-template <int R, int W>
+template <int R, int W, bool CL>
 struct GroupWalk {
-  SegmentWalk<R, 32> w;
+  typename WalkOf<CL, R>::T w;
   int g, n;             // the warp's current group of the segment, and the segment's groups
   __device__ __forceinline__ void count() {
     n = 2 * (w.i1 - w.i0);
-    if (w.i1 == w.it.cnt && (w.it.p1 & 31) < 16) --n;      // the last tile's second half holds no position seen
+    if (n > 0 && w.i1 == w.it.cnt && (w.it.p1 & 31) < 16) --n;      // the last tile's second half holds no position seen
     if (w.it.p1 < 0) n = 0;
   }
-  __device__ __forceinline__ int base() const { return w.it.tile(w.i0 + (g >> 1)) * 32 + (g & 1) * 16; }
+  __device__ __forceinline__ int base_of(int g) const { return w.it.tile(w.i0 + (g >> 1)) * 32 + (g & 1) * 16; }
 };
 
-template <int HD, int MT, bool QF32, bool Q8>
-__global__ void __launch_bounds__(Pr<HD, MT, QF32, Q8>::NT, 1)
+template <int HD, int MT, bool QF32, bool Q8, bool CL>
+__global__ void __launch_bounds__(Pr<HD, MT, QF32, Q8, CL>::NT, 1)
     paged_rows_kernel(const __grid_constant__ PagedAttnArgs a, PartSlots parts) {
-  using G = Pr<HD, MT, QF32, Q8>;
+  using G = Pr<HD, MT, QF32, Q8, CL>;
   constexpr int W = G::W, R = G::R, NS = G::NS, KS = G::KS, ROW = G::ROW, PIECES = ROW / 16;
   extern __shared__ __align__(16) char smem_pr[];
   PrCtl* c = reinterpret_cast<PrCtl*>(smem_pr);
@@ -132,35 +167,56 @@ __global__ void __launch_bounds__(Pr<HD, MT, QF32, Q8>::NT, 1)
   float* s_o = reinterpret_cast<float*>(smem_pr + 1024 + G::QB);          // [W][16][PITCH]
   float* s_m = s_o + W * 16 * G::PITCH;                                   // [W][R]
   float* s_l = s_m + W * R;
+  float* s_joined = s_l + W * R;                                          // CL: [R][HD], maxima [R], sums [R]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  const uint32_t ring = smem_u32(smem_pr + 1024 + G::QB + G::MERGE) + warp * NS * G::STAGE;
+  const uint32_t ring = smem_u32(smem_pr + 1024 + G::QB + (CL ? 0 : G::MERGE)) + warp * NS * G::STAGE;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!CL) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) c->bad = 0;
-  cta_work<R, 32, G::NT>(a, c->scan, &c->work);
-  const CtaWork work = c->work;
+  JoinRecord rec = {};       // thread 0's
+  long long per = 1;
+  GroupWalk<R, W, CL> u, cp;
+  if constexpr (CL) {
+    u.w.begin(a, blockIdx.x / kPrCluster, gridDim.x / kPrCluster, blockIdx.x % kPrCluster, kPrCluster);
+  } else {
+    CtaWork work;
+    if (a.b.n_seqs <= 32) {
+      work = warp_work<R, 32>(a);
+    } else {
+      cta_work<R, 32, G::NT>(a, c->scan, &c->work);
+      work = c->work;
+    }
+    per = work.per;
+    u.w.begin(a, work);
+  }
 
   // ------------------------------------------------------------------ copies
-  GroupWalk<R, W> cp;
-  cp.w.begin(a, work);
-  cp.g = warp;
-  if (cp.w.live()) cp.count();
-  // brings cp to the warp's next group; the page row of it, or -1 (no copy)
-  auto settle = [&]() -> int {
-    while (cp.w.live() && cp.g >= cp.n) {
-      cp.w.next(a);
-      cp.g = warp;
-      if (cp.w.live()) cp.count();
-    }
-    return cp.w.live() ? paged_row(a.kv, a.b, cp.w.seq, cp.base(), cp.w.head) : -1;
-  };
+  cp.w = u.w;
   uint32_t n_cp = 0, n_use = 0;
-  int next_row = settle();
-  auto copy = [&]() {       // the group at cp into the next stage; always one commit
-    if (cp.w.live()) {
+  // Page rows of the warp's next 32 groups in cp's segment, one per lane, from its group rows0 on.
+  int rows_of = -1, rows0 = 0;
+  auto look_up = [&]() {
+    const int g = cp.g + lane * W;
+    rows0 = cp.g;
+    rows_of = g < cp.n ? paged_row(a.kv, a.b, cp.w.seq, cp.base_of(g), cp.w.head) : -1;
+  };
+  auto enter = [&]() {      // cp's segment
+    cp.g = warp;
+    cp.count();
+    look_up();
+  };
+  auto copy = [&]() {       // the warp's next group into the next stage; always one commit
+    if (!CL) {
+      while (cp.w.live() && cp.g >= cp.n) {
+        cp.w.next(a);
+        if (cp.w.live()) enter();
+      }
+    }
+    if (cp.w.live() && cp.g < cp.n) {
+      if (cp.g - rows0 >= 32 * W) look_up();
       const int stage = n_cp % NS;
       const uint32_t to = ring + stage * G::STAGE;
-      const int r0 = next_row;
+      const int r0 = __shfl_sync(~0u, rows_of, (cp.g - rows0) / W);
       if (lane == 0) c->row[warp][stage] = r0;
       if (r0 >= 0) {
         const char* k = static_cast<const char*>(a.kv.k) + static_cast<size_t>(r0) * ROW;
@@ -181,20 +237,21 @@ __global__ void __launch_bounds__(Pr<HD, MT, QF32, Q8>::NT, 1)
       }
       ++n_cp;
       cp.g += W;
-      next_row = settle();
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-#pragma unroll 1
-  for (int i = 0; i < NS - 1; ++i) copy();
+  if (cp.w.live()) enter();
 
   // ------------------------------------------------------------------ items
-  GroupWalk<R, W> u;
-  u.w.begin(a, work);
   int seg = 0;
   for (; u.w.live(); u.w.next(a), ++seg) {
-    const SegmentWalk<R, 32>& w = u.w;
+    const auto& w = u.w;
     const int rows = w.rows(), row0 = w.j * R, first = w.sp.len - w.sp.n_new;
+    if constexpr (!CL) join_note(&rec, w, per);
+    if (CL && seg > 0) {
+      cp.w = u.w;
+      enter();
+    }
     // queries in operand order: lane (g, t) of product ks holds rows g and g + 8
     for (int x = tid; x < MT * KS * 32; x += G::NT) {
       const int mt = x / (KS * 32), ks = x / 32 % KS, xl = x & 31, xg = xl >> 2, xt = xl & 3;
@@ -205,7 +262,7 @@ __global__ void __launch_bounds__(Pr<HD, MT, QF32, Q8>::NT, 1)
         const int rr = mt * 16 + xg + (i & 1) * 8, r = row0 + rr;
         hi[i] = lo[i] = 0;
         if (rr < rows) {
-          const int64_t at = (w.sp.t0 + r / a.group) * a.q_ld + (w.head * a.group + r % a.group) * HD + (i < 2 ? e0 : e1);
+          const int64_t at = a.row_at(w.sp.t0, w.head, r, a.q_ld) + (i < 2 ? e0 : e1);
           if (QF32) {
             const float2 f = __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(a.q) + at));
             const __half2 h = __floats2half2_rn(f.x, f.y);
@@ -227,11 +284,15 @@ __global__ void __launch_bounds__(Pr<HD, MT, QF32, Q8>::NT, 1)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int rr = mt * 16 + g + h * 8;
-        p[mt][h] = rr < rows ? first + (row0 + rr) / a.group : -1;
+        p[mt][h] = rr < rows ? first + a.token_of(row0 + rr) : -1;
         m[mt][h] = -INFINITY, l[mt][h] = 0.f;
       }
 #pragma unroll
       for (int n = 0; n < HD / 8; ++n) o[mt][n][0] = o[mt][n][1] = o[mt][n][2] = o[mt][n][3] = 0.f;
+    }
+    if (CL || seg == 0) {
+#pragma unroll 1
+      for (int i = 0; i < NS - 1; ++i) copy();
     }
     __syncthreads();           // queries are there
     u.count();
@@ -243,14 +304,15 @@ __global__ void __launch_bounds__(Pr<HD, MT, QF32, Q8>::NT, 1)
       const int stage = n_use % NS;
       ++n_use;
       const uint32_t at = ring + stage * G::STAGE;
-      const int base = u.base();
+      const int base = u.base_of(u.g);
       if (c->row[warp][stage] >= 0) {
         // ---- scores
-        float s[MT][2][4];
+        // (two sums each, of the parts of an fp32 query or of every other product: shorter chains)
+        float s[MT][2][4], s2[MT][2][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.f;
+          for (int e = 0; e < 8; ++e) s[mt][e >> 2][e & 3] = s2[mt][e >> 2][e & 3] = 0.f;
         auto product = [&](int ks, const uint32_t (&b)[2][2]) {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
@@ -258,7 +320,7 @@ __global__ void __launch_bounds__(Pr<HD, MT, QF32, Q8>::NT, 1)
             for (int part = 0; part < (QF32 ? 2 : 1); ++part) {
               const uint4 q = s_q[((mt * (QF32 ? 2 : 1) + part) * KS + ks) * 32 + lane];
 #pragma unroll
-              for (int nt = 0; nt < 2; ++nt) pr_mma(s[mt][nt], q, b[nt][0], b[nt][1]);
+              for (int nt = 0; nt < 2; ++nt) pr_mma((QF32 ? part : ks & 1) ? s2[mt][nt] : s[mt][nt], q, b[nt][0], b[nt][1]);
             }
         };
         if (!Q8) {
@@ -294,6 +356,10 @@ __global__ void __launch_bounds__(Pr<HD, MT, QF32, Q8>::NT, 1)
             }
           }
         }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s[mt][e >> 2][e & 3] += s2[mt][e >> 2][e & 3];
         const bool whole = base + 15 <= w.it.p0 && (!a.window || base > w.it.p1 - a.window || base + 16 <= a.sinks);
         if (!whole) {
 #pragma unroll
@@ -395,6 +461,7 @@ __global__ void __launch_bounds__(Pr<HD, MT, QF32, Q8>::NT, 1)
       __syncwarp();            // the stage may be written again
     }
     if (found) *reinterpret_cast<volatile int*>(&c->bad) = seg + 1;
+    if (CL) __syncthreads();   // (the results take the ring's place)
     // ---- the warps' results meet, 16 rows at a time
     const bool whole_item = w.i0 == 0 && w.i1 == w.it.cnt;
     const int slot = w.i0 == 0 ? 1 : 0;
@@ -437,7 +504,7 @@ __global__ void __launch_bounds__(Pr<HD, MT, QF32, Q8>::NT, 1)
         }
         if (bad) {
           // values that were taken out of groups seen in part: back into the rows that see them
-          const int pr = first + r / a.group;
+          const int pr = first + a.token_of(r);
           for (int i = w.i0; i < w.i1; ++i)
             for (int b = 0; b < 2; ++b) {
               const int base = w.it.tile(i) * 32 + b * 16;
@@ -455,9 +522,12 @@ __global__ void __launch_bounds__(Pr<HD, MT, QF32, Q8>::NT, 1)
               }
             }
         }
-        if (whole_item) {
+        if (CL) {
+          *reinterpret_cast<float4*>(s_joined + (mt * 16 + rr) * HD + e) = make_float4(v[0], v[1], v[2], v[3]);
+          if (e == 0) s_joined[R * HD + mt * 16 + rr] = top, s_joined[R * (HD + 1) + mt * 16 + rr] = sum;
+        } else if (whole_item) {
           const float inv = sum == 0.f ? 0.f : 1.f / sum;
-          __half* out = a.out + static_cast<int64_t>(w.sp.t0 + r / a.group) * a.out_ld + (w.head * a.group + r % a.group) * HD + e;
+          __half* out = a.out + a.row_at(w.sp.t0, w.head, r, a.out_ld) + e;
           const uint2 y = make_uint2(as_u32(__floats2half2_rn(v[0] * inv, v[1] * inv)), as_u32(__floats2half2_rn(v[2] * inv, v[3] * inv)));
           *reinterpret_cast<uint2*>(out) = y;
         } else {
@@ -471,14 +541,48 @@ __global__ void __launch_bounds__(Pr<HD, MT, QF32, Q8>::NT, 1)
       }
       if (mt + 1 < MT) __syncthreads();        // the next item's queries are waited for anyway
     }
+    if constexpr (CL) {
+      // ---- the cluster's results meet: every CTA finishes its share of the outputs
+      cluster_sync();
+      const uint32_t own = smem_u32(s_joined);
+      for (int x = tid + w.rank * G::NT; x < rows * (HD / 4); x += G::NT * kPrCluster) {
+        const int rr = x / (HD / 4), e = x % (HD / 4) * 4;
+        float m8[kPrCluster], l8[kPrCluster];
+        float4 y[kPrCluster];
+#pragma unroll
+        for (int k = 0; k < kPrCluster; ++k) {
+          const uint32_t at = cluster_at(own, k);
+          m8[k] = cluster_ld(at + (R * HD + rr) * 4);
+          l8[k] = cluster_ld(at + (R * (HD + 1) + rr) * 4);
+          y[k] = cluster_ld4(at + (rr * HD + e) * 4);
+        }
+        float top = m8[0], sum = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 1; k < kPrCluster; ++k) top = fmaxf(top, m8[k]);
+#pragma unroll
+        for (int k = 0; k < kPrCluster; ++k) {
+          const float f = m8[k] == -INFINITY ? 0.f : pr_exp2(m8[k] - top);
+          sum += l8[k] * f;
+          v[0] += y[k].x * f, v[1] += y[k].y * f, v[2] += y[k].z * f, v[3] += y[k].w * f;
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        __half* out = a.out + a.row_at(w.sp.t0, w.head, row0 + rr, a.out_ld) + e;
+        *reinterpret_cast<uint2*>(out) = make_uint2(as_u32(__floats2half2_rn(v[0] * inv, v[1] * inv)),
+                                                    as_u32(__floats2half2_rn(v[2] * inv, v[3] * inv)));
+      }
+      cluster_sync();          // read by all before it is written again, or its CTA ends
+    }
   }
-  if (tid == 0) *parts.record(blockIdx.x) = join_record<R, 32>(a, work);
+  if (!CL && tid == 0) *parts.record(blockIdx.x) = rec;
 }
 
 template <int HD, int MT, bool QF32, bool Q8>
 cudaError_t prepare_rows() {
-  return cudaFuncSetAttribute(paged_rows_kernel<HD, MT, QF32, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Pr<HD, MT, QF32, Q8>::SMEM);
+  const cudaError_t e = cudaFuncSetAttribute(paged_rows_kernel<HD, MT, QF32, Q8, false>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, Pr<HD, MT, QF32, Q8, false>::SMEM);
+  if (e != cudaSuccess || MT > 1) return e;
+  return cudaFuncSetAttribute(paged_rows_kernel<HD, 1, QF32, Q8, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Pr<HD, 1, QF32, Q8, true>::SMEM);
 }
 
 template <int HD, int MT>
@@ -492,9 +596,28 @@ cudaError_t prepare_mt() {
 
 template <int HD, int MT, bool QF32, bool Q8>
 cudaError_t launch_rows(const PagedAttnArgs& a, void* ws, int grid, cudaStream_t s) {
-  using G = Pr<HD, MT, QF32, Q8>;
+  if constexpr (MT == 1) {
+    // Few items: a cluster each.  One token over 4096 positions of 8 value heads CL us against UN us, 512 CL us
+    // against UN us; with more items than clusters the even split wins.
+    const int items = a.b.n_seqs * a.kv.n_kv;
+    if (a.b.n_seqs <= 32 && items * kPrCluster <= grid) {
+      using G = Pr<HD, 1, QF32, Q8, true>;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(items * kPrCluster);
+      cfg.blockDim = dim3(G::NT);
+      cfg.dynamicSmemBytes = G::SMEM;
+      cfg.stream = s;
+      cudaLaunchAttribute at[1];
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = kPrCluster, at[0].val.clusterDim.y = 1, at[0].val.clusterDim.z = 1;
+      cfg.attrs = at;
+      cfg.numAttrs = 1;
+      return cudaLaunchKernelEx(&cfg, paged_rows_kernel<HD, 1, QF32, Q8, true>, a, PartSlots{});
+    }
+  }
+  using G = Pr<HD, MT, QF32, Q8, false>;
   PartSlots parts{static_cast<char*>(ws), G::R, HD};
-  paged_rows_kernel<HD, MT, QF32, Q8><<<grid, G::NT, G::SMEM, s>>>(a, parts);
+  paged_rows_kernel<HD, MT, QF32, Q8, false><<<grid, G::NT, G::SMEM, s>>>(a, parts);
   const cudaError_t e = cudaGetLastError();
   return e != cudaSuccess ? e : paged_join_launch(a, parts, grid, s);
 }

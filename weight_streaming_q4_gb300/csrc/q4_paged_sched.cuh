@@ -40,8 +40,8 @@ __device__ __forceinline__ ItemTiles item_tiles(const PagedAttnArgs& a, const Se
   ItemTiles t;
   const int rows = sp.n_new * a.group;
   const int first = sp.len - sp.n_new;
-  t.p0 = first + j * R / a.group;
-  t.p1 = first + (min(rows, j * R + R) - 1) / a.group;
+  t.p0 = first + a.token_of(j * R);
+  t.p1 = first + a.token_of(min(rows, j * R + R) - 1);
   t.n_sink = 0, t.lo = 0, t.cnt = 1;
   if (t.p1 < 0) return t;
   const int seen = a.window ? max(0, t.p0 - a.window + 1) : 0;     // first position inside the first row's window
@@ -106,7 +106,9 @@ __device__ void cta_work(const PagedAttnArgs& a, long long* s_scan, CtaWork* out
     for (int s = tid; s < n_seqs; s += NT) mine += seq_units<R, BN>(a, paged_span(a.kv, a.b, s));
     scan(mine, &total);
   }
-  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  // (64-bit divisions are slow; that many units are days of work)
+  const long long per = total < 0x7fffffff ? (static_cast<unsigned>(total) + gridDim.x - 1) / gridDim.x
+                                           : (total + gridDim.x - 1) / gridDim.x;
   const long long u0 = per * blockIdx.x;
   if (tid == 0) out->per = per, out->n = u0 < total ? static_cast<int>(min(per, total - u0)) : 0;
   auto place = [&](int s, long long end) {     // the thread whose sequence holds u0 finds the unit in it
@@ -116,7 +118,8 @@ __device__ void cta_work(const PagedAttnArgs& a, long long* s_scan, CtaWork* out
       const int cnt = item_tiles<R, BN>(a, sp, j).cnt;
       const long long of_j = static_cast<long long>(cnt) * a.kv.n_kv;
       if (u < of_j) {
-        out->seq = s, out->j = j, out->head = static_cast<int>(u / cnt), out->tile = static_cast<int>(u % cnt);
+        const unsigned u32 = static_cast<unsigned>(u);      // below cnt * n_kv: head by head
+        out->seq = s, out->j = j, out->head = static_cast<int>(u32 / cnt), out->tile = static_cast<int>(u32 % cnt);
         return;
       }
       u -= of_j;
@@ -140,6 +143,48 @@ __device__ void cta_work(const PagedAttnArgs& a, long long* s_scan, CtaWork* out
     }
   }
   __syncthreads();
+}
+
+// cta_work for at most 32 sequences, by every warp for itself: a sequence per
+// lane, no barrier and no shared memory.
+template <int R, int BN>
+__device__ __forceinline__ CtaWork warp_work(const PagedAttnArgs& a) {
+  const int lane = threadIdx.x & 31;
+  SeqSpan sp = {};
+  long long mine = 0;
+  if (lane < a.b.n_seqs) {
+    sp = paged_span(a.kv, a.b, lane);
+    mine = seq_units<R, BN>(a, sp);
+  }
+  long long end = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(~0u, end, d);
+    if (lane >= d) end += o;
+  }
+  const long long total = __shfl_sync(~0u, end, 31);
+  CtaWork w = {};
+  w.per = total < 0x7fffffff ? (static_cast<unsigned>(total) + gridDim.x - 1) / gridDim.x : (total + gridDim.x - 1) / gridDim.x;
+  const long long u0 = w.per * blockIdx.x;
+  w.n = u0 < total ? static_cast<int>(min(w.per, total - u0)) : 0;
+  const bool here = mine > 0 && u0 >= end - mine && u0 < end;
+  if (here) {
+    long long u = u0 - (end - mine);
+    for (int j = 0;; ++j) {
+      const int cnt = item_tiles<R, BN>(a, sp, j).cnt;
+      const long long of_j = static_cast<long long>(cnt) * a.kv.n_kv;
+      if (u < of_j) {
+        const unsigned u32 = static_cast<unsigned>(u);
+        w.j = j, w.head = static_cast<int>(u32 / cnt), w.tile = static_cast<int>(u32 % cnt);
+        break;
+      }
+      u -= of_j;
+    }
+  }
+  const unsigned who = __ballot_sync(~0u, here);
+  w.seq = who ? __ffs(who) - 1 : 0;
+  w.j = __shfl_sync(~0u, w.j, w.seq), w.head = __shfl_sync(~0u, w.head, w.seq), w.tile = __shfl_sync(~0u, w.tile, w.seq);
+  return w;
 }
 
 // A CTA's units as segments: the tiles of one item that it holds.  Every role
@@ -183,6 +228,57 @@ struct SegmentWalk {
   __device__ __forceinline__ int rows() const { return min(R, sp.n_new * group - j * R); }
 };
 
+// For few items (at most 32 sequences): C CTAs of a cluster share every item,
+// rank r the r-th part of its tiles, and join their results over distributed
+// shared memory; no second kernel and no workspace.
+template <int R, int BN>
+struct ClusterWalk {
+  int group;
+  int item, items, step, rank, ranks;      // the cluster's current item; all items; clusters
+  int seq, j, head;
+  SeqSpan sp;
+  ItemTiles it;
+  int i0, i1;
+  SeqSpan mine;                             // this lane's sequence
+  int end, count;                           // ... its last item + 1, and how many
+
+  __device__ __forceinline__ void begin(const PagedAttnArgs& a, int cluster, int clusters, int r, int n) {
+    const int lane = threadIdx.x & 31;
+    group = a.group, item = cluster, step = clusters, rank = r, ranks = n;
+    mine = {};
+    count = 0;
+    if (lane < a.b.n_seqs) {
+      mine = paged_span(a.kv, a.b, lane);
+      count = (mine.n_new * group + R - 1) / R * a.kv.n_kv;
+    }
+    end = count;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(~0u, end, d);
+      if (lane >= d) end += o;
+    }
+    items = __shfl_sync(~0u, end, 31);
+    find(a);
+  }
+  __device__ __forceinline__ void find(const PagedAttnArgs& a) {
+    if (item >= items) return;
+    seq = __ffs(__ballot_sync(~0u, item < end && item >= end - count)) - 1;
+    const int x = item - __shfl_sync(~0u, end - count, seq);
+    j = x / a.kv.n_kv, head = x - j * a.kv.n_kv;
+    sp.t0 = __shfl_sync(~0u, mine.t0, seq), sp.n_new = __shfl_sync(~0u, mine.n_new, seq);
+    sp.len = __shfl_sync(~0u, mine.len, seq);
+    it = item_tiles<R, BN>(a, sp, j);
+    const int per = (it.cnt + ranks - 1) / ranks;
+    i0 = min(it.cnt, rank * per), i1 = min(it.cnt, i0 + per);
+  }
+  __device__ __forceinline__ bool live() const { return item < items; }
+  __device__ __forceinline__ void next(const PagedAttnArgs& a) {
+    item += step;
+    find(a);
+  }
+  __device__ __forceinline__ int rows() const { return min(R, sp.n_new * group - j * R); }
+};
+
 // Workspace: a record per CTA, then the partial results of its two slots.
 struct JoinRecord {
   int n;                    // CTAs that hold a part of the item that slot 1 begins (0: none)
@@ -192,19 +288,13 @@ struct JoinRecord {
 constexpr size_t kPagedRecordBytes = kPagedMaxCtas * 32;
 static_assert(sizeof(JoinRecord) <= 32, "records are 32 bytes apart");
 
-// The record of a CTA that did `work`.
+// Notes in *rec the segment g if it begins an item that its CTA does not finish
+// (per: units of every CTA).
 template <int R, int BN>
-__device__ JoinRecord join_record(const PagedAttnArgs& a, const CtaWork& work) {
-  JoinRecord rec = {};
-  SegmentWalk<R, BN> g;
-  for (g.begin(a, work); g.live(); g.next(a)) {
-    if (g.left > g.i1 - g.i0) continue;
-    if (g.i0 == 0 && g.i1 < g.it.cnt) {       // the last segment begins an item and does not finish it
-      rec.n = 1 + static_cast<int>((g.it.cnt - g.i1 + work.per - 1) / work.per);
-      rec.t0 = g.sp.t0, rec.row0 = g.j * R, rec.rows = g.rows(), rec.head = g.head;
-    }
-  }
-  return rec;
+__device__ __forceinline__ void join_note(JoinRecord* rec, const SegmentWalk<R, BN>& g, long long per) {
+  if (g.i0 != 0 || g.i1 == g.it.cnt) return;
+  rec->n = 1 + (g.it.cnt - g.i1 + static_cast<int>(per) - 1) / static_cast<int>(per);
+  rec->t0 = g.sp.t0, rec->row0 = g.j * R, rec->rows = g.rows(), rec->head = g.head;
 }
 
 struct PartSlots {

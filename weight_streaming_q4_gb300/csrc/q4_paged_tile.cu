@@ -298,14 +298,18 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
     fence_mbar_init();
   }
   if (warp == G::W_MMA) tm_alloc(&c->tmem, 512);
-  cta_work<R, BN, G::THREADS>(a, c->scan, &c->work);     // ends synchronised
+  if (a.b.n_seqs > 32) cta_work<R, BN, G::THREADS>(a, c->scan, &c->work);
+  const bool few = a.b.n_seqs <= 32;
+  CtaWork work;
+  if (few) work = warp_work<R, BN>(a);
   tm_before();
   __syncthreads();
   tm_after();
   const uint32_t tmem = __shfl_sync(~0u, c->tmem, 0);
-  const CtaWork work = c->work;
+  if (!few) work = c->work;
   SegmentWalk<R, BN> w;
   w.begin(a, work);
+  JoinRecord rec = {};       // thread 0's
 
   if (warp < 4 * NQ)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::REG_S));
@@ -327,7 +331,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
       if (q * 128 >= rows) return;
       constexpr int PIECES = HD / 8;
       const int own = q * 128 + wl * 32 + lane, r = g.j * R + own;
-      const int64_t own_at = own < rows ? (g.sp.t0 + r / a.group) * a.q_ld + (g.head * a.group + r % a.group) * HD : -1;
+      const int64_t own_at = own < rows ? a.row_at(g.sp.t0, g.head, r, a.q_ld) : -1;
       if (!QF32) {
 #pragma unroll 4
         for (int x = lane; x < 32 * PIECES; x += 32) {
@@ -373,10 +377,11 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
     }
     while (w.live()) {
       const int rows = w.rows(), row0 = w.j * R;
+      join_note(&rec, w, work.per);
       const bool active = q * 128 < rows;
       const int r = row0 + q * 128 + wl * 32 + lane;       // this thread's row
       const bool mine = q * 128 + wl * 32 + lane < rows;
-      const int p = mine ? w.sp.len - w.sp.n_new + r / a.group : -1;
+      const int p = mine ? w.sp.len - w.sp.n_new + a.token_of(r) : -1;
       float m = -INFINITY, l = 0.f;
       if (!active) n_k += w.i1 - w.i0;
       for (int i = active ? w.i0 : w.i1; i < w.i1; ++i, ++n_s, ++n_k) {
@@ -493,8 +498,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
       // A thread holds a row, but stores go out with four lanes to a row, over shared memory: 64 bytes of
       // each row at a time, the 16-byte pieces exchanged by row so that they fall into different banks.
       // (A store of 16 bytes in each of 32 rows costs 32 passes.)
-      const int64_t out_at = static_cast<int64_t>(w.sp.t0 + (mine ? r / a.group : 0)) * a.out_ld +
-                             (w.head * a.group + (mine ? r % a.group : 0)) * HD;
+      const int64_t out_at = mine ? a.row_at(w.sp.t0, w.head, r, a.out_ld) : 0;
       char* const turn_at = tiles + G::QALL + NS * G::KB + G::NRAW * G::RAW + warp * 2048;
       char* const turn_mine = turn_at + lane * 64;
       float* const part0 = parts.out(blockIdx.x, slot) + static_cast<size_t>(q * 128 + wl * 32) * HD;
@@ -852,7 +856,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
       }
     }
   }
-  if (tid == 0) *parts.record(blockIdx.x) = join_record<R, BN>(a, work);
+  if (tid == 0) *parts.record(blockIdx.x) = rec;
   __syncwarp();
   tm_before();
   __syncthreads();
