@@ -21,6 +21,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "q4_paged_sched.cuh"
 
 namespace q4 {
@@ -32,13 +34,19 @@ constexpr int kPrCluster = 8;
 
 template <int HD, int MT, bool QF32, bool Q8, bool CL>
 struct Pr {
-  static constexpr int W = HD <= 128 ? 8 : 4;               // warps
+  // Positions of a group, a warp's step.  At head_dim 64 a step of 32 pays the shuffles, the comparison with the
+  // maximum and the copies' addresses half as often (16 sequences under a window 17.0 us against 18.4); above, it
+  // takes the registers of the warps that hide its latency.
+  static constexpr int GP = HD == 64 && MT == 1 ? 32 : 16;
+  // Warps.  12 for Q8, whose conversion makes it the issue slots that count (64 sequences of the 70B heads 175 us
+  // against 190 with 8).
+  static constexpr int W = HD > 128 ? 4 : HD == 128 && Q8 && MT == 1 ? 12 : 8;
   static constexpr int NT = W * 32;
   static constexpr int R = 16 * MT;
   static constexpr int KS = HD / 16;                        // products of a key group
   static constexpr int ROW = Q8 ? HD : 2 * HD;              // bytes of a staged key
-  static constexpr int SC = Q8 ? HD / 32 * 2 * 16 : 0;      // bytes of a group's scales
-  static constexpr int STAGE = 2 * 16 * ROW + 2 * SC;       // keys, values, their scales
+  static constexpr int SC = Q8 ? HD / 32 * 2 * GP : 0;      // bytes of a group's scales
+  static constexpr int STAGE = 2 * GP * ROW + 2 * SC;       // keys, values, their scales
   static constexpr int PITCH = HD + 8;                      // floats of a row of the warps' results
   static constexpr int QB = MT * (QF32 ? 2 : 1) * KS * 512; // queries as operands
   static constexpr int MERGE = W * 16 * PITCH * 4 + 2 * W * R * 4;
@@ -53,9 +61,9 @@ struct Pr {
 
 struct PrCtl {
   CtaWork work;
-  long long scan[9];
+  long long scan[17];
   int bad;                 // segment number + 1 in whose partly seen values a warp met infinities or NaN
-  int row[8][8];           // per warp and stage: page-memory row of the group (-1: hole)
+  uint32_t there[16][8];   // per warp and stage: bit i = positions 16 i .. of the group are in a page
 };
 static_assert(sizeof(PrCtl) <= 1024, "control data fits its place");
 
@@ -110,6 +118,7 @@ __device__ __forceinline__ float4 cluster_ld4(uint32_t at) {
   return v;
 }
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
 __device__ __forceinline__ float pr_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -144,16 +153,18 @@ struct WalkOf<true, R> {
 
 // A warp's groups, segment by segment: those of the copies run ahead of those
 // of the products.
-template <int R, int W, bool CL>
+template <int R, int W, int GP, bool CL>
 struct GroupWalk {
   typename WalkOf<CL, R>::T w;
   int g, n;             // the warp's current group of the segment, and the segment's groups
   __device__ __forceinline__ void count() {
-    n = 2 * (w.i1 - w.i0);
-    if (n > 0 && w.i1 == w.it.cnt && (w.it.p1 & 31) < 16) --n;      // the last tile's second half holds no position seen
+    n = 32 / GP * (w.i1 - w.i0);
+    if (GP == 16 && n > 0 && w.i1 == w.it.cnt && (w.it.p1 & 31) < 16) --n;      // the last tile's second half holds no position seen
     if (w.it.p1 < 0) n = 0;
   }
-  __device__ __forceinline__ int base_of(int g) const { return w.it.tile(w.i0 + (g >> 1)) * 32 + (g & 1) * 16; }
+  __device__ __forceinline__ int base_of(int g) const {
+    return GP == 32 ? w.it.tile(w.i0 + g) * 32 : w.it.tile(w.i0 + (g >> 1)) * 32 + (g & 1) * 16;
+  }
 };
 
 template <int HD, int MT, bool QF32, bool Q8, bool CL>
@@ -161,6 +172,7 @@ __global__ void __launch_bounds__(Pr<HD, MT, QF32, Q8, CL>::NT, 1)
     paged_rows_kernel(const __grid_constant__ PagedAttnArgs a, PartSlots parts) {
   using G = Pr<HD, MT, QF32, Q8, CL>;
   constexpr int W = G::W, R = G::R, NS = G::NS, KS = G::KS, ROW = G::ROW, PIECES = ROW / 16;
+  constexpr int GP = G::GP, SUB = GP / 16, NN = GP / 8;
   extern __shared__ __align__(16) char smem_pr[];
   PrCtl* c = reinterpret_cast<PrCtl*>(smem_pr);
   uint4* s_q = reinterpret_cast<uint4*>(smem_pr + 1024);                  // [MT][part][KS][lane]
@@ -175,7 +187,7 @@ __global__ void __launch_bounds__(Pr<HD, MT, QF32, Q8, CL>::NT, 1)
   if (tid == 0) c->bad = 0;
   JoinRecord rec = {};       // thread 0's
   long long per = 1;
-  GroupWalk<R, W, CL> u, cp;
+  GroupWalk<R, W, GP, CL> u, cp;
   if constexpr (CL) {
     u.w.begin(a, blockIdx.x / kPrCluster, gridDim.x / kPrCluster, blockIdx.x % kPrCluster, kPrCluster);
   } else {
@@ -193,12 +205,13 @@ __global__ void __launch_bounds__(Pr<HD, MT, QF32, Q8, CL>::NT, 1)
   // ------------------------------------------------------------------ copies
   cp.w = u.w;
   uint32_t n_cp = 0, n_use = 0;
-  // Page rows of the warp's next 32 groups in cp's segment, one per lane, from its group rows0 on.
+  // Page rows of the warp's next 32 / SUB groups in cp's segment, 16 positions per lane, from its group rows0 on.
   int rows_of = -1, rows0 = 0;
   auto look_up = [&]() {
-    const int g = cp.g + lane * W;
+    const int g = cp.g + lane / SUB * W;
     rows0 = cp.g;
-    rows_of = g < cp.n ? paged_row(a.kv, a.b, cp.w.seq, cp.base_of(g), cp.w.head) : -1;
+    const int at = g < cp.n ? cp.base_of(g) + lane % SUB * 16 : 0;
+    rows_of = g < cp.n && at <= cp.w.it.p1 ? paged_row(a.kv, a.b, cp.w.seq, at, cp.w.head) : -1;
   };
   auto enter = [&]() {      // cp's segment
     cp.g = warp;
@@ -213,28 +226,43 @@ __global__ void __launch_bounds__(Pr<HD, MT, QF32, Q8, CL>::NT, 1)
       }
     }
     if (cp.w.live() && cp.g < cp.n) {
-      if (cp.g - rows0 >= 32 * W) look_up();
+      if (cp.g - rows0 >= 32 / SUB * W) look_up();
       const int stage = n_cp % NS;
       const uint32_t to = ring + stage * G::STAGE;
-      const int r0 = __shfl_sync(~0u, rows_of, (cp.g - rows0) / W);
-      if (lane == 0) c->row[warp][stage] = r0;
-      if (r0 >= 0) {
+      uint32_t there = 0;
+#pragma unroll
+      for (int sub = 0; sub < SUB; ++sub) {
+        const int r0 = __shfl_sync(~0u, rows_of, (cp.g - rows0) / W * SUB + sub);
+        if (r0 < 0) {
+          // no page, or positions that no row sees: what counts beside weights of zero is that the values are finite
+          if (SUB > 1) {
+            constexpr int N = Q8 ? G::SC / SUB / 16 : 16 * PIECES;
+            const uint32_t at = Q8 ? to + 2 * GP * ROW + G::SC + sub * (G::SC / SUB) : to + GP * ROW + sub * 16 * ROW;
+#pragma unroll 1
+            for (int x = lane; x < N; x += 32)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + x * 16), "r"(0) : "memory");
+          }
+          continue;
+        }
+        there |= 1u << sub;
         const char* k = static_cast<const char*>(a.kv.k) + static_cast<size_t>(r0) * ROW;
         const char* v = static_cast<const char*>(a.kv.v) + static_cast<size_t>(r0) * ROW;
 #pragma unroll
         for (int x = lane; x < 16 * PIECES; x += 32)
-          pr_cp16(to + place<ROW, Q8>(x / PIECES, x % PIECES), k + x * 16);
+          pr_cp16(to + place<ROW, Q8>(sub * 16 + x / PIECES, x % PIECES), k + x * 16);
         if (Q8) {
-          constexpr int SP = G::SC / 16;
+          constexpr int SP = G::SC / SUB / 16;               // 16-byte pieces of 16 positions' scales
           const char* ks = reinterpret_cast<const char*>(a.kv.ks) + static_cast<size_t>(r0) * (HD / 16);
           const char* vs = reinterpret_cast<const char*>(a.kv.vs) + static_cast<size_t>(r0) * (HD / 16);
-          if (lane < SP) pr_cp16(to + 32 * ROW + lane * 16, ks + lane * 16);
-          else if (lane < 2 * SP) pr_cp16(to + 32 * ROW + lane * 16, vs + (lane - SP) * 16);
+          const uint32_t sc = to + 2 * GP * ROW + sub * SP * 16;
+          if (lane < SP) pr_cp16(sc + lane * 16, ks + lane * 16);
+          else if (lane < 2 * SP) pr_cp16(sc + G::SC + (lane - SP) * 16, vs + (lane - SP) * 16);
         }
 #pragma unroll
         for (int x = lane; x < 16 * PIECES; x += 32)
-          pr_cp16(to + 16 * ROW + place<ROW, false>(x / PIECES, x % PIECES), v + x * 16);
+          pr_cp16(to + GP * ROW + place<ROW, false>(sub * 16 + x / PIECES, x % PIECES), v + x * 16);
       }
+      if (lane == 0) c->there[warp][stage] = there;
       ++n_cp;
       cp.g += W;
     }
@@ -305,44 +333,52 @@ __global__ void __launch_bounds__(Pr<HD, MT, QF32, Q8, CL>::NT, 1)
       ++n_use;
       const uint32_t at = ring + stage * G::STAGE;
       const int base = u.base_of(u.g);
-      if (c->row[warp][stage] >= 0) {
+      const uint32_t there = c->there[warp][stage];
+      if (there) {
         // ---- scores
-        // (two sums each, of the parts of an fp32 query or of every other product: shorter chains)
-        float s[MT][2][4], s2[MT][2][4];
+        // (with two column tiles, two sums each, of the parts of an fp32 query or of every other product: shorter chains)
+        float s[MT][NN][4], s2[MT][NN][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) s[mt][e >> 2][e & 3] = s2[mt][e >> 2][e & 3] = 0.f;
-        auto product = [&](int ks, const uint32_t (&b)[2][2]) {
+          for (int e = 0; e < 4 * NN; ++e) s[mt][e >> 2][e & 3] = s2[mt][e >> 2][e & 3] = 0.f;
+        auto product = [&](int ks, const uint32_t (&b)[NN][2]) {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int part = 0; part < (QF32 ? 2 : 1); ++part) {
               const uint4 q = s_q[((mt * (QF32 ? 2 : 1) + part) * KS + ks) * 32 + lane];
 #pragma unroll
-              for (int nt = 0; nt < 2; ++nt) pr_mma((QF32 ? part : ks & 1) ? s2[mt][nt] : s[mt][nt], q, b[nt][0], b[nt][1]);
+              for (int nt = 0; nt < NN; ++nt)
+                pr_mma(NN == 2 && (QF32 ? part : ks & 1) ? s2[mt][nt] : s[mt][nt], q, b[nt][0], b[nt][1]);
             }
         };
         if (!Q8) {
 #pragma unroll
           for (int k2 = 0; k2 < KS / 2; ++k2) {
-            uint32_t r[2][4];
+            uint32_t r[NN][4], b[NN][2];
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) pr_ldsm(r[nt], at + place<ROW, false>(nt * 8 + (lane & 7), k2 * 4 + (lane >> 3)));
-            const uint32_t b0[2][2] = {{r[0][0], r[0][1]}, {r[1][0], r[1][1]}};
-            const uint32_t b1[2][2] = {{r[0][2], r[0][3]}, {r[1][2], r[1][3]}};
-            product(2 * k2, b0);
-            product(2 * k2 + 1, b1);
+            for (int nt = 0; nt < NN; ++nt) {
+              pr_ldsm(r[nt], at + place<ROW, false>(nt * 8 + (lane & 7), k2 * 4 + (lane >> 3)));
+              b[nt][0] = r[nt][0], b[nt][1] = r[nt][1];
+            }
+            product(2 * k2, b);
+#pragma unroll
+            for (int nt = 0; nt < NN; ++nt) b[nt][0] = r[nt][2], b[nt][1] = r[nt][3];
+            product(2 * k2 + 1, b);
           }
         } else {
 #pragma unroll
           for (int j = 0; j < HD / 64; ++j) {
-            __half2 h[2][8];
+            __half2 h[NN][8];
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
+            for (int nt = 0; nt < NN; ++nt) {
               const uint4 q = pr_lds16(at + place<ROW, true>(nt * 8 + g, t + 4 * j));
               uint16_t d;
-              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(d) : "r"(at + 32 * ROW + (nt * 8 + g) * (HD / 16) + ((t >> 1) + 2 * j) * 2) : "memory");
+              asm volatile("ld.shared.u16 %0, [%1];"
+                           : "=h"(d)
+                           : "r"(at + 2 * GP * ROW + (nt * 8 + g) * (HD / 16) + ((t >> 1) + 2 * j) * 2)
+                           : "memory");
               const __half2 d2 = __half2half2(__ushort_as_half(d));
               q8_values4(q.x, d2, h[nt][0], h[nt][1]);
               q8_values4(q.y, d2, h[nt][2], h[nt][3]);
@@ -351,34 +387,42 @@ __global__ void __launch_bounds__(Pr<HD, MT, QF32, Q8, CL>::NT, 1)
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const uint32_t b[2][2] = {{as_u32(h[0][2 * k]), as_u32(h[0][2 * k + 1])}, {as_u32(h[1][2 * k]), as_u32(h[1][2 * k + 1])}};
+              uint32_t b[NN][2];
+#pragma unroll
+              for (int nt = 0; nt < NN; ++nt) b[nt][0] = as_u32(h[nt][2 * k]), b[nt][1] = as_u32(h[nt][2 * k + 1]);
               product(4 * j + k, b);
             }
           }
         }
+        if (NN == 2) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+          for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) s[mt][e >> 2][e & 3] += s2[mt][e >> 2][e & 3];
-        const bool whole = base + 15 <= w.it.p0 && (!a.window || base > w.it.p1 - a.window || base + 16 <= a.sinks);
+            for (int e = 0; e < 4 * NN; ++e) s[mt][e >> 2][e & 3] += s2[mt][e >> 2][e & 3];
+        }
+        const bool whole = there == (1u << SUB) - 1 && base + GP - 1 <= w.it.p0 &&
+                           (!a.window || base > w.it.p1 - a.window || base + GP <= a.sinks);
         if (!whole) {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < 4 * NN; ++e) {
               const int pr = p[mt][(e >> 1) & 1], x = base + (e >> 2) * 8 + 2 * t + (e & 1);
-              if (x > pr || (a.window && x <= pr - a.window && x >= a.sinks)) s[mt][e >> 2][e & 3] = -INFINITY;
+              if (x > pr || (a.window && x <= pr - a.window && x >= a.sinks) || !((there >> (e >> 3)) & 1))
+                s[mt][e >> 2][e & 3] = -INFINITY;
             }
         }
         // ---- weights
-        uint4 pw[MT];
+        uint4 pw[MT][SUB];
         float top[MT][2];
         bool raise = false;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            float x = fmaxf(fmaxf(s[mt][0][2 * h], s[mt][0][2 * h + 1]), fmaxf(s[mt][1][2 * h], s[mt][1][2 * h + 1]));
+            float x = -INFINITY;
+#pragma unroll
+            for (int nt = 0; nt < NN; ++nt) x = fmaxf(x, fmaxf(s[mt][nt][2 * h], s[mt][nt][2 * h + 1]));
             x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
             x = fmaxf(x, __shfl_xor_sync(~0u, x, 2)) * a.scale;
             top[mt][h] = x;
@@ -402,61 +446,82 @@ __global__ void __launch_bounds__(Pr<HD, MT, QF32, Q8, CL>::NT, 1)
         }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          uint32_t x[2][2];
+          uint32_t x[NN][2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const float mm = m[mt][h] == -INFINITY ? 0.f : m[mt][h];
+            float sum = 0.f;
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
+            for (int nt = 0; nt < NN; ++nt) {
               const float w0 = pr_exp2(fmaf(s[mt][nt][2 * h], a.scale, -mm)), w1 = pr_exp2(fmaf(s[mt][nt][2 * h + 1], a.scale, -mm));
-              l[mt][h] += w0 + w1;
+              sum += w0 + w1;
               x[nt][h] = as_u32(__floats2half2_rn(w0, w1));
             }
+            l[mt][h] += sum;
           }
-          pw[mt] = make_uint4(x[0][0], x[0][1], x[1][0], x[1][1]);
+#pragma unroll
+          for (int sub = 0; sub < SUB; ++sub)
+            pw[mt][sub] = make_uint4(x[2 * sub][0], x[2 * sub][1], x[2 * sub + 1][0], x[2 * sub + 1][1]);
         }
-        // ---- values
-        const int vr = (lane & 7) + (lane & 8);
-        __half2 d0[HD / 32], d1[HD / 32];       // Q8: scales of positions 2t, 2t + 1 and of 8 further on
-        if (Q8) {
-          const uint32_t sc = at + 32 * ROW + G::SC;
+        // ---- values, 16 positions at a time
+        auto values = [&](auto cleaning) {      // (code of its own for the few groups to be cleaned)
+          const int vr = (lane & 7) + (lane & 8);
 #pragma unroll
-          for (int b = 0; b < HD / 32; ++b) {
-            uint16_t x[4];
+          for (int sub = 0; sub < SUB; ++sub) {
+            __half2 d0[HD / 32], d1[HD / 32];       // Q8: scales of positions 2t, 2t + 1 and of 8 further on
+            if (Q8) {
+              const uint32_t sc = at + 2 * GP * ROW + G::SC + sub * 16 * (HD / 16);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x[i]) : "r"(sc + (2 * t + (i & 1) + (i >> 1) * 8) * (HD / 16) + b * 2) : "memory");
-            d0[b] = __halves2half2(__ushort_as_half(x[0]), __ushort_as_half(x[1]));
-            d1[b] = __halves2half2(__ushort_as_half(x[2]), __ushort_as_half(x[3]));
-          }
-        }
+              for (int b = 0; b < HD / 64; ++b) {   // two blocks' scales at a time
+                uint32_t x[4];
 #pragma unroll
-        for (int i = 0; i < PIECES / 2; ++i) {
-          uint32_t r[4];
-          pr_ldsm_t(r, at + 16 * ROW + place<ROW, false>(vr, 2 * i + (lane >> 4)));
-          if (!Q8) {
-            if (!whole) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) r[e] = pr_finite(r[e], &found);
+                for (int i = 0; i < 4; ++i)
+                  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x[i]) : "r"(sc + (2 * t + (i & 1) + (i >> 1) * 8) * (HD / 16) + b * 4) : "memory");
+                uint32_t y;
+                asm("prmt.b32 %0, %1, %2, 0x5410;" : "=r"(y) : "r"(x[0]), "r"(x[1]));
+                d0[2 * b] = as_h2(y);
+                asm("prmt.b32 %0, %1, %2, 0x7632;" : "=r"(y) : "r"(x[0]), "r"(x[1]));
+                d0[2 * b + 1] = as_h2(y);
+                asm("prmt.b32 %0, %1, %2, 0x5410;" : "=r"(y) : "r"(x[2]), "r"(x[3]));
+                d1[2 * b] = as_h2(y);
+                asm("prmt.b32 %0, %1, %2, 0x7632;" : "=r"(y) : "r"(x[2]), "r"(x[3]));
+                d1[2 * b + 1] = as_h2(y);
+              }
             }
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              pr_mma(o[mt][2 * i], pw[mt], r[0], r[1]);
-              pr_mma(o[mt][2 * i + 1], pw[mt], r[2], r[3]);
-            }
-          } else {
+            for (int i = 0; i < PIECES / 2; ++i) {
+              uint32_t r[4];
+              pr_ldsm_t(r, at + GP * ROW + place<ROW, false>(sub * 16 + vr, 2 * i + (lane >> 4)));
+              if (!Q8) {
+                if (decltype(cleaning)::value) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {       // 16 codes' even and odd columns, of two pieces
-              const int pc = 2 * i + (e >> 1);
-              const uint32_t sel = (e & 1) ? 0x4341u : 0x4240u;
-              uint32_t b0 = as_u32(__hmul2(q8_pair(r[(e >> 1) * 2] ^ 0x80808080u, sel), d0[pc / 2]));
-              uint32_t b1 = as_u32(__hmul2(q8_pair(r[(e >> 1) * 2 + 1] ^ 0x80808080u, sel), d1[pc / 2]));
-              if (!whole) b0 = pr_finite(b0, &found), b1 = pr_finite(b1, &found);
+                  for (int e = 0; e < 4; ++e) r[e] = pr_finite(r[e], &found);
+                }
 #pragma unroll
-              for (int mt = 0; mt < MT; ++mt) pr_mma(o[mt][2 * pc + (e & 1)], pw[mt], b0, b1);
+                for (int mt = 0; mt < MT; ++mt) {
+                  pr_mma(o[mt][2 * i], pw[mt][sub], r[0], r[1]);
+                  pr_mma(o[mt][2 * i + 1], pw[mt][sub], r[2], r[3]);
+                }
+              } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {       // 16 codes' even and odd columns, of two pieces
+                  const int pc = 2 * i + (e >> 1);
+                  const uint32_t sel = (e & 1) ? 0x4341u : 0x4240u;
+                  uint32_t b0 = as_u32(__hmul2(q8_pair(r[(e >> 1) * 2] ^ 0x80808080u, sel), d0[pc / 2]));
+                  uint32_t b1 = as_u32(__hmul2(q8_pair(r[(e >> 1) * 2 + 1] ^ 0x80808080u, sel), d1[pc / 2]));
+                  if (decltype(cleaning)::value) b0 = pr_finite(b0, &found), b1 = pr_finite(b1, &found);
+#pragma unroll
+                  for (int mt = 0; mt < MT; ++mt) pr_mma(o[mt][2 * pc + (e & 1)], pw[mt][sub], b0, b1);
+                }
+              }
             }
           }
-        }
+        
+        };
+        if (whole)
+          values(std::false_type{});
+        else
+          values(std::true_type{});
       }
       __syncwarp();            // the stage may be written again
     }
@@ -506,9 +571,12 @@ __global__ void __launch_bounds__(Pr<HD, MT, QF32, Q8, CL>::NT, 1)
           // values that were taken out of groups seen in part: back into the rows that see them
           const int pr = first + a.token_of(r);
           for (int i = w.i0; i < w.i1; ++i)
-            for (int b = 0; b < 2; ++b) {
-              const int base = w.it.tile(i) * 32 + b * 16;
-              if (base + 15 <= w.it.p0 && (!a.window || base > w.it.p1 - a.window || base + 16 <= a.sinks)) continue;
+            for (int b = 0; b < 32; b += 16) {
+              const int base = w.it.tile(i) * 32 + b, from_g = base & ~(GP - 1);
+              // (the values that were looked at are those of groups not seen whole; a hole makes a group one)
+              if (from_g + GP - 1 <= w.it.p0 && (!a.window || from_g > w.it.p1 - a.window || from_g + GP <= a.sinks) &&
+                  paged_row(a.kv, a.b, w.seq, from_g, w.head) >= 0 && paged_row(a.kv, a.b, w.seq, from_g + GP - 16, w.head) >= 0)
+                continue;
               for (int q = base; q < base + 16 && q <= pr; ++q) {
                 if (a.window && q <= pr - a.window && q >= a.sinks) continue;
                 const int vrow = paged_row(a.kv, a.b, w.seq, q, w.head);

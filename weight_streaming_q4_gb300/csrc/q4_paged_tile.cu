@@ -37,6 +37,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "q4_paged_sched.cuh"
 
 namespace q4 {
@@ -698,47 +700,53 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
             // groups of 32 pieces go round the warps from tile to tile
             constexpr int PARTS = PIECES / 32, BATCH = 3;
             const int j0 = (warp - 8 + G::CONV - static_cast<int>(n * PARTS % G::CONV)) % G::CONV;
+            auto convert = [&](auto cleaning) {          // (code of its own for the few tiles to be cleaned)
 #pragma unroll 1
-            for (int jb = j0; jb < PARTS; jb += BATCH * G::CONV) {
-              uint4 codes[BATCH];
-              __half sc[BATCH];
+              for (int jb = j0; jb < PARTS; jb += BATCH * G::CONV) {
+                uint4 codes[BATCH];
+                __half sc[BATCH];
 #pragma unroll
-              for (int y = 0; y < BATCH; ++y) {
-                const int x = min(jb + y * G::CONV, PARTS - 1) * 32 + lane;
-                codes[y] = *reinterpret_cast<const uint4*>(from + x * 16);
-                sc[y] = *reinterpret_cast<const __half*>(from + BN * HD + (x >> 1) * 2);
-              }
-#pragma unroll
-              for (int y = 0; y < BATCH; ++y) {
-                if (jb + y * G::CONV >= PARTS) break;
-                const int x = (jb + y * G::CONV) * 32 + lane, row = x / (HD / 16), pc = x % (HD / 16);
-                uint4 u[2];
-                __half2* h = reinterpret_cast<__half2*>(u);
-                const __half2 d = __half2half2(sc[y]);
-                // the two halves of a piece in an order that keeps 8 lanes' stores in different banks
-                const bool odd = (pc >> 2) & 1;
-                q8_values4(odd ? codes[y].z : codes[y].x, d, h[0], h[1]);
-                q8_values4(odd ? codes[y].w : codes[y].y, d, h[2], h[3]);
-                q8_values4(odd ? codes[y].x : codes[y].z, d, h[4], h[5]);
-                q8_values4(odd ? codes[y].y : codes[y].w, d, h[6], h[7]);
-                if (clean) {
-                  if (((there >> (row >> 4)) & 1) && row <= last && (row >= first || row < sk)) {
-                    uint32_t* b = reinterpret_cast<uint32_t*>(u);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                      if ((b[e] & 0x7c00u) == 0x7c00u) b[e] &= 0xffff0000u, found = true;
-                      if ((b[e] & 0x7c000000u) == 0x7c000000u) b[e] &= 0x0000ffffu, found = true;
-                    }
-                  } else {
-                    u[0] = u[1] = make_uint4(0, 0, 0, 0);
-                  }
+                for (int y = 0; y < BATCH; ++y) {
+                  const int x = min(jb + y * G::CONV, PARTS - 1) * 32 + lane;
+                  codes[y] = *reinterpret_cast<const uint4*>(from + x * 16);
+                  sc[y] = *reinterpret_cast<const __half*>(from + BN * HD + (x >> 1) * 2);
                 }
-                char* to = dst + (pc >> 2) * (BN * 128) + row * 128;
-                const int p0 = (pc & 3) * 2 + odd;
-                *reinterpret_cast<uint4*>(to + ((p0 ^ (row & 7)) << 4)) = u[0];
-                *reinterpret_cast<uint4*>(to + (((p0 ^ 1) ^ (row & 7)) << 4)) = u[1];
+#pragma unroll
+                for (int y = 0; y < BATCH; ++y) {
+                  if (jb + y * G::CONV >= PARTS) break;
+                  const int x = (jb + y * G::CONV) * 32 + lane, row = x / (HD / 16), pc = x % (HD / 16);
+                  uint4 u[2];
+                  __half2* h = reinterpret_cast<__half2*>(u);
+                  const __half2 d = __half2half2(sc[y]);
+                  // the two halves of a piece in an order that keeps 8 lanes' stores in different banks
+                  const bool odd = (pc >> 2) & 1;
+                  q8_values4(odd ? codes[y].z : codes[y].x, d, h[0], h[1]);
+                  q8_values4(odd ? codes[y].w : codes[y].y, d, h[2], h[3]);
+                  q8_values4(odd ? codes[y].x : codes[y].z, d, h[4], h[5]);
+                  q8_values4(odd ? codes[y].y : codes[y].w, d, h[6], h[7]);
+                  if (decltype(cleaning)::value) {
+                    if (((there >> (row >> 4)) & 1) && row <= last && (row >= first || row < sk)) {
+                      uint32_t* b = reinterpret_cast<uint32_t*>(u);
+#pragma unroll
+                      for (int e = 0; e < 8; ++e) {
+                        if ((b[e] & 0x7c00u) == 0x7c00u) b[e] &= 0xffff0000u, found = true;
+                        if ((b[e] & 0x7c000000u) == 0x7c000000u) b[e] &= 0x0000ffffu, found = true;
+                      }
+                    } else {
+                      u[0] = u[1] = make_uint4(0, 0, 0, 0);
+                    }
+                  }
+                  char* to = dst + (pc >> 2) * (BN * 128) + row * 128;
+                  const int p0 = (pc & 3) * 2 + odd;
+                  *reinterpret_cast<uint4*>(to + ((p0 ^ (row & 7)) << 4)) = u[0];
+                  *reinterpret_cast<uint4*>(to + (((p0 ^ 1) ^ (row & 7)) << 4)) = u[1];
+                }
               }
-            }
+            };
+            if (clean)
+              convert(std::true_type{});
+            else
+              convert(std::false_type{});
             if (found) *reinterpret_cast<volatile int*>(&c->bad[seg & 7]) = seg + 1;
             fence_async();
             __syncwarp();
