@@ -198,13 +198,38 @@ def _ptr(t):
     return t.data_ptr()
 
 
+# The current CUDA device and its current stream's handle.  torch.cuda.current_stream()
+# builds an object per call (2.9 us on a Grace core, a launch takes 2); after a
+# first call of it, which initialises CUDA, the handle is asked for directly
+# where this torch has the functions.
+_device = None
+_raw_stream = None
+
+
+def _init_current():
+    global _device, _raw_stream
+    import torch
+    torch.cuda.current_stream()
+    get, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    _device = dev or torch.cuda.current_device
+    _raw_stream = (lambda: get(dev())) if get and dev else (lambda: torch.cuda.current_stream().cuda_stream)
+
+
+def _on_device(t) -> bool:
+    """Whether a tensor is on the current CUDA device (a host tensor's device is -1)."""
+    if not t.is_cuda:
+        return False
+    if _device is None:
+        _init_current()
+    return t.get_device() == _device()
+
+
 def _dev_ptr(t, itemsize=None):
     """_ptr of a tensor that the kernels can reach: contiguous, on the current
     CUDA device, of the given element size (an integer is taken as an address)."""
     if t is None or isinstance(t, int):
         return t
-    import torch
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if not _on_device(t):
         raise Q4Error(Q4_ERR_ARG, f"a tensor on {t.device}, not the current CUDA device")
     if not t.is_contiguous() or (itemsize and t.element_size() != itemsize):
         raise Q4Error(Q4_ERR_ARG, f"a {t.dtype} tensor of strides {tuple(t.stride())}")
@@ -217,9 +242,8 @@ def _rows_ptr(t, what, rows, row, ld, kind):
     that starts inside a wider row does: its storage counts)."""
     if t is None or isinstance(t, int):
         return t
-    import torch
     size = 4 if kind == Q4_TYPE_F32 else 2
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if not _on_device(t):
         raise Q4Error(Q4_ERR_ARG, f"{what}: a tensor on {t.device}, not the current CUDA device")
     if t.element_size() != size:
         raise Q4Error(Q4_ERR_ARG, f"{what}: a {t.dtype} tensor for {size}-byte values")
@@ -230,8 +254,9 @@ def _rows_ptr(t, what, rows, row, ld, kind):
 
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None:
+            _init_current()
+        return _raw_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream
