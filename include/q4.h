@@ -513,7 +513,7 @@ typedef struct q4_paged_kv {
  *   kv_lens        device int [n_seqs], taken within 0..table_width * page_size
  *   page_table     device int [n_seqs][table_width]
  *   n_tokens       rows of the caller's buffers; rows that belong to no
- *                  sequence are neither read nor written
+ *                  sequence are not written, and their content does not matter
  *   max_new        the most new tokens of one sequence, as far as the caller
  *                  knows: it chooses the kernel, results do not depend on it
  *                  beyond the error bound

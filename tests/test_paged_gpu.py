@@ -308,6 +308,31 @@ def test_write_and_read(n_kv, hd, page, f32, q8):
         assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(got[~np.isnan(got)], want[~np.isnan(want)])
 
 
+def test_codes_next_to_ties():
+    """Values on and beside n + 1/2 steps of every kind of scale, subnormal ones too: the codes are those of exact arithmetic."""
+    rng = np.random.default_rng(40)
+    n = 4096
+    c = ref.Cache([n], [n], 1, 64, 256, True, seed=41)
+    d = np.abs(rng.normal(size=(n, 2)) * np.exp2(rng.integers(-26, 8, size=(n, 2)))).astype(np.float16)
+    d[:64] = np.arange(1, 129, dtype=np.float64).reshape(64, 2) * 2.0 ** -24       # subnormal scales
+    d = np.maximum(d, np.float16(2.0 ** -24)).astype(np.float32)
+    q = rng.integers(0, 127, size=(n, 2, 32)).astype(np.float32) + np.float32(0.5)
+    x = (d[..., None] * q).astype(np.float32)                                      # exact: 11 + 8 bits
+    side = rng.integers(-1, 2, size=x.shape)
+    x = np.where(side > 0, np.nextafter(x, np.float32(np.inf)), np.where(side < 0, np.nextafter(x, np.float32(0)), x))
+    x *= rng.choice([-1, 1], size=x.shape).astype(np.float32)
+    x[:, :, 0] = 127 * d                                                           # the maximum that gives this scale
+    x = np.clip(x, -127 * d[..., None], 127 * d[..., None]).reshape(n, 64).astype(np.float32)
+    dv = Dev(c)
+    xd = dev(x)
+    q4.q4_paged_write(dv.kv, dv.batch, xd, xd, q4.Q4_TYPE_F32, 64)
+    torch.cuda.synchronize()
+    codes, scales = ref.quantise(x)
+    at = (c.table[0, np.arange(n) // 256], 0, np.arange(n) % 256)
+    assert np.array_equal(dv.scales["k"].cpu().numpy()[at], scales)
+    assert np.array_equal(dv.pages["k"].cpu().numpy()[at], codes)
+
+
 def test_write_and_read_skip_holes_and_negative_positions():
     c = ref.Cache([4, 2], [2, 40], 2, 64, 16, seed=25, n_tokens=7)
     c.table[1, 2] = c.n_pages

@@ -6,20 +6,25 @@
 // Method, "Offloading architecture").
 //
 // Both are one pass over the rows: 8 values per thread and step (16 or 32
-// bytes of the row, 16 or 8 of the page), a warp per 32 such chunks of a
+// bytes of the row, 16 or 8 of the page), a warp per 32 or 128 such chunks of a
 // token's key and value.  A Q8 block of 32 values is four neighbouring lanes:
 // its maximum is two shuffles.  They are bound by HBM bandwidth for many
 // tokens and by the launch and three dependent loads (starts, length, page)
 // for few.
 //
-// Exactness of the quantiser in 32 bits: amax / 127 and x / d are IEEE
-// divisions.  A quotient can only round across a tie of the next rounding (a
-// binary16 midpoint for d, n + 1/2 for a code) if the true quotient lies within
-// half an fp32 step of the tie without being it.  tie * divisor has at most
-// 12 + 7 and 8 + 11 significant bits, so it is an fp32 number, and the dividend
-// differs from it by a whole fp32 step or not at all: relative to the tie at
-// least 2^-23 / m with the dividend's mantissa m < 2, more than the quotient's
-// half step.  So d and the codes are those of exact arithmetic.
+// The quantiser is exact: d and the codes are those of exact arithmetic.
+// d: amax / 127 is an IEEE division, and a quotient can only round across a tie
+// of the next rounding (a binary16 midpoint) if the true quotient lies within half an
+// fp32 step of the tie without being it.  tie * 127 has at most 12 + 7 significant
+// bits, so it is an fp32 number, and amax differs from it by a whole fp32 step or
+// not at all: relative to the tie at least 2^-23 / m with amax's mantissa m < 2,
+// more than the quotient's half step.
+// Codes: x * (1 / d) is within 2^-23 of the quotient relative to it, at most 127.5
+// (a block with a subnormal d: clamped), so its nearest integer n is the
+// quotient's or, next to a tie, one beside it.  r = x - n d is exact (n d has 18 bits, and r is
+// a multiple of x's last bit no larger than d), so comparing |r| with d / 2 tells,
+// ties going to the even n.  An IEEE division per value took a third of the kernel's
+// instructions.
 #include <cuda_fp16.h>
 #include <stdint.h>
 
@@ -49,126 +54,222 @@ __device__ __forceinline__ void load8(const void* row, int64_t at, float (&x)[8]
   }
 }
 
-// A warp per 32 chunks of one token: chunk c of the token's 2 * n_kv * hd / 8
-// is 8 values of its key (first half) or its value.
-template <bool F32, bool Q8>
+// rint(x / d) within -127..127 of 8 values, as bytes; 0 where d is 0 or NaN.
+__device__ __forceinline__ uint2 q8_codes(const float (&x)[8], float d) {
+  if (!(d > 0.f)) return make_uint2(0, 0);
+  constexpr float kMagic = 12582912.f;       // 1.5 * 2^23: a number added to it is rounded to an integer, in its low bits
+  const float inv = __fdiv_rn(1.f, d), half = 0.5f * d;
+  const bool small = d < 6.103515625e-05f;   // subnormal binary16: the codes may pass 127
+  uint32_t n[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float t = __fmaf_rn(x[j], inv, kMagic);
+    const float r = __fmaf_rn(kMagic - t, d, x[j]);
+    int q = __float_as_int(t);
+    if (fabsf(r) > half || (fabsf(r) == half && (q & 1))) q += r > 0.f ? 1 : -1;
+    if (small) q = min(max(q, 0x4b400000 - 127), 0x4b400000 + 127);
+    n[j] = static_cast<uint32_t>(q);
+  }
+  return make_uint2(__byte_perm(__byte_perm(n[0], n[1], 0x0040), __byte_perm(n[2], n[3], 0x0040), 0x5410),
+                    __byte_perm(__byte_perm(n[4], n[5], 0x0040), __byte_perm(n[6], n[7], 0x0040), 0x5410));
+}
+
+// Where a warp's part of a token lives.  Chunk c of a token's 2 * n_kv * HD / 8
+// is 8 values of its key (first half) or its value; a warp takes U * 32 chunks
+// in a row, and looks up the token's page once.
+template <int HD>
+struct TokenAt {
+  int page, slot;           // page: -1 when the token is in none
+  bool mine;                // the row belongs to a sequence
+  __device__ __forceinline__ TokenAt(const PagedKv& kv, const PagedBatch& b, int row) {
+    page = -1, slot = 0;
+    const int s = paged_seq_of(b, row);
+    mine = s >= 0;
+    if (!mine) return;
+    const SeqSpan sp = paged_span(kv, b, s);
+    const int p = sp.len - sp.n_new + row - sp.t0, e = p >> kv.page_log2;
+    if (p < 0 || e >= b.width) return;
+    page = __ldg(b.table + static_cast<size_t>(s) * b.width + e);
+    if (static_cast<unsigned>(page) >= static_cast<unsigned>(kv.n_pages)) page = -1;
+    slot = p & ((1 << kv.page_log2) - 1);
+  }
+  // first of the chunk's values in the page memory; at: its first value within the key or value row
+  __device__ __forceinline__ size_t value(const PagedKv& kv, int at) const {
+    const int head = at / HD;
+    return ((static_cast<size_t>(page) * kv.n_kv + head) << kv.page_log2) * HD + static_cast<size_t>(slot) * HD + (at - head * HD);
+  }
+};
+
+template <int HD, bool F32, bool Q8, int U>
 __global__ void __launch_bounds__(kPcThreads) paged_write_kernel(PagedKv kv, PagedBatch b, const void* k, const void* v,
                                                                 int64_t ld, int groups) {
   const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kPcThreads + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
-  const int row = static_cast<int>(warp / groups), c = static_cast<int>(warp % groups) * 32 + lane;
+  const int row = static_cast<int>(warp / groups), c0 = static_cast<int>(warp % groups) * 32 * U + lane;
   if (row >= b.n_tokens) return;
-  const int s = paged_seq_of(b, row);
-  if (s < 0) return;
-  const SeqSpan sp = paged_span(kv, b, s);
-  const int p = sp.len - sp.n_new + row - sp.t0;
-  const int half = kv.n_kv * kv.hd / 8;
-  const bool live = c < 2 * half && p >= 0;
-  const int at = c < half ? c : c - half, e = at * 8;
-  const int head = e / kv.hd, i = e - head * kv.hd;
-  const int dst = live ? paged_row(kv, b, s, p, head) : -1;
-  float x[8] = {};
-  if (dst >= 0) load8<F32>(c < half ? k : v, row * ld + e, x);
-  if (!Q8) {
-    if (dst < 0) return;
-    uint4 o;
-    __half2* h = reinterpret_cast<__half2*>(&o);
+  const int half = kv.n_kv * HD / 8;
+  // the rows do not wait for the page (a row that is in none is read for nothing)
+  float x[U][8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) h[j] = __floats2half2_rn(x[2 * j], x[2 * j + 1]);
-    *reinterpret_cast<uint4*>(static_cast<__half*>(c < half ? kv.k : kv.v) + static_cast<size_t>(dst) * kv.hd + i) = o;
-    return;
+  for (int u = 0; u < U; ++u) {
+    const int c = c0 + u * 32;
+    if (c < 2 * half) load8<F32>(c < half ? k : v, row * ld + (c < half ? c : c - half) * 8, x[u]);
   }
-  // the block's maximum and whether it holds a NaN (fmaxf drops NaN): the four
-  // lanes of a block share its fate (a head is a whole number of blocks)
-  float m = 0.f;
-  bool nan = false;
+  const TokenAt<HD> t(kv, b, row);
+  if (t.page < 0) return;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(x[j])), nan |= x[j] != x[j];
-  m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
-  m = fmaxf(m, __shfl_xor_sync(~0u, m, 2));
-  const unsigned nans = __ballot_sync(~0u, nan);
-  nan = (nans >> (lane & 28)) & 15;
-  if (dst < 0) return;
-  __half d = __float2half_rn(__fdiv_rn(m, 127.f));
-  if (nan || !(__half2float(d) <= 65504.f)) d = __ushort_as_half(0x7fff);
-  const float df = __half2float(d);
-  uint2 o;
-  int8_t* q = reinterpret_cast<int8_t*>(&o);
+  for (int u = 0; u < U; ++u) {
+    const int c = c0 + u * 32;
+    const bool live = c < 2 * half;
+    const size_t to = live ? t.value(kv, (c < half ? c : c - half) * 8) : 0;
+    if (!Q8) {
+      uint4 o;
+      __half2* h = reinterpret_cast<__half2*>(&o);
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    q[j] = df > 0.f ? static_cast<int8_t>(fminf(fmaxf(rintf(__fdiv_rn(x[j], df)), -127.f), 127.f)) : int8_t(0);
-  const size_t to = static_cast<size_t>(dst) * kv.hd + i;
-  *reinterpret_cast<uint2*>(static_cast<int8_t*>(c < half ? kv.k : kv.v) + to) = o;
-  if ((lane & 3) == 0) (c < half ? kv.ks : kv.vs)[to / 32] = d;
+      for (int j = 0; j < 4; ++j) h[j] = __floats2half2_rn(x[u][2 * j], x[u][2 * j + 1]);
+      if (live) *reinterpret_cast<uint4*>(static_cast<__half*>(c < half ? kv.k : kv.v) + to) = o;
+      continue;
+    }
+    // the block's maximum and whether it holds a NaN (fmaxf drops NaN): the four
+    // lanes of a block share its fate (a head is a whole number of blocks)
+    float m = 0.f;
+    bool nan = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (!live) x[u][j] = 0.f;
+      m = fmaxf(m, fabsf(x[u][j])), nan |= x[u][j] != x[u][j];
+    }
+    m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(~0u, m, 2));
+    const unsigned nans = __ballot_sync(~0u, nan);
+    nan = (nans >> (lane & 28)) & 15;
+    __half d = __float2half_rn(__fdiv_rn(m, 127.f));
+    if (nan || !(__half2float(d) <= 65504.f)) d = __ushort_as_half(0x7fff);
+    const uint2 o = q8_codes(x[u], __half2float(d));
+    if (!live) continue;
+    *reinterpret_cast<uint2*>(static_cast<int8_t*>(c < half ? kv.k : kv.v) + to) = o;
+    if ((lane & 3) == 0) (c < half ? kv.ks : kv.vs)[to / 32] = d;
+  }
 }
 
-template <bool F32, bool Q8>
+template <int HD, bool F32, bool Q8, int U>
 __global__ void __launch_bounds__(kPcThreads) paged_read_kernel(PagedKv kv, PagedBatch b, void* k, void* v, int64_t ld,
                                                                int groups) {
   const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kPcThreads + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
-  const int row = static_cast<int>(warp / groups), c = static_cast<int>(warp % groups) * 32 + lane;
+  const int row = static_cast<int>(warp / groups), c0 = static_cast<int>(warp % groups) * 32 * U + lane;
   if (row >= b.n_tokens) return;
-  const int s = paged_seq_of(b, row);
-  if (s < 0) return;
-  const SeqSpan sp = paged_span(kv, b, s);
-  const int p = sp.len - sp.n_new + row - sp.t0;
-  const int half = kv.n_kv * kv.hd / 8;
-  if (c >= 2 * half) return;
-  const int at = c < half ? c : c - half, e = at * 8;
-  const int head = e / kv.hd, i = e - head * kv.hd;
-  const int src = p >= 0 ? paged_row(kv, b, s, p, head) : -1;
-  uint4 u = make_uint4(0, 0, 0, 0);
-  __half2* h = reinterpret_cast<__half2*>(&u);
-  if (src >= 0) {
-    const size_t from = static_cast<size_t>(src) * kv.hd + i;
+  const TokenAt<HD> t(kv, b, row);
+  if (!t.mine) return;
+  const int half = kv.n_kv * HD / 8;
+  uint4 f[U];               // binary16 values, or Q8 codes in the first half
+  __half d[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int c = c0 + u * 32;
+    f[u] = make_uint4(0, 0, 0, 0);
+    d[u] = __ushort_as_half(0);
+    if (c >= 2 * half || t.page < 0) continue;
+    const size_t from = t.value(kv, (c < half ? c : c - half) * 8);
     if (Q8) {
       const uint2 q = __ldg(reinterpret_cast<const uint2*>(static_cast<const int8_t*>(c < half ? kv.k : kv.v) + from));
-      const __half2 d = __half2half2((c < half ? kv.ks : kv.vs)[from / 32]);
-      q8_values4(q.x, d, h[0], h[1]);
-      q8_values4(q.y, d, h[2], h[3]);
+      f[u].x = q.x, f[u].y = q.y;
+      d[u] = (c < half ? kv.ks : kv.vs)[from / 32];
     } else {
-      u = __ldg(reinterpret_cast<const uint4*>(static_cast<const __half*>(c < half ? kv.k : kv.v) + from));
+      f[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __half*>(c < half ? kv.k : kv.v) + from));
     }
   }
-  void* out = c < half ? k : v;
-  if (F32) {
-    float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + row * ld + e);
-    const float2 f0 = __half22float2(h[0]), f1 = __half22float2(h[1]), f2 = __half22float2(h[2]), f3 = __half22float2(h[3]);
-    o[0] = make_float4(f0.x, f0.y, f1.x, f1.y);
-    o[1] = make_float4(f2.x, f2.y, f3.x, f3.y);
-  } else {
-    *reinterpret_cast<uint4*>(static_cast<__half*>(out) + row * ld + e) = u;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int c = c0 + u * 32;
+    if (c >= 2 * half) continue;
+    const int64_t to = row * ld + (c < half ? c : c - half) * 8;
+    uint4 y = f[u];
+    __half2* h = reinterpret_cast<__half2*>(&y);
+    if (Q8) {
+      const __half2 d2 = __half2half2(d[u]);
+      q8_values4(f[u].x, d2, h[0], h[1]);
+      q8_values4(f[u].y, d2, h[2], h[3]);
+    }
+    void* out = c < half ? k : v;
+    if (F32) {
+      float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + to);
+      const float2 f0 = __half22float2(h[0]), f1 = __half22float2(h[1]), f2 = __half22float2(h[2]), f3 = __half22float2(h[3]);
+      o[0] = make_float4(f0.x, f0.y, f1.x, f1.y);
+      o[1] = make_float4(f2.x, f2.y, f3.x, f3.y);
+    } else {
+      *reinterpret_cast<uint4*>(static_cast<__half*>(out) + to) = y;
+    }
   }
 }
 
-// Grid of a warp per 32 chunks of a row.  The blocks fit an int: 2^31 of them
-// would be 4 TB of rows.
-unsigned blocks_of(const PagedKv& kv, const PagedBatch& b, int* groups) {
-  *groups = (2 * kv.n_kv * kv.hd / 8 + 31) / 32;
+// U * 32 chunks of a row per warp.  Where the rows fill the GPU anyway, four
+// loads per lane under way and one look-up for them; few rows (a step's tokens)
+// are spread over as many warps as they have.
+constexpr int kPcMany = 4;
+bool many_rows(const PagedKv& kv, const PagedBatch& b) {
+  return static_cast<int64_t>(b.n_tokens) * kv.n_kv * kv.hd >= int64_t{1} << 20;
+}
+unsigned blocks_of(const PagedKv& kv, const PagedBatch& b, int u, int* groups) {
+  *groups = (2 * kv.n_kv * kv.hd / 8 + 32 * u - 1) / (32 * u);
+  // (the blocks fit an int: 2^31 of them would be 4 TB of rows)
   const int64_t warps = static_cast<int64_t>(b.n_tokens) * *groups;
   return static_cast<unsigned>((warps * 32 + kPcThreads - 1) / kPcThreads);
 }
+
+template <int HD, bool F32, bool Q8>
+void launch_write(const PagedKv& kv, const PagedBatch& b, const void* k, const void* v, int64_t ld, cudaStream_t s) {
+  int groups;
+  if (many_rows(kv, b)) {
+    const unsigned n = blocks_of(kv, b, kPcMany, &groups);
+    paged_write_kernel<HD, F32, Q8, kPcMany><<<n, kPcThreads, 0, s>>>(kv, b, k, v, ld, groups);
+  } else {
+    const unsigned n = blocks_of(kv, b, 1, &groups);
+    paged_write_kernel<HD, F32, Q8, 1><<<n, kPcThreads, 0, s>>>(kv, b, k, v, ld, groups);
+  }
+}
+
+template <int HD, bool F32, bool Q8>
+void launch_read(const PagedKv& kv, const PagedBatch& b, void* k, void* v, int64_t ld, cudaStream_t s) {
+  int groups;
+  if (many_rows(kv, b)) {
+    const unsigned n = blocks_of(kv, b, kPcMany, &groups);
+    paged_read_kernel<HD, F32, Q8, kPcMany><<<n, kPcThreads, 0, s>>>(kv, b, k, v, ld, groups);
+  } else {
+    const unsigned n = blocks_of(kv, b, 1, &groups);
+    paged_read_kernel<HD, F32, Q8, 1><<<n, kPcThreads, 0, s>>>(kv, b, k, v, ld, groups);
+  }
+}
+
+// f<HD, F32, Q8>(...) of the types at hand.
+#define Q4_BY_TYPE(f, hd, f32, q8, ...)                                                          \
+  do {                                                                                           \
+    switch (hd) {                                                                                \
+      case 64: f32 ? (q8 ? f<64, true, true>(__VA_ARGS__) : f<64, true, false>(__VA_ARGS__))     \
+                   : (q8 ? f<64, false, true>(__VA_ARGS__) : f<64, false, false>(__VA_ARGS__));  \
+        break;                                                                                   \
+      case 128: f32 ? (q8 ? f<128, true, true>(__VA_ARGS__) : f<128, true, false>(__VA_ARGS__))  \
+                    : (q8 ? f<128, false, true>(__VA_ARGS__) : f<128, false, false>(__VA_ARGS__)); \
+        break;                                                                                   \
+      case 192: f32 ? (q8 ? f<192, true, true>(__VA_ARGS__) : f<192, true, false>(__VA_ARGS__))  \
+                    : (q8 ? f<192, false, true>(__VA_ARGS__) : f<192, false, false>(__VA_ARGS__)); \
+        break;                                                                                   \
+      default: f32 ? (q8 ? f<256, true, true>(__VA_ARGS__) : f<256, true, false>(__VA_ARGS__))   \
+                   : (q8 ? f<256, false, true>(__VA_ARGS__) : f<256, false, false>(__VA_ARGS__)); \
+    }                                                                                            \
+  } while (0)
 
 }  // namespace
 
 cudaError_t paged_write_launch(const PagedKv& kv, const PagedBatch& b, const void* k, const void* v, bool f32,
                                int64_t ld, bool q8, cudaStream_t s) {
-  int groups;
-  const unsigned n = blocks_of(kv, b, &groups);
-  auto kern = f32 ? (q8 ? paged_write_kernel<true, true> : paged_write_kernel<true, false>)
-                  : (q8 ? paged_write_kernel<false, true> : paged_write_kernel<false, false>);
-  kern<<<n, kPcThreads, 0, s>>>(kv, b, k, v, ld, groups);
+  Q4_BY_TYPE(launch_write, kv.hd, f32, q8, kv, b, k, v, ld, s);
   return cudaGetLastError();
 }
 
 cudaError_t paged_read_launch(const PagedKv& kv, const PagedBatch& b, void* k, void* v, bool f32, int64_t ld, bool q8,
                               cudaStream_t s) {
-  int groups;
-  const unsigned n = blocks_of(kv, b, &groups);
-  auto kern = f32 ? (q8 ? paged_read_kernel<true, true> : paged_read_kernel<true, false>)
-                  : (q8 ? paged_read_kernel<false, true> : paged_read_kernel<false, false>);
-  kern<<<n, kPcThreads, 0, s>>>(kv, b, k, v, ld, groups);
+  Q4_BY_TYPE(launch_read, kv.hd, f32, q8, kv, b, k, v, ld, s);
   return cudaGetLastError();
 }
 
