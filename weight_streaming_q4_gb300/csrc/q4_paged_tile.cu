@@ -108,12 +108,6 @@ __device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t* x) {
       Q4_IN8(x, 0), Q4_IN8(x, 8), Q4_IN8(x, 16), Q4_IN8(x, 24)
       : "memory");
 }
-__device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t* x) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
-      Q4_IN8(x, 0), Q4_IN8(x, 8)
-      : "memory");
-}
 __device__ __forceinline__ void tm_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // True for one lane of the (converged) warp.
@@ -146,9 +140,11 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// Whether one of two binary16 values is infinite or NaN.
-__device__ __forceinline__ bool h2_bad(uint32_t u) {
-  return (u & 0x7c00u) == 0x7c00u || (u & 0x7c000000u) == 0x7c000000u;
+// Whether one of eight binary16 values is infinite or NaN: an exponent of all
+// ones carries into the sign's place.
+__device__ __forceinline__ bool h2_any_bad(const uint4& u) {
+  constexpr uint32_t M = 0x7c007c00u, A = 0x04000400u;
+  return ((((u.x & M) + A) | ((u.y & M) + A) | ((u.z & M) + A) | ((u.w & M) + A)) & 0x80008000u) != 0;
 }
 
 // ------------------------------------------------------------------ geometry
@@ -171,8 +167,7 @@ struct Pt {
   // tensor memory columns: S of query tile q at q * 128, then O; with one query tile S has two places
   // that take turns, so that the next scores are computed while the softmax works on these
   static constexpr int O_COL = 256;
-  static constexpr int H = BN / 2;                      // positions of a half: P is handed over in halves
-  static constexpr int CHUNKS = KB / 16;                // 16-byte pieces of a tile
+  static constexpr int H = 64, NH = BN / 64;            // P is handed over 64 positions at a time ("halves")
   // warpgroups: two of softmax, then binary16: copies (warp 8), cleaning (9, 10), products (11);
   // Q8: conversion (8 to 13), copies (14), products (15)
   static constexpr int GROUPS = Q8 ? 4 : 3, THREADS = 128 * GROUPS;
@@ -278,7 +273,7 @@ template <int HD, bool QF32, bool Q8>
 __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
     paged_tile_kernel(const __grid_constant__ PagedAttnArgs a, PartSlots parts, const __grid_constant__ PtMaps maps) {
   using G = Pt<HD, QF32, Q8>;
-  constexpr int BN = G::BN, NQ = G::NQ, R = G::R, NS = G::NS, H = G::H;
+  constexpr int BN = G::BN, NQ = G::NQ, R = G::R, NS = G::NS, H = G::H, NH = G::NH;
   extern __shared__ char smem_raw[];
   PtCtl* c = reinterpret_cast<PtCtl*>(smem_raw);
   // tiles start on 1024-byte boundaries (the swizzle's period)
@@ -398,7 +393,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
         const bool part = !tv.whole || there != (1u << (BN / 16)) - 1;
         const uint32_t t_x = t_s + turn * BN;
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < NH; ++h) {
           uint32_t x[H];
           float* f = reinterpret_cast<float*>(x);
           float2 sum;
@@ -449,7 +444,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
             const float m2 = fmaxf(m, top);
             const float fac = m == m2 ? 1.f : exp2f(m - m2);
             if (i > w.i0 || h > 0) {
-              pt_wait_warp(c, &c->o_full[q][h ^ 1], (h ? n_s : n_s - 1) & 1);
+              pt_wait_warp(c, &c->o_full[q][h ? 0 : NH - 1], (h ? n_s : n_s - 1) & 1);
               tm_after();
 #pragma unroll 1
               for (int b = 0; b < HD; b += 32) {
@@ -468,12 +463,9 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
           // With one query tile these scores came ahead of the last tile's product.  Before P goes out that
           // product is done (the next could not start earlier anyway): so a wait for a turn of o_full, here,
           // above or below, only ever finds that turn open or just over, never the one after it.
-          if (NQ == 1 && h == 0 && n_s > 0) pt_wait_warp(c, &c->o_full[q][1], (n_s - 1) & 1);
+          if (NQ == 1 && h == 0 && n_s > 0) pt_wait_warp(c, &c->o_full[q][NH - 1], (n_s - 1) & 1);
           // P over the scores' first columns (their half has been read)
-          if (H == 64)
-            tm_st32(t_x + h * (H / 2), x);
-          else
-            tm_st16(t_x + h * (H / 2), x);
+          tm_st32(t_x + h * (H / 2), x);
           tm_st_wait();
           tm_before();
           mbar_arrive(&c->p_full[NQ == 2 ? q : turn][h]);
@@ -490,7 +482,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
         continue;
       }
       // the item's (or the part's) end
-      pt_wait_warp(c, &c->o_full[q][1], (n_s - 1) & 1);
+      pt_wait_warp(c, &c->o_full[q][NH - 1], (n_s - 1) & 1);
       tm_after();
       if (next.live()) loaded_q(next);
       const bool whole_item = w.i0 == 0 && w.i1 == w.it.cnt;
@@ -616,16 +608,23 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
             if (lane == 0) mbar_arrive(&c->fixed[n % NS]);
             continue;
           }
+          // Positions that some row sees: up to `last`, from `first` on or below sk; that every row sees: up to
+          // all_last, from all_first on or below sk.  Only what lies between, or in a hole, is looked at.
           const int last = w.it.p1 - tv.base, first = a.window ? max(w.it.p0, 0) - a.window + 1 - tv.base : 0, sk = a.sinks - tv.base;
+          const int all_last = w.it.p0 - tv.base, all_first = a.window ? w.it.p1 - a.window + 1 - tv.base : 0;
           bool found = false;
-#pragma unroll 4
-          for (int x = tid - 9 * 32; x < G::CHUNKS; x += 64) {
-            const int row = x / (HD / 8), pc = x % (HD / 8);
+          constexpr int PIECES = HD / 8;
+          const int me = tid - 9 * 32;
+#pragma unroll 2
+          for (int x = me; x < BN * PIECES; x += 64) {
+            const int row = x / PIECES, pc = x % PIECES;
+            const bool in = (there >> (row >> 4)) & 1;
+            if (in && row <= all_last && (row >= all_first || row < sk)) continue;
             uint4* v = reinterpret_cast<uint4*>(tiles + G::QALL + (n % NS) * G::KB + (pc >> 3) * (BN * 128) + row * 128 +
                                                 (((pc & 7) ^ (row & 7)) << 4));
-            if (((there >> (row >> 4)) & 1) && row <= last && (row >= first || row < sk)) {
+            if (in && row <= last && (row >= first || row < sk)) {
               uint4 u = *v;
-              if (h2_bad(u.x) || h2_bad(u.y) || h2_bad(u.z) || h2_bad(u.w)) {
+              if (h2_any_bad(u)) {
                 __half* h = reinterpret_cast<__half*>(&u);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
@@ -828,7 +827,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
           }
           wait_v(at_v, n_v);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < NH; ++h) {
             pt_wait_warp(c, &c->p_full[now][h], par_p[now]);
             tm_after();
             values(0, tmem + now * BN, h, i > 0 || h > 0);
@@ -840,7 +839,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
           for (int q = 0; q < NQ; ++q) {
             if (q >= active) break;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < NH; ++h) {
               pt_wait_warp(c, &c->p_full[q][h], par_p[q]);
               tm_after();
               values(q, tmem + q * 128, h, i > 0 || h > 0);
