@@ -171,7 +171,8 @@ struct Pt {
   // warpgroups: two of softmax, then binary16: copies (warp 8), cleaning (9, 10), products (11);
   // Q8: conversion (8 to 13), copies (14), products (15)
   static constexpr int GROUPS = Q8 ? 4 : 3, THREADS = 128 * GROUPS;
-  static constexpr int W_COPY = Q8 ? 14 : 8, W_MMA = 4 * GROUPS - 1, CONV = 6;
+  static constexpr int W_SIDE = Q8 ? 8 : 9, CONV = Q8 ? 6 : 2;      // the cleaning or converting warps
+  static constexpr int W_COPY = Q8 ? 14 : 8, W_MMA = 4 * GROUPS - 1;
   // registers per thread after the split: softmax warpgroups, the others
   static constexpr int REG_S = Q8 ? 136 : 184;
   static constexpr int REG_O = Q8 ? 120 : (NQ == 2 ? 136 : 152);
@@ -283,7 +284,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) {
-    for (int i = 0; i < NS; ++i) mbar_init(&c->full[i], Q8 ? G::CONV : 1), mbar_init(&c->empty[i], 1), mbar_init(&c->fixed[i], 2);
+    for (int i = 0; i < NS; ++i) mbar_init(&c->full[i], Q8 ? G::CONV : 1), mbar_init(&c->empty[i], 1), mbar_init(&c->fixed[i], G::CONV);
     for (int q = 0; q < 2; ++q) {
       mbar_init(&c->q_full[q], 128);
       mbar_init(&c->s_full[q], 1);
@@ -497,6 +498,9 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
       char* const turn_mine = turn_at + lane * 64;
       float* const part0 = parts.out(blockIdx.x, slot) + static_cast<size_t>(q * 128 + wl * 32) * HD;
       const int n_mine = rows - q * 128 - wl * 32;                // rows of this warp
+      __half* to[4];                                              // of the rows this lane stores pieces of
+#pragma unroll
+      for (int k = 0; k < 4; ++k) to[k] = a.out + __shfl_sync(~0u, out_at, k * 8 + (lane >> 2)) + (lane & 3) * 8;
 #pragma unroll 1
       for (int b = 0; b < HD; b += 32) {
         uint32_t o[32];
@@ -523,9 +527,8 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int row = k * 8 + (lane >> 2), pc = lane & 3;
-            const int64_t at = __shfl_sync(~0u, out_at, row);
             const uint4 u = *reinterpret_cast<const uint4*>(turn_at + row * 64 + ((pc ^ ((row >> 1) & 3)) << 4));
-            if (row < n_mine) *reinterpret_cast<uint4*>(a.out + at + b + pc * 8) = u;
+            if (row < n_mine) *reinterpret_cast<uint4*>(to[k] + b) = u;
           }
         } else {
 #pragma unroll
@@ -596,7 +599,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
         if (w.live()) row = lookup(w, w.i0);
       }
     } else if (!Q8) {   // (warps 9 and 10)
-      // value tiles to be cleaned, by warps 9 and 10
+      // value tiles to be cleaned
       uint32_t n = 1;
       int seg = 0;
       for (; w.live(); w.next(a), ++seg) {
@@ -610,30 +613,60 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
           }
           // Positions that some row sees: up to `last`, from `first` on or below sk; that every row sees: up to
           // all_last, from all_first on or below sk.  Only what lies between, or in a hole, is looked at.
-          const int last = w.it.p1 - tv.base, first = a.window ? max(w.it.p0, 0) - a.window + 1 - tv.base : 0, sk = a.sinks - tv.base;
-          const int all_last = w.it.p0 - tv.base, all_first = a.window ? w.it.p1 - a.window + 1 - tv.base : 0;
+          const int last = min(w.it.p1 - tv.base, BN - 1), first = a.window ? max(w.it.p0, 0) - a.window + 1 - tv.base : 0;
+          const int all_last = w.it.p0 - tv.base, all_first = a.window ? w.it.p1 - a.window + 1 - tv.base : 0, sk = a.sinks - tv.base;
           bool found = false;
           constexpr int PIECES = HD / 8;
-          const int me = tid - 9 * 32;
-#pragma unroll 2
-          for (int x = me; x < BN * PIECES; x += 64) {
+          constexpr int N = G::CONV * 32;
+          const int me = tid - G::W_SIDE * 32;
+          char* const tile = tiles + G::QALL + (n % NS) * G::KB;
+          auto piece = [&](int x) {
             const int row = x / PIECES, pc = x % PIECES;
-            const bool in = (there >> (row >> 4)) & 1;
-            if (in && row <= all_last && (row >= all_first || row < sk)) continue;
-            uint4* v = reinterpret_cast<uint4*>(tiles + G::QALL + (n % NS) * G::KB + (pc >> 3) * (BN * 128) + row * 128 +
-                                                (((pc & 7) ^ (row & 7)) << 4));
-            if (in && row <= last && (row >= first || row < sk)) {
-              uint4 u = *v;
-              if (h2_any_bad(u)) {
-                __half* h = reinterpret_cast<__half*>(&u);
+            return reinterpret_cast<uint4*>(tile + (pc >> 3) * (BN * 128) + row * 128 + (((pc & 7) ^ (row & 7)) << 4));
+          };
+          auto clean = [&](uint4 u, uint4* v) {
+            if (!h2_any_bad(u)) return;
+            __half* h = reinterpret_cast<__half*>(&u);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  if (__hisinf(h[e]) || __hisnan(h[e])) h[e] = __ushort_as_half(0);
-                *v = u;
-                found = true;
-              }
-            } else {
-              *v = make_uint4(0, 0, 0, 0);
+            for (int e = 0; e < 8; ++e)
+              if (__hisinf(h[e]) || __hisnan(h[e])) h[e] = __ushort_as_half(0);
+            *v = u;
+            found = true;
+          };
+          auto clean_rows = [&](int from, int to) {        // four loads under way
+            const int end = to * PIECES;
+#pragma unroll 1
+            for (int x = from * PIECES + me; x < end; x += 4 * N) {
+              uint4 u[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) u[k] = *piece(min(x + N * k, end - 1));
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (x + N * k < end) clean(u[k], piece(x + N * k));
+            }
+          };
+          auto zero_rows = [&](int from, int to) {
+#pragma unroll 4
+            for (int x = from * PIECES + me; x < to * PIECES; x += N) *piece(x) = make_uint4(0, 0, 0, 0);
+          };
+          // rows [lo, hi) are those some row sees, of which [lo, lo2) and [hi2, hi) are seen in part
+          const int lo = max(first, 0), hi = last + 1, lo2 = min(max(all_first, lo), BN), hi2 = max(all_last + 1, 0);
+          const uint32_t wanted = hi > lo ? ((2u << ((hi - 1) >> 4)) - 1) & ~((1u << (lo >> 4)) - 1) : 0;
+          if (hi > lo && lo2 <= hi2 && (sk <= 0 || all_first <= 0) && (there & wanted) == wanted) {
+            clean_rows(lo, lo2);
+            clean_rows(hi2, hi);
+            zero_rows(0, lo);
+            zero_rows(hi, BN);
+          } else {
+#pragma unroll 1
+            for (int x = me; x < BN * PIECES; x += N) {
+              const int row = x / PIECES;
+              const bool in = (there >> (row >> 4)) & 1;
+              if (in && row <= all_last && (row >= all_first || row < sk)) continue;
+              if (in && row <= last && (row >= first || row < sk))
+                clean(*piece(x), piece(x));
+              else
+                *piece(x) = make_uint4(0, 0, 0, 0);
             }
           }
           if (found) *reinterpret_cast<volatile int*>(&c->bad[seg & 7]) = seg + 1;
@@ -642,7 +675,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
           if (lane == 0) mbar_arrive(&c->fixed[n % NS]);
         }
       }
-    } else if (warp == G::W_COPY) {
+    } else if (Q8 && warp == G::W_COPY) {
       // Q8: codes and scales into the staging ring
       constexpr int NRAW = G::NRAW > 0 ? G::NRAW : 1;
       char* const raw = tiles + G::QALL + NS * G::KB;
@@ -675,7 +708,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
         w.next(a);
         if (w.live()) row = lookup(w, w.i0);
       }
-    } else if (warp < 8 + G::CONV) {
+    } else if (Q8 && warp < 8 + G::CONV) {
       // Q8: staged codes to binary16
       constexpr int PIECES = BN * HD / 16;               // 16 codes each
       constexpr int NRAW = G::NRAW > 0 ? G::NRAW : 1;
