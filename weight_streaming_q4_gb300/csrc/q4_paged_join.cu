@@ -1,7 +1,7 @@
 // Joins the parts of items that several CTAs of a paged attention kernel share
 // (q4_paged_sched.cuh; sm_103a): out = sum_c O_c 2^(m_c - M) / sum_c l_c 2^(m_c - M)
 // over the CTAs c in order, M the largest m_c.  One block per CTA that begins
-// such an item and 32 of its rows, a warp per row at a time.  Launched as a
+// such an item and 8 of its rows, a warp per row.  Launched as a
 // programmatic dependent of that kernel: its blocks take their place while the
 // last CTAs finish and wait for them, so the second launch costs less than one
 // after the other.
@@ -16,18 +16,19 @@ namespace q4 {
 namespace {
 
 constexpr int kPjThreads = 256;
-constexpr int kPjRows = 32;
+constexpr int kPjRows = kPjThreads / 32;
 
 template <int HD>
 __global__ void __launch_bounds__(kPjThreads) paged_join_kernel(const __grid_constant__ PagedAttnArgs a, PartSlots parts) {
-  constexpr int E = HD / 32, B = 8;
+  constexpr int E = HD / 32, B = 4;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int cta = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const JoinRecord rec = *parts.record(cta);
   const int end = min(rec.rows, static_cast<int>(blockIdx.y + 1) * kPjRows);
   if (rec.n <= 0) return;
-  for (int r = blockIdx.y * kPjRows + warp; r < end; r += kPjThreads / 32) {
-    // Part 0 is slot 1 of this CTA, part c > 0 slot 0 of CTA cta + c.  Eight parts' loads at a time are
+  const int r = blockIdx.y * kPjRows + warp;
+  if (r < end) {
+    // Part 0 is slot 1 of this CTA, part c > 0 slot 0 of CTA cta + c.  Four parts' loads at a time are
     // under way together; the sums run in the order of the parts, rescaled when a later one raises the maximum.
     float top = -INFINITY, sum = 0.f, o[E] = {};
     for (int c0 = 0; c0 < rec.n; c0 += B) {
@@ -35,8 +36,10 @@ __global__ void __launch_bounds__(kPjThreads) paged_join_kernel(const __grid_con
       float2 v[B][E / 2];
 #pragma unroll
       for (int k = 0; k < B; ++k) {
-        const int c = min(c0 + k, rec.n - 1);
-        m[k] = c0 + k < rec.n ? parts.max(cta + c, c == 0)[r] : -INFINITY;
+        const int c = c0 + k;
+        m[k] = -INFINITY;
+        if (c >= rec.n) continue;
+        m[k] = parts.max(cta + c, c == 0)[r];
         l[k] = parts.sum(cta + c, c == 0)[r];
         const float* src = parts.out(cta + c, c == 0) + static_cast<size_t>(r) * HD + lane * 2;
 #pragma unroll
