@@ -21,7 +21,8 @@
 // swizzle) per 64 columns and page or 16 .. BN rows of it, issued by the lanes of
 // one warp side by side; a copy through the threads (16-byte cp.async) took 6700
 // cycles a tile where the products take 2050.  Q8: bulk copies of codes and
-// scales into a staging ring, from which six warps store f16(code * d).
+// scales into a staging place, from which six warps take them into registers
+// and store them as f16(code * d).
 // Positions that no row of the item sees must count as zeros in the product with
 // P = 0 (a stale or later value may be NaN, and 0 * NaN is NaN), and so must
 // values that are not finite in a tile that some rows see only in part: such
@@ -159,7 +160,7 @@ struct Pt {
   static constexpr int LIMIT = 232448 - 1024 - 1024;    // control data, and the alignment of the tiles
   static constexpr int QALL = QB * (QF32 ? 2 : NQ);
   static constexpr int RAW = Q8 ? BN * HD + BN * HD / 16 : 0;   // a staged Q8 tile: codes, then scales
-  static constexpr int NRAW = !Q8 ? 0 : (LIMIT - QALL - NQ * 8192 - 2 * RAW) / KB >= 2 ? 2 : 1;
+  static constexpr int NRAW = Q8 ? 1 : 0;
   static constexpr int OUT = NQ * 4 * 2048;             // per softmax warp: 32 rows of 64 bytes on their way out
   static constexpr int FIT = (LIMIT - QALL - OUT - NRAW * RAW) / KB;
   static constexpr int NS = FIT > 8 ? 8 : FIT;          // ring of key and value tiles
@@ -194,7 +195,7 @@ struct PtCtl {
                            // may be a tile ahead of the products), half h
   uint64_t o_full[2][2];   // the product with half h is done
   uint64_t fixed[8];       // the value tile in a ring slot has been looked at, and cleaned if need be
-  uint64_t raw[2], raw_free[2];   // a staged Q8 tile has landed; its place is free again
+  uint64_t raw, raw_free;  // a staged Q8 tile has landed; its place is free again
   uint32_t tmem;
   int dead;
   int bad[8];              // segment number (+ 1) in whose values the loaders met infinities or NaN, by number mod 8
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
       mbar_init(&c->s_full[q], 1);
       for (int h = 0; h < 2; ++h) mbar_init(&c->p_full[q][h], 128), mbar_init(&c->o_full[q][h], 1);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(&c->raw[i], 1), mbar_init(&c->raw_free[i], G::CONV);
+    mbar_init(&c->raw, 1), mbar_init(&c->raw_free, G::CONV);
     c->dead = 0;
     for (int i = 0; i < 8; ++i) c->bad[i] = 0;
     fence_mbar_init();
@@ -677,7 +678,6 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
       }
     } else if (Q8 && warp == G::W_COPY) {
       // Q8: codes and scales into the staging ring
-      constexpr int NRAW = G::NRAW > 0 ? G::NRAW : 1;
       char* const raw = tiles + G::QALL + NS * G::KB;
       uint32_t n = 0;
       int row = w.live() ? lookup(w, w.i0) : -1;
@@ -689,9 +689,9 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
           const uint32_t bytes = __popc(__ballot_sync(~0u, now >= 0)) * ((HD + HD / 16) << bl);
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv, ++n) {
-            char* const to = raw + n % NRAW * G::RAW;
-            uint64_t* bar = &c->raw[n % NRAW];
-            pt_wait_warp(c, &c->raw_free[n % NRAW], ((n / NRAW) & 1) ^ 1);
+            char* const to = raw;
+            uint64_t* bar = &c->raw;
+            pt_wait_warp(c, &c->raw_free, (n & 1) ^ 1);
             if (lane == 0) {
               if (kv == 0) *reinterpret_cast<volatile uint32_t*>(&c->there[(n / 2) & 7]) = there;
               mbar_arrive_expect_tx(bar, bytes);
@@ -711,7 +711,6 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
     } else if (Q8 && warp < 8 + G::CONV) {
       // Q8: staged codes to binary16
       constexpr int PIECES = BN * HD / 16;               // 16 codes each
-      constexpr int NRAW = G::NRAW > 0 ? G::NRAW : 1;
       const char* const raw = tiles + G::QALL + NS * G::KB;
       uint32_t n = 0;                                    // tiles stored (keys and values)
       int seg = 0;
@@ -722,57 +721,57 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
 #pragma unroll 1
           for (int kv = 0; kv < 2; ++kv, ++n) {
             const uint32_t slot = n % NS;
-            pt_wait_warp(c, &c->raw[n % NRAW], (n / NRAW) & 1);
-            pt_wait_warp(c, &c->empty[slot], ((n / NS) & 1) ^ 1);
+            pt_wait_warp(c, &c->raw, n & 1);
             const uint32_t there = *reinterpret_cast<volatile uint32_t*>(&c->there[(n / 2) & 7]);
             const bool clean = kv == 1 && !(tv.whole && there == ALL);
-            const char* from = raw + n % NRAW * G::RAW;
+            // Groups of 32 pieces go round the warps from tile to tile.  A warp's are taken into registers at once, so
+            // that the next tile is staged while they are converted (one staging place: two would cost a ring slot,
+            // without which the conversion of a tile waits for the products with the last).
+            constexpr int PARTS = PIECES / 32, MOST = (PARTS + G::CONV - 1) / G::CONV;
+            const int j0 = (warp - G::W_SIDE + G::CONV - static_cast<int>(n * PARTS % G::CONV)) % G::CONV;
+            uint4 codes[MOST];
+            __half sc[MOST];
+#pragma unroll
+            for (int y = 0; y < MOST; ++y) {
+              const int x = min(j0 + y * G::CONV, PARTS - 1) * 32 + lane;
+              codes[y] = *reinterpret_cast<const uint4*>(raw + x * 16);
+              sc[y] = *reinterpret_cast<const __half*>(raw + BN * HD + (x >> 1) * 2);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c->raw_free);
+            pt_wait_warp(c, &c->empty[slot], ((n / NS) & 1) ^ 1);
             char* const dst = tiles + G::QALL + slot * G::KB;
             bool found = false;
-            // groups of 32 pieces go round the warps from tile to tile
-            constexpr int PARTS = PIECES / 32, BATCH = 3;
-            const int j0 = (warp - 8 + G::CONV - static_cast<int>(n * PARTS % G::CONV)) % G::CONV;
             auto convert = [&](auto cleaning) {          // (code of its own for the few tiles to be cleaned)
-#pragma unroll 1
-              for (int jb = j0; jb < PARTS; jb += BATCH * G::CONV) {
-                uint4 codes[BATCH];
-                __half sc[BATCH];
 #pragma unroll
-                for (int y = 0; y < BATCH; ++y) {
-                  const int x = min(jb + y * G::CONV, PARTS - 1) * 32 + lane;
-                  codes[y] = *reinterpret_cast<const uint4*>(from + x * 16);
-                  sc[y] = *reinterpret_cast<const __half*>(from + BN * HD + (x >> 1) * 2);
-                }
+              for (int y = 0; y < MOST; ++y) {
+                if (j0 + y * G::CONV >= PARTS) break;
+                const int x = (j0 + y * G::CONV) * 32 + lane, row = x / (HD / 16), pc = x % (HD / 16);
+                uint4 u[2];
+                __half2* h = reinterpret_cast<__half2*>(u);
+                const __half2 d = __half2half2(sc[y]);
+                // the two halves of a piece in an order that keeps 8 lanes' stores in different banks
+                const bool odd = (pc >> 2) & 1;
+                q8_values4(odd ? codes[y].z : codes[y].x, d, h[0], h[1]);
+                q8_values4(odd ? codes[y].w : codes[y].y, d, h[2], h[3]);
+                q8_values4(odd ? codes[y].x : codes[y].z, d, h[4], h[5]);
+                q8_values4(odd ? codes[y].y : codes[y].w, d, h[6], h[7]);
+                if (decltype(cleaning)::value) {
+                  if (((there >> (row >> 4)) & 1) && row <= last && (row >= first || row < sk)) {
+                    uint32_t* b = reinterpret_cast<uint32_t*>(u);
 #pragma unroll
-                for (int y = 0; y < BATCH; ++y) {
-                  if (jb + y * G::CONV >= PARTS) break;
-                  const int x = (jb + y * G::CONV) * 32 + lane, row = x / (HD / 16), pc = x % (HD / 16);
-                  uint4 u[2];
-                  __half2* h = reinterpret_cast<__half2*>(u);
-                  const __half2 d = __half2half2(sc[y]);
-                  // the two halves of a piece in an order that keeps 8 lanes' stores in different banks
-                  const bool odd = (pc >> 2) & 1;
-                  q8_values4(odd ? codes[y].z : codes[y].x, d, h[0], h[1]);
-                  q8_values4(odd ? codes[y].w : codes[y].y, d, h[2], h[3]);
-                  q8_values4(odd ? codes[y].x : codes[y].z, d, h[4], h[5]);
-                  q8_values4(odd ? codes[y].y : codes[y].w, d, h[6], h[7]);
-                  if (decltype(cleaning)::value) {
-                    if (((there >> (row >> 4)) & 1) && row <= last && (row >= first || row < sk)) {
-                      uint32_t* b = reinterpret_cast<uint32_t*>(u);
-#pragma unroll
-                      for (int e = 0; e < 8; ++e) {
-                        if ((b[e] & 0x7c00u) == 0x7c00u) b[e] &= 0xffff0000u, found = true;
-                        if ((b[e] & 0x7c000000u) == 0x7c000000u) b[e] &= 0x0000ffffu, found = true;
-                      }
-                    } else {
-                      u[0] = u[1] = make_uint4(0, 0, 0, 0);
+                    for (int e = 0; e < 8; ++e) {
+                      if ((b[e] & 0x7c00u) == 0x7c00u) b[e] &= 0xffff0000u, found = true;
+                      if ((b[e] & 0x7c000000u) == 0x7c000000u) b[e] &= 0x0000ffffu, found = true;
                     }
+                  } else {
+                    u[0] = u[1] = make_uint4(0, 0, 0, 0);
                   }
-                  char* to = dst + (pc >> 2) * (BN * 128) + row * 128;
-                  const int p0 = (pc & 3) * 2 + odd;
-                  *reinterpret_cast<uint4*>(to + ((p0 ^ (row & 7)) << 4)) = u[0];
-                  *reinterpret_cast<uint4*>(to + (((p0 ^ 1) ^ (row & 7)) << 4)) = u[1];
                 }
+                char* to = dst + (pc >> 2) * (BN * 128) + row * 128;
+                const int p0 = (pc & 3) * 2 + odd;
+                *reinterpret_cast<uint4*>(to + ((p0 ^ (row & 7)) << 4)) = u[0];
+                *reinterpret_cast<uint4*>(to + (((p0 ^ 1) ^ (row & 7)) << 4)) = u[1];
               }
             };
             if (clean)
@@ -782,10 +781,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
             if (found) *reinterpret_cast<volatile int*>(&c->bad[seg & 7]) = seg + 1;
             fence_async();
             __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(&c->full[slot]);
-              mbar_arrive(&c->raw_free[n % NRAW]);
-            }
+            if (lane == 0) mbar_arrive(&c->full[slot]);
           }
         }
       }
