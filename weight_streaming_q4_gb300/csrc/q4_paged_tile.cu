@@ -175,8 +175,8 @@ struct Pt {
   static constexpr int W_SIDE = Q8 ? 8 : 9, CONV = Q8 ? 6 : 2;      // the cleaning or converting warps
   static constexpr int W_COPY = Q8 ? 14 : 8, W_MMA = 4 * GROUPS - 1;
   // registers per thread after the split: softmax warpgroups, the others
-  static constexpr int REG_S = Q8 ? 136 : 184;
-  static constexpr int REG_O = Q8 ? 120 : (NQ == 2 ? 136 : 152);
+  static constexpr int REG_S = Q8 ? 152 : 184;
+  static constexpr int REG_O = Q8 ? 104 : (NQ == 2 ? 136 : 152);
   static constexpr int REGS = (NQ * REG_S + (GROUPS - NQ) * REG_O) * 128;
   static_assert(NS >= (NQ == 2 ? 3 : 2), "a key and a value tile, and the next key tile beside two query tiles");
 };
