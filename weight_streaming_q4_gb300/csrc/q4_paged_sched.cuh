@@ -56,11 +56,15 @@ __device__ __forceinline__ ItemTiles item_tiles(const PagedAttnArgs& a, const Se
 // (one lane alone took 26 us over the 382 row tiles of two chunks).
 constexpr int kLaneTiles = 4;
 template <int R, int BN>
-__device__ __forceinline__ long long seq_units(const PagedAttnArgs& a, const SeqSpan& sp) {
+__device__ __forceinline__ long long seq_units(const PagedAttnArgs& a, const SeqSpan& sp, int* most = nullptr) {
   const int lane = threadIdx.x & 31;
   const int n = (sp.n_new * a.group + R - 1) / R;
   long long sum = 0;
-  for (int j = 0; j < min(n, kLaneTiles); ++j) sum += item_tiles<R, BN>(a, sp, j).cnt;
+  for (int j = 0; j < min(n, kLaneTiles); ++j) {
+    const int cnt = item_tiles<R, BN>(a, sp, j).cnt;
+    if (most) *most = max(*most, cnt);
+    sum += cnt;
+  }
   for (unsigned more = __ballot_sync(~0u, n > kLaneTiles); more; more &= more - 1) {
     const int who = __ffs(more) - 1;
     const SeqSpan s = {__shfl_sync(~0u, sp.t0, who), __shfl_sync(~0u, sp.n_new, who), __shfl_sync(~0u, sp.len, who)};
@@ -174,16 +178,36 @@ __device__ __forceinline__ CtaWork warp_work(const PagedAttnArgs& a) {
   const int lane = threadIdx.x & 31;
   SeqSpan sp = {};
   if (lane < a.b.n_seqs) sp = paged_span(a.kv, a.b, lane);
-  const long long mine = seq_units<R, BN>(a, sp);
+  int most = 0;                    // key tiles of the longest item, if every sequence has few
+  const long long mine = seq_units<R, BN>(a, sp, &most);
+  const int tiles = (sp.n_new * a.group + R - 1) / R;
   long long end = mine;
+  int tiles_end = tiles;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const long long o = __shfl_up_sync(~0u, end, d);
-    if (lane >= d) end += o;
+    const int t = __shfl_up_sync(~0u, tiles_end, d);
+    if (lane >= d) end += o, tiles_end += t;
   }
   const long long total = __shfl_sync(~0u, end, 31);
   CtaWork w = {};
   w.per = units_per_cta(total);
+  // With no more items than CTAs and none much longer than an even share, an item each: nothing to join, and
+  // one start and end per CTA instead of two.  16 sequences under a window, 33 tiles an item where an even share is
+  // 28: 13.7 us against 17.0; 10 sequences of 4000 positions, 125 tiles and 66: 38.7 against 34.0.
+  const int items = __shfl_sync(~0u, tiles_end, 31) * a.kv.n_kv;
+  most = __reduce_max_sync(~0u, tiles > kLaneTiles ? 0x3fffffff : most);
+  if (items <= static_cast<int>(gridDim.x) && items > 0 && most <= w.per + w.per / 2) {
+    const int item = blockIdx.x;
+    if (item < items) {
+      w.seq = __ffs(__ballot_sync(~0u, item < tiles_end * a.kv.n_kv)) - 1;
+      const int x = item - __shfl_sync(~0u, (tiles_end - tiles) * a.kv.n_kv, w.seq);
+      w.j = x / a.kv.n_kv, w.head = x - w.j * a.kv.n_kv;
+      const SeqSpan s = {__shfl_sync(~0u, sp.t0, w.seq), __shfl_sync(~0u, sp.n_new, w.seq), __shfl_sync(~0u, sp.len, w.seq)};
+      w.n = item_tiles<R, BN>(a, s, w.j).cnt;
+    }
+    return w;
+  }
   const long long u0 = w.per * blockIdx.x;
   w.n = u0 < total ? static_cast<int>(min(w.per, total - u0)) : 0;
   const unsigned here = __ballot_sync(~0u, mine > 0 && u0 >= end - mine && u0 < end);
