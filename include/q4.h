@@ -569,10 +569,11 @@ int q4_paged_read(const q4_paged_kv *kv, const q4_paged_batch *batch, void *k, v
  * first tokens that stay visible); never a position in a hole, so pages that
  * left the window may be given back.  A token that sees nothing gets zeros.
  * Values outside what a query sees (stale slots, NaN, infinities) do not
- * reach its output.  The new tokens' own keys and values must be in the pages
- * (q4_paged_write).
+ * reach its output; a query all of whose scores are -infinity gets zeros too.
+ * The new tokens' own keys and values must be in the pages (q4_paged_write).
  *   q      device, [n_tokens] rows of n_q_heads * head_dim values of q_type
- *          (Q4_TYPE_*), q_ld values from row to row, rows 16-byte aligned
+ *          (Q4_TYPE_*), q_ld values from row to row, rows 16-byte aligned;
+ *          fp32 queries within +-65504
  *   out    device, binary16 [n_tokens] rows of n_q_heads * head_dim, out_ld
  *          values from row to row, rows 16-byte aligned, written
  *   n_q_heads   a multiple of n_kv_heads, at most 64 query heads per value head
@@ -581,6 +582,8 @@ int q4_paged_read(const q4_paged_kv *kv, const q4_paged_batch *batch, void *k, v
  *   workspace   device, >= q4_attn_paged_workspace_bytes() bytes, 16-byte
  *               aligned; its content does not matter before or after.  Calls
  *               that may run at the same time need one each
+ * The first call on a device makes the kernels ready (before any stream
+ * capture).  Runs of the same arrays give the same bits.
  * Error bound, with S_t = sum |q k_t| / sqrt(head_dim) and w = softmax(s):
  * |out - exact| <= (2^-10 + 2^-19 max S_t) sum w|v| + (positions) 2^-25 max|v| + 2^-24.
  * Errors: Q4_ERR_ARG, Q4_ERR_ALIGN, Q4_ERR_OOM, Q4_ERR_CUDA.

@@ -244,6 +244,23 @@ def test_ragged_batches(max_new):
     check(Dev(c, max_new=max_new).attend(q, 8), c, q, 8)
 
 
+@pytest.mark.parametrize("new,n_kv", [([40], 2), ([3, 70], 1), ([0, 17, 1], 4)])
+def test_more_new_tokens_than_the_caller_knew_of(new, n_kv):
+    """max_new chooses the kernel alone: too small a value costs time only (few items: the cluster kernel)."""
+    c = ref.Cache(new, [n + 60 for n in new], n_kv, 128, 16, n_kv == 2, seed=42)
+    q = queries(c, 4 * n_kv, 43, True)
+    for max_new in (0, 1, 3):
+        check(Dev(c, max_new=max_new).attend(q, 4 * n_kv), c, q, 4 * n_kv)
+
+
+def test_windows_as_wide_as_an_int():
+    c = ref.Cache([40, 5], [20, 300], 2, 64, 16, seed=44)
+    q = queries(c, 4, 45, False)
+    for max_new in (1, 100):
+        for window, sinks in ((2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (5, 2 ** 31 - 1), (2 ** 30, 7)):
+            check(Dev(c, max_new=max_new).attend(q, 4, window, sinks), c, q, 4, window, sinks)
+
+
 def test_many_sequences():
     """More sequences than a block has threads, most of them empty or short."""
     rng = np.random.default_rng(20)

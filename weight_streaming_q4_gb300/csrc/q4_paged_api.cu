@@ -42,6 +42,9 @@ int check_batch(const q4_paged_kv* kv, const q4_paged_batch* b, q4::PagedKv* k, 
   return Q4_OK;
 }
 
+// Positions that the page table has entries for (at most 2^30).
+int positions_of(const q4::PagedAttnArgs& a) { return a.b.width << a.kv.page_log2; }
+
 // A buffer of rows of `row` values of a type, ld apart.
 int check_rows(const void* p, int type, int64_t ld, int64_t row) {
   if (!p || (type != Q4_TYPE_F32 && type != Q4_TYPE_F16) || ld < row || ld > (int64_t{1} << 31)) return Q4_ERR_ARG;
@@ -133,8 +136,10 @@ extern "C" int q4_attn_paged(const q4_paged_kv* kv, const q4_paged_batch* batch,
   a.out_ld = out_ld;
   a.group = n_q_heads / a.kv.n_kv;
   q4::paged_attn_divisor(&a);
-  a.window = window;
-  a.sinks = sinks;
+  // (a window over the whole table is none; the kernels' sums of positions and windows stay within an int)
+  const int capacity = positions_of(a);
+  a.window = window < capacity ? window : 0;
+  a.sinks = a.window ? (sinks < capacity ? sinks : capacity) : 0;
   a.scale = static_cast<float>(1.4426950408889634 / sqrt(static_cast<double>(a.kv.hd)));
   int grid = 0;
   if ((st = attn_grid(&grid)) != Q4_OK) return st;

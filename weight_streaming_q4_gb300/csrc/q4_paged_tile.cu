@@ -196,6 +196,7 @@ struct PtCtl {
   uint64_t o_full[2][2];   // the product with half h is done
   uint64_t fixed[8];       // the value tile in a ring slot has been looked at, and cleaned if need be
   uint64_t raw, raw_free;  // a staged Q8 tile has landed; its place is free again
+  uint64_t done;           // every product is done
   uint32_t tmem;
   int dead;
   int bad[8];              // segment number (+ 1) in whose values the loaders met infinities or NaN, by number mod 8
@@ -215,6 +216,13 @@ __device__ __forceinline__ void pt_wait(PtCtl* c, uint64_t* bar, uint32_t parity
     *reinterpret_cast<volatile int*>(&c->dead) = 1;
     atomicOr(&g_status_pt, ST_FULL_TIMEOUT);
   }
+}
+
+// Before the CTA ends: a copy or product of its own that is still in flight
+// (none is, unless a wait has run out), whatever ran out before.
+__device__ __forceinline__ void pt_drain(uint64_t* bar, uint32_t parity) {
+  if (!mbar_wait_bounded(bar, parity, kPtWaitLimit)) atomicOr(&g_status_pt, ST_DRAIN_TIMEOUT);
+  __syncwarp();
 }
 
 // As pt_wait for a whole warp, which is together again afterwards.
@@ -291,7 +299,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
       mbar_init(&c->s_full[q], 1);
       for (int h = 0; h < 2; ++h) mbar_init(&c->p_full[q][h], 128), mbar_init(&c->o_full[q][h], 1);
     }
-    mbar_init(&c->raw, 1), mbar_init(&c->raw_free, G::CONV);
+    mbar_init(&c->raw, 1), mbar_init(&c->raw_free, G::CONV), mbar_init(&c->done, 1);
     c->dead = 0;
     for (int i = 0; i < 8; ++i) c->bad[i] = 0;
     fence_mbar_init();
@@ -599,6 +607,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
         w.next(a);
         if (w.live()) row = lookup(w, w.i0);
       }
+      for (uint32_t t = n > NS ? n - NS : 0; t < n; ++t) pt_drain(&c->full[t % NS], (t / NS) & 1);
     } else if (!Q8) {   // (warps 9 and 10)
       // value tiles to be cleaned
       uint32_t n = 1;
@@ -708,6 +717,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
         w.next(a);
         if (w.live()) row = lookup(w, w.i0);
       }
+      if (n > 0) pt_drain(&c->raw, (n - 1) & 1);
     } else if (Q8 && warp < 8 + G::CONV) {
       // Q8: staged codes to binary16
       constexpr int PIECES = BN * HD / 16;               // 16 codes each
@@ -891,6 +901,9 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
 
       }
     }
+    if (one) tm_commit(&c->done);
+    __syncwarp();
+    pt_drain(&c->done, 0);
   }
   if (tid == 0) *parts.record(blockIdx.x) = rec;
   __syncwarp();
