@@ -94,6 +94,19 @@ def test_single_token_lengths(total, q8):
     check(Dev(c).attend(q, 8), c, q, 8)
 
 
+@pytest.mark.parametrize("seqs", [1, 3, 12], ids=["one", "few", "many"])
+@pytest.mark.parametrize("hd", [64, 128, 192, 256])
+@pytest.mark.parametrize("q8", [False, True], ids=["f16", "q8"])
+@pytest.mark.parametrize("f32", [False, True], ids=["qf16", "qf32"])
+def test_single_tokens_of_every_type(f32, q8, hd, seqs):
+    """One token of one, a few and many sequences: the cluster kernel, and the even split with and without an item per CTA."""
+    total = [1 + (997 * (i + 1)) % 1500 for i in range(seqs)]
+    c = ref.Cache([1] * seqs, total, 2, hd, 32, q8, seed=hd + seqs)
+    q = queries(c, 10, 46, f32)
+    check(Dev(c).attend(q, 10), c, q, 10)
+    check(Dev(c).attend(q, 10, 100, 3), c, q, 10, 100, 3)
+
+
 @pytest.mark.parametrize("new,total", [(1, 1), (2, 2), (31, 31), (32, 33), (33, 200), (64, 64), (65, 130), (127, 300), (128, 128), (129, 129), (200, 777), (257, 1025)])
 @pytest.mark.parametrize("q8", [False, True], ids=["f16", "q8"])
 def test_chunk_lengths(new, total, q8):

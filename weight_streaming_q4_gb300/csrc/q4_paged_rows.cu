@@ -665,10 +665,12 @@ cudaError_t prepare_mt() {
 template <int HD, int MT, bool QF32, bool Q8>
 cudaError_t launch_rows(const PagedAttnArgs& a, void* ws, int grid, cudaStream_t s) {
   if constexpr (MT == 1) {
-    // Few items: a cluster each.  One token over 4096 positions of 8 value heads CL us against UN us, 512 CL us
-    // against UN us; with more items than clusters the even split wins.
+    // Few items and a table of no great length: a cluster each.  One token of the 8B heads over 512, 2048, 4096 and
+    // 8192 positions 5.4, 7.2, 9.3 and 14.2 us, split evenly over all CTAs 9.1, 9.8, 13.2 and 18.2; over 32768 36.6
+    // against 32.6 (64 CTAs draw less of the bandwidth than 152).  16 items are more clusters than the GPU holds at
+    // once (a CTA fills an SM): 18.7 against 16.8.
     const int items = a.b.n_seqs * a.kv.n_kv;
-    if (a.b.n_seqs <= 32 && items * kPrCluster <= grid) {
+    if (items * kPrCluster * 2 <= grid && (a.b.width << a.kv.page_log2) <= 16384) {
       using G = Pr<HD, 1, QF32, Q8, true>;
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(items * kPrCluster);
