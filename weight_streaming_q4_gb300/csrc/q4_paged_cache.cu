@@ -23,8 +23,9 @@
 // (a block with a subnormal d: clamped), so its nearest integer n is the
 // quotient's or, next to a tie, one beside it.  r = x - n d is exact (n d has 18 bits, and r is
 // a multiple of x's last bit no larger than d), so comparing |r| with d / 2 tells,
-// ties going to the even n.  An IEEE division per value took a third of the kernel's
-// instructions.
+// ties going to the even n.  (An IEEE division per value took a third of the
+// kernel's instructions, this test for each value another third: it is one comparison
+// for all but the blocks with a value on a tie or across one.)
 #include <cuda_fp16.h>
 #include <stdint.h>
 
@@ -34,7 +35,7 @@ namespace q4 {
 
 namespace {
 
-constexpr int kPcThreads = 256;
+constexpr int kPcThreads = 128;
 
 template <bool F32>
 __device__ __forceinline__ void load8(const void* row, int64_t at, float (&x)[8]) {
@@ -54,21 +55,34 @@ __device__ __forceinline__ void load8(const void* row, int64_t at, float (&x)[8]
   }
 }
 
+// The larger of two numbers; NaN if one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
 // rint(x / d) within -127..127 of 8 values, as bytes; 0 where d is 0 or NaN.
 __device__ __forceinline__ uint2 q8_codes(const float (&x)[8], float d) {
   if (!(d > 0.f)) return make_uint2(0, 0);
   constexpr float kMagic = 12582912.f;       // 1.5 * 2^23: a number added to it is rounded to an integer, in its low bits
   const float inv = __fdiv_rn(1.f, d), half = 0.5f * d;
-  const bool small = d < 6.103515625e-05f;   // subnormal binary16: the codes may pass 127
   uint32_t n[8];
+  bool near = d < 6.103515625e-05f;          // (a subnormal scale: the codes may pass 127)
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float t = __fmaf_rn(x[j], inv, kMagic);
-    const float r = __fmaf_rn(kMagic - t, d, x[j]);
-    int q = __float_as_int(t);
-    if (fabsf(r) > half || (fabsf(r) == half && (q & 1))) q += r > 0.f ? 1 : -1;
-    if (small) q = min(max(q, 0x4b400000 - 127), 0x4b400000 + 127);
-    n[j] = static_cast<uint32_t>(q);
+    near |= fabsf(__fmaf_rn(kMagic - t, d, x[j])) >= half;
+    n[j] = __float_as_uint(t);
+  }
+  if (near) {                                // on a tie or across one: rare
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float r = __fmaf_rn(kMagic - __uint_as_float(n[j]), d, x[j]);
+      int q = static_cast<int>(n[j]);
+      if (fabsf(r) > half || (fabsf(r) == half && (q & 1))) q += r > 0.f ? 1 : -1;
+      n[j] = static_cast<uint32_t>(min(max(q, 0x4b400000 - 127), 0x4b400000 + 127));
+    }
   }
   return make_uint2(__byte_perm(__byte_perm(n[0], n[1], 0x0040), __byte_perm(n[2], n[3], 0x0040), 0x5410),
                     __byte_perm(__byte_perm(n[4], n[5], 0x0040), __byte_perm(n[6], n[7], 0x0040), 0x5410));
@@ -130,21 +144,18 @@ __global__ void __launch_bounds__(kPcThreads) paged_write_kernel(PagedKv kv, Pag
       if (live) *reinterpret_cast<uint4*>(static_cast<__half*>(c < half ? kv.k : kv.v) + to) = o;
       continue;
     }
-    // the block's maximum and whether it holds a NaN (fmaxf drops NaN): the four
-    // lanes of a block share its fate (a head is a whole number of blocks)
+    // the block's maximum, NaN if it holds one: the four lanes of a block share its fate (a head is a whole
+    // number of blocks)
     float m = 0.f;
-    bool nan = false;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       if (!live) x[u][j] = 0.f;
-      m = fmaxf(m, fabsf(x[u][j])), nan |= x[u][j] != x[u][j];
+      m = max_nan(m, fabsf(x[u][j]));
     }
-    m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
-    m = fmaxf(m, __shfl_xor_sync(~0u, m, 2));
-    const unsigned nans = __ballot_sync(~0u, nan);
-    nan = (nans >> (lane & 28)) & 15;
+    m = max_nan(m, __shfl_xor_sync(~0u, m, 1));
+    m = max_nan(m, __shfl_xor_sync(~0u, m, 2));
     __half d = __float2half_rn(__fdiv_rn(m, 127.f));
-    if (nan || !(__half2float(d) <= 65504.f)) d = __ushort_as_half(0x7fff);
+    if (!(__half2float(d) <= 65504.f)) d = __ushort_as_half(0x7fff);
     const uint2 o = q8_codes(x[u], __half2float(d));
     if (!live) continue;
     *reinterpret_cast<uint2*>(static_cast<int8_t*>(c < half ? kv.k : kv.v) + to) = o;
