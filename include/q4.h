@@ -511,7 +511,8 @@ typedef struct q4_paged_kv {
  * page not given out, or given back): nothing is read or written there.
  *   token_starts   device int [n_seqs + 1], not decreasing, within 0..n_tokens
  *   kv_lens        device int [n_seqs], taken within 0..table_width * page_size
- *   page_table     device int [n_seqs][table_width]
+ *   page_table     device int [n_seqs][table_width]; table_width * page_size at
+ *                  most 2^30, and that times n_kv_heads below 2^31
  *   n_tokens       rows of the caller's buffers; rows that belong to no
  *                  sequence are not written, and their content does not matter
  *   max_new        the most new tokens of one sequence, as far as the caller
@@ -521,8 +522,9 @@ typedef struct q4_paged_kv {
  * content of them.  A sequence may have no new token.  A row at a negative
  * position (kv_lens below the new tokens) is in no page: it is not written,
  * reads back as zeros, and sees nothing as a query.  n_seqs <= 65535; with no
- * sequence or no token a call does nothing.  Sequences may share pages that are only read; a page that
- * receives tokens in a call must belong to one sequence of that call only.
+ * sequence or no token a call does nothing.  Sequences may share pages that
+ * are only read; a page that receives tokens in a call must belong to one
+ * sequence of that call only.
  */
 typedef struct q4_paged_batch {
   const int *token_starts;

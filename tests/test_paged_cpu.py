@@ -52,6 +52,14 @@ def test_batch_checks(lib, over):
     assert calls(lib, kv(), batch(**over)) == [q4.Q4_ERR_ARG] * 3
 
 
+def test_positions_of_all_heads_are_counted_in_31_bits(lib):
+    widest = (1 << 30) // 16
+    assert calls(lib, kv(n_kv_heads=2, page_size=16), batch(table_width=widest)) == [q4.Q4_ERR_ARG] * 3          # 2^31
+    assert calls(lib, kv(n_kv_heads=1, page_size=16), batch(table_width=widest + 1), ld=64) == [q4.Q4_ERR_ARG] * 3
+    # (taken: the next check, of the rows, refuses)
+    assert calls(lib, kv(n_kv_heads=2, page_size=16), batch(table_width=widest - 1), row=A + 8) == [q4.Q4_ERR_ALIGN] * 3
+
+
 def test_null_structs(lib):
     assert lib.q4_paged_write(None, batch(), A, A, 0, 128, None) == q4.Q4_ERR_ARG
     assert lib.q4_paged_read(kv(), None, A, A, 0, 128, None) == q4.Q4_ERR_ARG

@@ -28,7 +28,9 @@ int check_batch(const q4_paged_kv* kv, const q4_paged_batch* b, q4::PagedKv* k, 
   if ((static_cast<int64_t>(kv->n_pages) * kv->n_kv_heads << log2) > INT32_MAX) return Q4_ERR_ARG;
   if (kv->type == Q4_KV_Q8 && (!kv->k_scales || !kv->v_scales)) return Q4_ERR_ARG;
   if (b->n_seqs < 0 || b->n_seqs > 65535 || b->n_tokens < 0 || b->table_width < 1 || b->max_new < 0) return Q4_ERR_ARG;
-  if ((static_cast<int64_t>(b->table_width) << log2) > (1 << 30)) return Q4_ERR_ARG;
+  // (the key tiles of a row tile's heads are counted in 32 bits)
+  const int64_t positions = static_cast<int64_t>(b->table_width) << log2;
+  if (positions > (1 << 30) || positions * kv->n_kv_heads > INT32_MAX) return Q4_ERR_ARG;
   if (!aligned(kv->k_pages, 16) || !aligned(kv->v_pages, 16)) return Q4_ERR_ALIGN;
   if (kv->type == Q4_KV_Q8 && (!aligned(kv->k_scales, 16) || !aligned(kv->v_scales, 16))) return Q4_ERR_ALIGN;
   *empty = b->n_seqs == 0 || b->n_tokens == 0;
