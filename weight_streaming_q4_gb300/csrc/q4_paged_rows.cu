@@ -1,7 +1,7 @@
 // Attention of few query rows over a paged KV cache (sm_103a): single tokens and
 // short drafts, where reading the keys and values is all there is to do.
 //
-// An item (q4_paged_sched.cuh) is R = 16 or 32 query rows of one value head, its
+// An item (q4_paged_sched.cuh) is R = 8 to 32 query rows of one value head, its
 // units are 32 positions.  Persistent, one CTA per SM.  Within a CTA every warp
 // works for itself: it takes every W-th group of 16 positions of the CTA's
 // units, copies their keys and values into its own ring with 16-byte cp.async
@@ -10,9 +10,12 @@
 // The warps' results meet in shared memory once per item.  The ring runs across
 // items: the next item's keys are on their way while an item is finished.
 //
-// Both products are mma.sync m16n8k16 (binary16 in, fp32 sums): 16 rows are one
-// operand tile of it, an eighth of a tcgen05 one, and the scores' registers are
-// the weights' operand as they lie.  fp32 queries enter as two binary16 parts.
+// Both products are mma.sync m16n8k16 (binary16 in, fp32 sums) with the positions,
+// then the value's columns, as its 16 rows and the query rows as its 8 columns: a
+// group of 4 or 8 query heads fills it, where a tcgen05 operand has 128 rows (with the query rows as
+// the 16, half of products, weights and output registers of such a group were zeros: 64
+// sequences of the 70B heads over Q8 175 us, so 133).  The scores' registers become the weights'
+// operand by one 8 x 8 transposition each.  fp32 queries enter as two binary16 parts.
 // Q8 pages stay codes in shared memory: a lane's 16 codes of a key are its share
 // of four instructions (the order of head_dim in the product is free, the
 // queries follow it), a transposed matrix load of value codes holds two columns of one
@@ -32,24 +35,27 @@ namespace {
 // CL: the CTAs of a cluster share every item (ClusterWalk).
 constexpr int kPrCluster = 8;
 
-template <int HD, int MT, bool QF32, bool Q8, bool CL>
+template <int HD, int NR, bool QF32, bool Q8, bool CL>
 struct Pr {
-  // Positions of a group, a warp's step.  At head_dim 64 a step of 32 pays the shuffles, the comparison with the
-  // maximum and the copies' addresses half as often (16 sequences under a window 17.0 us against 18.4); above, it
+  // Positions of a group, a warp's step.  At head_dim 64 a step of 32 pays the comparison with the
+  // maximum and the copies' addresses half as often (16 sequences under a window 12.7 us against 13.4); above, it
   // takes the registers of the warps that hide its latency.
-  static constexpr int GP = HD == 64 && MT == 1 ? 32 : 16;
-  // Warps.  12 for Q8, whose conversion makes it the issue slots that count (64 sequences of the 70B heads 175 us
-  // against 190 with 8).
-  static constexpr int W = HD > 128 ? 4 : HD == 128 && Q8 && MT == 1 ? 12 : 8;
+  static constexpr int GP = HD == 64 && NR <= 2 ? 32 : 16;
+  // Warps, as many as the registers allow (outputs: HD * NR / 4 of them) for Q8, whose conversion makes it the issue
+  // slots that count: 64 sequences of the 70B heads 133 us with 16, 139 with 12, 144 with 14 (a ring slot fewer).
+  // binary16 pages wait for memory, and the slots of the rings count.
+  static constexpr int W = HD > 128 ? 4 : HD == 128 && Q8 && NR <= 2 ? (NR == 1 ? 16 : 12) : 8;
   static constexpr int NT = W * 32;
-  static constexpr int R = 16 * MT;
+  static constexpr int R = 8 * NR;
   static constexpr int KS = HD / 16;                        // products of a key group
   static constexpr int ROW = Q8 ? HD : 2 * HD;              // bytes of a staged key
   static constexpr int SC = Q8 ? HD / 32 * 2 * GP : 0;      // bytes of a group's scales
   static constexpr int STAGE = 2 * GP * ROW + 2 * SC;       // keys, values, their scales
-  static constexpr int PITCH = HD + 8;                      // floats of a row of the warps' results
-  static constexpr int QB = MT * (QF32 ? 2 : 1) * KS * 512; // queries as operands
-  static constexpr int MERGE = W * 16 * PITCH * 4 + 2 * W * R * 4;
+  static constexpr int PITCH = HD + 4;                      // floats of a row of the warps' results
+  static constexpr bool QREG = NR == 1 && W <= 8;           // queries stay in registers (one token, 4096 positions: 7.8 us against 8.1)
+  static constexpr int QB = NR * KS * 32 * (QF32 ? 16 : 8); // queries as operands
+  static constexpr int RM = NR == 1 ? 8 : 16;               // rows that meet at a time
+  static constexpr int MERGE = W * RM * PITCH * 4 + 2 * W * R * 4;
   // In a cluster the ring is empty when the results meet, and they take its place.
   static constexpr int JOINED = CL ? R * (HD + 2) * 4 : 0;  // the CTA's result for the others of its cluster
   static constexpr int FIT = (231424 - 1024 - QB - (CL ? 0 : MERGE)) / (W * STAGE);
@@ -91,11 +97,17 @@ __device__ __forceinline__ uint4 pr_lds16(uint32_t at) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
   return v;
 }
-__device__ __forceinline__ void pr_mma(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+// The 8 x 8 matrix of which lane (g, t) holds row g, columns 2t and 2t + 1, transposed.
+__device__ __forceinline__ uint32_t pr_transposed(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ void pr_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // All CTAs of the cluster, with what they wrote to shared memory.
 __device__ __forceinline__ void cluster_sync() {
@@ -167,17 +179,19 @@ struct GroupWalk {
   }
 };
 
-template <int HD, int MT, bool QF32, bool Q8, bool CL>
-__global__ void __launch_bounds__(Pr<HD, MT, QF32, Q8, CL>::NT, 1)
+template <int HD, int NR, bool QF32, bool Q8, bool CL>
+__global__ void __launch_bounds__(Pr<HD, NR, QF32, Q8, CL>::NT, 1)
     paged_rows_kernel(const __grid_constant__ PagedAttnArgs a, PartSlots parts) {
-  using G = Pr<HD, MT, QF32, Q8, CL>;
+  using G = Pr<HD, NR, QF32, Q8, CL>;
   constexpr int W = G::W, R = G::R, NS = G::NS, KS = G::KS, ROW = G::ROW, PIECES = ROW / 16;
-  constexpr int GP = G::GP, SUB = GP / 16, NN = GP / 8;
+  constexpr int GP = G::GP, SUB = GP / 16;
+  constexpr bool TWO = NR * SUB <= 2;     // few sums of scores: two each, of the parts of an fp32 query or of every other product
   extern __shared__ __align__(16) char smem_pr[];
   PrCtl* c = reinterpret_cast<PrCtl*>(smem_pr);
-  uint4* s_q = reinterpret_cast<uint4*>(smem_pr + 1024);                  // [MT][part][KS][lane]
-  float* s_o = reinterpret_cast<float*>(smem_pr + 1024 + G::QB);          // [W][16][PITCH]
-  float* s_m = s_o + W * 16 * G::PITCH;                                   // [W][R]
+  using Query = typename std::conditional<QF32, uint4, uint2>::type;
+  Query* s_q = reinterpret_cast<Query*>(smem_pr + 1024);                  // [NR][KS][lane]
+  float* s_o = reinterpret_cast<float*>(smem_pr + 1024 + G::QB);          // [W][RM][PITCH]
+  float* s_m = s_o + W * G::RM * G::PITCH;                                // [W][R]
   float* s_l = s_m + W * R;
   float* s_joined = s_l + W * R;                                          // CL: [R][HD], maxima [R], sums [R]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -280,43 +294,46 @@ __global__ void __launch_bounds__(Pr<HD, MT, QF32, Q8, CL>::NT, 1)
       cp.w = u.w;
       enter();
     }
-    // queries in operand order: lane (g, t) of product ks holds rows g and g + 8
-    for (int x = tid; x < MT * KS * 32; x += G::NT) {
-      const int mt = x / (KS * 32), ks = x / 32 % KS, xl = x & 31, xg = xl >> 2, xt = xl & 3;
-      const int e0 = Q8 ? (xt + 4 * (ks >> 2)) * 16 + 4 * (ks & 3) : ks * 16 + xt * 2, e1 = e0 + (Q8 ? 2 : 8);
-      uint32_t hi[4], lo[4];
+    // queries in operand order: lane (g, t) of product ks holds row g
+    for (int x = tid; x < NR * KS * 32; x += G::NT) {
+      const int nr = x / (KS * 32), ks = x / 32 % KS, xl = x & 31, xt = xl & 3, rr = nr * 8 + (xl >> 2);
+      const int e0 = Q8 ? (xt + 4 * (ks >> 2)) * 16 + 4 * (ks & 3) : ks * 16 + xt * 2;
+      uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+      if (rr < rows) {
+        const int64_t at = a.row_at(w.sp.t0, w.head, row0 + rr, a.q_ld) + e0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int rr = mt * 16 + xg + (i & 1) * 8, r = row0 + rr;
-        hi[i] = lo[i] = 0;
-        if (rr < rows) {
-          const int64_t at = a.row_at(w.sp.t0, w.head, r, a.q_ld) + (i < 2 ? e0 : e1);
+        for (int i = 0; i < 2; ++i) {
+          const int64_t e = at + i * (Q8 ? 2 : 8);
           if (QF32) {
-            const float2 f = __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(a.q) + at));
+            const float2 f = __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(a.q) + e));
             const __half2 h = __floats2half2_rn(f.x, f.y);
             const float2 b = __half22float2(h);
             hi[i] = as_u32(h);
             lo[i] = as_u32(__floats2half2_rn(f.x - b.x, f.y - b.y));
           } else {
-            hi[i] = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const __half*>(a.q) + at));
+            hi[i] = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const __half*>(a.q) + e));
           }
         }
       }
-      s_q[(mt * (QF32 ? 2 : 1) * KS + ks) * 32 + xl] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      if (QF32) s_q[((mt * 2 + 1) * KS + ks) * 32 + xl] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      if constexpr (QF32)
+        s_q[x] = make_uint4(hi[0], hi[1], lo[0], lo[1]);
+      else
+        s_q[x] = make_uint2(hi[0], hi[1]);
     }
-    int p[MT][2];              // positions of this lane's rows
-    float m[MT][2], l[MT][2], o[MT][HD / 8][4];
+    // of this lane's rows 2t, 2t + 1 of every 8
+    int p[NR][2];              // positions
+    float m[NR][2], l[NR][2];
+    float o[NR][KS][4];        // columns g (two of them) of 16, in rows 2t, 2t + 1
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int nr = 0; nr < NR; ++nr) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int rr = mt * 16 + g + h * 8;
-        p[mt][h] = rr < rows ? first + a.token_of(row0 + rr) : -1;
-        m[mt][h] = -INFINITY, l[mt][h] = 0.f;
+        const int rr = nr * 8 + 2 * t + h;
+        p[nr][h] = rr < rows ? first + a.token_of(row0 + rr) : -1;
+        m[nr][h] = -INFINITY, l[nr][h] = 0.f;
       }
 #pragma unroll
-      for (int n = 0; n < HD / 8; ++n) o[mt][n][0] = o[mt][n][1] = o[mt][n][2] = o[mt][n][3] = 0.f;
+      for (int n = 0; n < KS; ++n) o[nr][n][0] = o[nr][n][1] = o[nr][n][2] = o[nr][n][3] = 0.f;
     }
     if (CL || seg == 0) {
 #pragma unroll 1
@@ -325,6 +342,11 @@ __global__ void __launch_bounds__(Pr<HD, MT, QF32, Q8, CL>::NT, 1)
     __syncthreads();           // queries are there
     u.count();
     bool found = false;
+    Query qr[G::QREG ? KS : 1];
+    if (G::QREG) {
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) qr[G::QREG ? ks : 0] = s_q[ks * 32 + lane];
+    }
     for (u.g = warp; u.g < u.n; u.g += W) {
       copy();
       pr_wait<NS - 1>();
@@ -335,133 +357,122 @@ __global__ void __launch_bounds__(Pr<HD, MT, QF32, Q8, CL>::NT, 1)
       const int base = u.base_of(u.g);
       const uint32_t there = c->there[warp][stage];
       if (there) {
-        // ---- scores
-        // (with two column tiles, two sums each, of the parts of an fp32 query or of every other product: shorter chains)
-        float s[MT][NN][4], s2[MT][NN][4];
+        // ---- scores: of positions g, g + 8 (of 16), rows 2t, 2t + 1
+        float s[NR][SUB][4], s2[NR][SUB][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-          for (int e = 0; e < 4 * NN; ++e) s[mt][e >> 2][e & 3] = s2[mt][e >> 2][e & 3] = 0.f;
-        auto product = [&](int ks, const uint32_t (&b)[NN][2]) {
+          for (int e = 0; e < 4 * SUB; ++e) s[nr][e >> 2][e & 3] = s2[nr][e >> 2][e & 3] = 0.f;
+        auto product = [&](int sub, int ks, uint32_t k0, uint32_t k1, uint32_t k2, uint32_t k3) {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int part = 0; part < (QF32 ? 2 : 1); ++part) {
-              const uint4 q = s_q[((mt * (QF32 ? 2 : 1) + part) * KS + ks) * 32 + lane];
-#pragma unroll
-              for (int nt = 0; nt < NN; ++nt)
-                pr_mma(NN == 2 && (QF32 ? part : ks & 1) ? s2[mt][nt] : s[mt][nt], q, b[nt][0], b[nt][1]);
-            }
+          for (int nr = 0; nr < NR; ++nr) {
+            const Query q = G::QREG ? qr[G::QREG ? ks : 0] : s_q[(nr * KS + ks) * 32 + lane];
+            pr_mma(TWO && !QF32 && (ks & 1) ? s2[nr][sub] : s[nr][sub], k0, k1, k2, k3, q.x, q.y);
+            if constexpr (QF32) pr_mma(TWO ? s2[nr][sub] : s[nr][sub], k0, k1, k2, k3, q.z, q.w);
+          }
         };
         if (!Q8) {
 #pragma unroll
-          for (int k2 = 0; k2 < KS / 2; ++k2) {
-            uint32_t r[NN][4], b[NN][2];
+          for (int k2 = 0; k2 < KS / 2; ++k2)
 #pragma unroll
-            for (int nt = 0; nt < NN; ++nt) {
-              pr_ldsm(r[nt], at + place<ROW, false>(nt * 8 + (lane & 7), k2 * 4 + (lane >> 3)));
-              b[nt][0] = r[nt][0], b[nt][1] = r[nt][1];
+            for (int sub = 0; sub < SUB; ++sub) {
+              uint32_t r[2][4];
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                pr_ldsm(r[i], at + place<ROW, false>(sub * 16 + i * 8 + (lane & 7), k2 * 4 + (lane >> 3)));
+              product(sub, 2 * k2, r[0][0], r[1][0], r[0][1], r[1][1]);
+              product(sub, 2 * k2 + 1, r[0][2], r[1][2], r[0][3], r[1][3]);
             }
-            product(2 * k2, b);
-#pragma unroll
-            for (int nt = 0; nt < NN; ++nt) b[nt][0] = r[nt][2], b[nt][1] = r[nt][3];
-            product(2 * k2 + 1, b);
-          }
         } else {
 #pragma unroll
-          for (int j = 0; j < HD / 64; ++j) {
-            __half2 h[NN][8];
+          for (int j = 0; j < HD / 64; ++j)
 #pragma unroll
-            for (int nt = 0; nt < NN; ++nt) {
-              const uint4 q = pr_lds16(at + place<ROW, true>(nt * 8 + g, t + 4 * j));
-              uint16_t d;
-              asm volatile("ld.shared.u16 %0, [%1];"
-                           : "=h"(d)
-                           : "r"(at + 2 * GP * ROW + (nt * 8 + g) * (HD / 16) + ((t >> 1) + 2 * j) * 2)
-                           : "memory");
-              const __half2 d2 = __half2half2(__ushort_as_half(d));
-              q8_values4(q.x, d2, h[nt][0], h[nt][1]);
-              q8_values4(q.y, d2, h[nt][2], h[nt][3]);
-              q8_values4(q.z, d2, h[nt][4], h[nt][5]);
-              q8_values4(q.w, d2, h[nt][6], h[nt][7]);
+            for (int sub = 0; sub < SUB; ++sub) {
+              __half2 h[2][8];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int pos = sub * 16 + i * 8 + g;
+                const uint4 q = pr_lds16(at + place<ROW, true>(pos, t + 4 * j));
+                uint16_t d;
+                asm volatile("ld.shared.u16 %0, [%1];"
+                             : "=h"(d)
+                             : "r"(at + 2 * GP * ROW + pos * (HD / 16) + ((t >> 1) + 2 * j) * 2)
+                             : "memory");
+                const __half2 d2 = __half2half2(__ushort_as_half(d));
+                q8_values4(q.x, d2, h[i][0], h[i][1]);
+                q8_values4(q.y, d2, h[i][2], h[i][3]);
+                q8_values4(q.z, d2, h[i][4], h[i][5]);
+                q8_values4(q.w, d2, h[i][6], h[i][7]);
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                product(sub, 4 * j + k, as_u32(h[0][2 * k]), as_u32(h[1][2 * k]), as_u32(h[0][2 * k + 1]), as_u32(h[1][2 * k + 1]));
             }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t b[NN][2];
-#pragma unroll
-              for (int nt = 0; nt < NN; ++nt) b[nt][0] = as_u32(h[nt][2 * k]), b[nt][1] = as_u32(h[nt][2 * k + 1]);
-              product(4 * j + k, b);
-            }
-          }
         }
-        if (NN == 2) {
+        if (TWO) {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
+          for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-            for (int e = 0; e < 4 * NN; ++e) s[mt][e >> 2][e & 3] += s2[mt][e >> 2][e & 3];
+            for (int e = 0; e < 4 * SUB; ++e) s[nr][e >> 2][e & 3] += s2[nr][e >> 2][e & 3];
         }
         const bool whole = there == (1u << SUB) - 1 && base + GP - 1 <= w.it.p0 &&
                            (!a.window || base > w.it.p1 - a.window || base + GP <= a.sinks);
         if (!whole) {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
+          for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-            for (int e = 0; e < 4 * NN; ++e) {
-              const int pr = p[mt][(e >> 1) & 1], x = base + (e >> 2) * 8 + 2 * t + (e & 1);
-              if (x > pr || (a.window && x <= pr - a.window && x >= a.sinks) || !((there >> (e >> 3)) & 1))
-                s[mt][e >> 2][e & 3] = -INFINITY;
+            for (int e = 0; e < 4 * SUB; ++e) {
+              const int pr = p[nr][e & 1], x = base + (e >> 1) * 8 + g;
+              if (x > pr || (a.window && x <= pr - a.window && x >= a.sinks) || !((there >> (e >> 2)) & 1))
+                s[nr][e >> 2][e & 3] = -INFINITY;
             }
         }
         // ---- weights
-        uint4 pw[MT][SUB];
-        float top[MT][2];
+        // (a row's maximum is wanted of all lanes only when one of them has raised it)
+        float top[NR][2];
         bool raise = false;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float x = -INFINITY;
 #pragma unroll
-            for (int nt = 0; nt < NN; ++nt) x = fmaxf(x, fmaxf(s[mt][nt][2 * h], s[mt][nt][2 * h + 1]));
-            x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
-            x = fmaxf(x, __shfl_xor_sync(~0u, x, 2)) * a.scale;
-            top[mt][h] = x;
-            raise |= x > m[mt][h] + 8.f || (m[mt][h] == -INFINITY && x > m[mt][h]);
+            for (int e = h; e < 4 * SUB; e += 2) x = fmaxf(x, s[nr][e >> 2][e & 3]);
+            x *= a.scale;
+            top[nr][h] = x;
+            raise |= x > m[nr][h] + 8.f || (m[nr][h] == -INFINITY && x > m[nr][h]);
           }
         if (__any_sync(~0u, raise)) {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
+          for (int nr = 0; nr < NR; ++nr) {
             float f[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const float m2 = fmaxf(m[mt][h], top[mt][h]);
-              f[h] = m2 == m[mt][h] ? 1.f : pr_exp2(m[mt][h] - m2);
-              m[mt][h] = m2;
-              l[mt][h] *= f[h];
+              float m2 = fmaxf(m[nr][h], top[nr][h]);
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) m2 = fmaxf(m2, __shfl_xor_sync(~0u, m2, d));
+              f[h] = m2 == m[nr][h] ? 1.f : pr_exp2(m[nr][h] - m2);
+              m[nr][h] = m2;
+              l[nr][h] *= f[h];
             }
 #pragma unroll
-            for (int n = 0; n < HD / 8; ++n)
-              o[mt][n][0] *= f[0], o[mt][n][1] *= f[0], o[mt][n][2] *= f[1], o[mt][n][3] *= f[1];
+            for (int n = 0; n < KS; ++n)
+              o[nr][n][0] *= f[0], o[nr][n][1] *= f[1], o[nr][n][2] *= f[0], o[nr][n][3] *= f[1];
           }
         }
+        uint32_t pw[NR][SUB][2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          uint32_t x[NN][2];
+        for (int nr = 0; nr < NR; ++nr) {
+          float mm[2];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float mm = m[mt][h] == -INFINITY ? 0.f : m[mt][h];
-            float sum = 0.f;
+          for (int h = 0; h < 2; ++h) mm[h] = m[nr][h] == -INFINITY ? 0.f : m[nr][h];
 #pragma unroll
-            for (int nt = 0; nt < NN; ++nt) {
-              const float w0 = pr_exp2(fmaf(s[mt][nt][2 * h], a.scale, -mm)), w1 = pr_exp2(fmaf(s[mt][nt][2 * h + 1], a.scale, -mm));
-              sum += w0 + w1;
-              x[nt][h] = as_u32(__floats2half2_rn(w0, w1));
-            }
-            l[mt][h] += sum;
+          for (int e = 0; e < 4 * SUB; e += 2) {
+            const float w0 = pr_exp2(fmaf(s[nr][e >> 2][e & 3], a.scale, -mm[0]));
+            const float w1 = pr_exp2(fmaf(s[nr][e >> 2][(e & 3) + 1], a.scale, -mm[1]));
+            l[nr][0] += w0, l[nr][1] += w1;
+            pw[nr][e >> 2][(e >> 1) & 1] = pr_transposed(as_u32(__floats2half2_rn(w0, w1)));
           }
-#pragma unroll
-          for (int sub = 0; sub < SUB; ++sub)
-            pw[mt][sub] = make_uint4(x[2 * sub][0], x[2 * sub][1], x[2 * sub + 1][0], x[2 * sub + 1][1]);
         }
         // ---- values, 16 positions at a time
         auto values = [&](auto cleaning) {      // (code of its own for the few groups to be cleaned)
@@ -498,25 +509,24 @@ __global__ void __launch_bounds__(Pr<HD, MT, QF32, Q8, CL>::NT, 1)
                   for (int e = 0; e < 4; ++e) r[e] = pr_finite(r[e], &found);
                 }
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                  pr_mma(o[mt][2 * i], pw[mt][sub], r[0], r[1]);
-                  pr_mma(o[mt][2 * i + 1], pw[mt][sub], r[2], r[3]);
-                }
+                for (int nr = 0; nr < NR; ++nr) pr_mma(o[nr][i], r[0], r[2], r[1], r[3], pw[nr][sub][0], pw[nr][sub][1]);
               } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {       // 16 codes' even and odd columns, of two pieces
-                  const int pc = 2 * i + (e >> 1);
-                  const uint32_t sel = (e & 1) ? 0x4341u : 0x4240u;
-                  uint32_t b0 = as_u32(__hmul2(q8_pair(r[(e >> 1) * 2] ^ 0x80808080u, sel), d0[pc / 2]));
-                  uint32_t b1 = as_u32(__hmul2(q8_pair(r[(e >> 1) * 2 + 1] ^ 0x80808080u, sel), d1[pc / 2]));
-                  if (decltype(cleaning)::value) b0 = pr_finite(b0, &found), b1 = pr_finite(b1, &found);
+                for (int k = 0; k < 2; ++k) {       // two pieces; of each the 16 codes' even columns, then the odd ones
+                  const int pc = 2 * i + k;
+                  const uint32_t x0 = r[2 * k] ^ 0x80808080u, x1 = r[2 * k + 1] ^ 0x80808080u;
+                  uint32_t v[4] = {as_u32(__hmul2(q8_pair(x0, 0x4240u), d0[pc / 2])), as_u32(__hmul2(q8_pair(x0, 0x4341u), d0[pc / 2])),
+                                   as_u32(__hmul2(q8_pair(x1, 0x4240u), d1[pc / 2])), as_u32(__hmul2(q8_pair(x1, 0x4341u), d1[pc / 2]))};
+                  if (decltype(cleaning)::value) {
 #pragma unroll
-                  for (int mt = 0; mt < MT; ++mt) pr_mma(o[mt][2 * pc + (e & 1)], pw[mt][sub], b0, b1);
+                    for (int e = 0; e < 4; ++e) v[e] = pr_finite(v[e], &found);
+                  }
+#pragma unroll
+                  for (int nr = 0; nr < NR; ++nr) pr_mma(o[nr][pc], v[0], v[1], v[2], v[3], pw[nr][sub][0], pw[nr][sub][1]);
                 }
               }
             }
           }
-        
         };
         if (whole)
           values(std::false_type{});
@@ -527,44 +537,46 @@ __global__ void __launch_bounds__(Pr<HD, MT, QF32, Q8, CL>::NT, 1)
     }
     if (found) *reinterpret_cast<volatile int*>(&c->bad) = seg + 1;
     if (CL) __syncthreads();   // (the results take the ring's place)
-    // ---- the warps' results meet, 16 rows at a time
+    // ---- the warps' results meet, RM rows at a time
     const bool whole_item = w.i0 == 0 && w.i1 == w.it.cnt;
     const int slot = w.i0 == 0 ? 1 : 0;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      float* mine = s_o + warp * 16 * G::PITCH;
+    for (int r8 = 0; r8 < NR; r8 += G::RM / 8) {
+      float* mine = s_o + warp * G::RM * G::PITCH;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int rr = g + h * 8;
-        float sum = l[mt][h];
-        sum += __shfl_xor_sync(~0u, sum, 1);
-        sum += __shfl_xor_sync(~0u, sum, 2);
-        if (t == 0) s_m[warp * R + mt * 16 + rr] = m[mt][h], s_l[warp * R + mt * 16 + rr] = sum;
-        if (!Q8) {
+      for (int i = 0; i < G::RM / 8; ++i)
 #pragma unroll
-          for (int n = 0; n < HD / 8; ++n)
-            *reinterpret_cast<float2*>(mine + rr * G::PITCH + n * 8 + 2 * t) = make_float2(o[mt][n][2 * h], o[mt][n][2 * h + 1]);
-        } else {
+        for (int h = 0; h < 2; ++h) {
+          const int nr = r8 + i;
+          if (nr >= NR) break;
+          const int rr = (nr - r8) * 8 + 2 * t + h;
+          float sum = l[nr][h];
 #pragma unroll
-          for (int pc = 0; pc < HD / 16; ++pc)
-            *reinterpret_cast<float4*>(mine + rr * G::PITCH + pc * 16 + 4 * t) =
-                make_float4(o[mt][2 * pc][2 * h], o[mt][2 * pc + 1][2 * h], o[mt][2 * pc][2 * h + 1], o[mt][2 * pc + 1][2 * h + 1]);
+          for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(~0u, sum, d);
+          if (g == 0) s_m[warp * R + r8 * 8 + rr] = m[nr][h], s_l[warp * R + r8 * 8 + rr] = sum;
+#pragma unroll
+          for (int n = 0; n < KS; ++n) {
+            float* to = mine + rr * G::PITCH + n * 16;
+            if (Q8)
+              *reinterpret_cast<float2*>(to + 2 * g) = make_float2(o[nr][n][h], o[nr][n][2 + h]);
+            else
+              to[g] = o[nr][n][h], to[8 + g] = o[nr][n][2 + h];
+          }
         }
-      }
       __syncthreads();
       const bool bad = c->bad == seg + 1;
-      const int n_rows = min(16, rows - mt * 16);
+      const int n_rows = min(G::RM, rows - r8 * 8);
       for (int x = tid; x < n_rows * (HD / 4); x += G::NT) {
-        const int rr = x / (HD / 4), e = x % (HD / 4) * 4, r = row0 + mt * 16 + rr;
+        const int rr = x / (HD / 4), e = x % (HD / 4) * 4, r = row0 + r8 * 8 + rr;
         float top = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < W; ++k) top = fmaxf(top, s_m[k * R + mt * 16 + rr]);
+        for (int k = 0; k < W; ++k) top = fmaxf(top, s_m[k * R + r8 * 8 + rr]);
         float sum = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < W; ++k) {
-          const float mk = s_m[k * R + mt * 16 + rr], f = mk == -INFINITY ? 0.f : pr_exp2(mk - top);
-          const float4 y = *reinterpret_cast<const float4*>(s_o + (k * 16 + rr) * G::PITCH + e);
-          sum += s_l[k * R + mt * 16 + rr] * f;
+          const float mk = s_m[k * R + r8 * 8 + rr], f = mk == -INFINITY ? 0.f : pr_exp2(mk - top);
+          const float4 y = *reinterpret_cast<const float4*>(s_o + (k * G::RM + rr) * G::PITCH + e);
+          sum += s_l[k * R + r8 * 8 + rr] * f;
           v[0] += y.x * f, v[1] += y.y * f, v[2] += y.z * f, v[3] += y.w * f;
         }
         if (bad) {
@@ -591,23 +603,23 @@ __global__ void __launch_bounds__(Pr<HD, MT, QF32, Q8, CL>::NT, 1)
             }
         }
         if (CL) {
-          *reinterpret_cast<float4*>(s_joined + (mt * 16 + rr) * HD + e) = make_float4(v[0], v[1], v[2], v[3]);
-          if (e == 0) s_joined[R * HD + mt * 16 + rr] = top, s_joined[R * (HD + 1) + mt * 16 + rr] = sum;
+          *reinterpret_cast<float4*>(s_joined + (r8 * 8 + rr) * HD + e) = make_float4(v[0], v[1], v[2], v[3]);
+          if (e == 0) s_joined[R * HD + r8 * 8 + rr] = top, s_joined[R * (HD + 1) + r8 * 8 + rr] = sum;
         } else if (whole_item) {
           const float inv = sum == 0.f ? 0.f : 1.f / sum;
           __half* out = a.out + a.row_at(w.sp.t0, w.head, r, a.out_ld) + e;
           const uint2 y = make_uint2(as_u32(__floats2half2_rn(v[0] * inv, v[1] * inv)), as_u32(__floats2half2_rn(v[2] * inv, v[3] * inv)));
           *reinterpret_cast<uint2*>(out) = y;
         } else {
-          *reinterpret_cast<float4*>(parts.out(blockIdx.x, slot) + static_cast<size_t>(mt * 16 + rr) * HD + e) =
+          *reinterpret_cast<float4*>(parts.out(blockIdx.x, slot) + static_cast<size_t>(r8 * 8 + rr) * HD + e) =
               make_float4(v[0], v[1], v[2], v[3]);
           if (e == 0) {
-            parts.max(blockIdx.x, slot)[mt * 16 + rr] = top;
-            parts.sum(blockIdx.x, slot)[mt * 16 + rr] = sum;
+            parts.max(blockIdx.x, slot)[r8 * 8 + rr] = top;
+            parts.sum(blockIdx.x, slot)[r8 * 8 + rr] = sum;
           }
         }
       }
-      if (mt + 1 < MT) __syncthreads();        // the next item's queries are waited for anyway
+      if (r8 + G::RM / 8 < NR) __syncthreads();        // the next item's queries are waited for anyway
     }
     if constexpr (CL) {
       // ---- the cluster's results meet: every CTA finishes its share of the outputs
@@ -644,34 +656,37 @@ __global__ void __launch_bounds__(Pr<HD, MT, QF32, Q8, CL>::NT, 1)
   if (!CL && tid == 0) *parts.record(blockIdx.x) = rec;
 }
 
-template <int HD, int MT, bool QF32, bool Q8>
+template <int HD, int NR, bool QF32, bool Q8>
 cudaError_t prepare_rows() {
-  const cudaError_t e = cudaFuncSetAttribute(paged_rows_kernel<HD, MT, QF32, Q8, false>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, Pr<HD, MT, QF32, Q8, false>::SMEM);
-  if (e != cudaSuccess || MT > 1) return e;
-  return cudaFuncSetAttribute(paged_rows_kernel<HD, 1, QF32, Q8, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Pr<HD, 1, QF32, Q8, true>::SMEM);
+  const cudaError_t e = cudaFuncSetAttribute(paged_rows_kernel<HD, NR, QF32, Q8, false>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, Pr<HD, NR, QF32, Q8, false>::SMEM);
+  if constexpr (NR <= 2) {
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(paged_rows_kernel<HD, NR, QF32, Q8, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Pr<HD, NR, QF32, Q8, true>::SMEM);
+  }
+  return e;
 }
 
-template <int HD, int MT>
-cudaError_t prepare_mt() {
-  const cudaError_t e[4] = {prepare_rows<HD, MT, false, false>(), prepare_rows<HD, MT, false, true>(),
-                            prepare_rows<HD, MT, true, false>(), prepare_rows<HD, MT, true, true>()};
+template <int HD, int NR>
+cudaError_t prepare_nr() {
+  const cudaError_t e[4] = {prepare_rows<HD, NR, false, false>(), prepare_rows<HD, NR, false, true>(),
+                            prepare_rows<HD, NR, true, false>(), prepare_rows<HD, NR, true, true>()};
   for (cudaError_t x : e)
     if (x != cudaSuccess) return x;
   return cudaSuccess;
 }
 
-template <int HD, int MT, bool QF32, bool Q8>
+template <int HD, int NR, bool QF32, bool Q8>
 cudaError_t launch_rows(const PagedAttnArgs& a, void* ws, int grid, cudaStream_t s) {
-  if constexpr (MT == 1) {
-    // Few items and a table of no great length: a cluster each.  One token of the 8B heads over 512, 2048, 4096 and
-    // 8192 positions 5.4, 7.2, 9.3 and 14.2 us, split evenly over all CTAs 9.1, 9.8, 13.2 and 18.2; over 32768 36.6
-    // against 32.6 (64 CTAs draw less of the bandwidth than 152).  16 items are more clusters than the GPU holds at
-    // once (a CTA fills an SM): 18.7 against 16.8.
+  if constexpr (NR <= 2) {
+    // Few items and a table of no great length: a cluster each.  One token of the 8B heads over 512, 2048, 4096, 8192
+    // and 32768 positions 5.0, 6.4, 7.8, 12.4 and 30.0 us, split evenly over all CTAs 8.5, 9.1, 12.1, 17.4 and 31.6
+    // (64 CTAs draw less of the bandwidth than 152, so longer tables are split).  16 items are more clusters than the
+    // GPU holds at once (a CTA fills an SM): 16.9 against 15.6 for 2 sequences of 4096 positions.
     const int items = a.b.n_seqs * a.kv.n_kv;
-    if (items * kPrCluster * 2 <= grid && (a.b.width << a.kv.page_log2) <= 16384) {
-      using G = Pr<HD, 1, QF32, Q8, true>;
+    if (items * kPrCluster * 2 <= grid && (a.b.width << a.kv.page_log2) <= 32768) {
+      using G = Pr<HD, NR, QF32, Q8, true>;
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(items * kPrCluster);
       cfg.blockDim = dim3(G::NT);
@@ -682,27 +697,39 @@ cudaError_t launch_rows(const PagedAttnArgs& a, void* ws, int grid, cudaStream_t
       at[0].val.clusterDim.x = kPrCluster, at[0].val.clusterDim.y = 1, at[0].val.clusterDim.z = 1;
       cfg.attrs = at;
       cfg.numAttrs = 1;
-      return cudaLaunchKernelEx(&cfg, paged_rows_kernel<HD, 1, QF32, Q8, true>, a, PartSlots{});
+      return cudaLaunchKernelEx(&cfg, paged_rows_kernel<HD, NR, QF32, Q8, true>, a, PartSlots{});
     }
   }
-  using G = Pr<HD, MT, QF32, Q8, false>;
+  using G = Pr<HD, NR, QF32, Q8, false>;
   PartSlots parts{static_cast<char*>(ws), G::R, HD};
-  paged_rows_kernel<HD, MT, QF32, Q8, false><<<grid, G::NT, G::SMEM, s>>>(a, parts);
+  paged_rows_kernel<HD, NR, QF32, Q8, false><<<grid, G::NT, G::SMEM, s>>>(a, parts);
   const cudaError_t e = cudaGetLastError();
   return e != cudaSuccess ? e : paged_join_launch(a, parts, grid, s);
 }
 
-template <int HD, int MT>
-cudaError_t launch_mt(const PagedAttnArgs& a, bool f32, bool q8, void* ws, int grid, cudaStream_t s) {
-  if (f32) return q8 ? launch_rows<HD, MT, true, true>(a, ws, grid, s) : launch_rows<HD, MT, true, false>(a, ws, grid, s);
-  return q8 ? launch_rows<HD, MT, false, true>(a, ws, grid, s) : launch_rows<HD, MT, false, false>(a, ws, grid, s);
+template <int HD, int NR>
+cudaError_t launch_nr(const PagedAttnArgs& a, bool f32, bool q8, void* ws, int grid, cudaStream_t s) {
+  if (f32) return q8 ? launch_rows<HD, NR, true, true>(a, ws, grid, s) : launch_rows<HD, NR, true, false>(a, ws, grid, s);
+  return q8 ? launch_rows<HD, NR, false, true>(a, ws, grid, s) : launch_rows<HD, NR, false, false>(a, ws, grid, s);
+}
+
+// As many rows at once as the item has; above head_dim 128, whose outputs fill the registers, at most 16.
+template <int HD>
+cudaError_t launch_hd(const PagedAttnArgs& a, bool f32, bool q8, int rows, void* ws, int grid, cudaStream_t s) {
+  if (rows <= 8) return launch_nr<HD, 1>(a, f32, q8, ws, grid, s);
+  if constexpr (HD <= 128) {
+    if (rows > 24) return launch_nr<HD, 4>(a, f32, q8, ws, grid, s);
+    if (rows > 16) return launch_nr<HD, 3>(a, f32, q8, ws, grid, s);
+  }
+  return launch_nr<HD, 2>(a, f32, q8, ws, grid, s);
 }
 
 }  // namespace
 
 cudaError_t paged_rows_prepare() {
-  const cudaError_t e[6] = {prepare_mt<64, 1>(), prepare_mt<64, 2>(), prepare_mt<128, 1>(), prepare_mt<128, 2>(),
-                            prepare_mt<192, 1>(), prepare_mt<256, 1>()};
+  const cudaError_t e[12] = {prepare_nr<64, 1>(),  prepare_nr<64, 2>(),  prepare_nr<64, 3>(),  prepare_nr<64, 4>(),
+                             prepare_nr<128, 1>(), prepare_nr<128, 2>(), prepare_nr<128, 3>(), prepare_nr<128, 4>(),
+                             prepare_nr<192, 1>(), prepare_nr<192, 2>(), prepare_nr<256, 1>(), prepare_nr<256, 2>()};
   for (cudaError_t x : e)
     if (x != cudaSuccess) return x;
   return cudaSuccess;
@@ -710,10 +737,10 @@ cudaError_t paged_rows_prepare() {
 
 cudaError_t paged_rows_launch(const PagedAttnArgs& a, bool q_f32, bool q8, int rows, void* ws, int grid, cudaStream_t s) {
   switch (a.kv.hd) {
-    case 64: return rows <= 16 ? launch_mt<64, 1>(a, q_f32, q8, ws, grid, s) : launch_mt<64, 2>(a, q_f32, q8, ws, grid, s);
-    case 128: return rows <= 16 ? launch_mt<128, 1>(a, q_f32, q8, ws, grid, s) : launch_mt<128, 2>(a, q_f32, q8, ws, grid, s);
-    case 192: return launch_mt<192, 1>(a, q_f32, q8, ws, grid, s);
-    default: return launch_mt<256, 1>(a, q_f32, q8, ws, grid, s);
+    case 64: return launch_hd<64>(a, q_f32, q8, rows, ws, grid, s);
+    case 128: return launch_hd<128>(a, q_f32, q8, rows, ws, grid, s);
+    case 192: return launch_hd<192>(a, q_f32, q8, rows, ws, grid, s);
+    default: return launch_hd<256>(a, q_f32, q8, rows, ws, grid, s);
   }
 }
 
