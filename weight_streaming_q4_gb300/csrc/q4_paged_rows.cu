@@ -14,7 +14,7 @@
 // then the value's columns, as its 16 rows and the query rows as its 8 columns: a
 // group of 4 or 8 query heads fills it, where a tcgen05 operand has 128 rows (with the query rows as
 // the 16, half of products, weights and output registers of such a group were zeros: 64
-// sequences of the 70B heads over Q8 175 us, so 133).  The scores' registers become the weights'
+// sequences of the 70B heads over Q8 175 us, so 133 at that step).  The scores' registers become the weights'
 // operand by one 8 x 8 transposition each.  fp32 queries enter as two binary16 parts.
 // Q8 pages stay codes in shared memory: a lane's 16 codes of a key are its share
 // of four instructions (the order of head_dim in the product is free, the
@@ -42,7 +42,7 @@ struct Pr {
   // takes the registers of the warps that hide its latency.
   static constexpr int GP = HD == 64 && NR <= 2 ? 32 : 16;
   // Warps, as many as the registers allow (outputs: HD * NR / 4 of them) for Q8, whose conversion makes it the issue
-  // slots that count: 64 sequences of the 70B heads 133 us with 16, 139 with 12, 144 with 14 (a ring slot fewer).
+  // slots that count: 64 sequences of the 70B heads 133 us with 16, 139 with 12, 144 with 14, whose rings hold no more than 16's.
   // binary16 pages wait for memory, and the slots of the rings count.
   static constexpr int W = HD > 128 ? 4 : HD == 128 && Q8 && NR <= 2 ? (NR == 1 ? 16 : 12) : 8;
   static constexpr int NT = W * 32;
@@ -55,7 +55,7 @@ struct Pr {
   static constexpr bool QREG = NR == 1 && W <= 8;           // queries stay in registers (one token, 4096 positions: 7.8 us against 8.1)
   static constexpr int QB = NR * KS * 32 * (QF32 ? 16 : 8); // queries as operands
   static constexpr int RM = NR == 1 ? 8 : 16;               // rows that meet at a time
-  static constexpr int MERGE = W * RM * PITCH * 4 + 2 * W * R * 4;
+  static constexpr int MERGE = (W * RM * PITCH * 4 + 2 * W * R * 4 + 511) / 512 * 512;
   // In a cluster the ring is empty when the results meet, and they take its place.
   static constexpr int JOINED = CL ? R * (HD + 2) * 4 : 0;  // the CTA's result for the others of its cluster
   static constexpr int FIT = (231424 - 1024 - QB - (CL ? 0 : MERGE)) / (W * STAGE);
@@ -63,6 +63,7 @@ struct Pr {
   static constexpr int RING = W * NS * STAGE;
   static constexpr int SMEM = 1024 + QB + (CL ? (RING > MERGE + JOINED ? RING : MERGE + JOINED) : MERGE + RING);
   static_assert(NS >= 2, "a group is copied while one is read");
+  static_assert(ROW > 512 || 512 % ROW || ((1024 + QB) % ROW == 0 && MERGE % ROW == 0 && STAGE % ROW == 0), "groups start on a multiple of the row");
 };
 
 struct PrCtl {
@@ -154,6 +155,11 @@ __device__ __forceinline__ int place(int r, int c) {
   return r * ROW + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
+// Rows whose pieces' numbers are whole bits of the address (a group starts on a multiple of the row): the place of
+// piece c ^ x is that of piece c, xored with x * 16.
+template <int ROW>
+constexpr bool kByXor = ROW == 128 || ROW == 256 || ROW == 512;
+
 template <bool CL, int R>
 struct WalkOf {
   using T = SegmentWalk<R, 32>;
@@ -186,7 +192,7 @@ __global__ void __launch_bounds__(Pr<HD, NR, QF32, Q8, CL>::NT, 1)
   constexpr int W = G::W, R = G::R, NS = G::NS, KS = G::KS, ROW = G::ROW, PIECES = ROW / 16;
   constexpr int GP = G::GP, SUB = GP / 16;
   constexpr bool TWO = NR * SUB <= 2;     // few sums of scores: two each, of the parts of an fp32 query or of every other product
-  extern __shared__ __align__(16) char smem_pr[];
+  extern __shared__ __align__(512) char smem_pr[];     // (kByXor)
   PrCtl* c = reinterpret_cast<PrCtl*>(smem_pr);
   using Query = typename std::conditional<QF32, uint4, uint2>::type;
   Query* s_q = reinterpret_cast<Query*>(smem_pr + 1024);                  // [NR][KS][lane]
@@ -218,7 +224,7 @@ __global__ void __launch_bounds__(Pr<HD, NR, QF32, Q8, CL>::NT, 1)
 
   // ------------------------------------------------------------------ copies
   cp.w = u.w;
-  uint32_t n_cp = 0, n_use = 0;
+  int st_cp = 0, st_use = 0;      // the next stage to copy into, to read
   // Page rows of the warp's next 32 / SUB groups in cp's segment, 16 positions per lane, from its group rows0 on.
   int rows_of = -1, rows0 = 0;
   auto look_up = [&]() {
@@ -232,6 +238,22 @@ __global__ void __launch_bounds__(Pr<HD, NR, QF32, Q8, CL>::NT, 1)
     cp.count();
     look_up();
   };
+  // 16 rows of keys or values to `to`.  Where a row's pieces divide a warp's 32, a lane's pieces lie 512 bytes apart, but
+  // for the exchange, whose part that changes from one to the next is a constant: no addresses to compute
+  // (64 sequences over Q8 127.5 us against 132.7, 32 rows 37.7 against 38.4).
+  auto pieces = [&](uint32_t to, const char* from, auto key8) {
+    constexpr bool K8 = decltype(key8)::value;
+    if constexpr (32 % PIECES == 0) {
+      const uint32_t d = to + place<ROW, K8>(lane / PIECES, lane % PIECES);
+      const char* f = from + lane * 16;
+#pragma unroll
+      for (int i = 0; i < PIECES / 2; ++i)
+        pr_cp16((d ^ (kByXor<ROW> && !K8 ? (i * (32 / PIECES) & 7) << 4 : 0)) + i * 512, f + i * 512);
+    } else {
+#pragma unroll
+      for (int x = lane; x < 16 * PIECES; x += 32) pr_cp16(to + place<ROW, K8>(x / PIECES, x % PIECES), from + x * 16);
+    }
+  };
   auto copy = [&]() {       // the warp's next group into the next stage; always one commit
     if (!CL) {
       while (cp.w.live() && cp.g >= cp.n) {
@@ -241,7 +263,7 @@ __global__ void __launch_bounds__(Pr<HD, NR, QF32, Q8, CL>::NT, 1)
     }
     if (cp.w.live() && cp.g < cp.n) {
       if (cp.g - rows0 >= 32 / SUB * W) look_up();
-      const int stage = n_cp % NS;
+      const int stage = st_cp;
       const uint32_t to = ring + stage * G::STAGE;
       uint32_t there = 0;
 #pragma unroll
@@ -261,23 +283,20 @@ __global__ void __launch_bounds__(Pr<HD, NR, QF32, Q8, CL>::NT, 1)
         there |= 1u << sub;
         const char* k = static_cast<const char*>(a.kv.k) + static_cast<size_t>(r0) * ROW;
         const char* v = static_cast<const char*>(a.kv.v) + static_cast<size_t>(r0) * ROW;
-#pragma unroll
-        for (int x = lane; x < 16 * PIECES; x += 32)
-          pr_cp16(to + place<ROW, Q8>(sub * 16 + x / PIECES, x % PIECES), k + x * 16);
+        pieces(to + sub * 16 * ROW, k, std::integral_constant<bool, Q8>{});
         if (Q8) {
           constexpr int SP = G::SC / SUB / 16;               // 16-byte pieces of 16 positions' scales
           const char* ks = reinterpret_cast<const char*>(a.kv.ks) + static_cast<size_t>(r0) * (HD / 16);
           const char* vs = reinterpret_cast<const char*>(a.kv.vs) + static_cast<size_t>(r0) * (HD / 16);
           const uint32_t sc = to + 2 * GP * ROW + sub * SP * 16;
-          if (lane < SP) pr_cp16(sc + lane * 16, ks + lane * 16);
-          else if (lane < 2 * SP) pr_cp16(sc + G::SC + (lane - SP) * 16, vs + (lane - SP) * 16);
+          const bool of_v = lane >= SP;
+          const int x = (of_v ? lane - SP : lane) * 16;
+          if (lane < 2 * SP) pr_cp16(sc + (of_v ? G::SC : 0) + x, (of_v ? vs : ks) + x);
         }
-#pragma unroll
-        for (int x = lane; x < 16 * PIECES; x += 32)
-          pr_cp16(to + GP * ROW + place<ROW, false>(sub * 16 + x / PIECES, x % PIECES), v + x * 16);
+        pieces(to + GP * ROW + sub * 16 * ROW, v, std::false_type{});
       }
       if (lane == 0) c->there[warp][stage] = there;
-      ++n_cp;
+      st_cp = st_cp + 1 == NS ? 0 : st_cp + 1;
       cp.g += W;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -351,12 +370,15 @@ __global__ void __launch_bounds__(Pr<HD, NR, QF32, Q8, CL>::NT, 1)
       copy();
       pr_wait<NS - 1>();
       __syncwarp();
-      const int stage = n_use % NS;
-      ++n_use;
+      const int stage = st_use;
+      st_use = st_use + 1 == NS ? 0 : st_use + 1;
       const uint32_t at = ring + stage * G::STAGE;
       const int base = u.base_of(u.g);
       const uint32_t there = c->there[warp][stage];
       if (there) {
+        // where this lane's first pieces lie
+        const uint32_t kat = at + (Q8 ? place<ROW, true>(g, t) : place<ROW, false>(lane & 7, lane >> 3));
+        const uint32_t vat = at + GP * ROW + place<ROW, false>((lane & 7) + (lane & 8), lane >> 4);
         // ---- scores: of positions g, g + 8 (of 16), rows 2t, 2t + 1
         float s[NR][SUB][4], s2[NR][SUB][4];
 #pragma unroll
@@ -379,7 +401,8 @@ __global__ void __launch_bounds__(Pr<HD, NR, QF32, Q8, CL>::NT, 1)
               uint32_t r[2][4];
 #pragma unroll
               for (int i = 0; i < 2; ++i)
-                pr_ldsm(r[i], at + place<ROW, false>(sub * 16 + i * 8 + (lane & 7), k2 * 4 + (lane >> 3)));
+                pr_ldsm(r[i], kByXor<ROW> ? (kat ^ (k2 << 6)) + (sub * 16 + i * 8) * ROW
+                                          : at + place<ROW, false>(sub * 16 + i * 8 + (lane & 7), k2 * 4 + (lane >> 3)));
               product(sub, 2 * k2, r[0][0], r[1][0], r[0][1], r[1][1]);
               product(sub, 2 * k2 + 1, r[0][2], r[1][2], r[0][3], r[1][3]);
             }
@@ -392,7 +415,7 @@ __global__ void __launch_bounds__(Pr<HD, NR, QF32, Q8, CL>::NT, 1)
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 const int pos = sub * 16 + i * 8 + g;
-                const uint4 q = pr_lds16(at + place<ROW, true>(pos, t + 4 * j));
+                const uint4 q = pr_lds16(kByXor<ROW> ? (kat ^ (j << 6)) + (sub * 16 + i * 8) * ROW : at + place<ROW, true>(pos, t + 4 * j));
                 uint16_t d;
                 asm volatile("ld.shared.u16 %0, [%1];"
                              : "=h"(d)
@@ -502,7 +525,7 @@ __global__ void __launch_bounds__(Pr<HD, NR, QF32, Q8, CL>::NT, 1)
 #pragma unroll
             for (int i = 0; i < PIECES / 2; ++i) {
               uint32_t r[4];
-              pr_ldsm_t(r, at + GP * ROW + place<ROW, false>(sub * 16 + vr, 2 * i + (lane >> 4)));
+              pr_ldsm_t(r, kByXor<ROW> ? (vat ^ (i << 5)) + sub * 16 * ROW : at + GP * ROW + place<ROW, false>(sub * 16 + vr, 2 * i + (lane >> 4)));
               if (!Q8) {
                 if (decltype(cleaning)::value) {
 #pragma unroll
