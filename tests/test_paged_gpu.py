@@ -107,6 +107,24 @@ def test_single_tokens_of_every_type(f32, q8, hd, seqs):
     check(Dev(c).attend(q, 10, 100, 3), c, q, 10, 100, 3)
 
 
+@pytest.mark.parametrize("rows", [1, 7, 8, 9, 16, 17, 24, 25, 31, 32, 33, 64])
+@pytest.mark.parametrize("hd", [64, 128, 192, 256])
+@pytest.mark.parametrize("q8", [False, True], ids=["f16", "q8"])
+@pytest.mark.parametrize("f32", [False, True], ids=["qf16", "qf32"])
+def test_row_counts(f32, q8, hd, rows):
+    """Around every number of query rows that a kernel takes at once, few and many items, as one token and as a draft
+    whose last rows see more than its first."""
+    for seqs in (1, 6):
+        total = [40 + (613 * (i + 1)) % 700 for i in range(seqs)]
+        c = ref.Cache([1] * seqs, total, 2, hd, 16, q8, seed=rows + hd)
+        q = queries(c, 2 * rows, 47, f32)
+        check(Dev(c).attend(q, 2 * rows), c, q, 2 * rows)
+        c = ref.Cache([rows] + [1] * (seqs - 1), [rows + 33] + total[1:], 2, hd, 16, q8, seed=rows + hd + 1)
+        q = queries(c, 2, 48, f32)
+        check(Dev(c).attend(q, 2), c, q, 2)
+        check(Dev(c).attend(q, 2, 20, 2), c, q, 2, 20, 2)
+
+
 @pytest.mark.parametrize("new,total", [(1, 1), (2, 2), (31, 31), (32, 33), (33, 200), (64, 64), (65, 130), (127, 300), (128, 128), (129, 129), (200, 777), (257, 1025)])
 @pytest.mark.parametrize("q8", [False, True], ids=["f16", "q8"])
 def test_chunk_lengths(new, total, q8):
