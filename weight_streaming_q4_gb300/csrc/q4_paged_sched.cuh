@@ -194,7 +194,8 @@ __device__ __forceinline__ CtaWork warp_work(const PagedAttnArgs& a) {
   w.per = units_per_cta(total);
   // With no more items than CTAs and none much longer than an even share, an item each: nothing to join, and
   // one start and end per CTA instead of two.  16 sequences under a window, 33 tiles an item where an even share is
-  // 28: 13.7 us against 17.0; 10 sequences of 4000 positions, 125 tiles and 66: 38.7 against 34.0.
+  // 28: 12.0 us against 15.8; 16 sequences of 1000 positions, 32 and 27: 16.1 against 18.4; 10 of 4000, 125 and 66,
+  // are split: an item each takes 34.2 against 32.2.
   const int items = __shfl_sync(~0u, tiles_end, 31) * a.kv.n_kv;
   most = __reduce_max_sync(~0u, tiles > kLaneTiles ? 0x3fffffff : most);
   if (items <= static_cast<int>(gridDim.x) && items > 0 && most <= w.per + w.per / 2) {

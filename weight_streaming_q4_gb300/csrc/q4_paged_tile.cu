@@ -34,6 +34,13 @@
 // parts (22 bits; two products into the same S); P is rounded to binary16
 // (2^-11 relative, the output's own rounding again), the sum l is taken of the
 // unrounded weights.
+//
+// Measured: 2048 tokens of the 8B heads over 16384 positions 349 us, 1480 TFLOP/s, 77 %
+// of a library matrix product's rate; the scores -> weights -> product chain of one
+// query tile that the other one does not cover bounds it (tensor pipe 65 % busy), and power.  512
+// tokens of the 70B heads over 8192 positions of Q8 137 us, 970 TFLOP/s: the conversion
+// shares the issue slots with the softmax.  Eight ragged sequences of up to 2049 tokens 183 us,
+// 793 TFLOP/s: outputs 23 us of it, cleaning 14 (each by leaving it out).
 #include <cuda_fp16.h>
 #include <math.h>
 #include <stdint.h>
