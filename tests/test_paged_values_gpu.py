@@ -1,0 +1,85 @@
+"""q4_attn_paged where values are not finite or numbers are far from one, against paged_ref.py in 64 bits."""
+import numpy as np
+import pytest
+
+import paged_ref as ref
+import weight_streaming_q4_gb300 as q4
+from test_paged_gpu import Dev, check, queries
+from weight_streaming_q4_gb300 import build
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build.build()
+    yield
+    assert q4.q4_device_status() == 0, "a kernel wait failed"
+
+
+def put(c, s, t, kind, name="v", block=1):
+    """Block `block` of every head of sequence s's position t: NaN throughout, or infinities of both signs."""
+    p, slot, at = c.table[s, t // c.page], t % c.page, slice(32 * block, 32 * block + 32)
+    sign = np.where(np.arange(32) % 2, 1, -1)
+    if not c.q8:
+        c.pages[name][p, :, slot, at] = np.nan if kind == "nan" else sign * np.inf
+    else:
+        c.scales[name][p, :, slot, block] = np.nan if kind == "nan" else 6e4
+        c.pages[name][p, :, slot, at] = 0 if kind == "nan" else 100 * sign      # f16(100 * 6e4) is infinite
+
+
+def both_kernels(c, q, n_q, window=0, sinks=0):
+    """The kernel of few rows and that of many: which one runs must not show.  (An infinite bound takes any number, so
+    what is not finite has to be the same besides.)"""
+    want, _ = c.attend(q, n_q, window, sinks)
+    odd = ~np.isfinite(want)
+    odd[:c.starts[0]] = odd[c.starts[-1]:] = False      # rows of no sequence
+    for max_new in (1, 300):
+        got = Dev(c, max_new=max_new).attend(q, n_q, window, sinks)
+        check(got, c, q, n_q, window, sinks)
+        assert np.array_equal(got[:, :n_q * c.hd][odd], want[odd], equal_nan=True)
+
+
+@pytest.mark.parametrize("kind", ["nan", "inf"])
+@pytest.mark.parametrize("q8", [False, True], ids=["f16", "q8"])
+@pytest.mark.parametrize("hd", [64, 128, 192, 256])
+@pytest.mark.parametrize("chunk", [1, 5, 150])
+def test_a_hole_beside_a_value_that_all_rows_see(chunk, hd, q8, kind):
+    """A page missing from a key tile that every row sees whole, and a value in it that is not finite."""
+    c = ref.Cache([chunk, 1], [chunk + 300, 40], 1, hd, 16, q8, seed=hd + chunk, n_tokens=chunk + 1)
+    c.table[0, 3] = -1
+    put(c, 0, 2, kind)
+    put(c, 0, 70, kind, block=0)
+    q = queries(c, 3, 50, False, scale=0.5)
+    want, _ = c.attend(q, 3)
+    assert not np.isfinite(want[:chunk, :64]).any() and np.isfinite(want[chunk:]).all()
+    both_kernels(c, q, 3)
+
+
+@pytest.mark.parametrize("kind", ["nan", "inf"])
+@pytest.mark.parametrize("q8", [False, True], ids=["f16", "q8"])
+@pytest.mark.parametrize("hd", [64, 128, 192, 256])
+@pytest.mark.parametrize("chunk", [1, 5, 150])
+def test_values_that_some_rows_see(chunk, hd, q8, kind):
+    """Of blocks that are not finite, every row gets what those it sees make of it: at the causal edge, at a window's, among the
+    sinks, and in no row's sight (stale slots, positions between the sinks and the window)."""
+    total = chunk + 300
+    c = ref.Cache([chunk, 1], [total, 50], 1, hd, 16, q8, seed=hd + chunk + 1, n_tokens=chunk + 1)
+    for t in range(total, -(-total // 16) * 16):       # slots behind the last position
+        put(c, 0, t, kind)
+        put(c, 0, t, kind, name="k", block=0)
+    put(c, 0, total - 1, kind)                         # the last token alone
+    put(c, 0, total - 1 - chunk // 2, kind, block=0)   # half of the tokens
+    q = queries(c, 3, 51, True, scale=0.5)
+    both_kernels(c, q, 3)
+    if chunk > 1:
+        put(c, 0, total - 1, "nan", name="k")          # a score: the last token's row
+        got = Dev(c).attend(q, 3)
+        assert np.isnan(got[chunk - 1]).all() and np.isfinite(got[:chunk - 1 - chunk // 2]).all()
+    c = ref.Cache([chunk], [total], 1, hd, 16, q8, seed=hd + chunk + 2)
+    put(c, 0, 1, kind)                                 # a sink
+    put(c, 0, 40, kind)                                # between sinks and window
+    put(c, 0, total - 64 - chunk // 2 - 1, kind, block=0)    # only the first tokens' windows reach it
+    both_kernels(c, queries(c, 3, 52, False, scale=0.5), 3, 64, 3)
+    put(c, 0, 1, "nan", block=0)
+    both_kernels(c, queries(c, 3, 53, False, scale=0.5), 3, 64, 1)

@@ -735,6 +735,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
         for (int i = w.i0; i < w.i1; ++i) {
           const TileView tv = tile_view<BN>(a, w.it, i);
           const int last = w.it.p1 - tv.base, first = a.window ? max(w.it.p0, 0) - a.window + 1 - tv.base : 0, sk = a.sinks - tv.base;
+          const int all_last = w.it.p0 - tv.base, all_first = a.window ? w.it.p1 - a.window + 1 - tv.base : 0;
 #pragma unroll 1
           for (int kv = 0; kv < 2; ++kv, ++n) {
             const uint32_t slot = n % NS;
@@ -774,14 +775,17 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
                 q8_values4(odd ? codes[y].x : codes[y].z, d, h[4], h[5]);
                 q8_values4(odd ? codes[y].y : codes[y].w, d, h[6], h[7]);
                 if (decltype(cleaning)::value) {
-                  if (((there >> (row >> 4)) & 1) && row <= last && (row >= first || row < sk)) {
+                  // as binary16's: what every row sees stays as it is (add_taken_out passes over a tile of such positions
+                  // alone, holes or not)
+                  const bool in = (there >> (row >> 4)) & 1, all = in && row <= all_last && (row >= all_first || row < sk);
+                  if (!all && in && row <= last && (row >= first || row < sk)) {
                     uint32_t* b = reinterpret_cast<uint32_t*>(u);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                       if ((b[e] & 0x7c00u) == 0x7c00u) b[e] &= 0xffff0000u, found = true;
                       if ((b[e] & 0x7c000000u) == 0x7c000000u) b[e] &= 0x0000ffffu, found = true;
                     }
-                  } else {
+                  } else if (!all) {
                     u[0] = u[1] = make_uint4(0, 0, 0, 0);
                   }
                 }
