@@ -83,3 +83,15 @@ def test_values_that_some_rows_see(chunk, hd, q8, kind):
     both_kernels(c, queries(c, 3, 52, False, scale=0.5), 3, 64, 3)
     put(c, 0, 1, "nan", block=0)
     both_kernels(c, queries(c, 3, 53, False, scale=0.5), 3, 64, 1)
+
+
+@pytest.mark.parametrize("q8", [False, True], ids=["f16", "q8"])
+def test_many_items_that_some_rows_see_infinities_in(q8):
+    """Long runs of items of few rows between items of two query tiles, each with values that are not finite for its last token."""
+    new = [40 if s % 11 == 0 else 1 + s % 2 for s in range(1500)]
+    c = ref.Cache(new, [n + s % 60 for s, n in enumerate(new)], 2, 64, 16, q8, seed=60)
+    for s, n in enumerate(c.total):
+        if s % 3:
+            put(c, s, n - 1, "nan" if s % 2 else "inf", block=s % 2)
+    q = queries(c, 16, 54, False, scale=0.5)
+    both_kernels(c, q, 16)

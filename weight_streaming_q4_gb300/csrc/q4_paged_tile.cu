@@ -206,9 +206,12 @@ struct PtCtl {
   uint64_t done;           // every product is done
   uint32_t tmem;
   int dead;
-  int bad[8];              // segment number (+ 1) in whose values the loaders met infinities or NaN, by number mod 8
+  // Where the loaders met infinities or NaN among a segment's values: per query tile its own count of the segments in
+  // which it has rows (+ 1), by count mod 8.  A value tile's place in the ring is free only when every query tile with
+  // rows has used it, so the loaders are at most five key tiles, and five of a query tile's own segments, ahead of
+  // its softmax.  (Any number of segments without rows of the second query tile may pass while that one ends an item.)
+  int bad[2][8];
   uint32_t there[8];       // per key tile, by number mod 8: bit g = rows 16 g .. of the tile are in a page
-                           // (the loaders are at most five key tiles and five segments ahead of the softmax)
   CtaWork work;
   long long scan[17];
 };
@@ -308,7 +311,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
     }
     mbar_init(&c->raw, 1), mbar_init(&c->raw_free, G::CONV), mbar_init(&c->done, 1);
     c->dead = 0;
-    for (int i = 0; i < 8; ++i) c->bad[i] = 0;
+    for (int i = 0; i < 16; ++i) c->bad[i >> 3][i & 7] = 0;
     fence_mbar_init();
   }
   if (warp == G::W_MMA) tm_alloc(&c->tmem, 512);
@@ -335,7 +338,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
     const uint32_t t_s = tmem + q * 128 + (static_cast<uint32_t>(wl * 32) << 16);
     const uint32_t t_o = tmem + G::O_COL + q * 128 + (static_cast<uint32_t>(wl * 32) << 16);
     uint32_t n_s = 0;       // S tiles seen: parity of s_full, and of the product before it
-    int seg = 0;
+    int seg = 0;            // segments in which this query tile had rows
     uint32_t n_k = 0;       // key tiles of the CTA before the current one
     // The queries of this tile of an item into shared memory: the warp's 32 rows,
     // 16-byte pieces of a row side by side.  The products that read the last ones
@@ -495,7 +498,6 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
       if (!active) {
         if (next.live()) loaded_q(next);
         w = next;
-        ++seg;
         continue;
       }
       // the item's (or the part's) end
@@ -503,7 +505,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
       tm_after();
       if (next.live()) loaded_q(next);
       const bool whole_item = w.i0 == 0 && w.i1 == w.it.cnt;
-      const bool bad = *reinterpret_cast<volatile int*>(&c->bad[seg & 7]) == seg + 1;
+      const bool bad = *reinterpret_cast<volatile int*>(&c->bad[q][seg & 7]) == seg + 1;
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const int slot = w.i0 == 0 ? 1 : 0;
       // A thread holds a row, but stores go out with four lanes to a row, over shared memory: 64 bytes of
@@ -583,6 +585,11 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
       if (a.window && t + (1 << bl) <= max(g.it.p0, 0) - a.window + 1 && t >= a.sinks) return -1;
       return paged_row(a.kv, a.b, g.seq, t, g.head);
     };
+    // Values of the walk's segment were not finite; seg: the segments so far in which each query tile had rows.
+    auto note_bad = [&](const SegmentWalk<R, BN>& g, const int (&seg)[2]) {
+      *reinterpret_cast<volatile int*>(&c->bad[0][seg[0] & 7]) = seg[0] + 1;
+      if (g.rows() > 128) *reinterpret_cast<volatile int*>(&c->bad[1][seg[1] & 7]) = seg[1] + 1;
+    };
     // bit r / 16: rows r .. of the tile are in a page (and seen)
     auto there_of = [&](int row) {
       const int at = __shfl_sync(~0u, row, (((lane & 7) << 4) >> bl) * COLS);
@@ -618,8 +625,8 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
     } else if (!Q8) {   // (warps 9 and 10)
       // value tiles to be cleaned
       uint32_t n = 1;
-      int seg = 0;
-      for (; w.live(); w.next(a), ++seg) {
+      int seg[2] = {0, 0};
+      for (; w.live(); ++seg[0], seg[1] += w.rows() > 128, w.next(a)) {
         for (int i = w.i0; i < w.i1; ++i, n += 2) {
           pt_wait_warp(c, &c->full[n % NS], (n / NS) & 1);
           const TileView tv = tile_view<BN>(a, w.it, i);
@@ -686,7 +693,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
                 *piece(x) = make_uint4(0, 0, 0, 0);
             }
           }
-          if (found) *reinterpret_cast<volatile int*>(&c->bad[seg & 7]) = seg + 1;
+          if (found) note_bad(w, seg);
           fence_async();
           __syncwarp();
           if (lane == 0) mbar_arrive(&c->fixed[n % NS]);
@@ -730,8 +737,8 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
       constexpr int PIECES = BN * HD / 16;               // 16 codes each
       const char* const raw = tiles + G::QALL + NS * G::KB;
       uint32_t n = 0;                                    // tiles stored (keys and values)
-      int seg = 0;
-      for (; w.live(); w.next(a), ++seg) {
+      int seg[2] = {0, 0};
+      for (; w.live(); ++seg[0], seg[1] += w.rows() > 128, w.next(a)) {
         for (int i = w.i0; i < w.i1; ++i) {
           const TileView tv = tile_view<BN>(a, w.it, i);
           const int last = w.it.p1 - tv.base, first = a.window ? max(w.it.p0, 0) - a.window + 1 - tv.base : 0, sk = a.sinks - tv.base;
@@ -799,7 +806,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
               convert(std::true_type{});
             else
               convert(std::false_type{});
-            if (found) *reinterpret_cast<volatile int*>(&c->bad[seg & 7]) = seg + 1;
+            if (found) note_bad(w, seg);
             fence_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(&c->full[slot]);
