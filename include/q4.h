@@ -587,7 +587,10 @@ int q4_paged_read(const q4_paged_kv *kv, const q4_paged_batch *batch, void *k, v
  * The first call on a device makes the kernels ready (before any stream
  * capture).  Runs of the same arrays give the same bits.
  * Error bound, with S_t = sum |q k_t| / sqrt(head_dim) and w = softmax(s):
- * |out - exact| <= (2^-10 + 2^-19 max S_t) sum w|v| + (positions) 2^-25 max|v| + 2^-24.
+ * |out - exact| <= (2^-10 + 2^-19 max S_t) sum w|v| + (positions) 2^-25 max|v| + 2^-24;
+ * with fp32 queries, of which a product takes 22 bits or 2^-39 of the largest
+ * element of the query's row, T_t = max|q| sum|k_t| / sqrt(head_dim) adds
+ * 2^-38 max T_t to the bracket.
  * Errors: Q4_ERR_ARG, Q4_ERR_ALIGN, Q4_ERR_OOM, Q4_ERR_CUDA.
  */
 int q4_attn_paged(const q4_paged_kv *kv, const q4_paged_batch *batch, const void *q, int q_type, int64_t q_ld,

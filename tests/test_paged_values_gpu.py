@@ -95,3 +95,27 @@ def test_many_items_that_some_rows_see_infinities_in(q8):
             put(c, s, n - 1, "nan" if s % 2 else "inf", block=s % 2)
     q = queries(c, 16, 54, False, scale=0.5)
     both_kernels(c, q, 16)
+
+
+@pytest.mark.parametrize("q8", [False, True], ids=["f16", "q8"])
+@pytest.mark.parametrize("hd", [64, 128, 192, 256])
+@pytest.mark.parametrize("rows", [4, 12, 20, 28, 160])
+def test_small_fp32_queries_against_large_keys(rows, hd, q8):
+    """Queries whose last bits lie far below binary16's smallest number, against keys near its largest: 22 bits of a query count
+    whatever its size.  Heads of one item are of sizes from 1 down to fp32's subnormal numbers, and zero."""
+    c = ref.Cache([rows // 2, 1], [rows // 2 + 200, 90], 1, hd, 16, seed=hd + rows, n_tokens=rows // 2 + 1)
+    half = np.where(np.arange(hd) < hd // 2, 1, -1)
+    k = 6e4 * half * c.rng.choice([-1, 1], size=(c.n_pages, 1, 16, 1)) * np.exp2(-c.rng.integers(0, 3, size=(c.n_pages, 1, 16, 1)))
+    if q8:
+        c.q8 = True
+        v = c.pages["v"].astype(np.float32)
+        (c.pages["k"], c.scales["k"]), (c.pages["v"], c.scales["v"]) = ref.quantise(k.astype(np.float32)), ref.quantise(v)
+    else:
+        c.pages["k"] = k.astype(np.float16)
+    # 2^-12 and 0.49 or 0.51 steps of binary16's smallest number: errors of one sign along a key, were the rest rounded to such steps
+    one = 2.0 ** -12 + np.where(half > 0, 0.49, 0.51) * 2.0 ** -24
+    size = np.exp2(-(np.arange(c.n_tokens * 2) % 7) * (np.arange(c.n_tokens * 2) % 3)).reshape(c.n_tokens, 2, 1)
+    size[1::5, 1], size[2::5, 0], size[3::5, 1], size[4::5, 0] = 2.0 ** 12, 0.0, 2.0 ** -130, 2.0 ** 20
+    q = (one * size).astype(np.float32).reshape(c.n_tokens, 2 * hd)
+    check(Dev(c).attend(q, 2), c, q, 2)
+    both_kernels(c, q, 2)

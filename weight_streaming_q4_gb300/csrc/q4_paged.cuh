@@ -88,6 +88,31 @@ __device__ __forceinline__ void q8_values4(uint32_t codes, __half2 d, __half2& l
   hi = __hmul2(q8_pair(b, 0x4342), d);
 }
 
+// fp32 queries enter the products as two binary16 parts, of the query times a power of two that brings its largest
+// element to 2^14 .. 2^15: 22 bits of every element, or 2^-39 of the largest one (the first part rounds to 11 bits, the
+// second to 11 more or to binary16's smallest step).  Without it a query of elements near 2^-12 would keep 12 bits.  A
+// row's scores are scaled back with the softmax's constant.
+struct QueryScale {
+  float up, down;
+  // most: the bits of the row's largest |element|.  A row with an infinity or a NaN stays as it is.
+  __device__ __forceinline__ explicit QueryScale(uint32_t most) {
+    const int top = static_cast<int>(most >> 23);
+    const int e = top == 255 ? 0 : min(141 - top, 100);       // (both factors stay normal numbers, and with it the scale)
+    up = __int_as_float((127 + e) << 23);
+    down = __int_as_float((127 - e) << 23);
+  }
+};
+__device__ __forceinline__ uint32_t abs_bits(float2 f) {
+  return max(__float_as_uint(f.x) & 0x7fffffffu, __float_as_uint(f.y) & 0x7fffffffu);
+}
+// The two parts of a pair.
+__device__ __forceinline__ void query_parts(float2 f, float up, __half2* hi, __half2* lo) {
+  f.x *= up, f.y *= up;
+  *hi = __floats2half2_rn(f.x, f.y);
+  const float2 b = __half22float2(*hi);
+  *lo = __floats2half2_rn(f.x - b.x, f.y - b.y);
+}
+
 // Launchers (q4_paged_cache.cu).
 cudaError_t paged_write_launch(const PagedKv& kv, const PagedBatch& b, const void* k, const void* v, bool f32,
                                int64_t ld, bool q8, cudaStream_t s);

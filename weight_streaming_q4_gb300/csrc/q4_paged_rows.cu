@@ -15,7 +15,7 @@
 // group of 4 or 8 query heads fills it, where a tcgen05 operand has 128 rows (with the query rows as
 // the 16, half of products, weights and output registers of such a group were zeros: 64
 // sequences of the 70B heads over Q8 175 us, so 133 at that step).  The scores' registers become the weights'
-// operand by one 8 x 8 transposition each.  fp32 queries enter as two binary16 parts.
+// operand by one 8 x 8 transposition each.  fp32 queries enter as two binary16 parts of a scaled row (QueryScale).
 // Q8 pages stay codes in shared memory: a lane's 16 codes of a key are its share
 // of four instructions (the order of head_dim in the product is free, the
 // queries follow it), a transposed matrix load of value codes holds two columns of one
@@ -81,6 +81,7 @@ struct PrCtl {
   long long scan[17];
   int bad;                 // segment number + 1 in whose partly seen values a warp met infinities or NaN
   uint32_t there[16][8];   // per warp and stage: bit i = positions 16 i .. of the group are in a page
+  alignas(8) float scale[32];      // fp32 queries: what a row's scores are multiplied by
 };
 static_assert(sizeof(PrCtl) <= 1024, "control data fits its place");
 
@@ -324,30 +325,58 @@ __global__ void __launch_bounds__(Pr<HD, NR, QF32, Q8, CL>::NT, 1)
       enter();
     }
     // queries in operand order: lane (g, t) of product ks holds row g
-    for (int x = tid; x < NR * KS * 32; x += G::NT) {
-      const int nr = x / (KS * 32), ks = x / 32 % KS, xl = x & 31, xt = xl & 3, rr = nr * 8 + (xl >> 2);
-      const int e0 = Q8 ? (xt + 4 * (ks >> 2)) * 16 + 4 * (ks & 3) : ks * 16 + xt * 2;
-      uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
-      if (rr < rows) {
-        const int64_t at = a.row_at(w.sp.t0, w.head, row0 + rr, a.q_ld) + e0;
+    constexpr int RW = QF32 ? (R + W - 1) / W : 1;       // fp32: a warp per row, whose largest element it needs (QueryScale)
+    float2 qf[RW][HD / 64];                              // element pairs j * 64 + 2 * lane
+    if constexpr (QF32) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int64_t e = at + i * (Q8 ? 2 : 8);
-          if (QF32) {
-            const float2 f = __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(a.q) + e));
-            const __half2 h = __floats2half2_rn(f.x, f.y);
-            const float2 b = __half22float2(h);
-            hi[i] = as_u32(h);
-            lo[i] = as_u32(__floats2half2_rn(f.x - b.x, f.y - b.y));
-          } else {
-            hi[i] = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const __half*>(a.q) + e));
-          }
+      for (int k = 0; k < RW; ++k) {
+        const int rr = k * W + warp;
+        const int64_t at = rr < rows ? a.row_at(w.sp.t0, w.head, row0 + rr, a.q_ld) + lane * 2 : -1;
+#pragma unroll
+        for (int j = 0; j < HD / 64; ++j) {
+          qf[k][j] = make_float2(0.f, 0.f);
+          if (at >= 0) qf[k][j] = __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(a.q) + at + j * 64));
         }
       }
-      if constexpr (QF32)
-        s_q[x] = make_uint4(hi[0], hi[1], lo[0], lo[1]);
-      else
+    } else {
+      for (int x = tid; x < NR * KS * 32; x += G::NT) {
+        const int nr = x / (KS * 32), ks = x / 32 % KS, xl = x & 31, xt = xl & 3, rr = nr * 8 + (xl >> 2);
+        const int e0 = Q8 ? (xt + 4 * (ks >> 2)) * 16 + 4 * (ks & 3) : ks * 16 + xt * 2;
+        uint32_t hi[2] = {0, 0};
+        if (rr < rows) {
+          const int64_t at = a.row_at(w.sp.t0, w.head, row0 + rr, a.q_ld) + e0;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            hi[i] = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const __half*>(a.q) + at + i * (Q8 ? 2 : 8)));
+        }
         s_q[x] = make_uint2(hi[0], hi[1]);
+      }
+    }
+    if (CL || seg == 0) {
+#pragma unroll 1
+      for (int i = 0; i < NS - 1; ++i) copy();
+    }
+    if constexpr (QF32) {      // (after the copies are on their way: it waits for the queries)
+#pragma unroll
+      for (int k = 0; k < RW; ++k) {
+        const int rr = k * W + warp;
+        uint32_t most = 0;
+#pragma unroll
+        for (int j = 0; j < HD / 64; ++j) most = max(most, abs_bits(qf[k][j]));
+        const QueryScale qs(__reduce_max_sync(~0u, most));
+        if (rr >= R) break;
+        if (lane == 0) c->scale[rr] = a.scale * qs.down;
+        uint32_t* const to = reinterpret_cast<uint32_t*>(s_q + rr / 8 * KS * 32 + rr % 8 * 4);
+#pragma unroll
+        for (int j = 0; j < HD / 64; ++j) {
+          const int e = j * 64 + lane * 2, in = e & 15;
+          const int ks = Q8 ? e / 64 * 4 + in / 4 : e / 16, xt = Q8 ? e / 16 & 3 : in / 2 & 3, i = Q8 ? in / 2 & 1 : in / 8;
+          __half2 hi, lo;
+          query_parts(qf[k][j], qs.up, &hi, &lo);
+          to[(ks * 32 + xt) * 4 + i] = as_u32(hi);
+          to[(ks * 32 + xt) * 4 + i + 2] = as_u32(lo);
+        }
+      }
     }
     // of this lane's rows 2t, 2t + 1 of every 8
     int p[NR][2];              // positions
@@ -364,10 +393,6 @@ __global__ void __launch_bounds__(Pr<HD, NR, QF32, Q8, CL>::NT, 1)
 #pragma unroll
       for (int n = 0; n < KS; ++n) o[nr][n][0] = o[nr][n][1] = o[nr][n][2] = o[nr][n][3] = 0.f;
     }
-    if (CL || seg == 0) {
-#pragma unroll 1
-      for (int i = 0; i < NS - 1; ++i) copy();
-    }
     __syncthreads();           // queries are there
     u.count();
     bool found = false;
@@ -376,6 +401,16 @@ __global__ void __launch_bounds__(Pr<HD, NR, QF32, Q8, CL>::NT, 1)
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) qr[G::QREG ? ks : 0] = s_q[ks * 32 + lane];
     }
+    float scale[NR][2];        // of this lane's rows' scores
+    auto scales = [&]() {
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr) {
+        scale[nr][0] = scale[nr][1] = a.scale;
+        if (QF32)
+          asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(scale[nr][0]), "=f"(scale[nr][1]) : "r"(smem_u32(&c->scale[nr * 8 + 2 * t])));
+      }
+    };
+    scales();
     for (u.g = warp; u.g < u.n; u.g += W) {
       copy();
       pr_wait<NS - 1>();
@@ -461,6 +496,7 @@ __global__ void __launch_bounds__(Pr<HD, NR, QF32, Q8, CL>::NT, 1)
             }
         }
         // ---- weights
+        if (QF32 && NR > 1) scales();        // (loaded again: kept in registers, they spill)
         // (a row's maximum is wanted of all lanes only when one of them has raised it)
         float top[NR][2];
         bool raise = false;
@@ -471,7 +507,7 @@ __global__ void __launch_bounds__(Pr<HD, NR, QF32, Q8, CL>::NT, 1)
             float x = -INFINITY;
 #pragma unroll
             for (int e = h; e < 4 * SUB; e += 2) x = fmaxf(x, s[nr][e >> 2][e & 3]);
-            x *= a.scale;
+            x *= scale[nr][h];
             top[nr][h] = x;
             raise |= x > m[nr][h] + 8.f || (m[nr][h] == -INFINITY && x > m[nr][h]);
           }
@@ -501,8 +537,8 @@ __global__ void __launch_bounds__(Pr<HD, NR, QF32, Q8, CL>::NT, 1)
           for (int h = 0; h < 2; ++h) mm[h] = m[nr][h] == -INFINITY ? 0.f : m[nr][h];
 #pragma unroll
           for (int e = 0; e < 4 * SUB; e += 2) {
-            const float w0 = pr_exp2(fmaf(s[nr][e >> 2][e & 3], a.scale, -mm[0]));
-            const float w1 = pr_exp2(fmaf(s[nr][e >> 2][(e & 3) + 1], a.scale, -mm[1]));
+            const float w0 = pr_exp2(fmaf(s[nr][e >> 2][e & 3], scale[nr][0], -mm[0]));
+            const float w1 = pr_exp2(fmaf(s[nr][e >> 2][(e & 3) + 1], scale[nr][1], -mm[1]));
             l[nr][0] += w0, l[nr][1] += w1;
             pw[nr][e >> 2][(e >> 1) & 1] = pr_transposed(as_u32(__floats2half2_rn(w0, w1)));
           }

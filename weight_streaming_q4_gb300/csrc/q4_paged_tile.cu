@@ -31,7 +31,7 @@
 // it added at the end.  Keys need no cleaning: their scores are replaced.
 //
 // Precision: binary16 queries enter as they are, fp32 queries as two binary16
-// parts (22 bits; two products into the same S); P is rounded to binary16
+// parts (22 bits of a scaled row, QueryScale; two products into the same S); P is rounded to binary16
 // (2^-11 relative, the output's own rounding again), the sum l is taken of the
 // unrounded weights.
 //
@@ -340,6 +340,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
     uint32_t n_s = 0;       // S tiles seen: parity of s_full, and of the product before it
     int seg = 0;            // segments in which this query tile had rows
     uint32_t n_k = 0;       // key tiles of the CTA before the current one
+    float scale = a.scale;  // of this thread's row's scores
     // The queries of this tile of an item into shared memory: the warp's 32 rows,
     // 16-byte pieces of a row side by side.  The products that read the last ones
     // are done (their scores have been taken).
@@ -358,27 +359,29 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
           cp16_zfill(s_q + q * G::QB + off, static_cast<const __half*>(a.q) + (at < 0 ? 0 : at + pc * 8), at >= 0);
         }
       } else {
+        // a row at a time, 8 bytes per lane: its largest element is wanted (QueryScale)
 #pragma unroll 8
-        for (int x = lane; x < 32 * PIECES; x += 32) {
-          const int rl = x / PIECES, rr = wl * 32 + rl, pc = x % PIECES;
+        for (int rl = 0; rl < 32; ++rl) {
+          const int rr = wl * 32 + rl;
           const int64_t at = __shfl_sync(~0u, own_at, rl);
-          const uint32_t off = (pc >> 3) * (128 * 128) + rr * 128 + (((pc & 7) ^ (rr & 7)) << 4);
-          uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
-          if (at >= 0) {
-            const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at + pc * 8);
-            const float4 f0 = __ldg(p), f1 = __ldg(p + 1);
-            const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
-            __half2* h = reinterpret_cast<__half2*>(&hi);
-            __half2* l = reinterpret_cast<__half2*>(&lo);
+          float2 f[HD / 64];
+          uint32_t most = 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              h[e] = __floats2half2_rn(f[2 * e], f[2 * e + 1]);
-              const float2 b = __half22float2(h[e]);
-              l[e] = __floats2half2_rn(f[2 * e] - b.x, f[2 * e + 1] - b.y);
-            }
+          for (int j = 0; j < HD / 64; ++j) {
+            f[j] = make_float2(0.f, 0.f);
+            if (at >= 0) f[j] = __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(a.q) + at + j * 64 + lane * 2));
+            most = max(most, abs_bits(f[j]));
           }
-          *reinterpret_cast<uint4*>(tiles + G::QB + off) = lo;
-          *reinterpret_cast<uint4*>(tiles + q * G::QB + off) = hi;
+          const QueryScale qs(__reduce_max_sync(~0u, most));
+          if (lane == rl) scale = a.scale * qs.down;
+          char* const to = tiles + rr * 128 + (((lane >> 2) ^ (rr & 7)) << 4) + (lane & 3) * 4;
+#pragma unroll
+          for (int j = 0; j < HD / 64; ++j) {
+            __half2 hi, lo;
+            query_parts(f[j], qs.up, &hi, &lo);
+            *reinterpret_cast<__half2*>(to + j * (128 * 128)) = hi;
+            *reinterpret_cast<__half2*>(to + G::QB + j * (128 * 128)) = lo;
+          }
         }
       }
     };
@@ -443,7 +446,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
               }
             }
             const float mm = m == -INFINITY ? 0.f : m;
-            const float2 sc2 = make_float2(a.scale, a.scale), mm2 = make_float2(-mm, -mm);
+            const float2 sc2 = make_float2(scale, scale), mm2 = make_float2(-mm, -mm);
             float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
             float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -457,7 +460,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
               x[e / 2] = pack_h2(y.x, y.y);
             }
             sum = f2_add(sum2[0], sum2[1]);
-            const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * a.scale;
+            const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * scale;
             const bool raise = top > m + 8.f || (m == -INFINITY && top > m);
             if (!__any_sync(~0u, raise)) break;
             // raise the warp's maxima and rescale what O and l hold, after the product before this half's
