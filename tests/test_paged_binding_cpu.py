@@ -1,0 +1,66 @@
+"""What the paged calls' binding refuses of tensors (no GPU: host tensors that are taken for the current device's)."""
+import pytest
+
+import weight_streaming_q4_gb300 as q4
+from weight_streaming_q4_gb300 import _lib
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(autouse=True)
+def on_device(monkeypatch):
+    monkeypatch.setattr(_lib, "_on_device", lambda t: True)
+
+
+def refused(f, *args, **kw):
+    with pytest.raises(q4.Q4Error) as e:
+        f(*args, **kw)
+    return e.value.status == q4.Q4_ERR_ARG
+
+
+N_PAGES, PAGE, HEADS, HD = 3, 16, 2, 64
+SHAPE = (N_PAGES, HEADS, PAGE, HD)
+SIZES = (N_PAGES, PAGE, HEADS, HD)
+
+
+def f16(*shape):
+    return torch.zeros(shape, dtype=torch.float16)
+
+
+def i8(*shape):
+    return torch.zeros(shape, dtype=torch.int8)
+
+
+SCALES = SHAPE[:-1] + (HD // 32,)
+
+
+def test_caches_of_their_type_and_size_are_taken():
+    for t in (f16(*SHAPE), f16(*SHAPE).view(torch.int16), f16(N_PAGES + 1, *SHAPE[1:]), f16(N_PAGES * HEADS * PAGE * HD)):
+        kv = q4.PagedKV.of(t, t, *SIZES)
+        assert kv.k_pages == t.data_ptr() and kv.k_scales is None
+    for t in (i8(*SHAPE), i8(*SHAPE).view(torch.uint8)):
+        s = f16(*SCALES)
+        kv = q4.PagedKV.of(t, t, *SIZES, q4.Q4_KV_Q8, s, s)
+        assert kv.v_pages == t.data_ptr() and kv.v_scales == s.data_ptr()
+    assert q4.PagedKV.of(4096, 4096, *SIZES).k_pages == 4096
+
+
+@pytest.mark.parametrize("sizes", [(N_PAGES + 1, PAGE, HEADS, HD), (N_PAGES, 2 * PAGE, HEADS, HD), (N_PAGES, PAGE, HEADS + 1, HD),
+                                   (N_PAGES, PAGE, HEADS, 2 * HD)], ids=str)
+def test_caches_smaller_than_stated_are_refused(sizes):
+    t, big = f16(*SHAPE), f16(2, *SHAPE)
+    assert refused(q4.PagedKV.of, t, big, *sizes) and refused(q4.PagedKV.of, big, t, *sizes)
+    c, bigc, s, bigs = i8(*SHAPE), i8(2, *SHAPE), f16(*SCALES), f16(2, *SCALES)
+    assert refused(q4.PagedKV.of, c, bigc, *sizes, q4.Q4_KV_Q8, bigs, bigs)
+    assert refused(q4.PagedKV.of, bigc, bigc, *sizes, q4.Q4_KV_Q8, s, bigs)
+    assert refused(q4.PagedKV.of, bigc, bigc, *sizes, q4.Q4_KV_Q8, bigs, s)
+
+
+def test_caches_of_another_type_are_refused():
+    t, c, s = f16(*SHAPE), i8(*SHAPE), f16(*SCALES)
+    for bad in (t.bfloat16(), t.float(), c, c.view(torch.uint8)):
+        assert refused(q4.PagedKV.of, bad, t, *SIZES) and refused(q4.PagedKV.of, t, bad, *SIZES)
+    for bad in (t, t.float()):
+        assert refused(q4.PagedKV.of, bad, c, *SIZES, q4.Q4_KV_Q8, s, s) and refused(q4.PagedKV.of, c, bad, *SIZES, q4.Q4_KV_Q8, s, s)
+    for bad in (s.float(), s.bfloat16()):
+        assert refused(q4.PagedKV.of, c, c, *SIZES, q4.Q4_KV_Q8, bad, s) and refused(q4.PagedKV.of, c, c, *SIZES, q4.Q4_KV_Q8, s, bad)

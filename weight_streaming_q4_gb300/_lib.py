@@ -84,15 +84,19 @@ class KVCache(ctypes.Structure):
 
 
 class PagedKV(ctypes.Structure):
-    """q4_paged_kv.  Made once per layer cache; keeps its tensors alive."""
+    """q4_paged_kv.  Made once per layer cache; keeps its tensors alive, which
+    have to be of the cache's type and as large as it (or larger)."""
     _fields_ = [("k_pages", c_p), ("v_pages", c_p), ("k_scales", c_p), ("v_scales", c_p), ("n_pages", c_int),
                 ("page_size", c_int), ("n_kv_heads", c_int), ("head_dim", c_int), ("type", c_int)]
 
     @classmethod
     def of(cls, k_pages, v_pages, n_pages, page_size, n_kv_heads, head_dim, cache_type=Q4_KV_F16, k_scales=None,
            v_scales=None):
-        s = cls(_dev_ptr(k_pages), _dev_ptr(v_pages), _dev_ptr(k_scales), _dev_ptr(v_scales), n_pages, page_size,
-                n_kv_heads, head_dim, cache_type)
+        n = n_pages * n_kv_heads * page_size * head_dim
+        kinds = _CODES if cache_type == Q4_KV_Q8 else _BITS16
+        scales = (_BITS16, n // 32) if cache_type == Q4_KV_Q8 else ()
+        s = cls(_dev_ptr(k_pages, kinds, n), _dev_ptr(v_pages, kinds, n), _dev_ptr(k_scales, *scales),
+                _dev_ptr(v_scales, *scales), n_pages, page_size, n_kv_heads, head_dim, cache_type)
         s._keep = (k_pages, v_pages, k_scales, v_scales)
         return s
 
@@ -105,7 +109,7 @@ class PagedBatch(ctypes.Structure):
 
     @classmethod
     def of(cls, token_starts, kv_lens, page_table, n_seqs, n_tokens, table_width, max_new):
-        s = cls(_dev_ptr(token_starts, 4), _dev_ptr(kv_lens, 4), _dev_ptr(page_table, 4), n_seqs, n_tokens,
+        s = cls(_dev_ptr(token_starts, _INDEX), _dev_ptr(kv_lens, _INDEX), _dev_ptr(page_table, _INDEX), n_seqs, n_tokens,
                 table_width, max_new)
         s._keep = (token_starts, kv_lens, page_table)
         return s
@@ -224,15 +228,24 @@ def _on_device(t) -> bool:
     return t.get_device() == _device()
 
 
-def _dev_ptr(t, itemsize=None):
+# Tensor types that hold binary16 values (or their bits), and Q8 codes.
+_BITS16 = ("torch.float16", "torch.int16", "torch.uint16")
+_CODES = ("torch.int8", "torch.uint8")
+_INDEX = ("torch.int32",)
+
+
+def _dev_ptr(t, kinds=None, n=0):
     """_ptr of a tensor that the kernels can reach: contiguous, on the current
-    CUDA device, of the given element size (an integer is taken as an address)."""
+    CUDA device, of one of the given types and at least n elements (an integer
+    is taken as an address)."""
     if t is None or isinstance(t, int):
         return t
     if not _on_device(t):
         raise Q4Error(Q4_ERR_ARG, f"a tensor on {t.device}, not the current CUDA device")
-    if not t.is_contiguous() or (itemsize and t.element_size() != itemsize):
+    if not t.is_contiguous() or (kinds and str(t.dtype) not in kinds):
         raise Q4Error(Q4_ERR_ARG, f"a {t.dtype} tensor of strides {tuple(t.stride())}")
+    if t.numel() < n:
+        raise Q4Error(Q4_ERR_ARG, f"a tensor of {t.numel()} elements where {n} are meant")
     return t.data_ptr()
 
 
