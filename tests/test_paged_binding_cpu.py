@@ -64,3 +64,29 @@ def test_caches_of_another_type_are_refused():
         assert refused(q4.PagedKV.of, bad, c, *SIZES, q4.Q4_KV_Q8, s, s) and refused(q4.PagedKV.of, c, bad, *SIZES, q4.Q4_KV_Q8, s, s)
     for bad in (s.float(), s.bfloat16()):
         assert refused(q4.PagedKV.of, c, c, *SIZES, q4.Q4_KV_Q8, bad, s) and refused(q4.PagedKV.of, c, c, *SIZES, q4.Q4_KV_Q8, s, bad)
+
+
+def i32(*shape):
+    return torch.zeros(shape, dtype=torch.int32)
+
+
+def test_batches_of_their_sizes_are_taken():
+    for table in (i32(3, 5), i32(4, 5), i32(15)):
+        b = q4.PagedBatch.of(i32(4), i32(3), table, 3, 7, 5, 2)
+        assert b.page_table == table.data_ptr() and b.n_seqs == 3
+    assert q4.PagedBatch.of(i32(2), i32(1), i32(1, 9), 1, 7, 5, 2).table_width == 5       # one row: its first entries
+    assert q4.PagedBatch.of(None, None, None, 0, 0, 1, 0).n_seqs == 0
+    assert q4.PagedBatch.of(i32(0), i32(0), i32(0, 5), 0, 4, 5, 0).n_seqs == 0
+
+
+def test_batches_of_other_sizes_or_types_are_refused():
+    assert refused(q4.PagedBatch.of, i32(3), i32(3), i32(3, 5), 3, 7, 5, 2)
+    assert refused(q4.PagedBatch.of, i32(4), i32(2), i32(3, 5), 3, 7, 5, 2)
+    assert refused(q4.PagedBatch.of, i32(4), i32(3), i32(2, 5), 3, 7, 5, 2)
+    assert refused(q4.PagedBatch.of, i32(4), i32(3), i32(14), 3, 7, 5, 2)
+    assert refused(q4.PagedBatch.of, i32(4), i32(3), i32(3, 6), 3, 7, 5, 2)       # rows 6 apart, read as 5 apart
+    for bad in (torch.float32, torch.int64, torch.int16):
+        assert refused(q4.PagedBatch.of, i32(4).to(bad), i32(3), i32(3, 5), 3, 7, 5, 2)
+        assert refused(q4.PagedBatch.of, i32(4), i32(3).to(bad), i32(3, 5), 3, 7, 5, 2)
+        assert refused(q4.PagedBatch.of, i32(4), i32(3), i32(3, 5).to(bad), 3, 7, 5, 2)
+    assert refused(q4.PagedBatch.of, i32(4), i32(3), i32(5, 3).T, 3, 7, 5, 2)

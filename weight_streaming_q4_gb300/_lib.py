@@ -103,14 +103,18 @@ class PagedKV(ctypes.Structure):
 
 class PagedBatch(ctypes.Structure):
     """q4_paged_batch.  The kernels read the arrays, so one object serves every
-    content of them; keeps its tensors alive."""
+    content of them; keeps its tensors alive, int32 of at least n_seqs + 1,
+    n_seqs and n_seqs * table_width elements."""
     _fields_ = [("token_starts", c_p), ("kv_lens", c_p), ("page_table", c_p), ("n_seqs", c_int), ("n_tokens", c_int),
                 ("table_width", c_int), ("max_new", c_int)]
 
     @classmethod
     def of(cls, token_starts, kv_lens, page_table, n_seqs, n_tokens, table_width, max_new):
-        s = cls(_dev_ptr(token_starts, _INDEX), _dev_ptr(kv_lens, _INDEX), _dev_ptr(page_table, _INDEX), n_seqs, n_tokens,
-                table_width, max_new)
+        n = n_seqs if n_seqs > 0 else -1
+        s = cls(_dev_ptr(token_starts, _INDEX, n + 1), _dev_ptr(kv_lens, _INDEX, n),
+                _dev_ptr(page_table, _INDEX, n * table_width), n_seqs, n_tokens, table_width, max_new)
+        if hasattr(page_table, "dim") and page_table.dim() == 2 and n > 1 and page_table.shape[1] != table_width:
+            raise Q4Error(Q4_ERR_ARG, f"a page table of width {page_table.shape[1]}, not {table_width}")
         s._keep = (token_starts, kv_lens, page_table)
         return s
 
