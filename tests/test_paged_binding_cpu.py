@@ -90,3 +90,66 @@ def test_batches_of_other_sizes_or_types_are_refused():
         assert refused(q4.PagedBatch.of, i32(4), i32(3).to(bad), i32(3, 5), 3, 7, 5, 2)
         assert refused(q4.PagedBatch.of, i32(4), i32(3), i32(3, 5).to(bad), 3, 7, 5, 2)
     assert refused(q4.PagedBatch.of, i32(4), i32(3), i32(5, 3).T, 3, 7, 5, 2)
+
+
+class Lib:
+    """Stands for the library: notes the calls that reach it."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        return lambda *args: self.calls.append((name, args)) or q4.Q4_OK
+
+
+@pytest.fixture()
+def calls(monkeypatch):
+    stub = Lib()
+    monkeypatch.setattr(_lib, "lib", lambda: stub)
+    return stub.calls
+
+
+ROWS, ROW = 5, HEADS * HD
+
+
+def write(x, ld, kind=q4.Q4_TYPE_F32, rows=ROWS, other=4096):
+    kv = q4.PagedKV.of(4096, 4096, *SIZES)
+    b = q4.PagedBatch.of(4096, 4096, 4096, 1, rows, 3, 1)
+    q4.q4_paged_write(kv, b, x, other, kind, ld, stream=0)
+
+
+def test_rows_of_their_layout_are_taken(calls):
+    wide = torch.zeros(ROWS, 4 * ROW)
+    good = [(wide, 4 * ROW), (wide[:, ROW:], 4 * ROW), (wide[:, 3 * ROW:], 4 * ROW), (torch.zeros(ROWS, HEADS, HD), ROW), (torch.zeros(ROWS * ROW), ROW),
+            (torch.zeros(ROWS * HEADS, HD), ROW), (torch.zeros(2 * ROWS, ROW), ROW), (wide.view(ROWS, 4 * HEADS, HD)[:, HEADS:2 * HEADS], 4 * ROW)]
+    for x, ld in good:
+        write(x, ld)
+    for x in (f16(ROWS, ROW), f16(ROWS, ROW).view(torch.int16)):
+        write(x, ROW, q4.Q4_TYPE_F16)
+    write(torch.zeros(1, ROW), 4 * ROW, rows=1)
+    write(wide[:1, :ROW], ROW, rows=1)
+    assert len(calls) == len(good) + 4
+
+
+def test_rows_of_another_type_or_layout_are_refused(calls):
+    x = torch.zeros(ROWS, ROW)
+    for bad in (x.half().bfloat16(), x):
+        assert refused(write, bad, ROW, q4.Q4_TYPE_F16)
+    for bad in (x.half(), x.int(), x.double()):
+        assert refused(write, bad, ROW)
+    wide = torch.zeros(ROWS, 4 * ROW)
+    assert refused(write, torch.zeros(ROW, ROWS).T, ROW)                  # transposed
+    assert refused(write, wide[:, :ROW], ROW)                             # rows 4 * ROW apart
+    assert refused(write, wide, ROW)
+    assert refused(write, torch.zeros(2 * ROWS, ROW)[::2], ROW)
+    assert refused(write, torch.zeros(ROW).expand(ROWS, ROW), ROW)        # one row for all
+    assert refused(write, torch.zeros(ROWS, 2 * ROW)[:, ::2], 2 * ROW)    # values two apart
+    assert refused(write, torch.zeros(ROWS, HD, HEADS).transpose(1, 2), ROW)
+    assert refused(write, torch.zeros(2 * ROWS * ROW)[::2], ROW)
+    assert refused(write, 4096, ROW, other=x.T)
+    kv, b = q4.PagedKV.of(4096, 4096, *SIZES), q4.PagedBatch.of(4096, 4096, 4096, 1, ROWS, 3, 1)
+    assert refused(q4.q4_paged_read, kv, b, 4096, x.T, q4.Q4_TYPE_F32, ROW, stream=0)
+    assert refused(q4.q4_attn_paged, kv, b, x.T, q4.Q4_TYPE_F32, ROW, HEADS, 0, 0, 4096, ROW, 4096, 1 << 30, stream=0)
+    for out in (f16(ROW, ROWS).T, x, x.bfloat16()):
+        assert refused(q4.q4_attn_paged, kv, b, x, q4.Q4_TYPE_F32, ROW, HEADS, 0, 0, out, ROW, 4096, 1 << 30, stream=0)
+    assert not calls

@@ -236,6 +236,7 @@ def _on_device(t) -> bool:
 _BITS16 = ("torch.float16", "torch.int16", "torch.uint16")
 _CODES = ("torch.int8", "torch.uint8")
 _INDEX = ("torch.int32",)
+_F32 = ("torch.float32",)
 
 
 def _dev_ptr(t, kinds=None, n=0):
@@ -253,17 +254,29 @@ def _dev_ptr(t, kinds=None, n=0):
     return t.data_ptr()
 
 
+def _rows_apart(t, rows, ld) -> bool:
+    """Whether a tensor's rows (its first dimension, or all of it) lie ld values apart, each in one piece."""
+    if t.is_contiguous():
+        return rows <= 1 or t.dim() < 2 or t.shape[0] != rows or t.stride(0) == ld
+    if t.dim() == 2:
+        return t.stride(1) == 1 and (rows <= 1 or t.stride(0) == ld)
+    return t.dim() > 2 and t[0].is_contiguous() and (rows <= 1 or t.stride(0) == ld)
+
+
 def _rows_ptr(t, what, rows, row, ld, kind):
     """_ptr of a buffer of ``rows`` rows of ``row`` values, ``ld`` apart: a
     tensor has to be on the current device, of that type, and hold them (a view
-    that starts inside a wider row does: its storage counts)."""
+    that starts inside a wider row does: its storage counts).  Its own rows have
+    to be ld apart; a contiguous tensor of another number of rows is memory."""
     if t is None or isinstance(t, int):
         return t
     size = 4 if kind == Q4_TYPE_F32 else 2
     if not _on_device(t):
         raise Q4Error(Q4_ERR_ARG, f"{what}: a tensor on {t.device}, not the current CUDA device")
-    if t.element_size() != size:
-        raise Q4Error(Q4_ERR_ARG, f"{what}: a {t.dtype} tensor for {size}-byte values")
+    if str(t.dtype) not in (_F32 if kind == Q4_TYPE_F32 else _BITS16):
+        raise Q4Error(Q4_ERR_ARG, f"{what}: a {t.dtype} tensor for {'fp32' if size == 4 else 'binary16'} values")
+    if not _rows_apart(t, rows, ld):
+        raise Q4Error(Q4_ERR_ARG, f"{what}: a tensor of shape {tuple(t.shape)} and strides {tuple(t.stride())} for rows {ld} apart")
     if rows > 0 and t.storage_offset() + (rows - 1) * ld + row > t.untyped_storage().nbytes() // size:
         raise Q4Error(Q4_ERR_ARG, f"{what}: {rows} rows of {row} values {ld} apart do not fit its storage")
     return t.data_ptr()
