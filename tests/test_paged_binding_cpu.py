@@ -153,3 +153,17 @@ def test_rows_of_another_type_or_layout_are_refused(calls):
     for out in (f16(ROW, ROWS).T, x, x.bfloat16()):
         assert refused(q4.q4_attn_paged, kv, b, x, q4.Q4_TYPE_F32, ROW, HEADS, 0, 0, out, ROW, 4096, 1 << 30, stream=0)
     assert not calls
+
+
+def test_a_workspace_smaller_than_stated_is_refused(calls):
+    kv, b = q4.PagedKV.of(4096, 4096, *SIZES), q4.PagedBatch.of(4096, 4096, 4096, 1, ROWS, 3, 1)
+
+    def attend(ws, n):
+        q4.q4_attn_paged(kv, b, torch.zeros(ROWS, ROW), q4.Q4_TYPE_F32, ROW, HEADS, 0, 0, f16(ROWS, ROW), ROW, ws, n, stream=0)
+
+    for ws in (torch.zeros(4095, dtype=torch.uint8), torch.zeros(1023), torch.zeros(0), torch.zeros(64, 128).T):
+        assert refused(attend, ws, 4096)
+    assert not calls
+    for ws in (torch.zeros(4096, dtype=torch.uint8), torch.zeros(1024), 4096):
+        attend(ws, 4096)
+    assert len(calls) == 3

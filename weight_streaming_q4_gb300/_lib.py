@@ -254,6 +254,13 @@ def _dev_ptr(t, kinds=None, n=0):
     return t.data_ptr()
 
 
+def _bytes_ptr(t, n):
+    """_dev_ptr of a workspace of n bytes."""
+    if t is not None and not isinstance(t, int) and t.numel() * t.element_size() < n:
+        raise Q4Error(Q4_ERR_ARG, f"a workspace of {t.numel() * t.element_size()} bytes where {n} are meant")
+    return _dev_ptr(t)
+
+
 def _rows_apart(t, rows, ld) -> bool:
     """Whether a tensor's rows (its first dimension, or all of it) lie ld values apart, each in one piece."""
     if t.is_contiguous():
@@ -482,7 +489,7 @@ def q4_attn_paged(kv: PagedKV, batch: PagedBatch, q, q_type: int, q_ld: int, n_q
     _check(lib().q4_attn_paged(kv, batch, _rows_ptr(q, "q4_attn_paged: q", batch.n_tokens, row, q_ld, q_type), q_type,
                                q_ld, n_q_heads, window, sinks,
                                _rows_ptr(out, "q4_attn_paged: out", batch.n_tokens, row, out_ld, Q4_TYPE_F16), out_ld,
-                               _dev_ptr(workspace), workspace_bytes, _stream(stream)), "q4_attn_paged")
+                               _bytes_ptr(workspace, workspace_bytes), workspace_bytes, _stream(stream)), "q4_attn_paged")
 
 
 def q4_attn_paged_workspace_bytes(n_q_heads: int, n_kv_heads: int, head_dim: int) -> int:
