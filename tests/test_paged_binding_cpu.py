@@ -167,3 +167,24 @@ def test_a_workspace_smaller_than_stated_is_refused(calls):
     for ws in (torch.zeros(4096, dtype=torch.uint8), torch.zeros(1024), 4096):
         attend(ws, 4096)
     assert len(calls) == 3
+
+
+def test_descriptors_of_another_device_than_the_current_one_are_refused(calls, monkeypatch):
+    monkeypatch.setattr(_lib, "_device", lambda: -1)      # (a host tensor's device)
+    t = f16(*SHAPE)
+    kv, b = q4.PagedKV.of(t, t, *SIZES), q4.PagedBatch.of(i32(2), i32(1), i32(1, 3), 1, ROWS, 3, 1)
+    plain = q4.PagedKV.of(4096, 4096, *SIZES), q4.PagedBatch.of(4096, 4096, 4096, 1, ROWS, 3, 1)
+
+    def each(kv, b):
+        return [(q4.q4_paged_write, kv, b, 4096, 4096, q4.Q4_TYPE_F32, ROW), (q4.q4_paged_read, kv, b, 4096, 4096, q4.Q4_TYPE_F32, ROW),
+                (q4.q4_attn_paged, kv, b, 4096, q4.Q4_TYPE_F32, ROW, HEADS, 0, 0, 4096, ROW, 4096, 1 << 30)]
+
+    for f, *args in each(kv, b) + each(*plain):
+        f(*args, stream=0)
+    assert len(calls) == 6
+    monkeypatch.setattr(_lib, "_device", lambda: 1)
+    for f, *args in each(kv, plain[1]) + each(plain[0], b):
+        assert refused(f, *args, stream=0)
+    for f, *args in each(*plain):
+        f(*args, stream=0)
+    assert len(calls) == 9

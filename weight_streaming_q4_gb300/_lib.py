@@ -88,6 +88,7 @@ class PagedKV(ctypes.Structure):
     have to be of the cache's type and as large as it (or larger)."""
     _fields_ = [("k_pages", c_p), ("v_pages", c_p), ("k_scales", c_p), ("v_scales", c_p), ("n_pages", c_int),
                 ("page_size", c_int), ("n_kv_heads", c_int), ("head_dim", c_int), ("type", c_int)]
+    _at = None       # the device of its tensors
 
     @classmethod
     def of(cls, k_pages, v_pages, n_pages, page_size, n_kv_heads, head_dim, cache_type=Q4_KV_F16, k_scales=None,
@@ -98,6 +99,7 @@ class PagedKV(ctypes.Structure):
         s = cls(_dev_ptr(k_pages, kinds, n), _dev_ptr(v_pages, kinds, n), _dev_ptr(k_scales, *scales),
                 _dev_ptr(v_scales, *scales), n_pages, page_size, n_kv_heads, head_dim, cache_type)
         s._keep = (k_pages, v_pages, k_scales, v_scales)
+        s._at = _device_of(*s._keep)
         return s
 
 
@@ -107,6 +109,7 @@ class PagedBatch(ctypes.Structure):
     n_seqs and n_seqs * table_width elements."""
     _fields_ = [("token_starts", c_p), ("kv_lens", c_p), ("page_table", c_p), ("n_seqs", c_int), ("n_tokens", c_int),
                 ("table_width", c_int), ("max_new", c_int)]
+    _at = None
 
     @classmethod
     def of(cls, token_starts, kv_lens, page_table, n_seqs, n_tokens, table_width, max_new):
@@ -116,6 +119,7 @@ class PagedBatch(ctypes.Structure):
         if hasattr(page_table, "dim") and page_table.dim() == 2 and n > 1 and page_table.shape[1] != table_width:
             raise Q4Error(Q4_ERR_ARG, f"a page table of width {page_table.shape[1]}, not {table_width}")
         s._keep = (token_starts, kv_lens, page_table)
+        s._at = _device_of(*s._keep)
         return s
 
 
@@ -215,12 +219,14 @@ _raw_stream = None
 
 
 def _init_current():
+    """Finds them; returns the first."""
     global _device, _raw_stream
     import torch
     torch.cuda.current_stream()
     get, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
     _device = dev or torch.cuda.current_device
     _raw_stream = (lambda: get(dev())) if get and dev else (lambda: torch.cuda.current_stream().cuda_stream)
+    return _device
 
 
 def _on_device(t) -> bool:
@@ -252,6 +258,21 @@ def _dev_ptr(t, kinds=None, n=0):
     if t.numel() < n:
         raise Q4Error(Q4_ERR_ARG, f"a tensor of {t.numel()} elements where {n} are meant")
     return t.data_ptr()
+
+
+def _device_of(*tensors):
+    """The device of the tensors among the arguments, all of it the current one when they were taken (None: addresses)."""
+    for t in tensors:
+        if t is not None and not isinstance(t, int):
+            return t.get_device()
+    return None
+
+
+def _check_device(what, *made):
+    """The descriptors were made on the device that is current now: the kernels run there."""
+    for s in made:
+        if s._at is not None and s._at != (_device or _init_current())():
+            raise Q4Error(Q4_ERR_ARG, f"{what}: tensors on device {s._at}, not the current one")
 
 
 def _bytes_ptr(t, n):
@@ -469,6 +490,7 @@ def q4_kv_append(k, v, k_cache, v_cache, pos, capacity: int, kv_dim: int, stream
 def q4_paged_write(kv: PagedKV, batch: PagedBatch, k, v, kind: int, ld: int, stream=None):
     """The new tokens' keys and values (rows of Q4_TYPE_F32 or Q4_TYPE_F16 values, ld apart) into their pages."""
     row = kv.n_kv_heads * kv.head_dim
+    _check_device("q4_paged_write", kv, batch)
     _check(lib().q4_paged_write(kv, batch, _rows_ptr(k, "q4_paged_write: k", batch.n_tokens, row, ld, kind),
                                 _rows_ptr(v, "q4_paged_write: v", batch.n_tokens, row, ld, kind), kind, ld,
                                 _stream(stream)), "q4_paged_write")
@@ -477,6 +499,7 @@ def q4_paged_write(kv: PagedKV, batch: PagedBatch, k, v, kind: int, ld: int, str
 def q4_paged_read(kv: PagedKV, batch: PagedBatch, k, v, kind: int, ld: int, stream=None):
     """The batch's positions out of their pages into rows of Q4_TYPE_F32 or Q4_TYPE_F16 values, ld apart."""
     row = kv.n_kv_heads * kv.head_dim
+    _check_device("q4_paged_read", kv, batch)
     _check(lib().q4_paged_read(kv, batch, _rows_ptr(k, "q4_paged_read: k", batch.n_tokens, row, ld, kind),
                                _rows_ptr(v, "q4_paged_read: v", batch.n_tokens, row, ld, kind), kind, ld,
                                _stream(stream)), "q4_paged_read")
@@ -486,6 +509,7 @@ def q4_attn_paged(kv: PagedKV, batch: PagedBatch, q, q_type: int, q_ld: int, n_q
                   out, out_ld: int, workspace, workspace_bytes: int, stream=None):
     """Attention of the new tokens over their sequences' pages, into binary16 rows out_ld apart."""
     row = n_q_heads * kv.head_dim
+    _check_device("q4_attn_paged", kv, batch)
     _check(lib().q4_attn_paged(kv, batch, _rows_ptr(q, "q4_attn_paged: q", batch.n_tokens, row, q_ld, q_type), q_type,
                                q_ld, n_q_heads, window, sinks,
                                _rows_ptr(out, "q4_attn_paged: out", batch.n_tokens, row, out_ld, Q4_TYPE_F16), out_ld,
