@@ -9,7 +9,7 @@ torch = pytest.importorskip("torch")
 
 @pytest.fixture(autouse=True)
 def on_device(monkeypatch):
-    monkeypatch.setattr(_lib, "_on_device", lambda t: True)
+    monkeypatch.setattr(_lib, "_device", lambda: -1)      # (a host tensor's device)
 
 
 def refused(f, *args, **kw):
@@ -121,7 +121,7 @@ def write(x, ld, kind=q4.Q4_TYPE_F32, rows=ROWS, other=4096):
 def test_rows_of_their_layout_are_taken(calls):
     wide = torch.zeros(ROWS, 4 * ROW)
     good = [(wide, 4 * ROW), (wide[:, ROW:], 4 * ROW), (wide[:, 3 * ROW:], 4 * ROW), (torch.zeros(ROWS, HEADS, HD), ROW), (torch.zeros(ROWS * ROW), ROW),
-            (torch.zeros(ROWS * HEADS, HD), ROW), (torch.zeros(2 * ROWS, ROW), ROW), (wide.view(ROWS, 4 * HEADS, HD)[:, HEADS:2 * HEADS], 4 * ROW)]
+            (torch.zeros(ROWS * HEADS, HD), ROW), (torch.zeros(2 * ROWS, ROW), ROW), (torch.zeros(2 * ROWS, ROW)[ROWS:], ROW), (wide.view(ROWS, 4 * HEADS, HD)[:, HEADS:2 * HEADS], 4 * ROW)]
     for x, ld in good:
         write(x, ld)
     for x in (f16(ROWS, ROW), f16(ROWS, ROW).view(torch.int16)):
@@ -139,6 +139,7 @@ def test_rows_of_another_type_or_layout_are_refused(calls):
         assert refused(write, bad, ROW)
     wide = torch.zeros(ROWS, 4 * ROW)
     assert refused(write, torch.zeros(ROW, ROWS).T, ROW)                  # transposed
+    assert refused(write, x, ROW, rows=6) and refused(write, x[:, :HD], ROW, rows=6) and refused(write, torch.zeros(ROWS, HD), ROW)      # too few
     assert refused(write, wide[:, :ROW], ROW)                             # rows 4 * ROW apart
     assert refused(write, wide, ROW)
     assert refused(write, torch.zeros(2 * ROWS, ROW)[::2], ROW)
@@ -170,7 +171,6 @@ def test_a_workspace_smaller_than_stated_is_refused(calls):
 
 
 def test_descriptors_of_another_device_than_the_current_one_are_refused(calls, monkeypatch):
-    monkeypatch.setattr(_lib, "_device", lambda: -1)      # (a host tensor's device)
     t = f16(*SHAPE)
     kv, b = q4.PagedKV.of(t, t, *SIZES), q4.PagedBatch.of(i32(2), i32(1), i32(1, 3), 1, ROWS, 3, 1)
     plain = q4.PagedKV.of(4096, 4096, *SIZES), q4.PagedBatch.of(4096, 4096, 4096, 1, ROWS, 3, 1)
@@ -185,6 +185,9 @@ def test_descriptors_of_another_device_than_the_current_one_are_refused(calls, m
     monkeypatch.setattr(_lib, "_device", lambda: 1)
     for f, *args in each(kv, plain[1]) + each(plain[0], b):
         assert refused(f, *args, stream=0)
+    for x in (torch.zeros(ROWS, ROW), torch.zeros(ROWS * ROW)):
+        assert refused(q4.q4_paged_write, *plain, x, 4096, q4.Q4_TYPE_F32, ROW, stream=0)
+    assert refused(q4.q4_attn_paged, *plain, 4096, q4.Q4_TYPE_F32, ROW, HEADS, 0, 0, 4096, ROW, f16(64), 128, stream=0)
     for f, *args in each(*plain):
         f(*args, stream=0)
     assert len(calls) == 9

@@ -216,26 +216,27 @@ def _ptr(t):
 # where this torch has the functions.
 _device = None
 _raw_stream = None
+_stream_of = None       # the current stream's handle of a device, where torch gives it
 
 
 def _init_current():
-    """Finds them; returns the first."""
-    global _device, _raw_stream
+    global _device, _raw_stream, _stream_of
     import torch
     torch.cuda.current_stream()
     get, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
     _device = dev or torch.cuda.current_device
+    _stream_of = get
     _raw_stream = (lambda: get(dev())) if get and dev else (lambda: torch.cuda.current_stream().cuda_stream)
-    return _device
 
 
-def _on_device(t) -> bool:
-    """Whether a tensor is on the current CUDA device (a host tensor's device is -1)."""
-    if not t.is_cuda:
-        return False
+def _current_device() -> int:
+    """The current CUDA device; -2, where no tensor is, without one."""
     if _device is None:
+        import torch
+        if not torch.cuda.is_available():
+            return -2
         _init_current()
-    return t.get_device() == _device()
+    return _device()
 
 
 # Tensor types that hold binary16 values (or their bits), and Q8 codes.
@@ -251,7 +252,7 @@ def _dev_ptr(t, kinds=None, n=0):
     is taken as an address)."""
     if t is None or isinstance(t, int):
         return t
-    if not _on_device(t):
+    if t.get_device() != _current_device():
         raise Q4Error(Q4_ERR_ARG, f"a tensor on {t.device}, not the current CUDA device")
     if not t.is_contiguous() or (kinds and str(t.dtype) not in kinds):
         raise Q4Error(Q4_ERR_ARG, f"a {t.dtype} tensor of strides {tuple(t.stride())}")
@@ -268,42 +269,57 @@ def _device_of(*tensors):
     return None
 
 
-def _check_device(what, *made):
-    """The descriptors were made on the device that is current now: the kernels run there."""
-    for s in made:
-        if s._at is not None and s._at != (_device or _init_current())():
-            raise Q4Error(Q4_ERR_ARG, f"{what}: tensors on device {s._at}, not the current one")
+def _device_for(what, kv, batch) -> int:
+    """The current device, where the kernels will run: the descriptors have to have been made there."""
+    dev = _device() if _device else _current_device()
+    a, b = kv._at, batch._at
+    if a is not None and a != dev or b is not None and b != dev:
+        raise Q4Error(Q4_ERR_ARG, f"{what}: tensors on another device than the current one, {dev}")
+    return dev
 
 
-def _bytes_ptr(t, n):
-    """_dev_ptr of a workspace of n bytes."""
-    if t is not None and not isinstance(t, int) and t.numel() * t.element_size() < n:
-        raise Q4Error(Q4_ERR_ARG, f"a workspace of {t.numel() * t.element_size()} bytes where {n} are meant")
-    return _dev_ptr(t)
-
-
-def _rows_apart(t, rows, ld) -> bool:
-    """Whether a tensor's rows (its first dimension, or all of it) lie ld values apart, each in one piece."""
-    if t.is_contiguous():
-        return rows <= 1 or t.dim() < 2 or t.shape[0] != rows or t.stride(0) == ld
-    if t.dim() == 2:
-        return t.stride(1) == 1 and (rows <= 1 or t.stride(0) == ld)
-    return t.dim() > 2 and t[0].is_contiguous() and (rows <= 1 or t.stride(0) == ld)
-
-
-def _rows_ptr(t, what, rows, row, ld, kind):
-    """_ptr of a buffer of ``rows`` rows of ``row`` values, ``ld`` apart: a
-    tensor has to be on the current device, of that type, and hold them (a view
-    that starts inside a wider row does: its storage counts).  Its own rows have
-    to be ld apart; a contiguous tensor of another number of rows is memory."""
+def _bytes_ptr(t, n, dev):
+    """_ptr of a workspace of n bytes, contiguous and on the device."""
     if t is None or isinstance(t, int):
         return t
+    if t.nbytes < n or t.get_device() != dev or not t.is_contiguous():
+        raise Q4Error(Q4_ERR_ARG, f"workspace: a tensor of {t.nbytes} bytes and strides {tuple(t.stride())} on {t.device}, where {n} bytes are meant")
+    return t.data_ptr()
+
+
+_plain = {}      # torch's type of each Q4_TYPE_*
+
+
+def _find_plain():
+    import torch
+    _plain.update({Q4_TYPE_F32: torch.float32, Q4_TYPE_F16: torch.float16})
+    return _plain
+
+
+def _rows_ptr(t, what, rows, row, ld, kind, dev):
+    """_ptr of a buffer of ``rows`` rows of ``row`` values, ``ld`` apart: a
+    tensor has to be on the device, of that type, and hold them (a view that
+    starts inside a wider row does: its storage counts).  Its own rows have to
+    be ld apart; a contiguous tensor of another number of rows is memory."""
+    if t is None or isinstance(t, int):
+        return t
+    # (a matrix that holds the rows itself: the rest costs as much as a launch)
+    if (t.dtype is (_plain or _find_plain()).get(kind) and t.stride() == (ld, 1) and t.size(0) >= rows
+            and t.size(1) >= row and t.get_device() == dev):
+        return t.data_ptr()
     size = 4 if kind == Q4_TYPE_F32 else 2
-    if not _on_device(t):
+    if t.get_device() != dev:
         raise Q4Error(Q4_ERR_ARG, f"{what}: a tensor on {t.device}, not the current CUDA device")
     if str(t.dtype) not in (_F32 if kind == Q4_TYPE_F32 else _BITS16):
         raise Q4Error(Q4_ERR_ARG, f"{what}: a {t.dtype} tensor for {'fp32' if size == 4 else 'binary16'} values")
-    if not _rows_apart(t, rows, ld):
+    # its rows (the first dimension, or all of it) lie ld values apart, each in one piece
+    n = t.dim()
+    apart = rows <= 1 or n < 2 or t.stride(0) == ld
+    if t.is_contiguous():
+        apart = apart or t.size(0) != rows
+    else:
+        apart = apart and (t.stride(1) == 1 if n == 2 else n > 2 and t[0].is_contiguous())
+    if not apart:
         raise Q4Error(Q4_ERR_ARG, f"{what}: a tensor of shape {tuple(t.shape)} and strides {tuple(t.stride())} for rows {ld} apart")
     if rows > 0 and t.storage_offset() + (rows - 1) * ld + row > t.untyped_storage().nbytes() // size:
         raise Q4Error(Q4_ERR_ARG, f"{what}: {rows} rows of {row} values {ld} apart do not fit its storage")
@@ -318,6 +334,11 @@ def _stream(s):
     if isinstance(s, int):
         return s
     return s.cuda_stream
+
+
+def _stream_on(s, dev):
+    """_stream, with the current device known."""
+    return _stream_of(dev) if s is None and _stream_of else _stream(s)
 
 
 def _check(st: int, what: str):
@@ -489,31 +510,28 @@ def q4_kv_append(k, v, k_cache, v_cache, pos, capacity: int, kv_dim: int, stream
 
 def q4_paged_write(kv: PagedKV, batch: PagedBatch, k, v, kind: int, ld: int, stream=None):
     """The new tokens' keys and values (rows of Q4_TYPE_F32 or Q4_TYPE_F16 values, ld apart) into their pages."""
-    row = kv.n_kv_heads * kv.head_dim
-    _check_device("q4_paged_write", kv, batch)
-    _check(lib().q4_paged_write(kv, batch, _rows_ptr(k, "q4_paged_write: k", batch.n_tokens, row, ld, kind),
-                                _rows_ptr(v, "q4_paged_write: v", batch.n_tokens, row, ld, kind), kind, ld,
-                                _stream(stream)), "q4_paged_write")
+    dev, rows, row = _device_for("q4_paged_write", kv, batch), batch.n_tokens, kv.n_kv_heads * kv.head_dim
+    _check(lib().q4_paged_write(kv, batch, _rows_ptr(k, "q4_paged_write: k", rows, row, ld, kind, dev),
+                                _rows_ptr(v, "q4_paged_write: v", rows, row, ld, kind, dev), kind, ld,
+                                _stream_on(stream, dev)), "q4_paged_write")
 
 
 def q4_paged_read(kv: PagedKV, batch: PagedBatch, k, v, kind: int, ld: int, stream=None):
     """The batch's positions out of their pages into rows of Q4_TYPE_F32 or Q4_TYPE_F16 values, ld apart."""
-    row = kv.n_kv_heads * kv.head_dim
-    _check_device("q4_paged_read", kv, batch)
-    _check(lib().q4_paged_read(kv, batch, _rows_ptr(k, "q4_paged_read: k", batch.n_tokens, row, ld, kind),
-                               _rows_ptr(v, "q4_paged_read: v", batch.n_tokens, row, ld, kind), kind, ld,
-                               _stream(stream)), "q4_paged_read")
+    dev, rows, row = _device_for("q4_paged_read", kv, batch), batch.n_tokens, kv.n_kv_heads * kv.head_dim
+    _check(lib().q4_paged_read(kv, batch, _rows_ptr(k, "q4_paged_read: k", rows, row, ld, kind, dev),
+                               _rows_ptr(v, "q4_paged_read: v", rows, row, ld, kind, dev), kind, ld,
+                               _stream_on(stream, dev)), "q4_paged_read")
 
 
 def q4_attn_paged(kv: PagedKV, batch: PagedBatch, q, q_type: int, q_ld: int, n_q_heads: int, window: int, sinks: int,
                   out, out_ld: int, workspace, workspace_bytes: int, stream=None):
     """Attention of the new tokens over their sequences' pages, into binary16 rows out_ld apart."""
-    row = n_q_heads * kv.head_dim
-    _check_device("q4_attn_paged", kv, batch)
-    _check(lib().q4_attn_paged(kv, batch, _rows_ptr(q, "q4_attn_paged: q", batch.n_tokens, row, q_ld, q_type), q_type,
-                               q_ld, n_q_heads, window, sinks,
-                               _rows_ptr(out, "q4_attn_paged: out", batch.n_tokens, row, out_ld, Q4_TYPE_F16), out_ld,
-                               _bytes_ptr(workspace, workspace_bytes), workspace_bytes, _stream(stream)), "q4_attn_paged")
+    dev, rows, row = _device_for("q4_attn_paged", kv, batch), batch.n_tokens, n_q_heads * kv.head_dim
+    _check(lib().q4_attn_paged(kv, batch, _rows_ptr(q, "q4_attn_paged: q", rows, row, q_ld, q_type, dev), q_type, q_ld,
+                               n_q_heads, window, sinks,
+                               _rows_ptr(out, "q4_attn_paged: out", rows, row, out_ld, Q4_TYPE_F16, dev), out_ld,
+                               _bytes_ptr(workspace, workspace_bytes, dev), workspace_bytes, _stream_on(stream, dev)), "q4_attn_paged")
 
 
 def q4_attn_paged_workspace_bytes(n_q_heads: int, n_kv_heads: int, head_dim: int) -> int:
