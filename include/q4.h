@@ -571,7 +571,10 @@ int q4_paged_read(const q4_paged_kv *kv, const q4_paged_batch *batch, void *k, v
  * first tokens that stay visible); never a position in a hole, so pages that
  * left the window may be given back.  A token that sees nothing gets zeros.
  * Values outside what a query sees (stale slots, NaN, infinities) do not
- * reach its output; a query all of whose scores are -infinity gets zeros too.
+ * reach its output.  A value that it sees and that is not finite leaves that
+ * column of its output not finite, whatever its weight (an infinity, or NaN
+ * where the weight rounds to zero); a query all of whose scores are -infinity
+ * gets zeros otherwise.  An infinite key may make fp32 queries' scores NaN.
  * The new tokens' own keys and values must be in the pages (q4_paged_write).
  *   q      device, [n_tokens] rows of n_q_heads * head_dim values of q_type
  *          (Q4_TYPE_*), q_ld values from row to row, rows 16-byte aligned;

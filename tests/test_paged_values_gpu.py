@@ -119,3 +119,24 @@ def test_small_fp32_queries_against_large_keys(rows, hd, q8):
     q = (one * size).astype(np.float32).reshape(c.n_tokens, 2 * hd)
     check(Dev(c).attend(q, 2), c, q, 2)
     both_kernels(c, q, 2)
+
+
+@pytest.mark.parametrize("chunk", [1, 40])
+def test_values_that_are_not_finite_under_scores_of_minus_infinity(chunk):
+    """0 times an infinity is no number, however the positions are shared out: most of a long sequence's scores are -infinity, so whole
+    parts of it have no other, and some values there are infinite or NaN."""
+    c = ref.Cache([chunk], [40000], 1, 128, 256, seed=61)
+    far = c.table[0, :117]                             # positions 0 .. 29951
+    c.pages["k"][far, :, :, 0] = -np.inf
+    for i, kind in enumerate(("nan", "inf")):
+        put(c, 0, 100 + 9000 * i, kind, block=i)
+    q = queries(c, 8, 55, False, scale=0.5)
+    q.reshape(chunk, 8, 128)[:, :, 0] = 0.25
+    with np.errstate(invalid="ignore"):
+        want, _ = c.attend(q, 8)
+    odd = np.isnan(want)
+    assert odd.reshape(chunk, 8, 128)[:, :, :64].all() and np.isfinite(want[~odd]).all()
+    for max_new in (1, 300):
+        got = Dev(c, max_new=max_new).attend(q, 8)
+        check(got, c, q, 8)
+        assert np.array_equal(~np.isfinite(got), odd)

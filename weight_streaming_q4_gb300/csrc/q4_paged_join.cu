@@ -56,11 +56,8 @@ __global__ void __launch_bounds__(kPjThreads) paged_join_kernel(const __grid_con
       for (int e = 0; e < E; ++e) o[e] *= back;
 #pragma unroll
       for (int k = 0; k < B; ++k) {
-        if (m[k] == -INFINITY) {
-          if (c0 + k < rec.n) sum += l[k] * 0.f;       // (a sum that is not a number stays one)
-          continue;
-        }
-        const float f = exp2f(m[k] - top);
+        if (c0 + k >= rec.n) continue;
+        const float f = m[k] == -INFINITY ? 0.f : exp2f(m[k] - top);       // (times 0: what is not a number stays so)
         sum += l[k] * f;
 #pragma unroll
         for (int e = 0; e < E / 2; ++e) {
