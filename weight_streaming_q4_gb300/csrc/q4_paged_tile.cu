@@ -211,6 +211,7 @@ struct PtCtl {
   // rows has used it, so the loaders are at most five key tiles, and five of a query tile's own segments, ahead of
   // its softmax.  (Any number of segments without rows of the second query tile may pass while that one ends an item.)
   int bad[2][8];
+  int second[16];          // Q8: the second query tile's count, by each converting warp
   uint32_t there[8];       // per key tile, by number mod 8: bit g = rows 16 g .. of the tile are in a page
   CtaWork work;
   long long scan[17];
@@ -311,7 +312,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
     }
     mbar_init(&c->raw, 1), mbar_init(&c->raw_free, G::CONV), mbar_init(&c->done, 1);
     c->dead = 0;
-    for (int i = 0; i < 16; ++i) c->bad[i >> 3][i & 7] = 0;
+    for (int i = 0; i < 16; ++i) c->bad[i >> 3][i & 7] = c->second[i] = 0;
     fence_mbar_init();
   }
   if (warp == G::W_MMA) tm_alloc(&c->tmem, 512);
@@ -588,10 +589,25 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
       if (a.window && t + (1 << bl) <= max(g.it.p0, 0) - a.window + 1 && t >= a.sinks) return -1;
       return paged_row(a.kv, a.b, g.seq, t, g.head);
     };
-    // Values of the walk's segment were not finite; seg: the segments so far in which each query tile had rows.
-    auto note_bad = [&](const SegmentWalk<R, BN>& g, const int (&seg)[2]) {
-      *reinterpret_cast<volatile int*>(&c->bad[0][seg[0] & 7]) = seg[0] + 1;
-      if (g.rows() > 128) *reinterpret_cast<volatile int*>(&c->bad[1][seg[1] & 7]) = seg[1] + 1;
+    // Values of segment number seg were not finite.  The second query tile's own count of segments is in a register where
+    // there is one to spare (in shared memory: mixed_8 185.7 us, not 184.3), else in shared memory (in a register:
+    // chunk_512_q8 147 us, not 134.6).
+    int second = 0;
+    auto note_bad = [&](int seg) {
+      *reinterpret_cast<volatile int*>(&c->bad[0][seg & 7]) = seg + 1;
+      if (w.rows() > 128) {
+        const int own = Q8 ? *reinterpret_cast<volatile int*>(&c->second[warp]) : second;
+        *reinterpret_cast<volatile int*>(&c->bad[1][own & 7]) = own + 1;
+      }
+    };
+    auto next_segment = [&]() {
+      if (NQ == 2 && w.rows() > 128) {
+        if (!Q8)
+          ++second;
+        else if (lane == 0)
+          *reinterpret_cast<volatile int*>(&c->second[warp]) += 1;
+      }
+      w.next(a);
     };
     // bit r / 16: rows r .. of the tile are in a page (and seen)
     auto there_of = [&](int row) {
@@ -628,8 +644,8 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
     } else if (!Q8) {   // (warps 9 and 10)
       // value tiles to be cleaned
       uint32_t n = 1;
-      int seg[2] = {0, 0};
-      for (; w.live(); ++seg[0], seg[1] += w.rows() > 128, w.next(a)) {
+      int seg = 0;
+      for (; w.live(); ++seg, next_segment()) {
         for (int i = w.i0; i < w.i1; ++i, n += 2) {
           pt_wait_warp(c, &c->full[n % NS], (n / NS) & 1);
           const TileView tv = tile_view<BN>(a, w.it, i);
@@ -696,7 +712,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
                 *piece(x) = make_uint4(0, 0, 0, 0);
             }
           }
-          if (found) note_bad(w, seg);
+          if (found) note_bad(seg);
           fence_async();
           __syncwarp();
           if (lane == 0) mbar_arrive(&c->fixed[n % NS]);
@@ -740,8 +756,8 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
       constexpr int PIECES = BN * HD / 16;               // 16 codes each
       const char* const raw = tiles + G::QALL + NS * G::KB;
       uint32_t n = 0;                                    // tiles stored (keys and values)
-      int seg[2] = {0, 0};
-      for (; w.live(); ++seg[0], seg[1] += w.rows() > 128, w.next(a)) {
+      int seg = 0;
+      for (; w.live(); ++seg, next_segment()) {
         for (int i = w.i0; i < w.i1; ++i) {
           const TileView tv = tile_view<BN>(a, w.it, i);
           const int last = w.it.p1 - tv.base, first = a.window ? max(w.it.p0, 0) - a.window + 1 - tv.base : 0, sk = a.sinks - tv.base;
@@ -809,7 +825,7 @@ __global__ void __launch_bounds__(Pt<HD, QF32, Q8>::THREADS, 1)
               convert(std::true_type{});
             else
               convert(std::false_type{});
-            if (found) note_bad(w, seg);
+            if (found) note_bad(seg);
             fence_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(&c->full[slot]);
