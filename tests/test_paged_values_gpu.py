@@ -140,3 +140,35 @@ def test_values_that_are_not_finite_under_scores_of_minus_infinity(chunk):
         got = Dev(c, max_new=max_new).attend(q, 8)
         check(got, c, q, 8)
         assert np.array_equal(~np.isfinite(got), odd)
+
+
+@pytest.mark.parametrize("q8", [False, True], ids=["f16", "q8"])
+def test_stale_slots_cost_nothing(q8):
+    """What lies behind the sequences' last positions, NaN here, is not searched for: a call takes as long as with numbers there (it
+    took 2 to 3 times as long; the bound is half way)."""
+    import torch
+    c = ref.Cache([1] * 64, [2000 + 61 * s + s % 2 for s in range(64)], 4, 128, 64, q8, seed=62)
+    q = queries(c, 32, 56, True)
+    times = []
+    for stale in (False, True):
+        if stale:
+            for s, n in enumerate(c.total):
+                for t in range(n, -(-n // 64) * 64):
+                    for block in range(4):
+                        put(c, s, t, "nan", block=block)
+        d = Dev(c)
+        qd, out = torch.from_numpy(q).cuda(), torch.empty((64, 32 * 128), dtype=torch.float16, device="cuda")
+        nb = q4.q4_attn_paged_workspace_bytes(32, 4, 128)
+        ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+        best = 1e9
+        for _ in range(20):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(10):
+                q4.q4_attn_paged(d.kv, d.batch, qd, q4.Q4_TYPE_F32, 32 * 128, 32, 0, 0, out, 32 * 128, ws, nb)
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        times.append(best)
+        check(out.cpu().numpy().astype(np.float64), c, q, 32)
+    assert times[1] < 1.5 * times[0], times

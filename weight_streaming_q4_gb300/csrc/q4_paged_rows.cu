@@ -421,6 +421,23 @@ __global__ void __launch_bounds__(Pr<HD, NR, QF32, Q8, CL>::NT, 1)
       const int base = u.base_of(u.g);
       const uint32_t there = c->there[warp][stage];
       if (there) {
+        const bool whole = there == (1u << SUB) - 1 && base + GP - 1 <= w.it.p0 &&
+                           (!a.window || base > w.it.p1 - a.window || base + GP <= a.sinks);
+        if (!whole) {
+          // Values that no row sees become zeros (Q8: their scales), and are not noted: what lies behind the last
+          // position may be anything.
+          constexpr int N = Q8 ? HD / 32 : PIECES;       // stores per position
+#pragma unroll 1
+          for (int x = lane; x < GP * N; x += 32) {
+            const int r = x / N, pos = base + r;
+            if (pos <= w.it.p1 && (!a.window || pos > w.it.p0 - a.window || pos < a.sinks)) continue;
+            if (Q8)
+              asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + 2 * GP * ROW + G::SC + x * 2), "h"(static_cast<uint16_t>(0)) : "memory");
+            else
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + GP * ROW + x * 16), "r"(0) : "memory");
+          }
+          __syncwarp();
+        }
         // where this lane's first pieces lie
         const uint32_t kat = at + (Q8 ? place<ROW, true>(g, t) : place<ROW, false>(lane & 7, lane >> 3));
         const uint32_t vat = at + GP * ROW + place<ROW, false>((lane & 7) + (lane & 8), lane >> 4);
@@ -483,8 +500,6 @@ __global__ void __launch_bounds__(Pr<HD, NR, QF32, Q8, CL>::NT, 1)
 #pragma unroll
             for (int e = 0; e < 4 * SUB; ++e) s[nr][e >> 2][e & 3] += s2[nr][e >> 2][e & 3];
         }
-        const bool whole = there == (1u << SUB) - 1 && base + GP - 1 <= w.it.p0 &&
-                           (!a.window || base > w.it.p1 - a.window || base + GP <= a.sinks);
         if (!whole) {
 #pragma unroll
           for (int nr = 0; nr < NR; ++nr)
