@@ -582,7 +582,7 @@ int q4_paged_read(const q4_paged_kv *kv, const q4_paged_batch *batch, void *k, v
  *   out    device, binary16 [n_tokens] rows of n_q_heads * head_dim, out_ld
  *          values from row to row, rows 16-byte aligned, written
  *   n_q_heads   a multiple of n_kv_heads, at most 64 query heads per value head;
- *               n_tokens times the query heads per value head at most 2^31 - 1024
+ *               n_tokens times the query heads per value head at most 2^30
  *   window      0 (none) or the positions a query sees back, its own included
  *   sinks       first positions visible beside the window (0 without one)
  *   workspace   device, >= q4_attn_paged_workspace_bytes() bytes, 16-byte

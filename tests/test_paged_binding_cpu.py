@@ -193,7 +193,7 @@ def test_descriptors_of_another_device_than_the_current_one_are_refused(calls, m
     assert len(calls) == 9
 
 
-def test_query_rows_of_a_head_are_counted_in_31_bits():
+def test_query_rows_of_a_head_are_counted_in_30_bits():
     """(the library itself: fake addresses, which the next check refuses)"""
     from weight_streaming_q4_gb300 import build
     build.build()
@@ -205,6 +205,6 @@ def test_query_rows_of_a_head_are_counted_in_31_bits():
         b = q4.PagedBatch(token_starts=4096, kv_lens=4096, page_table=4096, n_seqs=1, n_tokens=n_tokens, table_width=3, max_new=1)
         return lib.q4_attn_paged(kv, b, 4096, 1, 4096, n_q, 0, 0, 4096, 4096, 4096 + 8, ws, None)       # the workspace: not aligned
 
-    assert attend((1 << 25) - 16) == q4.Q4_ERR_ALIGN and attend((1 << 31) - 1024, 1) == q4.Q4_ERR_ALIGN
-    for n_tokens, n_q in (((1 << 25) - 15, 64), (1 << 25, 64), (1 << 26, 64), ((1 << 31) - 1, 2), ((1 << 31) - 1023, 1)):
+    assert attend(1 << 24) == q4.Q4_ERR_ALIGN and attend(1 << 30, 1) == q4.Q4_ERR_ALIGN
+    for n_tokens, n_q in (((1 << 24) + 1, 64), (1 << 25, 64), (1 << 26, 64), ((1 << 31) - 1, 2), ((1 << 30) + 1, 1)):
         assert attend(n_tokens, n_q) == q4.Q4_ERR_ARG

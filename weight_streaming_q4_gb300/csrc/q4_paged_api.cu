@@ -125,8 +125,8 @@ extern "C" int q4_attn_paged(const q4_paged_kv* kv, const q4_paged_batch* batch,
   int st = check_batch(kv, batch, &a.kv, &a.b, &empty);
   if (st != Q4_OK) return st;
   if (!group_ok(n_q_heads, a.kv.n_kv) || window < 0 || sinks < 0 || (sinks > 0 && window == 0)) return Q4_ERR_ARG;
-  // (the kernels count a sequence's query rows of a head, rounded up to whole tiles, in an int)
-  if (static_cast<int64_t>(a.b.n_tokens) * (n_q_heads / a.kv.n_kv) > INT32_MAX - 1023) return Q4_ERR_ARG;
+  // (the kernels count a sequence's query rows of a head, and a window back from a negative position, in an int)
+  if (static_cast<int64_t>(a.b.n_tokens) * (n_q_heads / a.kv.n_kv) > (1 << 30)) return Q4_ERR_ARG;
   if (empty) return Q4_OK;
   const int64_t row = static_cast<int64_t>(n_q_heads) * a.kv.hd;
   if ((st = check_rows(q, q_type, q_ld, row)) != Q4_OK) return st;
