@@ -98,6 +98,9 @@ class Lib:
     def __init__(self):
         self.calls = []
 
+    def q4_status_string(self, st):
+        return b"refused"
+
     def __getattr__(self, name):
         return lambda *args: self.calls.append((name, args)) or q4.Q4_OK
 

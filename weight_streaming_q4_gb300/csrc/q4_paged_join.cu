@@ -5,7 +5,7 @@
 // programmatic dependent of that kernel: its blocks take their place while the
 // last CTAs finish and wait for them, so the second launch costs less than one
 // after the other.  A batch of chunks and single tokens takes 183 us with it and 171
-// without.
+// in a timing copy without.
 #include <cuda_fp16.h>
 #include <math.h>
 #include <stdint.h>

@@ -16,15 +16,17 @@
 // the 16, half of products, weights and output registers of such a group were zeros: 64
 // sequences of the 70B heads over Q8 175 us, so 133 at that step).  The scores' registers become the weights'
 // operand by one 8 x 8 transposition each.  fp32 queries enter as two binary16 parts of a scaled row (QueryScale).
+// The weights are rounded to binary16 once, as in the kernel of many rows (which one runs must not show beyond
+// the rounding): 2^-11 relative, as much as the output's own rounding; their sum is taken before it, in fp32.
 // Q8 pages stay codes in shared memory: a lane's 16 codes of a key are its share
 // of four instructions (the order of head_dim in the product is free, the
 // queries follow it), a transposed matrix load of value codes holds two columns of one
 // position pair per register; f16(code * d) is formed in registers.
 //
-// Measured: 64 sequences of the 70B heads of up to 8192 positions, binary16 183 us, 6.25 TB/s
-// (92 % of a copy's rate); Q8 127 us, 4.8 TB/s: the issue slots, 65 % busy, of which the
+// Measured, back to back in a graph: 64 sequences of the 70B heads of up to 8192 positions, binary16 180 us, 6.3 TB/s
+// (93 % of a copy's rate); Q8 127 us, 4.8 TB/s: the issue slots, 67 % busy, of which the
 // conversion takes 7 instructions per 4 values.  One token of the 8B heads over 512 and 4096 positions 4.8 and
-// 7.7 us: the launch and a chain of dependent loads.
+// 7.7 us (8.3 and 11.8 where the table is too wide for clusters): the launch and a chain of dependent loads.
 #include <cuda_fp16.h>
 #include <math.h>
 #include <stdint.h>

@@ -32,15 +32,15 @@
 //
 // Precision: binary16 queries enter as they are, fp32 queries as two binary16
 // parts (22 bits of a scaled row, QueryScale; two products into the same S); P is rounded to binary16
-// (2^-11 relative, the output's own rounding again), the sum l is taken of the
-// unrounded weights.
+// (2^-11 relative, as much as the output's own rounding; a second product with what that leaves out
+// would cost half again the products), the sum l is taken of the unrounded weights.
 //
-// Measured: 2048 tokens of the 8B heads over 16384 positions 349 us, 1480 TFLOP/s, 77 %
-// of a library matrix product's rate; the scores -> weights -> product chain of one
+// Measured, back to back in a graph: 2048 tokens of the 8B heads over 16384 positions 351 us, 1470 TFLOP/s, 76 %
+// of a library matrix product's rate (fp32 queries, one query tile and half again the products: 562 us); the scores -> weights -> product chain of one
 // query tile that the other one does not cover bounds it (tensor pipe 65 % busy), and power.  512
-// tokens of the 70B heads over 8192 positions of Q8 137 us, 970 TFLOP/s: the conversion
-// shares the issue slots with the softmax.  Eight ragged sequences of up to 2049 tokens 183 us,
-// 793 TFLOP/s: outputs 23 us of it, cleaning 14 (each by leaving it out).
+// tokens of the 70B heads over 8192 positions of Q8 135 us, 985 TFLOP/s: the conversion
+// shares the issue slots with the softmax.  Eight ragged sequences of up to 2049 tokens 184 us,
+// 792 TFLOP/s: outputs 23 us of it, cleaning 14 (each by leaving it out).
 #include <cuda_fp16.h>
 #include <math.h>
 #include <stdint.h>
