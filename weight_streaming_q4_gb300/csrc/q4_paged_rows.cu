@@ -767,7 +767,7 @@ template <int HD, int NR, bool QF32, bool Q8>
 cudaError_t launch_rows(const PagedAttnArgs& a, void* ws, int grid, cudaStream_t s) {
   if constexpr (NR <= 2) {
     // Few items and a table of no great length: a cluster each.  One token of the 8B heads over 512, 2048, 4096, 8192
-    // and 32768 positions 5.0, 6.4, 7.8, 12.4 and 30.0 us, split evenly over all CTAs 8.5, 9.1, 12.1, 17.4 and 31.6
+    // and 32768 positions 4.7, 6.1, 7.8, 11.9 and 30.0 us, split evenly over all CTAs 8.3, 8.9, 11.9, 16.7 and 31.1
     // (64 CTAs draw less of the bandwidth than 152, so longer tables are split).  16 items are more clusters than the
     // GPU holds at once (a CTA fills an SM): 16.9 against 15.6 for 2 sequences of 4096 positions.
     const int items = a.b.n_seqs * a.kv.n_kv;
