@@ -604,6 +604,167 @@ int q4_attn_paged(const q4_paged_kv *kv, const q4_paged_batch *batch, const void
 /* Bytes of the workspace of q4_attn_paged (0 for invalid sizes).  Host only. */
 size_t q4_attn_paged_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim);
 
+/* ------------------------------------------------------- a prompt's layer beside its attention */
+
+/*
+ * The rest of a layer for any number of token rows (a prompt's chunk, a ragged
+ * batch, a single token) around the paged cache and q4_attn_paged: products
+ * with an epilogue, the gated product, the norms around a block and rotary
+ * positions.  Rows are binary16 or fp32 (Q4_TYPE_*), `ld` values from row to
+ * row (ld >= the row); row r of an output depends on row r of the inputs
+ * alone, whatever the number of rows.  With no row a call does nothing.
+ */
+
+/* Activations. */
+#define Q4_ACT_NONE 0
+#define Q4_ACT_RELU 1         /* max(t, 0) */
+#define Q4_ACT_SILU 2         /* t / (1 + e^-t) */
+#define Q4_ACT_GELU 3         /* t (1 + erf(t / sqrt 2)) / 2 */
+#define Q4_ACT_GELU_TANH 4    /* t (1 + tanh(sqrt(2 / pi) (t + 0.044715 t^3))) / 2 */
+
+/* What a product's rows go through before they are stored. */
+typedef struct q4_epilogue {
+  const float *bias;       /* device, fp32 [n], or null: none */
+  int act;                 /* Q4_ACT_* */
+  float scale;             /* of the activated product (1: none) */
+  const void *residual;    /* device, rows of n values of residual_type, or null: none; may be y itself */
+  int residual_type;       /* Q4_TYPE_* */
+  int64_t residual_ld;
+} q4_epilogue;
+
+/*
+ * y = f16(residual + scale * act(W x + bias)) for every row of x.
+ * A weight of these products is the binary16 value f16((q - 8) * d), as an
+ * element of the Q8 cache is f16(code * d).  q4_gemv keeps (q - 8) * d whole;
+ * the two differ by at most 2^-11 sum |w x| + 2^-25 sum |x| (and (q - 8) * d
+ * beyond +-65504 becomes an infinity).  Of these weights' products the sum is
+ * off by at most k 2^-23 sum |w x|; y is rounded once.
+ *   w      device, Q4_0 [n][k/32] blocks, 16-byte aligned, read only
+ *   x      device, binary16 [rows] rows of k values, x_ld apart, each 16-byte
+ *          aligned, read only
+ *   y      device, binary16 [rows] rows of n values, y_ld apart, written; it
+ *          must not overlap w or x
+ *   n, k   n >= 1; k a multiple of 32.  k that is no multiple of 256 (rows
+ *          that do not start 16-byte aligned) is fetched row by row, and
+ *          q4_matrix_bytes(n, k) must then stay below 2^32
+ *   rows   0 .. 2^24
+ *   ep     null: y = f16(W x)
+ * The first call on a device makes the kernels ready (before any stream
+ * capture).  Runs of the same inputs give the same bits.
+ * Errors: Q4_ERR_ARG, Q4_ERR_ALIGN, Q4_ERR_CUDA.
+ */
+int q4_gemm(const void *w, const uint16_t *x, int64_t x_ld, int n, int k, int rows, const q4_epilogue *ep, uint16_t *y,
+            int64_t y_ld, void *stream);
+
+/* Of the gated product. */
+typedef struct q4_gated_epilogue {
+  const float *bias_gate;  /* device, fp32 [n], or null */
+  const float *bias_up;
+  int act;                 /* Q4_ACT_* */
+} q4_gated_epilogue;
+
+/*
+ * The first half of a gated feed-forward block in one kernel:
+ *   y = f16(act(Wgate x + bias_gate) * (Wup x + bias_up)),
+ * the sums in fp32 up to the one rounding at the end.  Both matrices are
+ * [n][k]; the other arguments as for q4_gemm (ep null: Q4_ACT_SILU, no bias).
+ * Errors: as q4_gemm.
+ */
+int q4_gemm_gated(const void *w_gate, const void *w_up, const uint16_t *x, int64_t x_ld, int n, int k, int rows,
+                  const q4_gated_epilogue *ep, uint16_t *y, int64_t y_ld, void *stream);
+
+#define Q4_NORM_RMS 0     /* norm(v) = v / sqrt(mean(v^2) + eps) */
+#define Q4_NORM_LAYER 1   /* norm(v) = (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) */
+
+/* The norms after and before a block, its gate and its scale.  Every vector is
+ * device, fp32 [n], or null: none (a factor of 1, a term of 0). */
+typedef struct q4_norms {
+  int kind;                 /* Q4_NORM_* */
+  float eps;                /* >= 0 */
+  int post;                 /* nonzero: the block's output is normalised before it is added */
+  const float *post_weight;
+  const float *post_bias;
+  float scale;
+  const float *gate;        /* [n] for all rows (gate_rows 0), or ceil(rows / gate_rows) vectors, gate_ld apart */
+  int64_t gate_ld;
+  int gate_rows;            /* row r takes vector r / gate_rows */
+  const float *weight;
+  const float *bias;
+} q4_norms;
+
+/*
+ * Between two blocks of a layer, in one pass: for every row
+ *   u = block, or norm(block) * post_weight + post_bias
+ *   t = residual + scale * gate * u
+ *   z = norm(t) * weight + bias
+ * with statistics and sums in fp32; z is taken of t before it is rounded.
+ *   block      device, rows of n values of block_type, or null: t = residual
+ *   residual   device, rows of n values of residual_type, or null: none (not
+ *              both null)
+ *   t          device, rows of n values of t_type, written, or null: not kept
+ *   z          device, rows of n values of z_type, written, or null: not wanted
+ *              (not both null)
+ *   n          1 .. 32768;  rows 0 .. 2^24
+ * t and z may each be the block or the residual itself (same type and ld), but
+ * not overlap one another or them in another way.  A value that is not finite
+ * leaves its own row not finite.  Squares are fp32: values within +-2^56.
+ * Errors: Q4_ERR_ARG, Q4_ERR_ALIGN, Q4_ERR_CUDA.
+ */
+int q4_block_norm(const q4_norms *norms, int rows, int n, const void *block, int block_type, int64_t block_ld,
+                  const void *residual, int residual_type, int64_t residual_ld, void *t, int t_type, int64_t t_ld,
+                  void *z, int z_type, int64_t z_ld, void *stream);
+
+/*
+ * Rotary positions.  The first rot_dim values of a head turn in pairs, the
+ * others stay; pair i turns by the angle position * frequency i, where the
+ * position is that of the pair's axis (text has one axis, an image two, a video
+ * three: time, height, width).  Made once by q4_rotation_init (host only).
+ */
+#define Q4_ROPE_HALVES 0      /* pair i: values i and i + rot_dim / 2 of the head */
+#define Q4_ROPE_ADJACENT 1    /* pair i: values 2 i and 2 i + 1 */
+#define Q4_ROPE_PAIRS 128     /* pairs of a head at most */
+#define Q4_ROPE_AXES 4
+
+typedef struct q4_rotation {
+  int head_dim, rot_dim, style, n_axes;
+  uint8_t axis[Q4_ROPE_PAIRS];     /* of each pair */
+  uint64_t turn[Q4_ROPE_PAIRS];    /* of each pair: the turns of one position, in 2^-64 of a circle, whole ones left out */
+} q4_rotation;
+
+/*
+ *   freqs      host, rot_dim / 2 finite values: radians per position
+ *   axes       host, rot_dim / 2 values 0 .. 3, or null: all 0
+ *   head_dim   2 .. 1024;  rot_dim even, 2 .. 256, at most head_dim
+ * Errors: Q4_ERR_ARG.
+ */
+int q4_rotation_init(q4_rotation *rot, int head_dim, int rot_dim, const double *freqs, const int *axes, int style);
+
+/* Where the rows stand. */
+typedef struct q4_places {
+  const int *positions;      /* device, [n_axes] rows of n_tokens positions, ld apart: axis a of token row r at a * ld + r */
+  int64_t ld;
+  int n_axes;                /* at least the rotation's */
+  const int *token_starts;   /* with positions null: as in q4_paged_batch, every axis at the row's position there */
+  const int *kv_lens;
+  int n_seqs;
+  int n_tokens;              /* rows of the caller's buffers: 0 .. 2^24 */
+} q4_places;
+
+/*
+ * Turns every head of the rows of x into y: pair (a, b) becomes
+ * (a cos - b sin, a sin + b cos), or with `inverse` turns back (keys that move
+ * to another position; the gradient of the turn).  Queries and keys that lie
+ * side by side are one call.  The angle is reduced in 64 bits, so a far
+ * position costs no accuracy: cos and sin are within 2^-22.
+ *   x      device, n_tokens rows of n_heads * head_dim values of x_type, x_ld apart
+ *   y      device, rows laid out likewise of y_type, written; x itself (same
+ *          type and ld) or memory that does not overlap x
+ * Rows that belong to no sequence are not written.  Positions may be negative.
+ * Errors: Q4_ERR_ARG, Q4_ERR_ALIGN, Q4_ERR_CUDA.
+ */
+int q4_rope(const q4_rotation *rot, const q4_places *places, int inverse, int n_heads, const void *x, int x_type,
+            int64_t x_ld, void *y, int y_type, int64_t y_ld, void *stream);
+
 /* ------------------------------------------------------- streamed layers */
 
 typedef struct q4_stream q4_stream;

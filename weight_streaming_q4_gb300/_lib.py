@@ -45,6 +45,17 @@ Q4_KV_F16 = 0
 Q4_KV_Q8 = 1
 Q4_TYPE_F32 = 0
 Q4_TYPE_F16 = 1
+Q4_ACT_NONE = 0
+Q4_ACT_RELU = 1
+Q4_ACT_SILU = 2
+Q4_ACT_GELU = 3
+Q4_ACT_GELU_TANH = 4
+Q4_NORM_RMS = 0
+Q4_NORM_LAYER = 1
+Q4_ROPE_HALVES = 0
+Q4_ROPE_ADJACENT = 1
+Q4_ROPE_PAIRS = 128
+Q4_ROPE_AXES = 4
 Q4_STREAM_POISON = 1
 Q4_STREAM_TENSOR_CORE = 2
 Q4_STREAM_CHUNKED = 4
@@ -123,6 +134,113 @@ class PagedBatch(ctypes.Structure):
         return s
 
 
+class Epilogue(ctypes.Structure):
+    """q4_epilogue.  Made once per product and residual buffer; keeps its
+    tensors alive: a bias of n fp32 values, a residual of ``rows`` rows of n
+    values residual_ld apart (0: n)."""
+    _fields_ = [("bias", c_p), ("act", c_int), ("scale", ctypes.c_float), ("residual", c_p), ("residual_type", c_int),
+                ("residual_ld", c_i64)]
+    _at = None
+    _of = None       # (n, rows) that its tensors hold
+
+    @classmethod
+    def of(cls, n, rows, act=Q4_ACT_NONE, scale=1.0, bias=None, residual=None, residual_type=Q4_TYPE_F16, residual_ld=0):
+        ld = residual_ld or n
+        r = _rows_ptr(residual, "Epilogue: residual", rows, n, ld, residual_type, _current_device())
+        s = cls(_dev_ptr(bias, _F32, n), act, scale, r, residual_type, ld)
+        s._keep = (bias, residual)
+        s._at = _device_of(*s._keep)
+        s._of = (n, rows if residual is not None else None)
+        return s
+
+
+class GatedEpilogue(ctypes.Structure):
+    """q4_gated_epilogue; keeps its tensors alive, fp32 of n values each."""
+    _fields_ = [("bias_gate", c_p), ("bias_up", c_p), ("act", c_int)]
+    _at = None
+    _of = None
+
+    @classmethod
+    def of(cls, n, act=Q4_ACT_SILU, bias_gate=None, bias_up=None):
+        s = cls(_dev_ptr(bias_gate, _F32, n), _dev_ptr(bias_up, _F32, n), act)
+        s._keep = (bias_gate, bias_up)
+        s._at = _device_of(*s._keep)
+        s._of = (n, None)
+        return s
+
+
+class BlockNorm(ctypes.Structure):
+    """q4_norms of rows of n values; keeps its tensors alive, fp32 of n values
+    each; a gate with gate_rows of ceil(rows / gate_rows) vectors gate_ld apart
+    (0: n).  A post_weight or post_bias stands for ``post`` too."""
+    _fields_ = [("kind", c_int), ("eps", ctypes.c_float), ("post", c_int), ("post_weight", c_p), ("post_bias", c_p),
+                ("scale", ctypes.c_float), ("gate", c_p), ("gate_ld", c_i64), ("gate_rows", c_int), ("weight", c_p), ("bias", c_p)]
+    _at = None
+    _of = None       # (n, rows): the rows its gate has vectors for, None for any
+
+    @classmethod
+    def of(cls, n, kind=Q4_NORM_RMS, eps=1e-5, weight=None, bias=None, post_weight=None, post_bias=None, scale=1.0, gate=None,
+           gate_ld=0, gate_rows=0, post=False):
+        ld, rows = gate_ld or n, None
+        if gate is not None and gate_rows > 0 and not isinstance(gate, int):
+            vectors = gate.numel() // n if gate.is_contiguous() and ld == n else gate.size(0)
+            g = _rows_ptr(gate, "BlockNorm: gate", vectors, n, ld, Q4_TYPE_F32, _current_device())
+            rows = vectors * gate_rows
+        else:
+            g = _dev_ptr(gate, _F32, n)
+        s = cls(kind, eps, bool(post) or post_weight is not None or post_bias is not None, _dev_ptr(post_weight, _F32, n),
+                _dev_ptr(post_bias, _F32, n), scale, g, ld, gate_rows, _dev_ptr(weight, _F32, n), _dev_ptr(bias, _F32, n))
+        s._keep = (weight, bias, post_weight, post_bias, gate)
+        s._at = _device_of(*s._keep)
+        s._of = (n, rows)
+        return s
+
+
+class Rope(ctypes.Structure):
+    """q4_rotation: ``freqs`` the radians per position of every pair, ``axes``
+    the axis of every pair (None: all 0)."""
+    _fields_ = [("head_dim", c_int), ("rot_dim", c_int), ("style", c_int), ("n_axes", c_int),
+                ("axis", ctypes.c_uint8 * Q4_ROPE_PAIRS), ("turn", ctypes.c_uint64 * Q4_ROPE_PAIRS)]
+
+    @classmethod
+    def of(cls, head_dim, freqs, axes=None, style=Q4_ROPE_HALVES):
+        n = len(freqs)
+        if axes is not None and len(axes) != n:
+            raise Q4Error(Q4_ERR_ARG, f"Rope: {len(axes)} axes for {n} pairs")
+        s = cls()
+        f = (ctypes.c_double * n)(*[float(v) for v in freqs])
+        a = None if axes is None else (c_int * n)(*[int(v) for v in axes])
+        _check(lib().q4_rotation_init(s, head_dim, 2 * n, f, a, style), "q4_rotation_init")
+        return s
+
+
+class RopePlaces(ctypes.Structure):
+    """q4_places: the positions of n_tokens rows on every axis, or those of a
+    paged batch.  The kernels read the arrays; keeps its tensors alive."""
+    _fields_ = [("positions", c_p), ("ld", c_i64), ("n_axes", c_int), ("token_starts", c_p), ("kv_lens", c_p), ("n_seqs", c_int),
+                ("n_tokens", c_int)]
+    _at = None
+
+    @classmethod
+    def of(cls, positions, n_axes, n_tokens, ld=0):
+        """int32 positions, n_axes rows of n_tokens values ld apart (0: n_tokens)."""
+        ld = ld or n_tokens
+        p = _dev_ptr(positions, _INDEX, (n_axes - 1) * ld + n_tokens if n_tokens > 0 else 0)
+        s = cls(p, ld, n_axes, None, None, 0, n_tokens)
+        s._keep = (positions,)
+        s._at = _device_of(positions)
+        return s
+
+    @classmethod
+    def of_batch(cls, token_starts, kv_lens, n_seqs, n_tokens):
+        """The positions that the arrays of a PagedBatch give the rows."""
+        n = max(n_seqs, 0)
+        s = cls(None, 0, 0, _dev_ptr(token_starts, _INDEX, n + 1), _dev_ptr(kv_lens, _INDEX, n), n_seqs, n_tokens)
+        s._keep = (token_starts, kv_lens)
+        s._at = _device_of(*s._keep)
+        return s
+
+
 def _declare(lib):
     sig = {
         "q4_status_string": ([c_int], ctypes.c_char_p),
@@ -162,6 +280,14 @@ def _declare(lib):
         "q4_attn_paged": ([ctypes.POINTER(PagedKV), ctypes.POINTER(PagedBatch), c_p, c_int, c_i64, c_int, c_int, c_int,
                            c_p, c_i64, c_p, c_size, c_p], c_int),
         "q4_attn_paged_workspace_bytes": ([c_int, c_int, c_int], c_size),
+        "q4_gemm": ([c_p, c_p, c_i64, c_int, c_int, c_int, ctypes.POINTER(Epilogue), c_p, c_i64, c_p], c_int),
+        "q4_gemm_gated": ([c_p, c_p, c_p, c_i64, c_int, c_int, c_int, ctypes.POINTER(GatedEpilogue), c_p, c_i64, c_p], c_int),
+        "q4_block_norm": ([ctypes.POINTER(BlockNorm), c_int, c_int, c_p, c_int, c_i64, c_p, c_int, c_i64, c_p, c_int, c_i64,
+                           c_p, c_int, c_i64, c_p], c_int),
+        "q4_rotation_init": ([ctypes.POINTER(Rope), c_int, c_int, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(c_int),
+                              c_int], c_int),
+        "q4_rope": ([ctypes.POINTER(Rope), ctypes.POINTER(RopePlaces), c_int, c_int, c_p, c_int, c_i64, c_p, c_int, c_i64, c_p],
+                    c_int),
         "q4_stream_status": ([c_p, c_p, ctypes.POINTER(c_int)], c_int),
         "q4_stream_tagged": ([c_p, ctypes.POINTER(c_int)], c_int),
         "q4_stream_timeline": ([c_p, c_p, c_int, c_p], c_int),
@@ -536,6 +662,73 @@ def q4_attn_paged(kv: PagedKV, batch: PagedBatch, q, q_type: int, q_ld: int, n_q
 
 def q4_attn_paged_workspace_bytes(n_q_heads: int, n_kv_heads: int, head_dim: int) -> int:
     return lib().q4_attn_paged_workspace_bytes(n_q_heads, n_kv_heads, head_dim)
+
+
+def _made_on(what, dev, *parts):
+    """The descriptors among the parts have to have been made on the device."""
+    for p in parts:
+        if p is not None and p._at is not None and p._at != dev:
+            raise Q4Error(Q4_ERR_ARG, f"{what}: tensors on another device than the current one, {dev}")
+
+
+def _holds(what, part, n, rows):
+    """A descriptor made for rows of n values, and for as many rows as it has memory for."""
+    if part is not None and part._of is not None and (part._of[0] != n or part._of[1] is not None and part._of[1] < rows):
+        raise Q4Error(Q4_ERR_ARG, f"{what}: an epilogue or norms of {part._of} for {rows} rows of {n} values")
+
+
+def _weights_ptr(w, what, n, k, dev):
+    """_ptr of an [n][k] Q4_0 matrix: bytes, in one piece, on the device."""
+    if w is None or isinstance(w, int):
+        return w
+    if w.get_device() != dev or w.element_size() != 1 or not w.is_contiguous() or w.numel() < n * k // 32 * 18:
+        raise Q4Error(Q4_ERR_ARG, f"{what}: a {w.dtype} tensor of shape {tuple(w.shape)} and strides {tuple(w.stride())} on {w.device} "
+                                  f"for the bytes of {n} x {k} weights")
+    return w.data_ptr()
+
+
+def q4_gemm(w, x, x_ld: int, n: int, k: int, rows: int, ep, y, y_ld: int, stream=None):
+    """y = f16(residual + scale * act(W x + bias)) for ``rows`` binary16 rows of x, x_ld apart; ep: an Epilogue or None."""
+    dev = _device() if _device else _current_device()
+    _made_on("q4_gemm", dev, ep)
+    _holds("q4_gemm", ep, n, rows)
+    _check(lib().q4_gemm(_weights_ptr(w, "q4_gemm: w", n, k, dev), _rows_ptr(x, "q4_gemm: x", rows, k, x_ld, Q4_TYPE_F16, dev), x_ld,
+                         n, k, rows, ep, _rows_ptr(y, "q4_gemm: y", rows, n, y_ld, Q4_TYPE_F16, dev), y_ld, _stream_on(stream, dev)),
+           "q4_gemm")
+
+
+def q4_gemm_gated(w_gate, w_up, x, x_ld: int, n: int, k: int, rows: int, ep, y, y_ld: int, stream=None):
+    """y = f16(act(Wgate x + bias_gate) * (Wup x + bias_up)); ep: a GatedEpilogue, or None for SiLU without biases."""
+    what = "q4_gemm_gated"
+    dev = _device() if _device else _current_device()
+    _made_on(what, dev, ep)
+    _holds(what, ep, n, rows)
+    _check(lib().q4_gemm_gated(_weights_ptr(w_gate, what + ": w_gate", n, k, dev), _weights_ptr(w_up, what + ": w_up", n, k, dev),
+                               _rows_ptr(x, what + ": x", rows, k, x_ld, Q4_TYPE_F16, dev), x_ld, n, k, rows, ep,
+                               _rows_ptr(y, what + ": y", rows, n, y_ld, Q4_TYPE_F16, dev), y_ld, _stream_on(stream, dev)), what)
+
+
+def q4_block_norm(norms: BlockNorm, rows: int, block, block_type: int, block_ld: int, residual, residual_type: int, residual_ld: int,
+                  t, t_type: int, t_ld: int, z, z_type: int, z_ld: int, n: int = 0, stream=None):
+    """t = residual + scale * gate * (block or its norm) and z = norm(t) * weight + bias; a missing buffer is None (n: the norms')."""
+    what = "q4_block_norm"
+    dev = _device() if _device else _current_device()
+    _made_on(what, dev, norms)
+    n = n or (norms._of[0] if norms._of else 0)
+    _holds(what, norms, n, rows)
+    _check(lib().q4_block_norm(norms, rows, n, _rows_ptr(block, what + ": block", rows, n, block_ld, block_type, dev), block_type, block_ld,
+                               _rows_ptr(residual, what + ": residual", rows, n, residual_ld, residual_type, dev), residual_type, residual_ld,
+                               _rows_ptr(t, what + ": t", rows, n, t_ld, t_type, dev), t_type, t_ld,
+                               _rows_ptr(z, what + ": z", rows, n, z_ld, z_type, dev), z_type, z_ld, _stream_on(stream, dev)), what)
+
+
+def q4_rope(rope: Rope, places: RopePlaces, n_heads: int, x, x_type: int, x_ld: int, y, y_type: int, y_ld: int, inverse: bool = False,
+            stream=None):
+    """The heads of x's rows turned by their positions (or back) into y, which may be x."""
+    dev, rows, row = _device() if _device else _current_device(), places.n_tokens, n_heads * rope.head_dim
+    _made_on("q4_rope", dev, places)
+    _check(lib().q4_rope(rope, places, 1 if inverse else 0, n_heads, _rows_ptr(x, "q4_rope: x", rows, row, x_ld, x_type, dev), x_type, x_ld,
+                         _rows_ptr(y, "q4_rope: y", rows, row, y_ld, y_type, dev), y_type, y_ld, _stream_on(stream, dev)), "q4_rope")
 
 
 def q4_stream_layers(st, hidden, stream=None, timeout_us: int = 0):
