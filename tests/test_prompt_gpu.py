@@ -36,7 +36,7 @@ def settled():
 
 ODD = [(1, 1, 32), (1, 64, 256), (2, 5, 64), (3, 130, 96), (7, 128, 512), (16, 127, 288), (17, 129, 768), (31, 255, 1024), (33, 256, 2048),
        (64, 257, 256), (65, 300, 1056), (100, 512, 4096), (128, 33, 14336), (129, 1000, 544), (200, 384, 1280), (255, 640, 256), (256, 513, 800),
-       (257, 260, 2304), (300, 1030, 512), (520, 700, 320), (1000, 257, 128), (37, 4099, 4128), (1, 4096, 4096), (4, 6144, 4096)]
+       (257, 260, 2304), (300, 1030, 512), (520, 700, 320), (1000, 257, 128), (1500, 5200, 96), (2100, 4100, 512), (37, 4099, 4128), (1, 4096, 4096), (4, 6144, 4096)]
 
 
 @pytest.mark.parametrize("rows,n,k", ODD)

@@ -492,6 +492,8 @@ cudaError_t oneshot_launch(const uint8_t* w, const uint16_t* x, float* y, int n,
 cudaError_t oneshot_read_status(int* out);
 // Status bits of the paged attention kernels (q4_paged_tile.cu).
 cudaError_t paged_read_status(int* out);
+// ... and of the products of many rows (q4_gemm.cu).
+cudaError_t gemm_read_status(int* out);
 // A product of another kernel was launched on `stream`: the next one-shot
 // product there does not start early.
 void oneshot_chain_break(cudaStream_t stream);
@@ -536,6 +538,11 @@ bool encode_q4_rows(CUtensorMap* m, const uint8_t* w, int n_rows, int k, int box
 // 64), box 64 columns by box_rows rows, stored with the 128-byte swizzle; false
 // if the driver cannot encode it.
 bool encode_f16_rows(CUtensorMap* m, const void* base, int64_t rows, int cols, int box_rows);
+// Host: as encode_f16_rows for rows of any number of values, ld apart (a multiple of 8; values past a row's end and
+// rows past the last read as zeros); and of rows of bytes that lie one behind the other (row_bytes a multiple of 16), not
+// swizzled.
+bool encode_f16_tile(CUtensorMap* m, const void* base, int64_t rows, int cols, int64_t ld, int box_rows);
+bool encode_bytes_tile(CUtensorMap* m, const void* base, int64_t rows, int64_t row_bytes, int box_bytes, int box_rows);
 // Glue launches; pdl as for mma_launch (each glue kernel waits for its inputs first).
 cudaError_t glue_norm(const uint16_t* src16, const float* src32, int batch, int dim, float eps, uint16_t* z,
                       cudaStream_t s, bool pdl = false);
