@@ -82,16 +82,6 @@ __device__ __forceinline__ void gm_wait_warp(GmCtl* c, uint64_t* bar, uint32_t p
   gm_wait(c, bar, parity);
   __syncwarp();
 }
-// ... on what threads of both CTAs arrive at.
-__device__ __forceinline__ void gm_wait_pair(GmCtl* c, uint64_t* bar, uint32_t parity) {
-  const uint32_t limit = *reinterpret_cast<volatile int*>(&c->dead) ? 0 : kGmWaitLimit;
-  if (!mbar_wait_cluster(bar, parity, limit)) {
-    *reinterpret_cast<volatile int*>(&c->dead) = 1;
-    atomicOr(&g_status_gm, ST_DATA_TIMEOUT);
-  }
-  __syncwarp();
-}
-
 // Before the CTA ends: what is still in flight (nothing is, unless a wait has run out), whatever ran out before.
 __device__ __forceinline__ void gm_drain(uint64_t* bar, uint32_t parity) {
   if (!mbar_wait_bounded(bar, parity, kGmWaitLimit)) atomicOr(&g_status_gm, ST_DRAIN_TIMEOUT);
@@ -322,11 +312,11 @@ __global__ void __launch_bounds__(kGmThreads, 1)
       const bool one = elect_one();
       Ring rx, ra, rd;
       for (int64_t t = first; t < tiles; t += stride) {
-        if (t != first) gm_wait_pair(c, &c->d_empty, rd.before());
+        if (t != first) gm_wait_warp(c, &c->d_empty, rd.before());
         tm_after();
         for (int s = 0; s < steps; ++s) {
           gm_wait_warp(c, &c->x_full[rx.slot], rx.turn);
-          gm_wait_pair(c, &c->a_full[ra.slot], ra.turn);
+          gm_wait_warp(c, &c->a_full[ra.slot], ra.turn);
           tm_after();
           if (one) {
             const uint64_t b = mma_sdesc(smem_u32(s_x) + rx.slot * x_stage, 0);
