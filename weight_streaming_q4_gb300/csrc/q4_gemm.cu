@@ -32,25 +32,21 @@ namespace {
 constexpr uint32_t kGmWaitLimit = 1u << 21;
 __device__ int g_status_gm;
 
-constexpr int kGmThreads = 512;
-constexpr int kGmConvert = 4, kGmEpilogue = 12;     // first warps of these roles
+constexpr int kGmThreads = 768;
+constexpr int kGmConvert = 4, kGmEpilogue = 20;     // first warps of these roles
 constexpr int kGmMaxX = 16, kGmMaxW = 8;            // stages of the rings at most
-constexpr int kGmMaxSplit = 4;                      // pairs of a cluster at most
 constexpr int kGmSmem = 232448 - 1024;              // dynamic shared memory at most
 
 template <int MATS, bool RAGGED>
 struct Gm {
-  // bytes between staged rows of W: 256 columns, and where rows do not start 16-byte aligned the pieces around them
-  // (a multiple of 16 whose 16-byte loads by 8 threads side by side fall in different banks)
+  // a staged row of W: the 16-byte pieces that hold 256 columns, and the bytes between rows (a multiple of 16 whose
+  // 16-byte loads by 8 threads side by side fall in different banks)
+  static constexpr int PIECES = RAGGED ? 10 : 9;
   static constexpr int PITCH = RAGGED ? 176 : 144;
   static constexpr int W_STAGE = MATS * 128 * PITCH;
   static constexpr int NA = 8 / MATS;               // operand ring in tensor memory: steps of 64 columns
   static constexpr int A_COL = 256, A_STEP = 32 * MATS;
   static constexpr int D_STEP = 128;                // columns between the two matrices' sums
-};
-
-struct GmMaps {
-  CUtensorMap w[2], x;
 };
 
 struct GmPlan {
@@ -114,6 +110,11 @@ __device__ __forceinline__ GmTile gm_tile(const GmPlan& p, int64_t t) {
   return r;
 }
 
+// 16 bytes to shared memory, those behind the first `bytes` as zeros.
+__device__ __forceinline__ void cp16_part(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 __device__ __forceinline__ __half2 bits_h2(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
@@ -123,15 +124,18 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
 }
 
 // Elements of a block from its d (twice) and one word of codes (elements 4j .. 4j + 3 in the low nibbles, 16 more in the
-// high ones): o[0], o[1] and o[8], o[9].  A nibble q as the low bits of 0x6400 is the binary16 value 1024 + q, a high
-// one 1024 + 16 q: one exact operation each leaves q - 8, and the product with d rounds once.
+// high ones): o[0], o[1] and o[8], o[9].  Two code bytes c as the low bytes of 0x6400 are the binary16 values
+// t = 1024 + c; with the low nibbles replaced by 8, h = 1032 + 16 (c >> 4).  t - h and h / 16 - 72.5 are the nibbles less
+// 8, exactly, and the product with d rounds once.  (Two permutations and two logical operations a word: they share the
+// integer pipe, which paces the conversion together with the eight binary16 ones; masking each nibble apart took six.)
 __device__ __forceinline__ void q4_values8(uint32_t codes, __half2 d, uint32_t* o) {
-  const __half2 bias = bits_h2(0x64086408u), sixteenth = bits_h2(0x2c002c00u), m72 = bits_h2(0xd480d480u);
-  const uint32_t lo = codes & 0x0f0f0f0fu, hi = codes & 0xf0f0f0f0u;
-  o[0] = h2_bits(__hmul2(__hsub2(bits_h2(prmt(lo, 0x64646464u, 0x4140)), bias), d));
-  o[1] = h2_bits(__hmul2(__hsub2(bits_h2(prmt(lo, 0x64646464u, 0x4342)), bias), d));
-  o[8] = h2_bits(__hmul2(__hfma2(bits_h2(prmt(hi, 0x64646464u, 0x4140)), sixteenth, m72), d));
-  o[9] = h2_bits(__hmul2(__hfma2(bits_h2(prmt(hi, 0x64646464u, 0x4342)), sixteenth, m72), d));
+  const __half2 sixteenth = bits_h2(0x2c002c00u), m72 = bits_h2(0xd488d488u);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t t = prmt(codes, 0x64646464u, i ? 0x4342 : 0x4140), h = (t & 0xfff0fff0u) | 0x00080008u;
+    o[i] = h2_bits(__hmul2(__hsub2(bits_h2(t), bits_h2(h)), d));
+    o[8 + i] = h2_bits(__hmul2(__hfma2(bits_h2(h), sixteenth, m72), d));
+  }
 }
 
 // Two blocks (9 words) into a row's 64 values: o[c] holds values 2c and 2c + 1.
@@ -144,6 +148,23 @@ __device__ __forceinline__ void q4_values64(const uint32_t* w, uint32_t* o) {
   }
 }
 
+// Step J (of the four of a staged row's 256 columns): its 9 words out of the 16-byte pieces that hold them.
+template <int J>
+__device__ __forceinline__ void staged_words(const char* row, uint32_t* w) {
+  uint32_t v[12];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const uint4 f = *reinterpret_cast<const uint4*>(row + 32 * J + 16 * i);
+    v[4 * i] = f.x, v[4 * i + 1] = f.y, v[4 * i + 2] = f.z, v[4 * i + 3] = f.w;
+  }
+#pragma unroll
+  for (int i = 0; i < 9; ++i) w[i] = v[J + i];
+}
+
+// t / (1 + e^z): SiLU with z = -t, and GELU's tanh form, since (1 + tanh y) / 2 = 1 / (1 + e^(-2 y)).  An exponent that
+// overflows leaves 0 for every finite t.
+__device__ __forceinline__ float over_1_and_exp(float t, float z) { return __fdividef(t, 1.f + __expf(z)); }
+
 // The activation of N values; the choice is the same for all.
 template <int N>
 __device__ __forceinline__ void activate(float* t, int act) {
@@ -154,7 +175,7 @@ __device__ __forceinline__ void activate(float* t, int act) {
       break;
     case Q4_ACT_SILU:
 #pragma unroll
-      for (int i = 0; i < N; ++i) t[i] = t[i] / (1.f + __expf(-t[i]));
+      for (int i = 0; i < N; ++i) t[i] = over_1_and_exp(t[i], -t[i]);
       break;
     case Q4_ACT_GELU:
 #pragma unroll
@@ -162,7 +183,7 @@ __device__ __forceinline__ void activate(float* t, int act) {
       break;
     case Q4_ACT_GELU_TANH:
 #pragma unroll
-      for (int i = 0; i < N; ++i) t[i] = 0.5f * t[i] * (1.f + tanhf(0.79788456f * (t[i] + 0.044715f * t[i] * t[i] * t[i])));
+      for (int i = 0; i < N; ++i) t[i] = over_1_and_exp(t[i], -1.5957691f * (t[i] + 0.044715f * t[i] * t[i] * t[i]));
       break;
     default: break;
   }
@@ -199,7 +220,7 @@ __device__ __forceinline__ void finish(const GemmArgs& a, int i, int row0, int r
 
 template <int MATS, bool RAGGED>
 __global__ void __launch_bounds__(kGmThreads, 1)
-    gemm_kernel(const __grid_constant__ GemmArgs a, const __grid_constant__ GmMaps maps, const __grid_constant__ GmPlan p) {
+    gemm_kernel(const __grid_constant__ GemmArgs a, const __grid_constant__ CUtensorMap x_map, const __grid_constant__ GmPlan p) {
   using G = Gm<MATS, RAGGED>;
   extern __shared__ char smem_raw[];
   GmCtl* c = reinterpret_cast<GmCtl*>(smem_raw);
@@ -214,12 +235,12 @@ __global__ void __launch_bounds__(kGmThreads, 1)
   const int part = static_cast<int>(rank >> 1);        // of k
   const int nb = a.k / kQK, units = (nb + 7) / 8;      // blocks, and groups of 256 columns, of a row
   const int u0 = units * part / p.split, u1 = units * (part + 1) / p.split;
-  const int steps = (min(nb, u1 * 8) - u0 * 8 + 1) / 2;        // of 64 columns, of a tile
+  const int steps = (u1 - u0) * 4;                     // of 64 columns, of a tile (past the end of a row zeros)
   const int64_t tiles = static_cast<int64_t>(p.tok_tiles) * p.row_tiles;
   const int64_t first = blockIdx.x / (2 * p.split), stride = gridDim.x / (2 * p.split);
 
   if (tid == 0) {
-    for (int i = 0; i < kGmMaxW; ++i) mbar_init(&c->w_full[i], 1), mbar_init(&c->w_empty[i], 4 * MATS);
+    for (int i = 0; i < kGmMaxW; ++i) mbar_init(&c->w_full[i], 64), mbar_init(&c->w_empty[i], 16);
     for (int i = 0; i < kGmMaxX; ++i) mbar_init(&c->x_full[i], 1), mbar_init(&c->x_empty[i], 1);
     for (int i = 0; i < 8; ++i) mbar_init(&c->a_full[i], 8 * MATS), mbar_init(&c->a_empty[i], 1);
     mbar_init(&c->d_full, 1), mbar_init(&c->d_empty, 8);
@@ -233,60 +254,41 @@ __global__ void __launch_bounds__(kGmThreads, 1)
   tm_after();
   const uint32_t tmem = __shfl_sync(~0u, c->tmem, 0);
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 3) {
     // ---------------------------------------------------------------- copies of W
+    // Two warps, a matrix each or half of the rows each: 8 threads to the first 128 bytes of a row, the rest of 16 or
+    // 32 rows at a time behind them.  (Tensor copies of 144-byte rows took 12.5 cycles a row, three times as long as the
+    // products of a step of few rows of x.)
+    constexpr int ROWS = MATS == 2 ? 128 : 64, REST = G::PIECES - 8;
+    const int which = warp == 3, mat = MATS == 2 ? which : 0, r0 = MATS == 2 ? 0 : 64 * which;
+    const int64_t row_bytes = static_cast<int64_t>(nb) * kBlockBytes, end = row_bytes * a.n;
+    const uint8_t* const w = a.w[mat];
+    const uint32_t to0 = smem_u32(s_w) + (mat * 128 + r0) * G::PITCH;
     Ring r;
     int64_t n = 0;
     for (int64_t t = first; t < tiles; t += stride) {
-      const int w0 = gm_tile(p, t).row * 256 + half * 128;
+      const int w0 = gm_tile(p, t).row * 256 + half * 128 + r0;
       for (int u = u0; u < u1; ++u, ++n) {
         if (n >= p.nw) gm_wait_warp(c, &c->w_empty[r.slot], r.before());
-        char* to = s_w + r.slot * G::W_STAGE;
-        if (!RAGGED) {
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&c->w_full[r.slot], G::W_STAGE);
-            for (int m = 0; m < MATS; ++m) tma_load_2d(to + m * 128 * G::PITCH, &maps.w[m], u * 144, w0, &c->w_full[r.slot]);
-          }
-        } else {
-          // a row's blocks with the bytes around them up to 16-byte boundaries, but not past the matrix's end: the
-          // few bytes behind the last boundary there are copied by hand
-          const int64_t row_bytes = static_cast<int64_t>(nb) * kBlockBytes, end = row_bytes * a.n;
-          const int bytes = min(8, nb - u * 8) * kBlockBytes;
-          uint32_t total = 0;
+        const uint32_t to = to0 + r.slot * G::W_STAGE;
+        auto copy = [&](int row, int piece) {
+          int64_t at = (w0 + row) * row_bytes + u * 144;
+          if (RAGGED) at &= ~int64_t{15};
+          at += piece * 16;
+          int bytes = w0 + row < a.n ? 16 : 0;
+          if (RAGGED && bytes) bytes = static_cast<int>(max(min(end - at, int64_t{16}), int64_t{0}));
+          cp16_part(to + row * G::PITCH + piece * 16, w + (bytes ? at : 0), bytes);
+        };
+#pragma unroll 8
+        for (int i = 0; i < ROWS; i += 4) copy(i + (lane >> 3), lane & 7);
 #pragma unroll
-          for (int i = 0; i < 4 * MATS; ++i) {
-            const int row = w0 + (i & 3) * 32 + lane;
-            if (row >= a.n) continue;
-            const int64_t at = row * row_bytes + u * 144, lo = at & ~int64_t{15};
-            const int64_t hi = min((at + bytes + 15) & ~int64_t{15}, end & ~int64_t{15});
-            total += static_cast<uint32_t>(max(hi - lo, int64_t{0}));
-            if (at + bytes > (end & ~int64_t{15})) {
-              char* d = to + ((i >> 2) * 128 + (i & 3) * 32 + lane) * G::PITCH;
-              for (int64_t b = max(end & ~int64_t{15}, lo); b < at + bytes; b += 2)
-                *reinterpret_cast<uint16_t*>(d + (b - lo)) = *reinterpret_cast<const uint16_t*>(a.w[i >> 2] + b);
-            }
-          }
-          fence_async();
-          total = __reduce_add_sync(~0u, total);
-          __syncwarp();
-          if (lane == 0) mbar_arrive_expect_tx(&c->w_full[r.slot], total);
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 4 * MATS; ++i) {
-            const int row = w0 + (i & 3) * 32 + lane;
-            if (row >= a.n) continue;
-            const int64_t at = row * row_bytes + u * 144, lo = at & ~int64_t{15};
-            const int64_t hi = min((at + bytes + 15) & ~int64_t{15}, end & ~int64_t{15});
-            if (hi > lo)
-              bulk_g2s(to + ((i >> 2) * 128 + (i & 3) * 32 + lane) * G::PITCH, a.w[i >> 2] + lo, static_cast<uint32_t>(hi - lo),
-                       &c->w_full[r.slot]);
-          }
-        }
-        __syncwarp();
+        for (int i = 0; i < ROWS; i += 32 / REST) copy(i + lane / REST, 8 + lane % REST);
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&c->w_full[r.slot])) : "memory");
         r.step(p.nw);
       }
     }
-    for (int64_t u = n > p.nw ? n - p.nw : 0; u < n; ++u) gm_drain(&c->w_full[u % p.nw], static_cast<uint32_t>(u / p.nw) & 1);
+    // the last copies have landed before the CTA ends
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == 1) {
     // ---------------------------------------------------------------- copies of x
     Ring r;
@@ -297,7 +299,7 @@ __global__ void __launch_bounds__(kGmThreads, 1)
         if (n >= p.nx) gm_wait_warp(c, &c->x_empty[r.slot], r.before());
         if (lane == 0) {
           if (half == 0) mbar_arrive_expect_tx(&c->x_full[r.slot], 2 * x_stage);
-          tma2_load_2d(s_x + r.slot * x_stage, &maps.x, u0 * 256 + s * 64, x0, cluster_addr(&c->x_full[r.slot], leader));
+          tma2_load_2d(s_x + r.slot * x_stage, &x_map, u0 * 256 + s * 64, x0, cluster_addr(&c->x_full[r.slot], leader));
         }
         __syncwarp();
         r.step(p.nx);
@@ -340,67 +342,65 @@ __global__ void __launch_bounds__(kGmThreads, 1)
     }
   } else if (warp >= kGmConvert && warp < kGmEpilogue) {
     // ---------------------------------------------------------------- conversion
-    // Warps q + 4 and q + 8 hold rows 32 q .. of the CTA: of one matrix the groups of 256 columns in turn, of two a
-    // matrix each.
+    // Four warps hold rows 32 q .. of the CTA.  Of one matrix each takes one of the four steps of every 256 columns, of
+    // two matrices two of the steps of one: a warp's place in the ring of operands is the same every time round.
     const int q = warp & 3, mine = (warp - kGmConvert) >> 2;
-    const int mat = MATS == 2 ? mine : 0;
+    const int mat = MATS == 2 ? mine & 1 : 0;
     const uint32_t to = tmem + G::A_COL + mat * 32 + (static_cast<uint32_t>(q * 32) << 16);
-    Ring rw, ra;
-    int64_t n = 0, step = 0;
+    const char* const row0 = s_w + (mat * 128 + q * 32 + lane) * G::PITCH;
+    const uint32_t full0 = cluster_addr(&c->a_full[0], leader);
+    Ring rw;
+    uint32_t n = 0;                                     // groups of 256 columns so far
     for (int64_t t = first; t < tiles; t += stride) {
       const int w0 = gm_tile(p, t).row * 256 + half * 128 + q * 32 + lane;
       const int shift = RAGGED ? static_cast<int>((static_cast<int64_t>(w0) * nb * kBlockBytes) & 15) : 0;
       for (int u = u0; u < u1; ++u, ++n) {
-        const int here = min(4, (nb - u * 8 + 1) / 2);
-        if (MATS == 1 && (n & 1) != mine) {
-          rw.step(p.nw);
-          for (int j = 0; j < here; ++j) ra.step(G::NA);
-          step += here;
-          continue;
-        }
         gm_wait_warp(c, &c->w_full[rw.slot], rw.turn);
-        const char* row = s_w + rw.slot * G::W_STAGE + (mat * 128 + q * 32 + lane) * G::PITCH;
-        uint32_t w[40];
-        if (!RAGGED) {
+        const char* row = row0 + rw.slot * G::W_STAGE;
 #pragma unroll
-          for (int i = 0; i < 9; ++i) {
-            const uint4 v = *reinterpret_cast<const uint4*>(row + 16 * i);
-            w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&c->w_empty[rw.slot]);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (j >= here) break;
-          uint32_t o[32];
+        for (int i = 0; i < MATS; ++i) {
+          const int j = MATS == 2 ? (mine >> 1) + 2 * i : mine;
+          uint32_t w[9], o[32];
           if (RAGGED) {
             const uint32_t* src = reinterpret_cast<const uint32_t*>(row + (shift & ~3) + 36 * j);
-            uint32_t v[10];
-#pragma unroll
-            for (int i = 0; i < 10; ++i) v[i] = src[i];
             const uint32_t by = (shift & 2) * 8;
+            uint32_t v = src[0];
 #pragma unroll
-            for (int i = 0; i < 9; ++i) w[9 * j + i] = __funnelshift_r(v[i], v[i + 1], by);
-            if (j == here - 1) {
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&c->w_empty[rw.slot]);
+            for (int e = 0; e < 9; ++e) {
+              const uint32_t next = src[e + 1];
+              w[e] = __funnelshift_r(v, next, by);
+              v = next;
+            }
+          } else {
+            switch (j) {
+              case 0: staged_words<0>(row, w); break;
+              case 1: staged_words<1>(row, w); break;
+              case 2: staged_words<2>(row, w); break;
+              default: staged_words<3>(row, w); break;
             }
           }
-          q4_values64(w + 9 * j, o);
-          if (RAGGED && u * 8 + 2 * j + 1 >= nb) {
+          q4_values64(w, o);
+          if (RAGGED) {
+            // (a row's last blocks: what lies behind them in memory is not its own)
+            const int left = nb - u * 8 - 2 * j;
+            if (left < 2) {
 #pragma unroll
-            for (int i = 16; i < 32; ++i) o[i] = 0;      // (a row of an odd number of blocks)
+              for (int e = 0; e < 32; ++e)
+                if (e >= 16 || left < 1) o[e] = 0;
+            }
           }
-          if (step >= G::NA) gm_wait_warp(c, &c->a_empty[ra.slot], ra.before());
+          // ring of two groups of one matrix's steps, one group of two matrices'
+          const uint32_t slot = MATS == 2 ? j : (n & 1) * 4 + j, turn = MATS == 2 ? n : n >> 1;
+          if (turn > 0) gm_wait_warp(c, &c->a_empty[slot], (turn & 1) ^ 1);
           tm_after();
-          tm_st32(to + ra.slot * G::A_STEP, o);
+          tm_st32(to + slot * G::A_STEP, o);
           tm_st_wait();
           tm_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(cluster_addr(&c->a_full[ra.slot], leader));
-          ra.step(G::NA);
-          ++step;
+          if (lane == 0) {
+            mbar_arrive_cluster(full0 + slot * 8);
+            if (i == MATS - 1) mbar_arrive(&c->w_empty[rw.slot]);
+          }
         }
         rw.step(p.nw);
       }
@@ -418,15 +418,15 @@ __global__ void __launch_bounds__(kGmThreads, 1)
       if (p.split > 1) break;
       const int i = tile.row * 256 + half * 128 + q * 32 + lane;
       const float bg = a.bias[0] && i < a.n ? __ldg(a.bias[0] + i) : 0.f, bu = MATS == 2 && a.bias[1] && i < a.n ? __ldg(a.bias[1] + i) : 0.f;
-      for (int b = 0; b < p.bn; b += 32) {
-        const int row0 = tile.tok * p.bn + b, rows = min(a.rows - row0, 32);
+      for (int b = 0; b < p.bn; b += 16) {
+        const int row0 = tile.tok * p.bn + b, rows = min(a.rows - row0, 16);
         if (rows <= 0) break;
-        uint32_t g[32], u[32];
-        tm_ld32(from + b, g);
-        if (MATS == 2) tm_ld32(from + G::D_STEP + b, u);
-        tm_ld_wait(g);
-        if (MATS == 2) tm_ld_waited(u);
-        finish<MATS, 32>(a, i, row0, rows, reinterpret_cast<float*>(g), reinterpret_cast<float*>(u), bg, bu);
+        uint32_t g[16], u[16];
+        tm_ld16(from + b, g);
+        if (MATS == 2) tm_ld16(from + G::D_STEP + b, u);
+        tm_ld16_wait(g);
+        if (MATS == 2) tm_ld16_waited(u);
+        finish<MATS, 16>(a, i, row0, rows, reinterpret_cast<float*>(g), reinterpret_cast<float*>(u), bg, bu);
       }
       tm_before();
       __syncwarp();
@@ -461,12 +461,12 @@ __global__ void __launch_bounds__(kGmThreads, 1)
         if (j == own) continue;
         const uint32_t to = cluster_addr(recv, 2 * j + half);
         for (int m = 0; m < MATS; ++m)
-          for (int b = 0; b < w; b += 32) {
-            uint32_t v[32];
-            tm_ld32(from + m * G::D_STEP + j * w + b, v);
-            tm_ld_wait(v);
+          for (int b = 0; b < w; b += 16) {
+            uint32_t v[16];
+            tm_ld16(from + m * G::D_STEP + j * w + b, v);
+            tm_ld16_wait(v);
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
+            for (int e = 0; e < 16; ++e)
               if (b + e < w)
                 asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(to + (((own * MATS + m) * w + b + e) * 128 + q * 32 + lane) * 4),
                              "r"(v[e])
@@ -479,26 +479,26 @@ __global__ void __launch_bounds__(kGmThreads, 1)
       const GmTile tile = gm_tile(p, first);
       const int i = tile.row * 256 + half * 128 + q * 32 + lane;
       const float bg = a.bias[0] && i < a.n ? __ldg(a.bias[0] + i) : 0.f, bu = MATS == 2 && a.bias[1] && i < a.n ? __ldg(a.bias[1] + i) : 0.f;
-      for (int b = 0; b < w; b += 32) {
+      for (int b = 0; b < w; b += 16) {
         const int col = own * w + b, row0 = tile.tok * p.bn + col;
-        const int rows = min(min(w - b, a.rows - row0), 32);
+        const int rows = min(min(w - b, a.rows - row0), 16);
         if (rows <= 0) break;
-        uint32_t v[MATS][32];
-        float sum[MATS][32];
+        float sum[MATS][16];
 #pragma unroll
         for (int m = 0; m < MATS; ++m) {
-          tm_ld32(from + m * G::D_STEP + col, v[m]);
-          tm_ld_wait(v[m]);
+          uint32_t v[16];
+          tm_ld16(from + m * G::D_STEP + col, v);
+          tm_ld16_wait(v);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) sum[m][e] = 0.f;
+          for (int e = 0; e < 16; ++e) sum[m][e] = 0.f;
           for (int j = 0; j < p.split; ++j) {
             const float* src = recv + ((j * MATS + m) * w + b) * 128 + q * 32 + lane;
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (e < rows) sum[m][e] += j == own ? __uint_as_float(v[m][e]) : src[e * 128];
+            for (int e = 0; e < 16; ++e)
+              if (e < rows) sum[m][e] += j == own ? __uint_as_float(v[e]) : src[e * 128];
           }
         }
-        finish<MATS, 32>(a, i, row0, rows, sum[0], sum[MATS - 1], bg, bu);
+        finish<MATS, 16>(a, i, row0, rows, sum[0], sum[MATS - 1], bg, bu);
       }
     }
     tm_before();
@@ -513,10 +513,10 @@ __global__ void __launch_bounds__(kGmThreads, 1)
 
 // ------------------------------------------------------------------ host
 
-// Time of a plan in cycles, roughly: waves of tiles, each as long as the slowest of its products, its conversion and its
-// copies, and its epilogue.
-GmPlan plan(const GemmArgs& a, int sms, int mats, int w_stage) {
-  const int pairs = sms / 2, units = (a.k + 255) / 256, most = 256 / mats;
+// Time of a plan in cycles, roughly: waves of tiles, each as long as the slower of its products and its conversion, and
+// its epilogue.
+GmPlan plan(const GemmArgs& a, const PromptDevice& d, int mats, int w_stage) {
+  const int units = (a.k + 255) / 256, most = 256 / mats;
   GmPlan best = {};
   best.row_tiles = (a.n + 255) / 256;
   double least = 0;
@@ -526,11 +526,12 @@ GmPlan plan(const GemmArgs& a, int sms, int mats, int w_stage) {
     const int bn = ((a.rows + tok - 1) / tok + 31) / 32 * 32;
     if (i > 0 && (bn < 64 || (a.rows + bn - 1) / bn != tok)) break;
     const int64_t tiles = static_cast<int64_t>(tok) * best.row_tiles;
-    for (int split = 1; split <= kGmMaxSplit; split *= 2) {
-      if (split > 1 && (tiles * split > pairs || units < 2 * split)) break;
-      const int64_t waves = (tiles + pairs - 1) / pairs;
+    for (int log = 0; log < 3; ++log) {
+      const int split = 1 << log;
+      if (log > 0 && (tiles > d.clusters[log] || units < 2 * split)) break;
+      const int64_t waves = (tiles + d.clusters[log] - 1) / d.clusters[log];
       const double step = 2. * bn * mats > 260. * mats ? 2. * bn * mats : 260. * mats;
-      const double time = waves * ((units + split - 1) / split * 4 * step + 1500 + 8. * bn * mats) + (split > 1 ? 3000 + 4. * bn * mats : 0);
+      const double time = waves * ((units + split - 1) / split * 4 * step + 1500 + 8. * bn * mats) + (log ? 3000 + 4. * bn * mats : 0);
       if (least == 0 || time < least) least = time, best.bn = bn, best.split = split, best.tok_tiles = tok;
     }
   }
@@ -545,47 +546,56 @@ GmPlan plan(const GemmArgs& a, int sms, int mats, int w_stage) {
   return best;
 }
 
-template <int MATS, bool RAGGED>
-cudaError_t launch(const GemmArgs& a, int sms, cudaStream_t s) {
-  using G = Gm<MATS, RAGGED>;
-  const GmPlan p = plan(a, sms, MATS, G::W_STAGE);
-  GmMaps maps = {};
-  if (!encode_f16_tile(&maps.x, a.x, a.rows, a.k, a.x_ld, p.bn / 2)) return cudaErrorInvalidValue;
-  for (int m = 0; m < MATS && !RAGGED; ++m)
-    if (!encode_bytes_tile(&maps.w[m], a.w[m], a.n, static_cast<int64_t>(a.k / kQK) * kBlockBytes, 144, 128)) return cudaErrorInvalidValue;
-  const int64_t tiles = static_cast<int64_t>(p.tok_tiles) * p.row_tiles;
-  const int64_t clusters = p.split > 1 || tiles < sms / 2 ? tiles : sms / 2;
+cudaLaunchConfig_t config(int clusters, int split, cudaLaunchAttribute* at, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(clusters * 2 * p.split));
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * 2 * split));
   cfg.blockDim = dim3(kGmThreads);
   cfg.dynamicSmemBytes = kGmSmem;
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = 2 * p.split, at[0].val.clusterDim.y = 1, at[0].val.clusterDim.z = 1;
+  at->id = cudaLaunchAttributeClusterDimension;
+  at->val.clusterDim.x = 2 * split, at->val.clusterDim.y = 1, at->val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gemm_kernel<MATS, RAGGED>, a, maps, p);
+  return cfg;
 }
 
 template <int MATS, bool RAGGED>
-cudaError_t prepare() {
-  return cudaFuncSetAttribute(gemm_kernel<MATS, RAGGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGmSmem);
+cudaError_t launch(const GemmArgs& a, const PromptDevice& d, cudaStream_t s) {
+  using G = Gm<MATS, RAGGED>;
+  const GmPlan p = plan(a, d, MATS, G::W_STAGE);
+  CUtensorMap x_map;
+  if (!encode_f16_tile(&x_map, a.x, a.rows, a.k, a.x_ld, p.bn / 2)) return cudaErrorInvalidValue;
+  const int64_t tiles = static_cast<int64_t>(p.tok_tiles) * p.row_tiles;
+  cudaLaunchAttribute at;
+  const cudaLaunchConfig_t cfg = config(static_cast<int>(tiles < d.clusters[0] ? tiles : d.clusters[0]), p.split, &at, s);
+  return cudaLaunchKernelEx(&cfg, gemm_kernel<MATS, RAGGED>, a, x_map, p);
+}
+
+template <int MATS, bool RAGGED>
+cudaError_t prepare(PromptDevice* d) {
+  cudaError_t e = cudaFuncSetAttribute(gemm_kernel<MATS, RAGGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGmSmem);
+  for (int log = 0; e == cudaSuccess && log < 3; ++log) {
+    cudaLaunchAttribute at;
+    const cudaLaunchConfig_t cfg = config(1, 1 << log, &at, nullptr);
+    e = cudaOccupancyMaxActiveClusters(&d->clusters[log], gemm_kernel<MATS, RAGGED>, &cfg);
+    if (e == cudaSuccess && d->clusters[log] < 1) e = cudaErrorInvalidConfiguration;
+  }
+  return e;
 }
 
 }  // namespace
 
-cudaError_t gemm_prepare() {
-  const cudaError_t e[4] = {prepare<1, false>(), prepare<1, true>(), prepare<2, false>(), prepare<2, true>()};
+cudaError_t gemm_prepare(PromptDevice* d) {
+  const cudaError_t e[4] = {prepare<1, false>(d), prepare<1, true>(d), prepare<2, false>(d), prepare<2, true>(d)};
   for (cudaError_t x : e)
     if (x != cudaSuccess) return x;
   return cudaSuccess;
 }
 
-cudaError_t gemm_launch(const GemmArgs& a, int sms, cudaStream_t s) {
+cudaError_t gemm_launch(const GemmArgs& a, const PromptDevice& d, cudaStream_t s) {
   const bool ragged = a.k % 256 != 0;
-  if (a.w[1]) return ragged ? launch<2, true>(a, sms, s) : launch<2, false>(a, sms, s);
-  return ragged ? launch<1, true>(a, sms, s) : launch<1, false>(a, sms, s);
+  if (a.w[1]) return ragged ? launch<2, true>(a, d, s) : launch<2, false>(a, d, s);
+  return ragged ? launch<1, true>(a, d, s) : launch<1, false>(a, d, s);
 }
 
 cudaError_t gemm_read_status(int* out) {

@@ -36,8 +36,13 @@ struct GemmArgs {
   __half* y;
   int64_t y_ld;
 };
-cudaError_t gemm_prepare();
-cudaError_t gemm_launch(const GemmArgs& a, int sms, cudaStream_t s);
+// What the kernels need to know of the device they run on.
+struct PromptDevice {
+  int sms;
+  int clusters[3];          // of 2, 4 and 8 CTAs of the product's kernel that run at once
+};
+cudaError_t gemm_prepare(PromptDevice* d);
+cudaError_t gemm_launch(const GemmArgs& a, const PromptDevice& d, cudaStream_t s);
 
 // ------------------------------------------------------------------ norms (q4_block_norm.cu)
 

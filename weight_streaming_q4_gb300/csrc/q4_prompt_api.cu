@@ -4,6 +4,8 @@
 #include <math.h>
 #include <stdint.h>
 #include <string.h>
+#include <stdio.h>
+#include <stdlib.h>
 
 #include <mutex>
 
@@ -31,21 +33,22 @@ int check_rows(const void* p, int type, int64_t ld, int64_t row) {
     if (e_ != cudaSuccess) return q4::record_cuda_error(e_);    \
   } while (0)
 
-// SMs of the current device, whose kernels are made ready on its first call.
-int sm_count(int* sms) {
+// The current device, whose kernels are made ready on its first call.
+int device_of(const q4::PromptDevice** out) {
   static std::mutex mutex;
-  static int known[64];
+  static q4::PromptDevice known[64];
   int dev = 0;
   Q4_CUDA(cudaGetDevice(&dev));
   if (dev < 0 || dev >= 64) return Q4_ERR_ARG;
   std::lock_guard<std::mutex> lock(mutex);
-  if (known[dev] == 0) {
-    int n = 0;
-    Q4_CUDA(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev));
-    Q4_CUDA(q4::gemm_prepare());
-    known[dev] = n;
+  if (known[dev].sms == 0) {
+    q4::PromptDevice d = {};
+    Q4_CUDA(q4::gemm_prepare(&d));
+    Q4_CUDA(cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev));
+    if (getenv("Q4DBG")) printf("clusters %d %d %d\n", d.clusters[0], d.clusters[1], d.clusters[2]);
+    known[dev] = d;
   }
-  *sms = known[dev];
+  *out = &known[dev];
   return Q4_OK;
 }
 
@@ -66,10 +69,10 @@ int run_gemm(const void* w0, const void* w1, const uint16_t* x, int64_t x_ld, in
   a.bias[0] = bias0, a.bias[1] = bias1;
   a.act = act, a.scale = scale, a.residual = residual;
   a.y = reinterpret_cast<__half*>(y), a.y_ld = y_ld;
-  int sms = 0;
-  const int st = sm_count(&sms);
+  const q4::PromptDevice* d = nullptr;
+  const int st = device_of(&d);
   if (st != Q4_OK) return st;
-  Q4_CUDA(q4::gemm_launch(a, sms, static_cast<cudaStream_t>(stream)));
+  Q4_CUDA(q4::gemm_launch(a, *d, static_cast<cudaStream_t>(stream)));
   return Q4_OK;
 }
 
@@ -171,8 +174,8 @@ extern "C" int q4_rope(const q4_rotation* rot, const q4_places* places, int inve
   a.rows = places->n_tokens, a.heads = n_heads, a.inverse = inverse != 0;
   a.x = {x, x_ld, x_type == Q4_TYPE_F32};
   a.y = {y, y_ld, y_type == Q4_TYPE_F32};
-  int sms = 0;
-  if ((st = sm_count(&sms)) != Q4_OK) return st;
-  Q4_CUDA(q4::rope_launch(a, sms, static_cast<cudaStream_t>(stream)));
+  const q4::PromptDevice* d = nullptr;
+  if ((st = device_of(&d)) != Q4_OK) return st;
+  Q4_CUDA(q4::rope_launch(a, d->sms, static_cast<cudaStream_t>(stream)));
   return Q4_OK;
 }

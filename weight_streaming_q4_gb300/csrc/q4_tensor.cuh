@@ -59,6 +59,18 @@ __device__ __forceinline__ void tm_ld_wait(uint32_t* x) {
 __device__ __forceinline__ void tm_ld_waited(uint32_t* x) {
   asm volatile("" : Q4_IO8(x, 0), Q4_IO8(x, 8), Q4_IO8(x, 16), Q4_IO8(x, 24)::"memory");
 }
+// ... of 16 columns.
+__device__ __forceinline__ void tm_ld16(uint32_t addr, uint32_t* x) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : Q4_OUT8(x, 0), Q4_OUT8(x, 8)
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tm_ld16_wait(uint32_t* x) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : Q4_IO8(x, 0), Q4_IO8(x, 8)::"memory");
+}
+__device__ __forceinline__ void tm_ld16_waited(uint32_t* x) { asm volatile("" : Q4_IO8(x, 0), Q4_IO8(x, 8)::"memory"); }
 __device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t* x) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
