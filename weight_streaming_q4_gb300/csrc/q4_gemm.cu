@@ -2,9 +2,8 @@
 //   y[r][i] = f16(residual + scale * act(sum_k W[i][k] x[r][k] + bias[i])),  or  f16(act(g) * u) of two matrices.
 //
 // The weights are the first operand of the tensor cores, 256 rows of W per
-// pair of CTAs (128 in each), and bn <= 256 rows of x the second (128 of two
-// matrices' shared x).  A pair walks tiles of 256 x bn outputs in steps of 64
-// columns of k:
+// pair of CTAs (128 in each), and bn <= 128 rows of x the second.  A pair walks
+// tiles of 256 x bn outputs along k:
 //   copies      W blocks as they lie in memory, 256 columns at a time, and the CTA's
 //               half of x's rows (128-byte swizzle), by TMA into two rings
 //   conversion  a thread per row of W: nibbles to f16((q - 8) * d) in registers,
@@ -36,6 +35,9 @@ constexpr int kGmThreads = 768;
 constexpr int kGmConvert = 4, kGmEpilogue = 20;     // first warps of these roles
 constexpr int kGmMaxX = 16, kGmMaxW = 8;            // stages of the rings at most
 constexpr int kGmSmem = 232448 - 1024;              // dynamic shared memory at most
+constexpr int kGmCols = 512, kGmSums = 256;         // columns of tensor memory, and of sums at most
+constexpr int kGmStage = 64;                        // columns of an operand stage
+constexpr int kGmMaxA = 7;                          // operand stages at most
 
 template <int MATS, bool RAGGED>
 struct Gm {
@@ -44,21 +46,19 @@ struct Gm {
   static constexpr int PIECES = RAGGED ? 10 : 9;
   static constexpr int PITCH = RAGGED ? 176 : 144;
   static constexpr int W_STAGE = MATS * 128 * PITCH;
-  static constexpr int NA = 8 / MATS;               // operand ring in tensor memory: steps of 64 columns
-  static constexpr int A_COL = 256, A_STEP = 32 * MATS;
-  static constexpr int D_STEP = 128;                // columns between the two matrices' sums
 };
 
 struct GmPlan {
   int bn;             // rows of x of a tile, a multiple of 32 (what a pair's product takes)
   int split;          // pairs that share a tile
-  int nx, nw;         // stages of the rings
+  int sums;           // tiles whose sums have a place: with two, one is finished while the next one is formed
+  int na, nx, nw;     // stages of the rings: operands in tensor memory, x, W
   int tok_tiles, row_tiles, group;      // tiles; tiles of x that follow one another before the next rows of W
 };
 
 struct GmCtl {
-  uint64_t w_full[kGmMaxW], w_empty[kGmMaxW], x_full[kGmMaxX], x_empty[kGmMaxX], a_full[8], a_empty[8];
-  uint64_t d_full, d_empty;
+  uint64_t w_full[kGmMaxW], w_empty[kGmMaxW], x_full[kGmMaxX], x_empty[kGmMaxX], a_full[kGmMaxA], a_empty[kGmMaxA];
+  uint64_t d_full[2], d_empty[2];
   uint32_t tmem;
   int dead;
 };
@@ -66,53 +66,60 @@ static_assert(sizeof(GmCtl) <= 1024, "control data fits its place");
 
 // A wait that gives up at once when one has run out before: the roles walk on and the kernel ends (its results do not
 // count: the status word says so).
-__device__ __forceinline__ void gm_wait(GmCtl* c, uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ void gm_wait_one(GmCtl* c, uint64_t* bar, uint32_t parity) {
   if (mbar_test_wait(bar, parity)) return;
-  const uint32_t limit = *reinterpret_cast<volatile int*>(&c->dead) ? 0 : kGmWaitLimit;
-  if (!mbar_wait_bounded(bar, parity, limit)) {
-    *reinterpret_cast<volatile int*>(&c->dead) = 1;
-    atomicOr(&g_status_gm, ST_FULL_TIMEOUT);
-  }
+  for (uint32_t i = 0; !mbar_try_wait(bar, parity); ++i)
+    if (i >= kGmWaitLimit || *reinterpret_cast<volatile int*>(&c->dead)) {
+      *reinterpret_cast<volatile int*>(&c->dead) = 1;
+      atomicOr(&g_status_gm, ST_FULL_TIMEOUT);
+      break;
+    }
 }
-__device__ __forceinline__ void gm_wait_warp(GmCtl* c, uint64_t* bar, uint32_t parity) {
-  gm_wait(c, bar, parity);
+__device__ __forceinline__ void gm_wait(GmCtl* c, uint64_t* bar, uint32_t parity) {
+  gm_wait_one(c, bar, parity);
   __syncwarp();
 }
+
 // Before the CTA ends: what is still in flight (nothing is, unless a wait has run out), whatever ran out before.
 __device__ __forceinline__ void gm_drain(uint64_t* bar, uint32_t parity) {
   if (!mbar_wait_bounded(bar, parity, kGmWaitLimit)) atomicOr(&g_status_gm, ST_DRAIN_TIMEOUT);
   __syncwarp();
 }
 
-// A place in a ring of n stages and the parity of its current turn.
+// A place in a ring of n stages and the parity of its current turn.  Waiting for turn ^ 1 is waiting for the end of the
+// turn before (a new barrier counts as having had one).
 struct Ring {
   int slot = 0;
   uint32_t turn = 0;
-  __device__ __forceinline__ void step(int n) {
-    if (++slot == n) slot = 0, turn ^= 1;
+  __device__ __forceinline__ void step(int n, int by = 1) {
+    slot += by;
+    if (slot >= n) slot -= n, turn ^= 1;
   }
-  // the turn's parity of the one before: what frees the slot (the first turn finds it free)
-  __device__ __forceinline__ uint32_t before() const { return turn ^ 1; }
 };
 
-// The tiles of one pair: tile t is `tok` of x and `row` of W.
+// The tiles of one pair: tile t is rows 256 row .. of W and x0 .. of x, bn of them (the last ones fewer, in steps of 32).
 struct GmTile {
-  int row, tok;
+  int row, x0, bn;
 };
-__device__ __forceinline__ GmTile gm_tile(const GmPlan& p, int64_t t) {
+__device__ __forceinline__ GmTile gm_tile(const GmPlan& p, int rows, int64_t t) {
   const int64_t in_group = static_cast<int64_t>(p.group) * p.row_tiles;
   const int g = static_cast<int>(t / in_group);
   const int64_t rest = t - g * in_group;
   const int width = min(p.group, p.tok_tiles - g * p.group);
   GmTile r;
   r.row = static_cast<int>(rest / width);
-  r.tok = g * p.group + static_cast<int>(rest - static_cast<int64_t>(r.row) * width);
+  r.x0 = (g * p.group + static_cast<int>(rest - static_cast<int64_t>(r.row) * width)) * p.bn;
+  r.bn = min(p.bn, (rows - r.x0 + 31) & ~31);
   return r;
 }
 
 // 16 bytes to shared memory, those behind the first `bytes` as zeros.
 __device__ __forceinline__ void cp16_part(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
@@ -138,14 +145,16 @@ __device__ __forceinline__ void q4_values8(uint32_t codes, __half2 d, uint32_t* 
   }
 }
 
-// Two blocks (9 words) into a row's 64 values: o[c] holds values 2c and 2c + 1.
-__device__ __forceinline__ void q4_values64(const uint32_t* w, uint32_t* o) {
-  const __half2 d0 = bits_h2(prmt(w[0], w[0], 0x1010)), d1 = bits_h2(prmt(w[4], w[4], 0x3232));
+// The blocks of two (9 words): o[c] holds values 2c and 2c + 1 of one.
+__device__ __forceinline__ void q4_first_block(const uint32_t* w, uint32_t* o) {
+  const __half2 d = bits_h2(prmt(w[0], w[0], 0x1010));
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    q4_values8(__funnelshift_r(w[j], w[j + 1], 16), d0, o + 2 * j);
-    q4_values8(w[5 + j], d1, o + 16 + 2 * j);
-  }
+  for (int j = 0; j < 4; ++j) q4_values8(__funnelshift_r(w[j], w[j + 1], 16), d, o + 2 * j);
+}
+__device__ __forceinline__ void q4_second_block(const uint32_t* w, uint32_t* o) {
+  const __half2 d = bits_h2(prmt(w[4], w[4], 0x3232));
+#pragma unroll
+  for (int j = 0; j < 4; ++j) q4_values8(w[5 + j], d, o + 2 * j);
 }
 
 // Step J (of the four of a staged row's 256 columns): its 9 words out of the 16-byte pieces that hold them.
@@ -189,33 +198,45 @@ __device__ __forceinline__ void activate(float* t, int act) {
   }
 }
 
+// The residual of N rows of x from row0 on (`rows` of them there), at this thread's row i of W.
+template <int N>
+__device__ __forceinline__ void load_residual(const GemmArgs& a, int i, int row0, int rows, float* r) {
+  if (i >= a.n) return;
+  const int64_t at = row0 * a.residual.ld + i;
+  if (a.residual.f32) {
+    const float* p = static_cast<const float*>(a.residual.p) + at;
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+      if (c < rows) r[c] = p[c * a.residual.ld];
+  } else {
+    const __half* p = static_cast<const __half*>(a.residual.p) + at;
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+      if (c < rows) r[c] = __half2float(p[c * a.residual.ld]);
+  }
+}
+
 // N columns of sums of this thread's row i of W, of x's rows row0 .. : epilogue and store.
 template <int MATS, int N>
-__device__ __forceinline__ void finish(const GemmArgs& a, int i, int row0, int rows, float* g, float* u, float bg, float bu) {
+__device__ __forceinline__ void finish(const GemmArgs& a, int i, int row0, int rows, float* g, float* u, const float* r, float bg, float bu) {
 #pragma unroll
   for (int c = 0; c < N; ++c) g[c] += bg;
   activate<N>(g, a.act);
 #pragma unroll
-  for (int c = 0; c < N; ++c) g[c] = MATS == 2 ? g[c] * (u[c] + bu) : g[c] * a.scale;
+  for (int c = 0; c < N; ++c) g[c] = MATS == 2 ? g[c] * (u[c] + bu) : a.residual.p ? fmaf(g[c], a.scale, r[c]) : g[c] * a.scale;
   if (i >= a.n) return;
-  if (MATS == 1 && a.residual.p) {
-    const int64_t at = row0 * a.residual.ld + i;
-    if (a.residual.f32) {
-      const float* r = static_cast<const float*>(a.residual.p) + at;
-#pragma unroll
-      for (int c = 0; c < N; ++c)
-        if (c < rows) g[c] += r[c * a.residual.ld];
-    } else {
-      const __half* r = static_cast<const __half*>(a.residual.p) + at;
-#pragma unroll
-      for (int c = 0; c < N; ++c)
-        if (c < rows) g[c] += __half2float(r[c * a.residual.ld]);
-    }
-  }
   __half* y = a.y + row0 * a.y_ld + i;
+  if (rows >= N) {
 #pragma unroll
-  for (int c = 0; c < N; ++c)
-    if (c < rows) y[c * a.y_ld] = __float2half_rn(g[c]);
+    for (int c = 0; c < N; ++c) {
+      *y = __float2half_rn(g[c]);
+      y += a.y_ld;
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+      if (c < rows) y[c * a.y_ld] = __float2half_rn(g[c]);
+  }
 }
 
 template <int MATS, bool RAGGED>
@@ -227,7 +248,7 @@ __global__ void __launch_bounds__(kGmThreads, 1)
   // (the swizzle's period; the same offset in every CTA of the cluster)
   const uint32_t base = (smem_u32(smem_raw) + sizeof(GmCtl) + 1023) & ~1023u;
   char* s_x = smem_raw + (base - smem_u32(smem_raw));
-  const int x_stage = p.bn * 64;                       // half of the rows, 128 bytes each
+  const int x_stage = p.bn * 128;                      // half of the rows, 64 columns twice
   char* s_w = s_x + p.nx * x_stage;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(~0u, tid >> 5, 0);
   const uint32_t rank = cluster_rank(), half = rank & 1, leader = rank & ~1u;
@@ -235,15 +256,15 @@ __global__ void __launch_bounds__(kGmThreads, 1)
   const int part = static_cast<int>(rank >> 1);        // of k
   const int nb = a.k / kQK, units = (nb + 7) / 8;      // blocks, and groups of 256 columns, of a row
   const int u0 = units * part / p.split, u1 = units * (part + 1) / p.split;
-  const int steps = (u1 - u0) * 4;                     // of 64 columns, of a tile (past the end of a row zeros)
+  const int steps = (u1 - u0) * 2;                     // of 128 columns, of a tile (past the end of a row zeros)
   const int64_t tiles = static_cast<int64_t>(p.tok_tiles) * p.row_tiles;
   const int64_t first = blockIdx.x / (2 * p.split), stride = gridDim.x / (2 * p.split);
 
   if (tid == 0) {
     for (int i = 0; i < kGmMaxW; ++i) mbar_init(&c->w_full[i], 64), mbar_init(&c->w_empty[i], 16);
     for (int i = 0; i < kGmMaxX; ++i) mbar_init(&c->x_full[i], 1), mbar_init(&c->x_empty[i], 1);
-    for (int i = 0; i < 8; ++i) mbar_init(&c->a_full[i], 8 * MATS), mbar_init(&c->a_empty[i], 1);
-    mbar_init(&c->d_full, 1), mbar_init(&c->d_empty, 8);
+    for (int i = 0; i < kGmMaxA; ++i) mbar_init(&c->a_full[i], 16), mbar_init(&c->a_empty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&c->d_full[i], 1), mbar_init(&c->d_empty[i], 8);
     c->dead = 0;
     fence_mbar_init();
   }
@@ -253,36 +274,48 @@ __global__ void __launch_bounds__(kGmThreads, 1)
   cluster_sync();
   tm_after();
   const uint32_t tmem = __shfl_sync(~0u, c->tmem, 0);
+  const int sums = p.bn * MATS;                        // columns of a tile's sums
+  const uint32_t t_a = tmem + p.sums * sums;           // the operand stages
 
   if (warp == 0 || warp == 3) {
     // ---------------------------------------------------------------- copies of W
     // Two warps, a matrix each or half of the rows each: 8 threads to the first 128 bytes of a row, the rest of 16 or
-    // 32 rows at a time behind them.  (Tensor copies of 144-byte rows took 12.5 cycles a row, three times as long as the
-    // products of a step of few rows of x.)
+    // 32 rows at a time behind them.
     constexpr int ROWS = MATS == 2 ? 128 : 64, REST = G::PIECES - 8;
     const int which = warp == 3, mat = MATS == 2 ? which : 0, r0 = MATS == 2 ? 0 : 64 * which;
     const int64_t row_bytes = static_cast<int64_t>(nb) * kBlockBytes, end = row_bytes * a.n;
     const uint8_t* const w = a.w[mat];
     const uint32_t to0 = smem_u32(s_w) + (mat * 128 + r0) * G::PITCH;
     Ring r;
-    int64_t n = 0;
     for (int64_t t = first; t < tiles; t += stride) {
-      const int w0 = gm_tile(p, t).row * 256 + half * 128 + r0;
-      for (int u = u0; u < u1; ++u, ++n) {
-        if (n >= p.nw) gm_wait_warp(c, &c->w_empty[r.slot], r.before());
+      const int w0 = gm_tile(p, a.rows, t).row * 256 + half * 128 + r0;
+      // every byte of the pieces lies in the matrix
+      const bool whole = w0 + ROWS < a.n || (!RAGGED && w0 + ROWS == a.n);
+      for (int u = u0; u < u1; ++u) {
+        gm_wait(c, &c->w_empty[r.slot], r.turn ^ 1);
         const uint32_t to = to0 + r.slot * G::W_STAGE;
-        auto copy = [&](int row, int piece) {
-          int64_t at = (w0 + row) * row_bytes + u * 144;
-          if (RAGGED) at &= ~int64_t{15};
-          at += piece * 16;
-          int bytes = w0 + row < a.n ? 16 : 0;
-          if (RAGGED && bytes) bytes = static_cast<int>(max(min(end - at, int64_t{16}), int64_t{0}));
-          cp16_part(to + row * G::PITCH + piece * 16, w + (bytes ? at : 0), bytes);
-        };
+        const uint32_t to_a = to + (lane >> 3) * G::PITCH + (lane & 7) * 16, to_b = to + (lane / REST) * G::PITCH + 128 + lane % REST * 16;
+        // (where rows do not start 16-byte aligned, the bytes around them up to such boundaries)
+        auto start = [&](int64_t at) { return RAGGED ? at & ~int64_t{15} : at; };
+        if (whole) {
+          int64_t at = (w0 + (lane >> 3)) * row_bytes;
+          const uint8_t* const src = w + u * 144 + (lane & 7) * 16;
 #pragma unroll 8
-        for (int i = 0; i < ROWS; i += 4) copy(i + (lane >> 3), lane & 7);
+          for (int i = 0; i < ROWS; i += 4, at += 4 * row_bytes) cp16(to_a + i * G::PITCH, src + start(at));
+          at = (w0 + lane / REST) * row_bytes;
 #pragma unroll
-        for (int i = 0; i < ROWS; i += 32 / REST) copy(i + lane / REST, 8 + lane % REST);
+          for (int i = 0; i < ROWS; i += 32 / REST, at += 32 / REST * row_bytes)
+            cp16(to_b + i * G::PITCH, w + u * 144 + 128 + lane % REST * 16 + start(at));
+        } else {
+          auto copy = [&](uint32_t dst, int row, int piece) {
+            const int64_t at = start((w0 + row) * row_bytes) + u * 144 + piece * 16;
+            const int64_t left = w0 + row < a.n ? end - at : 0;
+            const int bytes = static_cast<int>(left < 0 ? 0 : left > 16 ? 16 : left);
+            cp16_part(dst, w + (bytes ? at : 0), bytes);
+          };
+          for (int i = 0; i < ROWS; i += 4) copy(to_a + i * G::PITCH, i + (lane >> 3), lane & 7);
+          for (int i = 0; i < ROWS; i += 32 / REST) copy(to_b + i * G::PITCH, i + lane / REST, 8 + lane % REST);
+        }
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&c->w_full[r.slot])) : "memory");
         r.step(p.nw);
       }
@@ -294,12 +327,16 @@ __global__ void __launch_bounds__(kGmThreads, 1)
     Ring r;
     int64_t n = 0;
     for (int64_t t = first; t < tiles; t += stride) {
-      const int x0 = gm_tile(p, t).tok * p.bn + half * (p.bn / 2);
+      const GmTile tile = gm_tile(p, a.rows, t);
+      const int x0 = tile.x0 + half * (tile.bn / 2);
       for (int s = 0; s < steps; ++s, ++n) {
-        if (n >= p.nx) gm_wait_warp(c, &c->x_empty[r.slot], r.before());
+        gm_wait(c, &c->x_empty[r.slot], r.turn ^ 1);
         if (lane == 0) {
           if (half == 0) mbar_arrive_expect_tx(&c->x_full[r.slot], 2 * x_stage);
-          tma2_load_2d(s_x + r.slot * x_stage, &x_map, u0 * 256 + s * 64, x0, cluster_addr(&c->x_full[r.slot], leader));
+          const uint32_t full = cluster_addr(&c->x_full[r.slot], leader);
+          char* to = s_x + r.slot * x_stage;
+          tma2_load_2d(to, &x_map, u0 * 256 + s * 128, x0, full);
+          tma2_load_2d(to + x_stage / 2, &x_map, u0 * 256 + s * 128 + 64, x0, full);
         }
         __syncwarp();
         r.step(p.nx);
@@ -309,53 +346,62 @@ __global__ void __launch_bounds__(kGmThreads, 1)
       for (int64_t u = n > p.nx ? n - p.nx : 0; u < n; ++u) gm_drain(&c->x_full[u % p.nx], static_cast<uint32_t>(u / p.nx) & 1);
   } else if (warp == 2) {
     // ---------------------------------------------------------------- products
-    if (half == 0) {
-      const uint32_t idesc = mma_idesc(p.bn, false, 256);
-      const bool one = elect_one();
+    if (half == 0 && elect_one()) {
       Ring rx, ra, rd;
       for (int64_t t = first; t < tiles; t += stride) {
-        if (t != first) gm_wait_warp(c, &c->d_empty, rd.before());
-        tm_after();
+        const uint32_t idesc = mma_idesc(gm_tile(p, a.rows, t).bn, false, 256);
+        const uint32_t d = tmem + rd.slot * sums;
+        gm_wait_one(c, &c->d_empty[rd.slot], rd.turn ^ 1);
         for (int s = 0; s < steps; ++s) {
-          gm_wait_warp(c, &c->x_full[rx.slot], rx.turn);
-          gm_wait_warp(c, &c->a_full[ra.slot], ra.turn);
-          tm_after();
-          if (one) {
-            const uint64_t b = mma_sdesc(smem_u32(s_x) + rx.slot * x_stage, 0);
-            const uint32_t at = tmem + G::A_COL + ra.slot * G::A_STEP;
+          gm_wait_one(c, &c->x_full[rx.slot], rx.turn);
+          const uint64_t b = mma_sdesc(smem_u32(s_x) + rx.slot * x_stage, 0);
+          const uint32_t half_x = x_stage / 2 >> 4;        // (in the descriptor's units)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+          for (int h = 0; h < MATS; ++h) {
+            gm_wait_one(c, &c->a_full[ra.slot], ra.turn);
+            tm_after();
+            const uint32_t at = t_a + ra.slot * kGmStage;
 #pragma unroll
-              for (int m = 0; m < MATS; ++m)
-                tm2_mma_ts(tmem + m * G::D_STEP, at + m * 32 + k * 8, b + 2 * k, idesc, s > 0 || k > 0);
+            for (int i = 0; i < 2; ++i)              // one matrix: its columns 64 .. 127, two: the second one
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                tm2_mma_ts(MATS == 2 ? d + i * p.bn : d, at + i * 32 + k * 8, b + (MATS == 2 ? h : i) * half_x + 2 * k, idesc,
+                           s > 0 || h > 0 || k > 0 || (MATS == 1 && i > 0));
             tm2_commit(&c->a_empty[ra.slot], pair_mask);
-            tm2_commit(&c->x_empty[rx.slot], pair_mask);
+            ra.step(p.na);
           }
-          __syncwarp();
+          tm2_commit(&c->x_empty[rx.slot], pair_mask);
           rx.step(p.nx);
-          ra.step(G::NA);
         }
-        if (one) tm2_commit(&c->d_full, pair_mask);
-        __syncwarp();
-        rd.step(1);
+        tm2_commit(&c->d_full[rd.slot], pair_mask);
+        rd.step(p.sums);
       }
     }
   } else if (warp >= kGmConvert && warp < kGmEpilogue) {
     // ---------------------------------------------------------------- conversion
-    // Four warps hold rows 32 q .. of the CTA.  Of one matrix each takes one of the four steps of every 256 columns, of
-    // two matrices two of the steps of one: a warp's place in the ring of operands is the same every time round.
+    // Four warps hold rows 32 q .. of the CTA.  Of one matrix each takes one of the four 64 columns of every 256, of
+    // two matrices two of one of them.
     const int q = warp & 3, mine = (warp - kGmConvert) >> 2;
     const int mat = MATS == 2 ? mine & 1 : 0;
-    const uint32_t to = tmem + G::A_COL + mat * 32 + (static_cast<uint32_t>(q * 32) << 16);
+    const uint32_t to = t_a + (mine & 1) * 32 + (static_cast<uint32_t>(q * 32) << 16);
     const char* const row0 = s_w + (mat * 128 + q * 32 + lane) * G::PITCH;
     const uint32_t full0 = cluster_addr(&c->a_full[0], leader);
-    Ring rw;
-    uint32_t n = 0;                                     // groups of 256 columns so far
+    Ring rw, ra;
+    ra.step(p.na, mine >> 1);
+    int told = -1;                                      // the stage whose stores the products have not been told of
+    // (a warp's stores to tensor memory are waited for behind the next words' way out of shared memory)
+    auto tell = [&]() {
+      if (told < 0) return;
+      tm_st_wait();
+      tm_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(full0 + told * 8);
+    };
     for (int64_t t = first; t < tiles; t += stride) {
-      const int w0 = gm_tile(p, t).row * 256 + half * 128 + q * 32 + lane;
+      const int w0 = gm_tile(p, a.rows, t).row * 256 + half * 128 + q * 32 + lane;
       const int shift = RAGGED ? static_cast<int>((static_cast<int64_t>(w0) * nb * kBlockBytes) & 15) : 0;
-      for (int u = u0; u < u1; ++u, ++n) {
-        gm_wait_warp(c, &c->w_full[rw.slot], rw.turn);
+      for (int u = u0; u < u1; ++u) {
+        gm_wait(c, &c->w_full[rw.slot], rw.turn);
         const char* row = row0 + rw.slot * G::W_STAGE;
 #pragma unroll
         for (int i = 0; i < MATS; ++i) {
@@ -379,7 +425,9 @@ __global__ void __launch_bounds__(kGmThreads, 1)
               default: staged_words<3>(row, w); break;
             }
           }
-          q4_values64(w, o);
+          tell();
+          q4_first_block(w, o);
+          q4_second_block(w, o + 16);
           if (RAGGED) {
             // (a row's last blocks: what lies behind them in memory is not its own)
             const int left = nb - u * 8 - 2 * j;
@@ -389,48 +437,61 @@ __global__ void __launch_bounds__(kGmThreads, 1)
                 if (e >= 16 || left < 1) o[e] = 0;
             }
           }
-          // ring of two groups of one matrix's steps, one group of two matrices'
-          const uint32_t slot = MATS == 2 ? j : (n & 1) * 4 + j, turn = MATS == 2 ? n : n >> 1;
-          if (turn > 0) gm_wait_warp(c, &c->a_empty[slot], (turn & 1) ^ 1);
-          tm_after();
-          tm_st32(to + slot * G::A_STEP, o);
-          tm_st_wait();
-          tm_before();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive_cluster(full0 + slot * 8);
-            if (i == MATS - 1) mbar_arrive(&c->w_empty[rw.slot]);
+          if (i == MATS - 1) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c->w_empty[rw.slot]);
           }
+          gm_wait(c, &c->a_empty[ra.slot], ra.turn ^ 1);
+          tm_after();
+          tm_st32(to + ra.slot * kGmStage, o);
+          told = ra.slot;
+          ra.step(p.na, 2);
         }
         rw.step(p.nw);
       }
     }
+    tell();
   } else if (warp >= kGmEpilogue) {
     // ---------------------------------------------------------------- epilogue
     const int q = warp & 3;
     const uint32_t from = tmem + (static_cast<uint32_t>(q * 32) << 16);
     Ring rd;
     for (int64_t t = first; t < tiles; t += stride) {
-      const GmTile tile = gm_tile(p, t);
-      gm_wait_warp(c, &c->d_full, rd.turn);
-      tm_after();
-      rd.step(1);
-      if (p.split > 1) break;
+      const GmTile tile = gm_tile(p, a.rows, t);
       const int i = tile.row * 256 + half * 128 + q * 32 + lane;
       const float bg = a.bias[0] && i < a.n ? __ldg(a.bias[0] + i) : 0.f, bu = MATS == 2 && a.bias[1] && i < a.n ? __ldg(a.bias[1] + i) : 0.f;
-      for (int b = 0; b < p.bn; b += 16) {
-        const int row0 = tile.tok * p.bn + b, rows = min(a.rows - row0, 16);
-        if (rows <= 0) break;
+      const int last = min(tile.bn, a.rows - tile.x0);
+      const bool res = MATS == 1 && a.residual.p;
+      // (the tile's residual comes to L2 meanwhile: 8 rows of x a time, this warp's 32 values of each)
+      if (res && i - lane < a.n)
+        for (int b = lane >> 2; b < last; b += 8) {
+          const int size = a.residual.f32 ? 4 : 2, at = i - lane + (lane & 3) * 32 / size;
+          if (at < min(a.n, i - lane + 32))
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(a.residual.p) + ((tile.x0 + b) * a.residual.ld + at) * size));
+        }
+      float ra[16], rb[16];
+      if (res) load_residual<16>(a, i, tile.x0, last, ra);
+      gm_wait(c, &c->d_full[rd.slot], rd.turn);
+      tm_after();
+      if (p.split > 1) break;
+      const uint32_t at = from + rd.slot * sums;
+      auto chunk = [&](int b, const float* r, float* next) {
         uint32_t g[16], u[16];
-        tm_ld16(from + b, g);
-        if (MATS == 2) tm_ld16(from + G::D_STEP + b, u);
+        tm_ld16(at + b, g);
+        if (MATS == 2) tm_ld16(at + p.bn + b, u);
+        if (res && b + 16 < last) load_residual<16>(a, i, tile.x0 + b + 16, last - b - 16, next);
         tm_ld16_wait(g);
         if (MATS == 2) tm_ld16_waited(u);
-        finish<MATS, 16>(a, i, row0, rows, reinterpret_cast<float*>(g), reinterpret_cast<float*>(u), bg, bu);
+        finish<MATS, 16>(a, i, tile.x0 + b, last - b, reinterpret_cast<float*>(g), reinterpret_cast<float*>(u), r, bg, bu);
+      };
+      for (int b = 0; b < last; b += 32) {
+        chunk(b, ra, rb);
+        if (b + 16 < last) chunk(b + 16, rb, ra);
       }
       tm_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(cluster_addr(&c->d_empty, leader));
+      if (lane == 0) mbar_arrive_cluster(cluster_addr(&c->d_empty[rd.slot], leader));
+      rd.step(p.sums);
     }
   }
   __syncwarp();
@@ -438,8 +499,8 @@ __global__ void __launch_bounds__(kGmThreads, 1)
   if (warp == 3) {
     int64_t mine = 0;
     for (int64_t t = first; t < tiles; t += stride) mine += steps;
-    for (int64_t s = mine > G::NA ? mine - G::NA : 0; s < mine; ++s)
-      gm_drain(&c->a_empty[s % G::NA], static_cast<uint32_t>(s / G::NA) & 1);
+    for (int64_t s = mine * MATS > p.na ? mine * MATS - p.na : 0; s < mine * MATS; ++s)
+      gm_drain(&c->a_empty[s % p.na], static_cast<uint32_t>(s / p.na) & 1);
     for (int64_t s = mine > p.nx ? mine - p.nx : 0; s < mine; ++s)
       gm_drain(&c->x_empty[s % p.nx], static_cast<uint32_t>(s / p.nx) & 1);
   }
@@ -463,7 +524,7 @@ __global__ void __launch_bounds__(kGmThreads, 1)
         for (int m = 0; m < MATS; ++m)
           for (int b = 0; b < w; b += 16) {
             uint32_t v[16];
-            tm_ld16(from + m * G::D_STEP + j * w + b, v);
+            tm_ld16(from + m * p.bn + j * w + b, v);
             tm_ld16_wait(v);
 #pragma unroll
             for (int e = 0; e < 16; ++e)
@@ -476,18 +537,19 @@ __global__ void __launch_bounds__(kGmThreads, 1)
     }
     cluster_sync();
     if (warp >= kGmEpilogue) {
-      const GmTile tile = gm_tile(p, first);
+      const GmTile tile = gm_tile(p, a.rows, first);
       const int i = tile.row * 256 + half * 128 + q * 32 + lane;
       const float bg = a.bias[0] && i < a.n ? __ldg(a.bias[0] + i) : 0.f, bu = MATS == 2 && a.bias[1] && i < a.n ? __ldg(a.bias[1] + i) : 0.f;
       for (int b = 0; b < w; b += 16) {
-        const int col = own * w + b, row0 = tile.tok * p.bn + col;
+        const int col = own * w + b, row0 = tile.x0 + col;
         const int rows = min(min(w - b, a.rows - row0), 16);
         if (rows <= 0) break;
-        float sum[MATS][16];
+        float sum[MATS][16], r[16];
+        if (MATS == 1 && a.residual.p) load_residual<16>(a, i, row0, rows, r);
 #pragma unroll
         for (int m = 0; m < MATS; ++m) {
           uint32_t v[16];
-          tm_ld16(from + m * G::D_STEP + col, v);
+          tm_ld16(from + m * p.bn + col, v);
           tm_ld16_wait(v);
 #pragma unroll
           for (int e = 0; e < 16; ++e) sum[m][e] = 0.f;
@@ -498,7 +560,7 @@ __global__ void __launch_bounds__(kGmThreads, 1)
               if (e < rows) sum[m][e] += j == own ? __uint_as_float(v[e]) : src[e * 128];
           }
         }
-        finish<MATS, 16>(a, i, row0, rows, sum[0], sum[MATS - 1], bg, bu);
+        finish<MATS, 16>(a, i, row0, rows, sum[0], sum[MATS - 1], r, bg, bu);
       }
     }
     tm_before();
@@ -514,34 +576,37 @@ __global__ void __launch_bounds__(kGmThreads, 1)
 // ------------------------------------------------------------------ host
 
 // Time of a plan in cycles, roughly: waves of tiles, each as long as the slower of its products and its conversion, and
-// its epilogue.
+// its epilogue where nothing is formed meanwhile.
 GmPlan plan(const GemmArgs& a, const PromptDevice& d, int mats, int w_stage) {
-  const int units = (a.k + 255) / 256, most = 256 / mats;
+  const int units = (a.k + 255) / 256, most = kGmSums / mats;
+  const double convert = (a.k % 256 ? 330. : 240.) * mats;
   GmPlan best = {};
   best.row_tiles = (a.n + 255) / 256;
   double least = 0;
-  const int fewest = (a.rows + most - 1) / most;
-  for (int i = 0; i < 24; ++i) {
-    const int tok = fewest + i;
-    const int bn = ((a.rows + tok - 1) / tok + 31) / 32 * 32;
-    if (i > 0 && (bn < 64 || (a.rows + bn - 1) / bn != tok)) break;
+  for (int bn = 32; bn <= most; bn += 32) {
+    const int tok = (a.rows + bn - 1) / bn;
+    if (bn > 32 && (a.rows + bn - 33) / (bn - 32) == tok) continue;      // (a narrower tile does as well)
     const int64_t tiles = static_cast<int64_t>(tok) * best.row_tiles;
     for (int log = 0; log < 3; ++log) {
       const int split = 1 << log;
       if (log > 0 && (tiles > d.clusters[log] || units < 2 * split)) break;
       const int64_t waves = (tiles + d.clusters[log] - 1) / d.clusters[log];
-      const double step = 2. * bn * mats > 260. * mats ? 2. * bn * mats : 260. * mats;
-      const double time = waves * ((units + split - 1) / split * 4 * step + 1500 + 8. * bn * mats) + (log ? 3000 + 4. * bn * mats : 0);
+      const double step = 2. * bn * mats > convert ? 2. * bn * mats : convert;
+      const double time = waves * ((units + split - 1) / split * 4 * step + (bn * mats > kGmSums / 2 ? 12. * bn * mats : 0)) + (log ? 3000 + 4. * bn * mats : 0);
       if (least == 0 || time < least) least = time, best.bn = bn, best.split = split, best.tok_tiles = tok;
     }
   }
   // rows of x that stay in L2 while W passes by
   const int64_t group = (int64_t{48} << 20) / (static_cast<int64_t>(best.bn) * a.k * 2);
   best.group = group < 1 ? 1 : group > best.tok_tiles ? best.tok_tiles : static_cast<int>(group);
-  best.nw = best.bn * mats <= 128 ? 6 : 4;
+  const int sums = best.bn * mats;
+  best.sums = sums <= kGmSums / 2 ? 2 : 1;
+  best.na = (kGmCols - best.sums * sums) / kGmStage;
+  if (best.na > kGmMaxA) best.na = kGmMaxA;
+  best.nw = sums <= 128 ? 6 : 4;
   if (best.nw * w_stage > 140 * 1024) best.nw = 140 * 1024 / w_stage;
   const int room = kGmSmem - 2048 - best.nw * w_stage;
-  best.nx = room / (best.bn * 64);
+  best.nx = room / (best.bn * 128);
   if (best.nx > kGmMaxX) best.nx = kGmMaxX;
   return best;
 }
