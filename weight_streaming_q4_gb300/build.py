@@ -22,7 +22,7 @@ NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INC
 LIBS = {
     "libq4.so": ["q4_engine.cu", "q4_tc_engine.cu", "q4_bt_engine.cu", "q4_oneshot.cu", "q4_mma.cu", "q4_glue.cu", "q4_attn.cu", "q4_attn_cluster.cu", "q4_aux.cu", "q4_api.cu", "q4_noalloc.cu",
                  "q4_paged_cache.cu", "q4_paged_tile.cu", "q4_paged_rows.cu", "q4_paged_join.cu", "q4_paged_api.cu",
-                 "q4_gemm.cu", "q4_block_norm.cu", "q4_rope.cu", "q4_prompt_api.cu"],
+                 "q4_gemm.cu", "q4_gemm_few.cu", "q4_block_norm.cu", "q4_rope.cu", "q4_prompt_api.cu"],
     "libq4synth.so": ["synth.cu"],
 }
 
