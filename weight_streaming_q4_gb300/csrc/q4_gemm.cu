@@ -35,17 +35,20 @@ constexpr int kGmThreads = 768;
 constexpr int kGmConvert = 4, kGmEpilogue = 20;     // first warps of these roles
 constexpr int kGmMaxX = 16, kGmMaxW = 8;            // stages of the rings at most
 constexpr int kGmSmem = 232448 - 1024;              // dynamic shared memory at most
+constexpr int kGmWide = 64;                         // columns of a tile's sums up to which stages are twice as long
 constexpr int kGmCols = 512, kGmSums = 256;         // columns of tensor memory, and of sums at most
-constexpr int kGmStage = 64;                        // columns of an operand stage
 constexpr int kGmMaxA = 7;                          // operand stages at most
 
-template <int MATS, bool RAGGED>
+// WIDE: for few rows of x, where waits and signals cost more than the products, stages twice as long.
+template <int MATS, bool RAGGED, bool WIDE>
 struct Gm {
   // a staged row of W: the 16-byte pieces that hold 256 columns, and the bytes between rows (a multiple of 16 whose
   // 16-byte loads by 8 threads side by side fall in different banks)
   static constexpr int PIECES = RAGGED ? 10 : 9;
   static constexpr int PITCH = RAGGED ? 176 : 144;
   static constexpr int W_STAGE = MATS * 128 * PITCH;
+  // steps of 64 columns of k of a stage of x and of a stage of operands, and the latter's columns of tensor memory
+  static constexpr int XS = WIDE ? 4 : 2, AS = XS / MATS, A_COLS = AS * MATS * 32;
 };
 
 struct GmPlan {
@@ -167,16 +170,16 @@ __device__ __forceinline__ void finish(const GemmArgs& a, int i, int row0, int r
   }
 }
 
-template <int MATS, bool RAGGED>
+template <int MATS, bool RAGGED, bool WIDE>
 __global__ void __launch_bounds__(kGmThreads, 1)
     gemm_kernel(const __grid_constant__ GemmArgs a, const __grid_constant__ CUtensorMap x_map, const __grid_constant__ GmPlan p) {
-  using G = Gm<MATS, RAGGED>;
+  using G = Gm<MATS, RAGGED, WIDE>;
   extern __shared__ char smem_raw[];
   GmCtl* c = reinterpret_cast<GmCtl*>(smem_raw);
   // (the swizzle's period; the same offset in every CTA of the cluster)
   const uint32_t base = (smem_u32(smem_raw) + sizeof(GmCtl) + 1023) & ~1023u;
   char* s_x = smem_raw + (base - smem_u32(smem_raw));
-  const int x_stage = p.bn * 128;                      // half of the rows, 64 columns twice
+  const int x_step = p.bn * 64, x_stage = G::XS * x_step;      // half of the rows, 128 bytes each, a step
   char* s_w = s_x + p.nx * x_stage;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(~0u, tid >> 5, 0);
   const uint32_t rank = cluster_rank(), half = rank & 1, leader = rank & ~1u;
@@ -184,14 +187,13 @@ __global__ void __launch_bounds__(kGmThreads, 1)
   const int part = static_cast<int>(rank >> 1);        // of k
   const int nb = a.k / kQK, units = (nb + 7) / 8;      // blocks, and groups of 256 columns, of a row
   const int u0 = units * part / p.split, u1 = units * (part + 1) / p.split;
-  const int steps = (u1 - u0) * 2;                     // of 128 columns, of a tile (past the end of a row zeros)
   const int64_t tiles = static_cast<int64_t>(p.tok_tiles) * p.row_tiles;
   const int64_t first = blockIdx.x / (2 * p.split), stride = gridDim.x / (2 * p.split);
 
   if (tid == 0) {
     for (int i = 0; i < kGmMaxW; ++i) mbar_init(&c->w_full[i], 64), mbar_init(&c->w_empty[i], 16);
     for (int i = 0; i < kGmMaxX; ++i) mbar_init(&c->x_full[i], 1), mbar_init(&c->x_empty[i], 1);
-    for (int i = 0; i < kGmMaxA; ++i) mbar_init(&c->a_full[i], 16), mbar_init(&c->a_empty[i], 1);
+    for (int i = 0; i < kGmMaxA; ++i) mbar_init(&c->a_full[i], 8 * G::AS * MATS), mbar_init(&c->a_empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&c->d_full[i], 1), mbar_init(&c->d_empty[i], 8);
     c->dead = 0;
     fence_mbar_init();
@@ -257,14 +259,13 @@ __global__ void __launch_bounds__(kGmThreads, 1)
     for (int64_t t = first; t < tiles; t += stride) {
       const GmTile tile = gm_tile(p, a.rows, t);
       const int x0 = tile.x0 + half * (tile.bn / 2);
-      for (int s = 0; s < steps; ++s, ++n) {
+      for (int s = u0 * 4; s < u1 * 4; s += G::XS, ++n) {      // (past the end of a row: zeros)
         gm_wait(c, &c->x_empty[r.slot], r.turn ^ 1);
         if (lane == 0) {
           if (half == 0) mbar_arrive_expect_tx(&c->x_full[r.slot], 2 * x_stage);
           const uint32_t full = cluster_addr(&c->x_full[r.slot], leader);
-          char* to = s_x + r.slot * x_stage;
-          tma2_load_2d(to, &x_map, u0 * 256 + s * 128, x0, full);
-          tma2_load_2d(to + x_stage / 2, &x_map, u0 * 256 + s * 128 + 64, x0, full);
+#pragma unroll
+          for (int i = 0; i < G::XS; ++i) tma2_load_2d(s_x + r.slot * x_stage + i * x_step, &x_map, (s + i) * 64, x0, full);
         }
         __syncwarp();
         r.step(p.nx);
@@ -280,26 +281,29 @@ __global__ void __launch_bounds__(kGmThreads, 1)
         const uint32_t idesc = mma_idesc(gm_tile(p, a.rows, t).bn, false, 256);
         const uint32_t d = tmem + rd.slot * sums;
         gm_wait_one(c, &c->d_empty[rd.slot], rd.turn ^ 1);
-        for (int s = 0; s < steps; ++s) {
-          gm_wait_one(c, &c->x_full[rx.slot], rx.turn);
-          const uint64_t b = mma_sdesc(smem_u32(s_x) + rx.slot * x_stage, 0);
-          const uint32_t half_x = x_stage / 2 >> 4;        // (in the descriptor's units)
+        for (int u = u0; u < u1; ++u) {
 #pragma unroll
-          for (int h = 0; h < MATS; ++h) {
-            gm_wait_one(c, &c->a_full[ra.slot], ra.turn);
-            tm_after();
-            const uint32_t at = t_a + ra.slot * kGmStage;
+          for (int i = 0; i < 4; ++i) {
+            if (i % G::XS == 0) gm_wait_one(c, &c->x_full[rx.slot], rx.turn);
+            if (i % G::AS == 0) {
+              gm_wait_one(c, &c->a_full[ra.slot], ra.turn);
+              tm_after();
+            }
+            const uint64_t b = mma_sdesc(smem_u32(s_x) + rx.slot * x_stage + i % G::XS * x_step, 0);
+            const uint32_t at = t_a + ra.slot * G::A_COLS + i % G::AS * (32 * MATS);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)              // one matrix: its columns 64 .. 127, two: the second one
+            for (int m = 0; m < MATS; ++m)
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                tm2_mma_ts(MATS == 2 ? d + i * p.bn : d, at + i * 32 + k * 8, b + (MATS == 2 ? h : i) * half_x + 2 * k, idesc,
-                           s > 0 || h > 0 || k > 0 || (MATS == 1 && i > 0));
-            tm2_commit(&c->a_empty[ra.slot], pair_mask);
-            ra.step(p.na);
+              for (int k = 0; k < 4; ++k) tm2_mma_ts(d + m * p.bn, at + m * 32 + k * 8, b + 2 * k, idesc, u > u0 || i > 0 || k > 0);
+            if ((i + 1) % G::AS == 0) {
+              tm2_commit(&c->a_empty[ra.slot], pair_mask);
+              ra.step(p.na);
+            }
+            if ((i + 1) % G::XS == 0) {
+              tm2_commit(&c->x_empty[rx.slot], pair_mask);
+              rx.step(p.nx);
+            }
           }
-          tm2_commit(&c->x_empty[rx.slot], pair_mask);
-          rx.step(p.nx);
         }
         tm2_commit(&c->d_full[rd.slot], pair_mask);
         rd.step(p.sums);
@@ -311,20 +315,12 @@ __global__ void __launch_bounds__(kGmThreads, 1)
     // two matrices two of one of them.
     const int q = warp & 3, mine = (warp - kGmConvert) >> 2;
     const int mat = MATS == 2 ? mine & 1 : 0;
-    const uint32_t to = t_a + (mine & 1) * 32 + (static_cast<uint32_t>(q * 32) << 16);
+    const int j0 = MATS == 2 ? mine >> 1 : mine;        // its first step of 256 columns
+    const uint32_t to = t_a + j0 % G::AS * (32 * MATS) + mat * 32 + (static_cast<uint32_t>(q * 32) << 16);
     const char* const row0 = s_w + (mat * 128 + q * 32 + lane) * G::PITCH;
     const uint32_t full0 = cluster_addr(&c->a_full[0], leader);
     Ring rw, ra;
-    ra.step(p.na, mine >> 1);
-    int told = -1;                                      // the stage whose stores the products have not been told of
-    // (a warp's stores to tensor memory are waited for behind the next words' way out of shared memory)
-    auto tell = [&]() {
-      if (told < 0) return;
-      tm_st_wait();
-      tm_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(full0 + told * 8);
-    };
+    ra.step(p.na, j0 / G::AS);
     for (int64_t t = first; t < tiles; t += stride) {
       const int w0 = gm_tile(p, a.rows, t).row * 256 + half * 128 + q * 32 + lane;
       const int shift = RAGGED ? static_cast<int>((static_cast<int64_t>(w0) * nb * kBlockBytes) & 15) : 0;
@@ -333,7 +329,7 @@ __global__ void __launch_bounds__(kGmThreads, 1)
         const char* row = row0 + rw.slot * G::W_STAGE;
 #pragma unroll
         for (int i = 0; i < MATS; ++i) {
-          const int j = MATS == 2 ? (mine >> 1) + 2 * i : mine;
+          const int j = j0 + 2 * i;
           uint32_t w[9], o[32];
           if (RAGGED) {
             const uint32_t* src = reinterpret_cast<const uint32_t*>(row + (shift & ~3) + 36 * j);
@@ -353,7 +349,6 @@ __global__ void __launch_bounds__(kGmThreads, 1)
               default: staged_words<3>(row, w); break;
             }
           }
-          tell();
           q4_first_block(w, o);
           q4_second_block(w, o + 16);
           if (RAGGED) {
@@ -371,14 +366,16 @@ __global__ void __launch_bounds__(kGmThreads, 1)
           }
           gm_wait(c, &c->a_empty[ra.slot], ra.turn ^ 1);
           tm_after();
-          tm_st32(to + ra.slot * kGmStage, o);
-          told = ra.slot;
-          ra.step(p.na, 2);
+          tm_st32(to + ra.slot * G::A_COLS, o);
+          tm_st_wait();
+          tm_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(full0 + ra.slot * 8);
+          ra.step(p.na, MATS == 2 ? 2 / G::AS : 4 / G::AS);
         }
         rw.step(p.nw);
       }
     }
-    tell();
   } else if (warp >= kGmEpilogue) {
     // ---------------------------------------------------------------- epilogue
     const int q = warp & 3;
@@ -426,10 +423,10 @@ __global__ void __launch_bounds__(kGmThreads, 1)
   // The barriers that the last products' ends are told to are not gone before they are.
   if (warp == 3) {
     int64_t mine = 0;
-    for (int64_t t = first; t < tiles; t += stride) mine += steps;
-    for (int64_t s = mine * MATS > p.na ? mine * MATS - p.na : 0; s < mine * MATS; ++s)
+    for (int64_t t = first; t < tiles; t += stride) mine += (u1 - u0) * 4;
+    for (int64_t s = max(mine / G::AS - p.na, int64_t{0}); s < mine / G::AS; ++s)
       gm_drain(&c->a_empty[s % p.na], static_cast<uint32_t>(s / p.na) & 1);
-    for (int64_t s = mine > p.nx ? mine - p.nx : 0; s < mine; ++s)
+    for (int64_t s = max(mine / G::XS - p.nx, int64_t{0}); s < mine / G::XS; ++s)
       gm_drain(&c->x_empty[s % p.nx], static_cast<uint32_t>(s / p.nx) & 1);
   }
   __syncwarp();
@@ -529,12 +526,13 @@ GmPlan plan(const GemmArgs& a, const PromptDevice& d, int mats, int w_stage) {
   best.group = group < 1 ? 1 : group > best.tok_tiles ? best.tok_tiles : static_cast<int>(group);
   const int sums = best.bn * mats;
   best.sums = sums <= kGmSums / 2 ? 2 : 1;
-  best.na = (kGmCols - best.sums * sums) / kGmStage;
+  const bool wide = sums <= kGmWide;
+  best.na = (kGmCols - best.sums * sums) / (wide ? 128 : 64);
   if (best.na > kGmMaxA) best.na = kGmMaxA;
   best.nw = sums <= 128 ? 6 : 4;
   if (best.nw * w_stage > 140 * 1024) best.nw = 140 * 1024 / w_stage;
   const int room = kGmSmem - 2048 - best.nw * w_stage;
-  best.nx = room / (best.bn * 128);
+  best.nx = room / (best.bn * (wide ? 256 : 128));
   if (best.nx > kGmMaxX) best.nx = kGmMaxX;
   return best;
 }
@@ -554,23 +552,23 @@ cudaLaunchConfig_t config(int clusters, int split, cudaLaunchAttribute* at, cuda
 
 template <int MATS, bool RAGGED>
 cudaError_t launch(const GemmArgs& a, const PromptDevice& d, cudaStream_t s) {
-  using G = Gm<MATS, RAGGED>;
-  const GmPlan p = plan(a, d, MATS, G::W_STAGE);
+  const GmPlan p = plan(a, d, MATS, Gm<MATS, RAGGED, false>::W_STAGE);
   CUtensorMap x_map;
   if (!encode_f16_tile(&x_map, a.x, a.rows, a.k, a.x_ld, p.bn / 2)) return cudaErrorInvalidValue;
   const int64_t tiles = static_cast<int64_t>(p.tok_tiles) * p.row_tiles;
   cudaLaunchAttribute at;
   const cudaLaunchConfig_t cfg = config(static_cast<int>(tiles < d.clusters[0] ? tiles : d.clusters[0]), p.split, &at, s);
-  return cudaLaunchKernelEx(&cfg, gemm_kernel<MATS, RAGGED>, a, x_map, p);
+  if (p.bn * MATS <= kGmWide) return cudaLaunchKernelEx(&cfg, gemm_kernel<MATS, RAGGED, true>, a, x_map, p);
+  return cudaLaunchKernelEx(&cfg, gemm_kernel<MATS, RAGGED, false>, a, x_map, p);
 }
 
-template <int MATS, bool RAGGED>
+template <int MATS, bool RAGGED, bool WIDE>
 cudaError_t prepare(PromptDevice* d) {
-  cudaError_t e = cudaFuncSetAttribute(gemm_kernel<MATS, RAGGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGmSmem);
+  cudaError_t e = cudaFuncSetAttribute(gemm_kernel<MATS, RAGGED, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGmSmem);
   for (int log = 0; e == cudaSuccess && log < 3; ++log) {
     cudaLaunchAttribute at;
     const cudaLaunchConfig_t cfg = config(1, 1 << log, &at, nullptr);
-    e = cudaOccupancyMaxActiveClusters(&d->clusters[log], gemm_kernel<MATS, RAGGED>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&d->clusters[log], gemm_kernel<MATS, RAGGED, WIDE>, &cfg);
     if (e == cudaSuccess && d->clusters[log] < 1) e = cudaErrorInvalidConfiguration;
   }
   return e;
@@ -579,7 +577,9 @@ cudaError_t prepare(PromptDevice* d) {
 }  // namespace
 
 cudaError_t gemm_prepare(PromptDevice* d) {
-  const cudaError_t e[5] = {prepare<1, false>(d), prepare<1, true>(d), prepare<2, false>(d), prepare<2, true>(d), gemm_few_prepare()};
+  const cudaError_t e[9] = {prepare<1, false, false>(d), prepare<1, true, false>(d), prepare<2, false, false>(d), prepare<2, true, false>(d),
+                            prepare<1, false, true>(d),  prepare<1, true, true>(d),  prepare<2, false, true>(d),  prepare<2, true, true>(d),
+                            gemm_few_prepare()};
   for (cudaError_t x : e)
     if (x != cudaSuccess) return x;
   return cudaSuccess;
