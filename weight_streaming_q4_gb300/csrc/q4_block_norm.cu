@@ -74,6 +74,10 @@ __device__ __forceinline__ void load_vec(const float* p, int at, float* v) {
   }
 }
 
+__device__ __forceinline__ void cp16_once(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
 // Sum over the CTA, the same order in every thread.
 __device__ __forceinline__ float cta_sum(float v, float* red) {
 #pragma unroll
@@ -89,9 +93,11 @@ __device__ __forceinline__ float cta_sum(float v, float* red) {
   return v;
 }
 
-template <int V, int E, int T>
+// Rows of any alignment and length, a row per CTA.
+template <int E, int T>
 __global__ void __launch_bounds__(T) block_norm_kernel(const __grid_constant__ NormArgs a) {
   __shared__ float red[32];
+  constexpr int V = 1;
   const int64_t row = blockIdx.x;
   const int step = blockDim.x * V, at0 = threadIdx.x * V;
   const float inv_n = 1.f / static_cast<float>(a.n);
@@ -182,25 +188,218 @@ __global__ void __launch_bounds__(T) block_norm_kernel(const __grid_constant__ N
   }
 }
 
+// Rows of whole 16-byte pieces: persistent CTAs.  A thread's values of the CTA's next rows (block, residual, gate) are on
+// their way to its own place in shared memory by cp.async while a row is worked on, so that no thread reads what
+// another one fetched; the vectors stay in registers (8 values a thread: rows of up to 8192), since loads of them behind
+// each reduction cost twice what the row does.
+template <int C>
+__global__ void __launch_bounds__(1024) block_norm_ring_kernel(const __grid_constant__ NormArgs a, int depth, int staged_r, int staged_g) {
+  extern __shared__ __align__(16) char ring[];
+  __shared__ float red[2][32];
+  constexpr int E = 8 * C;
+  const q4_norms& p = a.p;
+  const int step = blockDim.x * 8, at0 = threadIdx.x * 8;
+  // (a residual that does not fit beside the block is read where it is added; so is a gate that the rows share, out of L1)
+  const int wide_b = a.block.p ? (a.block.f32 ? 32 : 16) : 0, wide_r = staged_r ? (a.residual.f32 ? 32 : 16) : 0;
+  const int wide_g = staged_g ? 32 : 0;
+  const int pieces = blockDim.x * C, off_r = pieces * wide_b, off_g = off_r + pieces * wide_r, stage = off_g + pieces * wide_g;
+  const float inv_n = 1.f / static_cast<float>(a.n);
+  const uint32_t base = smem_u32(ring);
+  int64_t next = blockIdx.x;                   // the row to fetch
+  int next_slot = 0;
+  const int gate_rows = p.gate_rows > 0 ? p.gate_rows : 0x7fffffff;
+  auto fetch = [&]() {
+    if (next < a.rows) {
+      const float* gate = wide_g ? p.gate + static_cast<int>(next) / gate_rows * p.gate_ld : nullptr;
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        const int at = at0 + j * step, place = j * blockDim.x + threadIdx.x;
+        if (at >= a.n) break;
+        const uint32_t to = base + next_slot * stage;
+        auto pull = [&](uint32_t dst, const char* src, int wide) {
+          if (wide) cp16_once(dst, src);
+          if (wide == 32) cp16_once(dst + 16, src + 16);
+        };
+        pull(to + place * wide_b, static_cast<const char*>(a.block.p) + (next * a.block.ld + at) * (wide_b >> 3), wide_b);
+        pull(to + off_r + place * wide_r, static_cast<const char*>(a.residual.p) + (next * a.residual.ld + at) * (wide_r >> 3), wide_r);
+        pull(to + off_g + place * wide_g, reinterpret_cast<const char*>(gate + at), wide_g);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    next += gridDim.x;
+    if (++next_slot == depth) next_slot = 0;
+  };
+  auto staged = [&](const char* src, int wide, float* v) {
+    if (wide == 32) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float4 f = *reinterpret_cast<const float4*>(src + 16 * i);
+        v[4 * i] = f.x, v[4 * i + 1] = f.y, v[4 * i + 2] = f.z, v[4 * i + 3] = f.w;
+      }
+    } else {
+      const uint4 u = *reinterpret_cast<const uint4*>(src);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        v[2 * i] = f.x, v[2 * i + 1] = f.y;
+      }
+    }
+  };
+  for (int s = 0; s < depth - 1; ++s) fetch();
+  // the vectors: [0], [1] those of the post norm, [2], [3] the others
+  constexpr bool KEEP = C == 1;
+  const float* const vec[4] = {p.post_weight, p.post_bias, p.weight, p.bias};
+  float kept[4][KEEP ? 8 : 1];
+  auto vector = [&](int which, int at, float* w) {
+    if (vec[which]) {
+      load_vec<8>(vec[which], at, w);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = which & 1 ? 0.f : 1.f;
+    }
+  };
+  if (KEEP)
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (at0 < a.n) vector(k, at0, kept[k]);
+  // x = x f w + b
+  auto affine = [&](int which, int at, float f, float* x) {
+    float w[8], b[8];
+    if (!KEEP) vector(which, at, w), vector(which + 1, at, b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i] * f, KEEP ? kept[which][i % (KEEP ? 8 : 1)] : w[i], KEEP ? kept[which + 1][i % (KEEP ? 8 : 1)] : b[i]);
+  };
+
+  int slot = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    fetch();
+    switch (depth) {
+      case 1: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+      case 2: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+      case 3: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+      default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    }
+    const char* const src = ring + slot * stage;
+    if (++slot == depth) slot = 0;
+    float v[E];
+    auto stats = [&]() {
+      float s = 0.f;
+      if (p.kind == Q4_NORM_LAYER) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) s += v[i];
+        const float mean = cta_sum(s, red[0]) * inv_n;
+#pragma unroll
+        for (int j = 0; j < C; ++j)
+          if (at0 + j * step < a.n)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[j * 8 + i] -= mean;
+        s = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < E; ++i) s = fmaf(v[i], v[i], s);
+      return 1.f / sqrtf(fmaf(cta_sum(s, red[1]), inv_n, p.eps));
+    };
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const int place = j * blockDim.x + threadIdx.x;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[j * 8 + i] = 0.f;
+      if (at0 + j * step < a.n) staged(wide_b ? src + place * wide_b : src + off_r + place * wide_r, wide_b ? wide_b : wide_r, v + j * 8);
+    }
+    if (wide_b) {
+      const float f = p.post ? stats() : 1.f;
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        const int at = at0 + j * step, place = j * blockDim.x + threadIdx.x;
+        if (at >= a.n) continue;
+        float w[8];
+        float* x = v + j * 8;
+        if (p.post) affine(0, at, f, x);
+        if (p.gate) {
+          if (wide_g)
+            staged(src + off_g + place * wide_g, wide_g, w);
+          else
+            load_vec<8>(p.gate + static_cast<int>(row) / gate_rows * p.gate_ld + at, 0, w);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] *= w[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = 0.f;
+        if (wide_r)
+          staged(src + off_r + place * wide_r, wide_r, w);
+        else if (a.residual.p)
+          load_row<8>(a.residual, row * a.residual.ld + at, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i], p.scale, w[i]);
+      }
+    }
+    if (a.t.p) {
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+        if (at0 + j * step < a.n) store_row<8>(a.t, row * a.t.ld + at0 + j * step, v + j * 8);
+    }
+    if (!a.z.p) continue;
+    const float f = stats();
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const int at = at0 + j * step;
+      if (at >= a.n) continue;
+      affine(2, at, f, v + j * 8);
+      store_row<8>(a.z, row * a.z.ld + at, v + j * 8);
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 bool rows16(const void* p, int64_t ld, int f32) {
   return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * (f32 ? 4 : 2) % 16 == 0);
 }
 bool vec16(const float* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
+constexpr int kBnMost = 226 * 1024;       // dynamic shared memory at most
+constexpr int kBnRing = 150 * 1024;       // shared memory of an SM that the rings take, if a row is not longer
+
 }  // namespace
 
-cudaError_t block_norm_launch(const NormArgs& a, cudaStream_t s) {
+cudaError_t block_norm_prepare() {
+  cudaError_t e = cudaSuccess;
+  for (void (*const kernel)(NormArgs, int, int, int) : {block_norm_ring_kernel<1>, block_norm_ring_kernel<2>, block_norm_ring_kernel<4>})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBnMost);
+  return e;
+}
+
+cudaError_t block_norm_launch(const NormArgs& a, int sms, cudaStream_t s) {
   const q4_norms& p = a.p;
   const bool wide = a.n % 8 == 0 && rows16(a.block.p, a.block.ld, a.block.f32) &&
                     rows16(a.residual.p, a.residual.ld, a.residual.f32) && rows16(a.t.p, a.t.ld, a.t.f32) &&
                     rows16(a.z.p, a.z.ld, a.z.f32) && vec16(p.post_weight) && vec16(p.post_bias) && vec16(p.gate) &&
                     (!p.gate || !p.gate_rows || p.gate_ld % 4 == 0) && vec16(p.weight) && vec16(p.bias);
-  // 16 values per thread up to 8192 of a row, else 32 (1024 threads take 32768)
+  const int c = a.n <= 8192 ? 1 : a.n <= 16384 ? 2 : 4;
+  const int threads_w = ((a.n + 8 * c - 1) / (8 * c) + 31) / 32 * 32;
+  // bytes of a row in the ring: the block (or the residual alone), the residual, and a gate that differs from row to row
+  int ctas = 1024 / threads_w;
+  if (ctas > 8) ctas = 8;
+  const int64_t most = static_cast<int64_t>(sms) * ctas, grid = a.rows < most ? a.rows : most;
+  const int values = threads_w * c * 2, first = a.block.p ? (a.block.f32 ? 2 : 1) : 0, second = a.residual.p ? (a.residual.f32 ? 2 : 1) : 0;
+  int row = values * 8 * first;
+  const bool stage_r = second && (!first || 2 * (row + values * 8 * second) <= kBnMost);
+  if (stage_r) row += values * 8 * second;
+  const bool stage_g = first && p.gate && p.gate_rows > 0 && p.gate_rows < grid && 2 * (row + values * 16) <= kBnMost;
+  if (stage_g) row += values * 16;
+  if (wide) {
+    int depth = kBnRing / ctas / row;
+    depth = depth > 4 ? 4 : depth >= 2 ? depth : 2 * row <= kBnMost ? 2 : 1;
+    void (*const kernel)(NormArgs, int, int, int) = c == 1 ? block_norm_ring_kernel<1> : c == 2 ? block_norm_ring_kernel<2> : block_norm_ring_kernel<4>;
+    kernel<<<static_cast<unsigned>(grid), threads_w, depth * row, s>>>(a, depth, stage_r, stage_g);
+    return cudaGetLastError();
+  }
+  // a value at a time: 16 per thread up to 8192 of a row, else 32 (1024 threads take 32768)
   const int e = a.n <= 8192 ? 16 : 32;
   const int threads = ((a.n + e - 1) / e + 31) / 32 * 32;
-  void (*const kernel)(NormArgs) = e == 16          ? (wide ? block_norm_kernel<8, 16, 512> : block_norm_kernel<1, 16, 512>)
-                                   : threads <= 512 ? (wide ? block_norm_kernel<8, 32, 512> : block_norm_kernel<1, 32, 512>)
-                                                    : (wide ? block_norm_kernel<8, 32, 1024> : block_norm_kernel<1, 32, 1024>);
+  void (*const kernel)(NormArgs) = e == 16          ? block_norm_kernel<16, 512>
+                                   : threads <= 512 ? block_norm_kernel<32, 512>
+                                                    : block_norm_kernel<32, 1024>;
   kernel<<<a.rows, threads, 0, s>>>(a);
   return cudaGetLastError();
 }

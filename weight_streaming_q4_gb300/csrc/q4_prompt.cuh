@@ -52,7 +52,8 @@ struct NormArgs {
   RowsIn block, residual;
   RowsOut t, z;
 };
-cudaError_t block_norm_launch(const NormArgs& a, cudaStream_t s);
+cudaError_t block_norm_prepare();
+cudaError_t block_norm_launch(const NormArgs& a, int sms, cudaStream_t s);
 
 // ------------------------------------------------------------------ rotary positions (q4_rope.cu)
 

@@ -44,6 +44,7 @@ int device_of(const q4::PromptDevice** out) {
   if (known[dev].sms == 0) {
     q4::PromptDevice d = {};
     Q4_CUDA(q4::gemm_prepare(&d));
+    Q4_CUDA(q4::block_norm_prepare());
     Q4_CUDA(cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev));
     if (getenv("Q4DBG")) printf("clusters %d %d %d\n", d.clusters[0], d.clusters[1], d.clusters[2]);
     known[dev] = d;
@@ -119,7 +120,9 @@ extern "C" int q4_block_norm(const q4_norms* norms, int rows, int n, const void*
   a.residual = {residual, residual_ld, residual_type == Q4_TYPE_F32};
   a.t = {t, t_ld, t_type == Q4_TYPE_F32};
   a.z = {z, z_ld, z_type == Q4_TYPE_F32};
-  Q4_CUDA(q4::block_norm_launch(a, static_cast<cudaStream_t>(stream)));
+  const q4::PromptDevice* d = nullptr;
+  if ((st = device_of(&d)) != Q4_OK) return st;
+  Q4_CUDA(q4::block_norm_launch(a, d->sms, static_cast<cudaStream_t>(stream)));
   return Q4_OK;
 }
 
