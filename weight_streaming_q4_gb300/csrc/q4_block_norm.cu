@@ -78,13 +78,13 @@ __device__ __forceinline__ void cp16_once(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// Sum over the CTA, the same order in every thread.
+// Sum over the CTA, the same order in every thread.  red: not the place of the sum before it (whose readers are known to be
+// done only behind this one's barrier).
 __device__ __forceinline__ float cta_sum(float v, float* red) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
   const int warps = blockDim.x >> 5;
   if (warps == 1) return v;
-  __syncthreads();                      // (the sums before this one have been read)
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
   v = (threadIdx.x & 31) < warps ? red[threadIdx.x & 31] : 0.f;
@@ -96,7 +96,8 @@ __device__ __forceinline__ float cta_sum(float v, float* red) {
 // Rows of any alignment and length, a row per CTA.
 template <int E, int T>
 __global__ void __launch_bounds__(T) block_norm_kernel(const __grid_constant__ NormArgs a) {
-  __shared__ float red[32];
+  __shared__ float red[2][32];
+  int turn = 0;
   constexpr int V = 1;
   const int64_t row = blockIdx.x;
   const int step = blockDim.x * V, at0 = threadIdx.x * V;
@@ -110,7 +111,7 @@ __global__ void __launch_bounds__(T) block_norm_kernel(const __grid_constant__ N
     if (p.kind == Q4_NORM_LAYER) {
 #pragma unroll
       for (int i = 0; i < E; ++i) s += v[i];
-      const float mean = cta_sum(s, red) * inv_n;
+      const float mean = cta_sum(s, red[turn ^= 1]) * inv_n;
 #pragma unroll
       for (int j = 0; j < E / V; ++j)
         if (at0 + j * step < a.n)
@@ -120,7 +121,7 @@ __global__ void __launch_bounds__(T) block_norm_kernel(const __grid_constant__ N
     }
 #pragma unroll
     for (int i = 0; i < E; ++i) s = fmaf(v[i], v[i], s);
-    return 1.f / sqrtf(fmaf(cta_sum(s, red), inv_n, p.eps));
+    return rsqrtf(fmaf(cta_sum(s, red[turn ^= 1]), inv_n, p.eps));
   };
 
   float r[E];
@@ -196,6 +197,7 @@ template <int C>
 __global__ void __launch_bounds__(1024) block_norm_ring_kernel(const __grid_constant__ NormArgs a, int depth, int staged_r, int staged_g) {
   extern __shared__ __align__(16) char ring[];
   __shared__ float red[2][32];
+  int turn = 0;
   constexpr int E = 8 * C;
   const q4_norms& p = a.p;
   const int step = blockDim.x * 8, at0 = threadIdx.x * 8;
@@ -288,7 +290,7 @@ __global__ void __launch_bounds__(1024) block_norm_ring_kernel(const __grid_cons
       if (p.kind == Q4_NORM_LAYER) {
 #pragma unroll
         for (int i = 0; i < E; ++i) s += v[i];
-        const float mean = cta_sum(s, red[0]) * inv_n;
+        const float mean = cta_sum(s, red[turn ^= 1]) * inv_n;
 #pragma unroll
         for (int j = 0; j < C; ++j)
           if (at0 + j * step < a.n)
@@ -298,7 +300,7 @@ __global__ void __launch_bounds__(1024) block_norm_ring_kernel(const __grid_cons
       }
 #pragma unroll
       for (int i = 0; i < E; ++i) s = fmaf(v[i], v[i], s);
-      return 1.f / sqrtf(fmaf(cta_sum(s, red[1]), inv_n, p.eps));
+      return rsqrtf(fmaf(cta_sum(s, red[turn ^= 1]), inv_n, p.eps));
     };
 #pragma unroll
     for (int j = 0; j < C; ++j) {
@@ -358,7 +360,7 @@ bool rows16(const void* p, int64_t ld, int f32) {
 bool vec16(const float* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 constexpr int kBnMost = 226 * 1024;       // dynamic shared memory at most
-constexpr int kBnRing = 150 * 1024;       // shared memory of an SM that the rings take, if a row is not longer
+constexpr int kBnRing = 100 * 1024;       // shared memory of an SM that the rings take, if a row is not longer
 
 }  // namespace
 
