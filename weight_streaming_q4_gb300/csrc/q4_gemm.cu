@@ -33,6 +33,7 @@ __device__ int g_status_gm;
 
 constexpr int kGmThreads = 768;
 constexpr int kGmConvert = 4, kGmEpilogue = 20;     // first warps of these roles
+constexpr int kGmTeams = 5;                         // of four warps, that finish the last tile
 constexpr int kGmMaxX = 16, kGmMaxW = 8;            // stages of the rings at most
 constexpr int kGmSmem = 232448 - 1024;              // dynamic shared memory at most
 constexpr int kGmWide = 64;                         // columns of a tile's sums up to which stages are twice as long
@@ -198,10 +199,12 @@ __global__ void __launch_bounds__(kGmThreads, 1)
     c->dead = 0;
     fence_mbar_init();
   }
-  if (warp == 3) tm2_alloc(&c->tmem, 512);
+  if (warp == 2) tm2_alloc(&c->tmem, 512);
   tm_before();
   __syncthreads();
-  cluster_sync();
+  // (the copies of W need no other CTA: they do not wait for it)
+  cluster_arrive();
+  if (warp != 0 && warp != 3) cluster_wait();
   tm_after();
   const uint32_t tmem = __shfl_sync(~0u, c->tmem, 0);
   const int sums = p.bn * MATS;                        // columns of a tile's sums
@@ -252,6 +255,8 @@ __global__ void __launch_bounds__(kGmThreads, 1)
     }
     // the last copies have landed before the CTA ends
     asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+    cluster_wait();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- copies of x
     Ring r;
@@ -394,11 +399,11 @@ __global__ void __launch_bounds__(kGmThreads, 1)
           if (at < min(a.n, i - lane + 32))
             asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(a.residual.p) + ((tile.x0 + b) * a.residual.ld + at) * size));
         }
+      if (t + stride >= tiles) break;                  // (the last one is every warp's)
       float ra[16], rb[16];
       if (res) load_residual<16>(a, i, tile.x0, last, ra);
       gm_wait(c, &c->d_full[rd.slot], rd.turn);
       tm_after();
-      if (p.split > 1) break;
       const uint32_t at = from + rd.slot * sums;
       auto chunk = [&](int b, const float* r, float* next) {
         uint32_t g[16], u[16];
@@ -430,44 +435,55 @@ __global__ void __launch_bounds__(kGmThreads, 1)
       gm_drain(&c->x_empty[s % p.nx], static_cast<uint32_t>(s / p.nx) & 1);
   }
   __syncwarp();
-  tm_before();
-  __syncthreads();
-  tm_after();
 
-  if (p.split > 1 && first < tiles) {
-    // The pairs' parts of the one tile: pair j adds up columns [j w, (j + 1) w).  The others' parts of them lie in the
-    // rings' place, [pair][matrix][column][row of W] fp32.
-    const int w = p.bn / p.split;
-    const int q = warp & 3, own = part;
-    float* recv = reinterpret_cast<float*>(s_x);
-    const uint32_t from = tmem + (static_cast<uint32_t>(q * 32) << 16);
-    cluster_sync();
-    if (warp >= kGmEpilogue) {
-      for (int j = 0; j < p.split; ++j) {
-        if (j == own) continue;
-        const uint32_t to = cluster_addr(recv, 2 * j + half);
-        for (int m = 0; m < MATS; ++m)
-          for (int b = 0; b < w; b += 16) {
-            uint32_t v[16];
-            tm_ld16(from + m * p.bn + j * w + b, v);
-            tm_ld16_wait(v);
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (b + e < w)
-                asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(to + (((own * MATS + m) * w + b + e) * 128 + q * 32 + lane) * 4),
-                             "r"(v[e])
-                             : "memory");
-          }
+  // The last tile (with a split: the only one) is finished by the converting warps too, 16 rows of x at a time.
+  const int64_t before = (tiles - 1 - first) / stride;       // this pair's tiles before it
+  const GmTile tile = gm_tile(p, a.rows, first + before * stride);
+  const int q = warp & 3, team = (warp - kGmConvert) >> 2;
+  const int i = tile.row * 256 + half * 128 + q * 32 + lane;
+  const uint32_t from = tmem + static_cast<uint32_t>(before % p.sums) * sums + (static_cast<uint32_t>(q * 32) << 16);
+  float bg = 0.f, bu = 0.f;
+  if (warp >= kGmConvert) {
+    if (a.bias[0] && i < a.n) bg = __ldg(a.bias[0] + i);
+    if (MATS == 2 && a.bias[1] && i < a.n) bu = __ldg(a.bias[1] + i);
+    gm_wait(c, &c->d_full[before % p.sums], static_cast<uint32_t>(before / p.sums) & 1);
+    tm_after();
+  }
+  if (p.split == 1) {
+    const int last = min(tile.bn, a.rows - tile.x0);
+    if (warp >= kGmConvert)
+      for (int b = team * 16; b < last; b += kGmTeams * 16) {
+        float r[16];
+        if (MATS == 1 && a.residual.p) load_residual<16>(a, i, tile.x0 + b, last - b, r);
+        uint32_t g[16], u[16];
+        tm_ld16(from + b, g);
+        if (MATS == 2) tm_ld16(from + p.bn + b, u);
+        tm_ld16_wait(g);
+        if (MATS == 2) tm_ld16_waited(u);
+        finish<MATS, 16>(a, i, tile.x0 + b, last - b, reinterpret_cast<float*>(g), reinterpret_cast<float*>(u), r, bg, bu);
       }
-    }
+  } else {
+    // The pairs' parts: pair j adds up columns [j w, (j + 1) w).  The others' parts of them lie in the rings' place,
+    // [pair][matrix][column][row of W] fp32.
+    const int w = p.bn / p.split, own = part, chunks = (w + 15) / 16;
+    float* recv = reinterpret_cast<float*>(s_x);
     cluster_sync();
-    if (warp >= kGmEpilogue) {
-      const GmTile tile = gm_tile(p, a.rows, first);
-      const int i = tile.row * 256 + half * 128 + q * 32 + lane;
-      const float bg = a.bias[0] && i < a.n ? __ldg(a.bias[0] + i) : 0.f, bu = MATS == 2 && a.bias[1] && i < a.n ? __ldg(a.bias[1] + i) : 0.f;
-      for (int b = 0; b < w; b += 16) {
-        const int col = own * w + b, row0 = tile.x0 + col;
-        const int rows = min(min(w - b, a.rows - row0), 16);
+    if (warp >= kGmConvert)
+      for (int e = team; e < p.split * MATS * chunks; e += kGmTeams) {
+        const int j = e / (MATS * chunks), m = e / chunks % MATS, b = e % chunks * 16;
+        if (j == own) continue;
+        const uint32_t to = cluster_addr(recv, 2 * j + half) + (((own * MATS + m) * w + b) * 128 + q * 32 + lane) * 4;
+        uint32_t v[16];
+        tm_ld16(from + m * p.bn + j * w + b, v);
+        tm_ld16_wait(v);
+#pragma unroll
+        for (int col = 0; col < 16; ++col)
+          if (b + col < w) asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(to + col * 512), "r"(v[col]) : "memory");
+      }
+    cluster_sync();
+    if (warp >= kGmConvert)
+      for (int b = team * 16; b < w; b += kGmTeams * 16) {
+        const int col = own * w + b, row0 = tile.x0 + col, rows = min(min(w - b, a.rows - row0), 16);
         if (rows <= 0) break;
         float sum[MATS][16], r[16];
         if (MATS == 1 && a.residual.p) load_residual<16>(a, i, row0, rows, r);
@@ -487,12 +503,12 @@ __global__ void __launch_bounds__(kGmThreads, 1)
         }
         finish<MATS, 16>(a, i, row0, rows, sum[0], sum[MATS - 1], r, bg, bu);
       }
-    }
-    tm_before();
-    __syncthreads();
   }
+  __syncwarp();
+  tm_before();
+  __syncthreads();
   cluster_sync();
-  if (warp == 3) {
+  if (warp == 2) {
     tm_after();
     tm2_free(tmem, 512);
   }
