@@ -37,7 +37,7 @@ constexpr int kGmTeams = 5;                         // of four warps, that finis
 constexpr int kGmMaxX = 16, kGmMaxW = 8;            // stages of the rings at most
 constexpr int kGmSmem = 232448 - 1024;              // dynamic shared memory at most
 constexpr int kGmWide = 64;                         // columns of a tile's sums up to which stages are twice as long
-constexpr int kGmCols = 512, kGmSums = 256;         // columns of tensor memory, and of sums at most
+constexpr int kGmCols = 512;                        // columns of tensor memory
 constexpr int kGmMaxA = 7;                          // operand stages at most
 
 // WIDE: for few rows of x, where waits and signals cost more than the products, stages twice as long.
@@ -519,8 +519,8 @@ __global__ void __launch_bounds__(kGmThreads, 1)
 // Time of a plan in cycles, roughly: waves of tiles, each as long as the slower of its products and its conversion, and
 // its epilogue where nothing is formed meanwhile.
 GmPlan plan(const GemmArgs& a, const PromptDevice& d, int mats, int w_stage) {
-  const int units = (a.k + 255) / 256, most = kGmSums / mats;
-  const double convert = (a.k % 256 ? 330. : 240.) * mats;
+  const int units = (a.k + 255) / 256, most = mats == 2 ? 192 : 256;
+  const double convert = (mats == 2 ? 600. : 370.) * (a.k % 256 ? 1.2 : 1.);
   GmPlan best = {};
   best.row_tiles = (a.n + 255) / 256;
   double least = 0;
@@ -533,7 +533,7 @@ GmPlan plan(const GemmArgs& a, const PromptDevice& d, int mats, int w_stage) {
       if (log > 0 && (tiles > d.clusters[log] || units < 2 * split)) break;
       const int64_t waves = (tiles + d.clusters[log] - 1) / d.clusters[log];
       const double step = 2. * bn * mats > convert ? 2. * bn * mats : convert;
-      const double time = waves * ((units + split - 1) / split * 4 * step + (bn * mats > kGmSums / 2 ? 12. * bn * mats : 0)) + (log ? 3000 + 4. * bn * mats : 0);
+      const double time = waves * ((units + split - 1) / split * 4 * step + (bn * mats > 128 ? 12. * bn * mats : 0)) + (log ? 3000 + 4. * bn * mats : 0);
       if (least == 0 || time < least) least = time, best.bn = bn, best.split = split, best.tok_tiles = tok;
     }
   }
@@ -541,7 +541,7 @@ GmPlan plan(const GemmArgs& a, const PromptDevice& d, int mats, int w_stage) {
   const int64_t group = (int64_t{48} << 20) / (static_cast<int64_t>(best.bn) * a.k * 2);
   best.group = group < 1 ? 1 : group > best.tok_tiles ? best.tok_tiles : static_cast<int>(group);
   const int sums = best.bn * mats;
-  best.sums = sums <= kGmSums / 2 ? 2 : 1;
+  best.sums = sums <= 128 ? 2 : 1;
   const bool wide = sums <= kGmWide;
   best.na = (kGmCols - best.sums * sums) / (wide ? 128 : 64);
   if (best.na > kGmMaxA) best.na = kGmMaxA;
