@@ -32,7 +32,7 @@ def gemm(lib, **over):
 
 @pytest.mark.parametrize("over", [dict(w=None), dict(x=None), dict(y=None), dict(n=0), dict(n=-1), dict(k=0), dict(k=48), dict(rows=-1), dict(rows=(1 << 24) + 1), dict(x_ld=56),
                                   dict(y_ld=7), dict(act=5), dict(act=-1), dict(n=1 << 20, k=(1 << 14) - 32, x_ld=1 << 14, y_ld=1 << 20), dict(x_ld=(1 << 31) + 8),
-                                  dict(y_ld=(1 << 31) + 1)], ids=str)
+                                  dict(y_ld=(1 << 31) + 1), dict(n=(1 << 30) + 1, y_ld=1 << 31, residual_ld=1 << 31)], ids=str)
 def test_product_arguments(lib, over):
     assert gemm(lib, **over) == (ARG, ARG)
 

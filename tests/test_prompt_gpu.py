@@ -36,7 +36,9 @@ def settled():
 
 ODD = [(1, 1, 32), (1, 64, 256), (2, 5, 64), (3, 130, 96), (7, 128, 512), (16, 127, 288), (17, 129, 768), (31, 255, 1024), (33, 256, 2048),
        (64, 257, 256), (65, 300, 1056), (100, 512, 4096), (128, 33, 14336), (129, 1000, 544), (200, 384, 1280), (255, 640, 256), (256, 513, 800),
-       (257, 260, 2304), (300, 1030, 512), (520, 700, 320), (1000, 257, 128), (1500, 5200, 96), (2100, 4100, 512), (37, 4099, 4128), (1, 4096, 4096), (4, 6144, 4096)]
+       (257, 260, 2304), (300, 1030, 512), (520, 700, 320), (1000, 257, 128), (1500, 5200, 96), (2100, 4100, 512), (37, 4099, 4128), (1, 4096, 4096), (4, 6144, 4096),
+       # more tiles than run at once, by the rows of x that a tile takes
+       (30, 20000, 288), (64, 20000, 256), (100, 20000, 256), (150, 500, 320), (190, 700, 512), (384, 10300, 256), (8, 12000, 256), (9, 5000, 96)]
 
 
 @pytest.mark.parametrize("rows,n,k", ODD)
@@ -92,6 +94,22 @@ def test_defaults_and_flat_buffers(rows, n, k):
     q4.q4_gemm(dev(blocks), xb, k, n, k, 0, None, y, n)
     settled()
     assert torch.all(y == 3)
+
+
+def test_a_chained_product_waits_for_the_product_before_it():
+    """A chained matrix-vector product whose x a many-row product has just written."""
+    n, k, rng = 4096, 4096, np.random.default_rng(5)
+    blocks = [dev(ref.q4_bytes(n, k, i)) for i in range(2)]
+    x = rows_of(rng, 64, k)[0]
+    for _ in range(4):
+        y, z = torch.zeros((64, n), dtype=torch.float16, device="cuda"), torch.zeros((2, n), device="cuda")
+        q4.q4_gemv(blocks[1], x[0], z[1], n, k, 1)
+        q4.q4_gemm(blocks[0], x, k, n, k, 64, None, y, n)
+        q4.q4_gemv(blocks[1], y[63], z[0], n, k, 1, chain=True)
+        torch.cuda.synchronize()
+        q4.q4_gemv(blocks[1], y[63], z[1], n, k, 1)
+        settled()
+        assert torch.equal(z[0], z[1])
 
 
 @pytest.mark.parametrize("rows", [1, 20, 300])
@@ -281,7 +299,7 @@ def test_norms_of_rows_that_are_zero_or_not_finite():
 
 # ------------------------------------------------------------------ rotary positions
 
-HEADS = [(1, 2, 2), (3, 6, 4), (5, 64, 64), (40, 128, 128), (8, 80, 40), (2, 80, 38), (3, 192, 96), (2, 256, 256), (7, 100, 10), (1, 1024, 256)]
+HEADS = [(1, 2, 2), (3, 6, 4), (3, 7, 4), (65, 9, 2), (5, 64, 64), (40, 128, 128), (8, 80, 40), (2, 80, 38), (3, 192, 96), (2, 256, 256), (7, 100, 10), (1, 1024, 256)]
 
 
 @pytest.mark.parametrize("heads,head_dim,rot", HEADS)

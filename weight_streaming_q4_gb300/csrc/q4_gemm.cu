@@ -21,6 +21,7 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include "q4_frag.cuh"
 #include "q4_gemm.cuh"
 #include "q4_tensor.cuh"
 
@@ -191,6 +192,7 @@ __global__ void __launch_bounds__(kGmThreads, 1)
   const int64_t tiles = static_cast<int64_t>(p.tok_tiles) * p.row_tiles;
   const int64_t first = blockIdx.x / (2 * p.split), stride = gridDim.x / (2 * p.split);
 
+  griddep_launch_dependents();
   if (tid == 0) {
     for (int i = 0; i < kGmMaxW; ++i) mbar_init(&c->w_full[i], 64), mbar_init(&c->w_empty[i], 16);
     for (int i = 0; i < kGmMaxX; ++i) mbar_init(&c->x_full[i], 1), mbar_init(&c->x_empty[i], 1);
@@ -204,6 +206,7 @@ __global__ void __launch_bounds__(kGmThreads, 1)
   __syncthreads();
   // (the copies of W need no other CTA: they do not wait for it)
   cluster_arrive();
+  griddep_wait();
   if (warp != 0 && warp != 3) cluster_wait();
   tm_after();
   const uint32_t tmem = __shfl_sync(~0u, c->tmem, 0);
@@ -553,12 +556,11 @@ GmPlan plan(const GemmArgs& a, const PromptDevice& d, int mats, int w_stage) {
   return best;
 }
 
-cudaLaunchConfig_t config(int clusters, int split, cudaLaunchAttribute* at, cudaStream_t s) {
+cudaLaunchConfig_t config(int clusters, int split, cudaLaunchAttribute* at) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * 2 * split));
   cfg.blockDim = dim3(kGmThreads);
   cfg.dynamicSmemBytes = kGmSmem;
-  cfg.stream = s;
   at->id = cudaLaunchAttributeClusterDimension;
   at->val.clusterDim.x = 2 * split, at->val.clusterDim.y = 1, at->val.clusterDim.z = 1;
   cfg.attrs = at;
@@ -572,10 +574,18 @@ cudaError_t launch(const GemmArgs& a, const PromptDevice& d, cudaStream_t s) {
   CUtensorMap x_map;
   if (!encode_f16_tile(&x_map, a.x, a.rows, a.k, a.x_ld, p.bn / 2)) return cudaErrorInvalidValue;
   const int64_t tiles = static_cast<int64_t>(p.tok_tiles) * p.row_tiles;
-  cudaLaunchAttribute at;
-  const cudaLaunchConfig_t cfg = config(static_cast<int>(tiles < d.clusters[0] ? tiles : d.clusters[0]), p.split, &at, s);
-  if (p.bn * MATS <= kGmWide) return cudaLaunchKernelEx(&cfg, gemm_kernel<MATS, RAGGED, true>, a, x_map, p);
-  return cudaLaunchKernelEx(&cfg, gemm_kernel<MATS, RAGGED, false>, a, x_map, p);
+  const int clusters = static_cast<int>(tiles < d.clusters[0] ? tiles : d.clusters[0]);
+  void (*const kernel)(GemmArgs, CUtensorMap, GmPlan) = p.bn * MATS <= kGmWide ? gemm_kernel<MATS, RAGGED, true> : gemm_kernel<MATS, RAGGED, false>;
+  cudaLaunchAttribute at[2];
+  cudaLaunchConfig_t cfg = config(clusters, p.split, at);
+  cfg.stream = s;
+  // It may start while the kernel before it on the stream ends (its CTAs take their places and wait before they touch
+  // global memory): 1 to 2 us less in a chain of products.  Where several CTAs share an SM, as in the kernels of few
+  // rows, norms and rotations, the waiting ones took more than that.
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, a, x_map, p);
 }
 
 template <int MATS, bool RAGGED, bool WIDE>
@@ -583,7 +593,7 @@ cudaError_t prepare(PromptDevice* d) {
   cudaError_t e = cudaFuncSetAttribute(gemm_kernel<MATS, RAGGED, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGmSmem);
   for (int log = 0; e == cudaSuccess && log < 3; ++log) {
     cudaLaunchAttribute at;
-    const cudaLaunchConfig_t cfg = config(1, 1 << log, &at, nullptr);
+    const cudaLaunchConfig_t cfg = config(1, 1 << log, &at);
     e = cudaOccupancyMaxActiveClusters(&d->clusters[log], gemm_kernel<MATS, RAGGED, WIDE>, &cfg);
     if (e == cudaSuccess && d->clusters[log] < 1) e = cudaErrorInvalidConfiguration;
   }

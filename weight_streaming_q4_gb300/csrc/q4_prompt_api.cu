@@ -4,8 +4,6 @@
 #include <math.h>
 #include <stdint.h>
 #include <string.h>
-#include <stdio.h>
-#include <stdlib.h>
 
 #include <mutex>
 
@@ -15,7 +13,7 @@
 
 namespace {
 
-constexpr int kMostRows = 1 << 24;
+constexpr int kMostRows = 1 << 24, kMostOutputs = 1 << 30;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -46,7 +44,6 @@ int device_of(const q4::PromptDevice** out) {
     Q4_CUDA(q4::gemm_prepare(&d));
     Q4_CUDA(q4::block_norm_prepare());
     Q4_CUDA(cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev));
-    if (getenv("Q4DBG")) printf("clusters %d %d %d\n", d.clusters[0], d.clusters[1], d.clusters[2]);
     known[dev] = d;
   }
   *out = &known[dev];
@@ -55,7 +52,7 @@ int device_of(const q4::PromptDevice** out) {
 
 int run_gemm(const void* w0, const void* w1, const uint16_t* x, int64_t x_ld, int n, int k, int rows, const float* bias0,
              const float* bias1, int act, float scale, q4::RowsIn residual, uint16_t* y, int64_t y_ld, void* stream) {
-  if (!w0 || n < 1 || k < q4::kQK || k % q4::kQK || rows < 0 || rows > kMostRows) return Q4_ERR_ARG;
+  if (!w0 || n < 1 || n > kMostOutputs || k < q4::kQK || k % q4::kQK || rows < 0 || rows > kMostRows) return Q4_ERR_ARG;
   if (act < Q4_ACT_NONE || act > Q4_ACT_GELU_TANH) return Q4_ERR_ARG;
   // (rows that do not start 16-byte aligned are addressed by 16-bit elements in 31 bits)
   if (k % 256 && static_cast<int64_t>(n) * (k / q4::kQK) > ((int64_t{1} << 32) - 1) / q4::kBlockBytes) return Q4_ERR_ARG;
@@ -73,6 +70,8 @@ int run_gemm(const void* w0, const void* w1, const uint16_t* x, int64_t x_ld, in
   const q4::PromptDevice* d = nullptr;
   const int st = device_of(&d);
   if (st != Q4_OK) return st;
+  // (a chained q4_gemv behind this product starts after it)
+  q4::oneshot_chain_break(static_cast<cudaStream_t>(stream));
   Q4_CUDA(q4::gemm_launch(a, *d, static_cast<cudaStream_t>(stream)));
   return Q4_OK;
 }
