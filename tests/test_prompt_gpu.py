@@ -96,6 +96,28 @@ def test_defaults_and_flat_buffers(rows, n, k):
     assert torch.all(y == 3)
 
 
+@pytest.mark.parametrize("rows", [1, 8, 9, 150])
+@pytest.mark.parametrize("k", [32, 96, 160, 224, 256, 288, 480])
+@pytest.mark.parametrize("n", [16, 31, 64, 65, 129, 257])
+def test_matrices_that_end_inside_a_copy(rows, n, k):
+    """Narrow matrices at the end of a buffer: a copy of 256 or 1024 columns spans rows, and the last ones would leave the matrix."""
+    rng = np.random.default_rng(n + k)
+    blocks, (xb, x) = [ref.q4_bytes(n, k, k + i) for i in range(2)], rows_of(rng, rows, k)
+    behind = []
+    for b in blocks:
+        buf = torch.full((1 << 16 | b.size,), 255, dtype=torch.uint8, device="cuda")
+        behind.append(buf[buf.numel() - b.size & ~15:][:b.size])
+        behind[-1].copy_(dev(b).view(-1))
+    w = [ref.weights(b) for b in blocks]
+    y = torch.zeros((rows, n), dtype=torch.float16, device="cuda")
+    q4.q4_gemm(behind[0], xb, k, n, k, rows, None, y, n)
+    settled()
+    ref.assert_near(ref.host(y), *ref.gemm(w[0], x))
+    q4.q4_gemm_gated(*behind, xb, k, n, k, rows, None, y, n)
+    settled()
+    ref.assert_near(ref.host(y), *ref.gated(*w, x))
+
+
 def test_a_chained_product_waits_for_the_product_before_it():
     """A chained matrix-vector product whose x a many-row product has just written."""
     n, k, rng = 4096, 4096, np.random.default_rng(5)

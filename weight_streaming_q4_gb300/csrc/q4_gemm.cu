@@ -2,22 +2,34 @@
 //   y[r][i] = f16(residual + scale * act(sum_k W[i][k] x[r][k] + bias[i])),  or  f16(act(g) * u) of two matrices.
 //
 // The weights are the first operand of the tensor cores, 256 rows of W per
-// pair of CTAs (128 in each), and bn <= 128 rows of x the second.  A pair walks
-// tiles of 256 x bn outputs along k:
-//   copies      W blocks as they lie in memory, 256 columns at a time, and the CTA's
-//               half of x's rows (128-byte swizzle), by TMA into two rings
+// pair of CTAs (128 in each), and bn <= 256 rows of x the second (192 with two
+// matrices).  A pair walks tiles of 256 x bn outputs along k:
+//   copies      W as it lies in memory, 256 columns at a time, by 16-byte cp.async; the
+//               CTA's half of x's rows by tensor copies (128-byte swizzle): two rings
 //   conversion  a thread per row of W: nibbles to f16((q - 8) * d) in registers,
 //               stored into a ring of operands in tensor memory
 //   products    one thread of the leading CTA: tcgen05.mma over both CTAs, operand A
 //               in tensor memory, B in shared memory, fp32 sums in tensor memory
 //   epilogue    a thread per row of W: bias, activation, residual, one rounding
-// Weights never exist in binary16 outside tensor memory, so that a step moves
-// 36 bytes of shared memory per row of W where an unpacked operand would move
-// 128, and with a pair each CTA fetches half of x only.
+// Weights never exist in binary16 outside tensor memory, so that a step of 64
+// columns moves 36 bytes of shared memory per row of W where an unpacked operand
+// would move 128 in and out, and with a pair each CTA fetches half of x only.  W's blocks
+// are converted again for every bn rows of x: about 340 cycles of a scheduler
+// per 32 rows and 64 columns (106 instructions, 64 of them on the half-rate
+// binary16 pipe), beside products of 2 bn (two matrices 4 bn) cycles a step, which
+// is why tiles are as wide as tensor memory lets them be and the plan weighs
+// both times.
 //
-// With few tiles, a cluster of 2, 4 or 8 CTAs shares one tile: each pair takes
-// a part of k and the parts are added, in a fixed order, over distributed
-// shared memory.
+// With few tiles, a cluster of 4 or 8 CTAs shares one tile: each pair takes a part
+// of k and the parts are added, in a fixed order, over distributed shared memory.
+//
+// The tensor cores cut the fp32 sums at every step instead of rounding them:
+// 1.7e-5 of a sum of 14336 products, far below the rounding to binary16.
+//
+// Measured in a graph, other inputs every time: 2048 rows, gated 14336 x 4096 289 us, 1666 TFLOP/s (88 % of a library
+// matrix product's rate); 4096 x 14336 with a residual 154 us, 1557 (two rounds of tiles where 1.68 would do); 300 rows, gated
+// 28672 x 8192 171 us, 1646.  16 rows, gated 14336 x 4096 27 us, 2.5 TB/s of W: the conversion bounds it, and 56 of
+// the 76 pairs have a tile.
 #include <cuda_fp16.h>
 #include <stdint.h>
 
@@ -37,7 +49,9 @@ constexpr int kGmConvert = 4, kGmEpilogue = 20;     // first warps of these role
 constexpr int kGmTeams = 5;                         // of four warps, that finish the last tile
 constexpr int kGmMaxX = 16, kGmMaxW = 8;            // stages of the rings at most
 constexpr int kGmSmem = 232448 - 1024;              // dynamic shared memory at most
-constexpr int kGmWide = 64;                         // columns of a tile's sums up to which stages are twice as long
+// Columns of a tile's sums up to which stages are twice as long: 9 rows of 4096 x 4096 take 14.6 us so and 16.2
+// otherwise; from 128 on there is no tensor memory for three such stages.
+constexpr int kGmWide = 64;
 constexpr int kGmCols = 512;                        // columns of tensor memory
 constexpr int kGmMaxA = 7;                          // operand stages at most
 
@@ -225,8 +239,8 @@ __global__ void __launch_bounds__(kGmThreads, 1)
     Ring r;
     for (int64_t t = first; t < tiles; t += stride) {
       const int w0 = gm_tile(p, a.rows, t).row * 256 + half * 128 + r0;
-      // every byte of the pieces lies in the matrix
-      const bool whole = w0 + ROWS < a.n || (!RAGGED && w0 + ROWS == a.n);
+      // every byte of the pieces lies in the matrix: those of the last row's last columns end last
+      const bool whole = (w0 + ROWS - 1) * row_bytes + (units - 1) * 144 + G::PIECES * 16 <= end;
       for (int u = u0; u < u1; ++u) {
         gm_wait(c, &c->w_empty[r.slot], r.turn ^ 1);
         const uint32_t to = to0 + r.slot * G::W_STAGE;
@@ -519,8 +533,10 @@ __global__ void __launch_bounds__(kGmThreads, 1)
 
 // ------------------------------------------------------------------ host
 
-// Time of a plan in cycles, roughly: waves of tiles, each as long as the slower of its products and its conversion, and
-// its epilogue where nothing is formed meanwhile.
+// Time of a plan in cycles, roughly: rounds of tiles, each as long as the slower of its products and its conversion, and
+// its epilogue where nothing is formed meanwhile.  The conversion's 370 (two matrices 600) cycles a step decide between
+// narrow and wide tiles: 500 rows of 4096 x 14336 46.3 us with 370 and 49.2 with 300, 500 rows of the gated 28672 x 8192
+// 344 us with 740 and 326 with 600; 300 rows of that 262 us with tiles of at most 128 rows of x, 184 with up to 192.
 GmPlan plan(const GemmArgs& a, const PromptDevice& d, int mats, int w_stage) {
   const int units = (a.k + 255) / 256, most = mats == 2 ? 192 : 256;
   const double convert = (mats == 2 ? 600. : 370.) * (a.k % 256 ? 1.2 : 1.);
@@ -548,6 +564,7 @@ GmPlan plan(const GemmArgs& a, const PromptDevice& d, int mats, int w_stage) {
   const bool wide = sums <= kGmWide;
   best.na = (kGmCols - best.sums * sums) / (wide ? 128 : 64);
   if (best.na > kGmMaxA) best.na = kGmMaxA;
+  // (what shared memory holds beside two to four stages of x)
   best.nw = sums <= 128 ? 6 : 4;
   if (best.nw * w_stage > 140 * 1024) best.nw = 140 * 1024 / w_stage;
   const int room = kGmSmem - 2048 - best.nw * w_stage;
