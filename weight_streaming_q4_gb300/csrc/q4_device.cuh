@@ -539,10 +539,8 @@ bool encode_q4_rows(CUtensorMap* m, const uint8_t* w, int n_rows, int k, int box
 // if the driver cannot encode it.
 bool encode_f16_rows(CUtensorMap* m, const void* base, int64_t rows, int cols, int box_rows);
 // Host: as encode_f16_rows for rows of any number of values, ld apart (a multiple of 8; values past a row's end and
-// rows past the last read as zeros); and of rows of bytes that lie one behind the other (row_bytes a multiple of 16), not
-// swizzled.
+// rows past the last read as zeros).
 bool encode_f16_tile(CUtensorMap* m, const void* base, int64_t rows, int cols, int64_t ld, int box_rows);
-bool encode_bytes_tile(CUtensorMap* m, const void* base, int64_t rows, int64_t row_bytes, int box_bytes, int box_rows);
 // Glue launches; pdl as for mma_launch (each glue kernel waits for its inputs first).
 cudaError_t glue_norm(const uint16_t* src16, const float* src32, int batch, int dim, float eps, uint16_t* z,
                       cudaStream_t s, bool pdl = false);
