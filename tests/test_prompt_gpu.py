@@ -260,29 +260,50 @@ def test_rows_beyond_31_bits():
 WIDTHS = [1, 7, 8, 33, 64, 255, 500, 512, 1000, 1024, 2048, 4096, 5120, 8184, 8192, 8200, 10007, 16384, 16392, 28672, 32768]
 
 
-@pytest.mark.parametrize("n", WIDTHS)
-@pytest.mark.parametrize("kind", ["rms", "layer"])
-def test_block_norm(n, kind):
+def check_norm(rows, n, kind, i, pads):
+    """One call against the formula; i picks types, gates and vectors, pads are what lies beside the rows of block, residual, t and z."""
     rng = np.random.default_rng(n)
-    i = WIDTHS.index(n) + (kind == "layer") * 7
-    rows, post, gate_rows = 5, i % 2 == 0, [0, 2, 1, 5, None][i % 5]
+    post, gate_rows = i % 2 == 0, [0, 2, 1, rows, None][i % 5]
+    b_ld, r_ld, t_ld, z_ld = (n + pad for pad in pads)
     bt, rt, tt, zt = (F32 if i >> j & 1 else F16 for j in range(4))
     vec = lambda: rng.normal(size=n).astype(np.float32)     # noqa: E731
-    block, b = rows_of(rng, rows, n, bt, n + i % 3, scale=3.0)
-    res, r = rows_of(rng, rows, n, rt, n + i % 2) if i % 4 else (None, None)
+    block, b = rows_of(rng, rows, n, bt, b_ld, scale=3.0)
+    res, r = rows_of(rng, rows, n, rt, r_ld) if i % 4 else (None, None)
     weight, bias, pw, pb = vec(), vec() if i % 3 else None, vec() if post and i % 4 else None, vec() if post and i % 3 else None
     gates = None if gate_rows is None else rng.normal(size=(-(-rows // gate_rows) if gate_rows else 1, n)).astype(np.float32)
     gate = None if gates is None else gates[np.arange(rows) // gate_rows] if gate_rows else gates
     d = lambda v: None if v is None else dev(v)     # noqa: E731
     norms = q4.BlockNorm.of(n, q4.Q4_NORM_LAYER if kind == "layer" else q4.Q4_NORM_RMS, 1e-5, d(weight), d(bias), d(pw), d(pb), 0.5, d(gates), n, gate_rows or 0, post)
-    t = torch.full((rows + 1, n + 2), 7.0, dtype=TORCH[tt], device="cuda")
-    z = torch.full((rows + 1, n + 4), 7.0, dtype=TORCH[zt], device="cuda")
-    q4.q4_block_norm(norms, rows, block, bt, n + i % 3, res, rt, n + i % 2, t, tt, n + 2, z, zt, n + 4)
+    t = torch.full((rows + 1, t_ld), 7.0, dtype=TORCH[tt], device="cuda")
+    z = torch.full((rows + 1, z_ld), 7.0, dtype=TORCH[zt], device="cuda")
+    q4.q4_block_norm(norms, rows, block, bt, b_ld, res, rt, r_ld, t, tt, t_ld, z, zt, z_ld)
     settled()
     want = ref.block_norm(b, r, kind, float(np.float32(1e-5)), post, pw, pb, 0.5, gate, weight, bias)
     for got, typ, (v, off) in ((t, tt, want[0]), (z, zt, want[1])):
         ref.assert_near(ref.host(got[:rows, :n]), v, ref.rounded(v, off) if typ == F16 else off + 2.0 ** -23 * np.abs(v), f"{n} {kind}")
         assert torch.all(got[rows:] == 7) and torch.all(got[:, n:] == 7), "memory behind the rows or values was written"
+
+
+@pytest.mark.parametrize("n", WIDTHS)
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_block_norm(n, kind):
+    i = WIDTHS.index(n) + (kind == "layer") * 7
+    check_norm(5, n, kind, i, (i % 3, i % 2, 2, 4))
+
+
+@pytest.mark.parametrize("n", [n for n in WIDTHS if n % 8 == 0])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_block_norm_of_whole_pieces(n, kind):
+    i = WIDTHS.index(n) + (kind == "layer") * 7
+    check_norm(5, n, kind, i + 1, (0, 8, 16, 0))
+
+
+@pytest.mark.parametrize("rows,n", [(6000, 24), (3000, 136), (700, 1024), (640, 4096), (500, 8192), (470, 8200), (310, 16384), (320, 16392), (310, 32768),
+                                    (6000, 17), (3000, 33), (700, 1125), (500, 4095), (330, 4097), (152, 5935), (330, 5935), (310, 8193), (310, 16385)])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("turn", range(3))
+def test_more_rows_than_run_at_once(rows, n, kind, turn):
+    check_norm(rows, n, kind, n + 5 * turn + (kind == "layer") + turn // 2, (8, 0, 0, 16) if n % 8 == 0 else (0, turn, 1, 0))
 
 
 @pytest.mark.parametrize("n", [72, 4096])

@@ -10,6 +10,7 @@
 // Measured in a graph, other buffers every time: 2048 rows of 8192, binary16 block onto an fp32 residual, t and z: 34 us,
 // 5.9 TB/s (a copy of as many bytes 31); with a post norm, its bias and gates 44 us on the same card, since
 // one row's statistics, gate and second statistics follow one another on an SM.  16 rows of 4096: 2.9 us, a launch.
+// Rows that are not whole pieces, 2048 of 8191 with all of it: 78 us (eight scalar loads for a wide one).
 #include <cuda_fp16.h>
 #include <stdint.h>
 
@@ -19,12 +20,10 @@ namespace q4 {
 
 namespace {
 
-// E values of a row per thread, V side by side: chunk j of V values starts at (j * threads + thread) * V.
+// V values side by side.
 template <int V>
 __device__ __forceinline__ void load_row(const RowsIn& r, int64_t at, float* v) {
-  if (V == 1) {
-    v[0] = r.f32 ? static_cast<const float*>(r.p)[at] : __half2float(static_cast<const __half*>(r.p)[at]);
-  } else if (r.f32) {
+  if (r.f32) {
     const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(r.p) + at);
 #pragma unroll
     for (int i = 0; i < V / 4; ++i) {
@@ -66,14 +65,10 @@ __device__ __forceinline__ void store_row(const RowsOut& r, int64_t at, const fl
 
 template <int V>
 __device__ __forceinline__ void load_vec(const float* p, int at, float* v) {
-  if (V == 1) {
-    v[0] = __ldg(p + at);
-  } else {
 #pragma unroll
-    for (int i = 0; i < V / 4; ++i) {
-      const float4 f = __ldg(reinterpret_cast<const float4*>(p + at) + i);
-      v[4 * i] = f.x, v[4 * i + 1] = f.y, v[4 * i + 2] = f.z, v[4 * i + 3] = f.w;
-    }
+  for (int i = 0; i < V / 4; ++i) {
+    const float4 f = __ldg(reinterpret_cast<const float4*>(p + at) + i);
+    v[4 * i] = f.x, v[4 * i + 1] = f.y, v[4 * i + 2] = f.z, v[4 * i + 3] = f.w;
   }
 }
 
@@ -96,99 +91,111 @@ __device__ __forceinline__ float cta_sum(float v, float* red) {
   return v;
 }
 
-// Rows of any alignment and length, a row per CTA.
-template <int E, int T>
-__global__ void __launch_bounds__(T) block_norm_kernel(const __grid_constant__ NormArgs a) {
+// Rows of any alignment and length: persistent CTAs, a value per access (a warp takes 32 side by side).  Every load of a
+// batch is issued before any of them is used, and with AHEAD the next row is on its way, as the bits it has in memory,
+// while a row is worked on.
+template <int E, int T, bool AHEAD>
+__global__ void __launch_bounds__(T, 1) block_norm_any_kernel(const __grid_constant__ NormArgs a) {
   __shared__ float red[2][32];
   int turn = 0;
-  constexpr int V = 1;
-  const int64_t row = blockIdx.x;
-  const int step = blockDim.x * V, at0 = threadIdx.x * V;
   const float inv_n = 1.f / static_cast<float>(a.n);
   const q4_norms& p = a.p;
-  float v[E];
+  // (a warp's values side by side, so that a thread's lie at fixed distances from its first one)
+  constexpr int step = 32;
+  const int at0 = static_cast<int>(threadIdx.x >> 5) * 32 * E + static_cast<int>(threadIdx.x & 31);
+  const bool has_block = a.block.p != nullptr, post = has_block && p.post;
+  // (without a block the residual takes its place)
+  const RowsIn first{has_block ? a.block.p : a.residual.p, has_block ? a.block.ld : a.residual.ld, has_block ? a.block.f32 : a.residual.f32};
+  const RowsIn second{has_block ? a.residual.p : nullptr, a.residual.ld, a.residual.f32};
 
-  // v: centred (Q4_NORM_LAYER) and the factor 1 / sqrt(mean of squares + eps) of it
-  auto stats = [&]() {
-    float s = 0.f;
-    if (p.kind == Q4_NORM_LAYER) {
+  // COUNT values of a row from chunk j0 on, as their bits
+  auto get = [&](const RowsIn& r, int64_t row, int j0, auto& raw) {
+    constexpr int COUNT = sizeof(raw) / sizeof(raw[0]);
+    const int left = row < a.rows && r.p ? a.n : 0;
+    if (r.f32) {
+      const uint32_t* src = static_cast<const uint32_t*>(r.p) + row * r.ld + at0;
 #pragma unroll
-      for (int i = 0; i < E; ++i) s += v[i];
-      const float mean = cta_sum(s, red[turn ^= 1]) * inv_n;
+      for (int j = 0; j < COUNT; ++j) raw[j] = at0 + (j0 + j) * step < left ? src[(j0 + j) * step] : 0;
+    } else {
+      const uint16_t* src = static_cast<const uint16_t*>(r.p) + row * r.ld + at0;
 #pragma unroll
-      for (int j = 0; j < E / V; ++j)
-        if (at0 + j * step < a.n)
-#pragma unroll
-          for (int i = 0; i < V; ++i) v[j * V + i] -= mean;
-      s = 0.f;
+      for (int j = 0; j < COUNT; ++j) raw[j] = at0 + (j0 + j) * step < left ? src[(j0 + j) * step] : 0;
     }
+  };
+  auto value = [](const RowsIn& r, uint32_t raw) {
+    return r.f32 ? __uint_as_float(raw) : __half2float(__ushort_as_half(static_cast<unsigned short>(raw)));
+  };
+  auto vector = [&](const float* src, int j0, float other, auto& w) {
+    constexpr int COUNT = sizeof(w) / sizeof(w[0]);
+    const int left = src ? a.n : 0;
 #pragma unroll
-    for (int i = 0; i < E; ++i) s = fmaf(v[i], v[i], s);
-    return rsqrtf(fmaf(cta_sum(s, red[turn ^= 1]), inv_n, p.eps));
+    for (int j = 0; j < COUNT; ++j) w[j] = at0 + (j0 + j) * step < left ? __ldg(src + at0 + (j0 + j) * step) : other;
   };
 
-  float r[E];
+  uint32_t next1[E], next2[AHEAD ? E : 1];
+  if (AHEAD) get(first, blockIdx.x, 0, next1), get(second, blockIdx.x, 0, next2);
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    float v[E], r[AHEAD ? E : 1];
+    if (!AHEAD) get(first, row, 0, next1);
 #pragma unroll
-  for (int j = 0; j < E / V; ++j) {
-    const int at = at0 + j * step;
+    for (int j = 0; j < E; ++j) v[j] = value(first, next1[j]);
+    if (AHEAD) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[j * V + i] = r[j * V + i] = 0.f;
-    if (at < a.n) {
-      if (a.block.p) load_row<V>(a.block, row * a.block.ld + at, v + j * V);
-      if (a.residual.p) load_row<V>(a.residual, row * a.residual.ld + at, r + j * V);
+      for (int j = 0; j < E; ++j) r[j % (AHEAD ? E : 1)] = value(second, next2[j % (AHEAD ? E : 1)]);
+      get(first, row + gridDim.x, 0, next1), get(second, row + gridDim.x, 0, next2);
     }
-  }
-  const bool post = a.block.p && p.post;
-  const float f = post ? stats() : 1.f;
-  const float* gate = !p.gate ? nullptr : p.gate + (p.gate_rows ? row / p.gate_rows * p.gate_ld : 0);
+    // v: centred (Q4_NORM_LAYER) and the factor 1 / sqrt(mean of squares + eps) of it
+    auto stats = [&]() {
+      float s = 0.f;
+      if (p.kind == Q4_NORM_LAYER) {
 #pragma unroll
-  for (int j = 0; j < E / V; ++j) {
-    const int at = at0 + j * step;
-    if (at >= a.n) continue;
-    float w[V];
-    if (post) {
+        for (int j = 0; j < E; ++j) s += v[j];
+        const float mean = cta_sum(s, red[turn ^= 1]) * inv_n;
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[j * V + i] *= f;
-      if (p.post_weight) {
-        load_vec<V>(p.post_weight, at, w);
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[j * V + i] *= w[i];
+        for (int j = 0; j < E; ++j)
+          if (at0 + j * step < a.n) v[j] -= mean;
+        s = 0.f;
       }
-      if (p.post_bias) {
-        load_vec<V>(p.post_bias, at, w);
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[j * V + i] += w[i];
+      for (int j = 0; j < E; ++j) s = fmaf(v[j], v[j], s);
+      return rsqrtf(fmaf(cta_sum(s, red[turn ^= 1]), inv_n, p.eps));
+    };
+    if (has_block) {
+      const float f = post ? stats() : 1.f;
+      const float* gate = !p.gate ? nullptr : p.gate + (p.gate_rows ? row / p.gate_rows * p.gate_ld : 0);
+#pragma unroll
+      for (int j0 = 0; j0 < E; j0 += 4) {
+        float w[4], b[4], g[4];
+        uint32_t raw[4] = {};
+        if (post) vector(p.post_weight, j0, 1.f, w), vector(p.post_bias, j0, 0.f, b);
+        vector(gate, j0, 1.f, g);
+        if (!AHEAD) get(second, row, j0, raw);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float x = v[j0 + j];
+          if (post) x = fmaf(x * f, w[j], b[j]);
+          x = fmaf(x * g[j], p.scale, AHEAD ? r[(j0 + j) % (AHEAD ? E : 1)] : value(second, raw[j]));
+          v[j0 + j] = at0 + (j0 + j) * step < a.n ? x : 0.f;
+        }
       }
     }
-    if (gate) {
-      load_vec<V>(gate, at, w);
+    if (a.t.p) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[j * V + i] *= w[i];
+      for (int j = 0; j < E; ++j)
+        if (at0 + j * step < a.n) store_row<1>(a.t, row * a.t.ld + at0 + j * step, v + j);
     }
+    if (!a.z.p) continue;
+    const float f = stats();
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[j * V + i] = a.block.p ? fmaf(v[j * V + i], p.scale, r[j * V + i]) : r[j * V + i];
-    if (a.t.p) store_row<V>(a.t, row * a.t.ld + at, v + j * V);
-  }
-  if (!a.z.p) return;
-  const float g = stats();
+    for (int j0 = 0; j0 < E; j0 += 4) {
+      float w[4], b[4];
+      vector(p.weight, j0, 1.f, w), vector(p.bias, j0, 0.f, b);
 #pragma unroll
-  for (int j = 0; j < E / V; ++j) {
-    const int at = at0 + j * step;
-    if (at >= a.n) continue;
-    float w[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[j * V + i] *= g;
-    if (p.weight) {
-      load_vec<V>(p.weight, at, w);
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[j * V + i] *= w[i];
+      for (int j = 0; j < 4; ++j) {
+        const float x = fmaf(v[j0 + j] * f, w[j], b[j]);
+        if (at0 + (j0 + j) * step < a.n) store_row<1>(a.z, row * a.z.ld + at0 + (j0 + j) * step, &x);
+      }
     }
-    if (p.bias) {
-      load_vec<V>(p.bias, at, w);
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[j * V + i] += w[i];
-    }
-    store_row<V>(a.z, row * a.z.ld + at, v + j * V);
   }
 }
 
@@ -399,13 +406,18 @@ cudaError_t block_norm_launch(const NormArgs& a, int sms, cudaStream_t s) {
     kernel<<<static_cast<unsigned>(grid), threads_w, depth * row, s>>>(a, depth, stage_r, stage_g);
     return cudaGetLastError();
   }
-  // a value at a time: 16 per thread up to 8192 of a row, else 32 (1024 threads take 32768)
-  const int e = a.n <= 8192 ? 16 : 32;
+  // A value at a time, up to 32 a thread (1024 threads take 32768).  From 4096 on two rows in registers leave room for 512
+  // threads: 1852 rows of 5935 in 59 us so, 64 with 1024 threads and a row; 13 rows, of which no CTA has a second, 6.1 and
+  // 5.2.  2048 rows of 16383: 16 values a thread 151 us, 32 201.
+  const bool ahead = a.n <= 4096 || (a.n <= 8192 && a.rows > sms);
+  const int e = a.n <= 4096 || (a.n <= 8192 && !ahead) ? 8 : a.n <= 16384 ? 16 : 32;
   const int threads = ((a.n + e - 1) / e + 31) / 32 * 32;
-  void (*const kernel)(NormArgs) = e == 16          ? block_norm_kernel<16, 512>
-                                   : threads <= 512 ? block_norm_kernel<32, 512>
-                                                    : block_norm_kernel<32, 1024>;
-  kernel<<<a.rows, threads, 0, s>>>(a);
+  const int64_t room = static_cast<int64_t>(sms) * (threads < 512 ? 512 / threads : 1);
+  void (*const kernel)(NormArgs) = ahead ? (e == 8 ? block_norm_any_kernel<8, 512, true> : block_norm_any_kernel<16, 512, true>)
+                                   : e == 8  ? block_norm_any_kernel<8, 1024, false>
+                                   : e == 16 ? block_norm_any_kernel<16, 1024, false>
+                                             : block_norm_any_kernel<32, 1024, false>;
+  kernel<<<static_cast<unsigned>(a.rows < room ? a.rows : room), threads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
