@@ -627,7 +627,7 @@ typedef struct q4_epilogue {
   const float *bias;       /* device, fp32 [n], or null: none */
   int act;                 /* Q4_ACT_* */
   float scale;             /* of the activated product (1: none) */
-  const void *residual;    /* device, rows of n values of residual_type, or null: none; may be y itself */
+  const void *residual;    /* device, rows of n values of residual_type, or null: none; may be y itself (binary16, y_ld apart) */
   int residual_type;       /* Q4_TYPE_* */
   int64_t residual_ld;
 } q4_epilogue;
@@ -705,8 +705,8 @@ typedef struct q4_norms {
  *   z          device, rows of n values of z_type, written, or null: not wanted
  *              (not both null)
  *   n          1 .. 32768;  rows 0 .. 2^24
- * t and z may each be the block or the residual itself (same type and ld), but
- * not overlap one another or them in another way.  A value that is not finite
+ * t and z may each be the block or the residual itself (of the same type and
+ * ld, else Q4_ERR_ARG), but not overlap one another or them in another way.  A value that is not finite
  * leaves its own row not finite.  Squares are fp32: values within +-2^56.
  * Errors: Q4_ERR_ARG, Q4_ERR_ALIGN, Q4_ERR_CUDA.
  */

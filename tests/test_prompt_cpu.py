@@ -50,6 +50,14 @@ def test_products_own_arguments(lib):
     assert gemm(lib, rows=0, x=None, y=None) == (OK, OK)
 
 
+def test_products_onto_their_inputs(lib):
+    far = dict(w=2 * A, w_up=3 * A, x=4 * A, y=A)
+    assert gemm(lib, **{**far, "x": A}) == (ARG, ARG) and gemm(lib, **{**far, "w": A}) == (ARG, ARG) and gemm(lib, **{**far, "w_up": A})[1] == ARG
+    # the residual may be y, in y's rows
+    assert gemm(lib, **far, residual=A, residual_type=F32)[0] == ARG and gemm(lib, **far, residual=A, residual_ld=9)[0] == ARG
+    assert gemm(lib, **far, rows=1, residual=A, residual_type=F32)[0] == ARG
+
+
 def norm(lib, kind=0, eps=1e-5, gate=None, gate_ld=8, gate_rows=0, weight=None, rows=2, n=8, block=A, residual=None, t=None, z=A, types=(F16,) * 4, ld=8):
     p = q4.BlockNorm(kind, eps, 0, None, None, 1.0, gate, gate_ld, gate_rows, weight, None)
     return lib.q4_block_norm(p, rows, n, block, types[0], ld, residual, types[1], ld, t, types[2], ld, z, types[3], ld, None)
@@ -69,6 +77,15 @@ def test_norm_alignment(lib, over):
     assert norm(lib, **over) == ALIGN
     assert lib.q4_block_norm(None, 1, 8, A, F16, 8, None, F16, 8, None, F16, 8, A, F16, 8, None) == ARG
     assert norm(lib, rows=0, block=None, z=None) == OK
+
+
+def test_norms_onto_their_inputs(lib):
+    assert norm(lib, block=A, t=2 * A, z=2 * A) == ARG
+    for over in (dict(block=A, z=A, types=(F16, F16, F16, F32)), dict(block=A, z=2 * A, t=A, types=(F32, F16, F16, F16)),
+                 dict(block=A, residual=2 * A, z=2 * A, types=(F16, F32, F16, F16)), dict(block=A, residual=2 * A, t=2 * A, z=3 * A, types=(F16, F16, F32, F16))):
+        assert norm(lib, **over) == ARG
+    p = q4.BlockNorm(0, 1e-5, 0, None, None, 1.0, None, 0, 0, None, None)
+    assert lib.q4_block_norm(p, 2, 8, A, F16, 8, None, F16, 8, None, F16, 8, A, F16, 16, None) == ARG
 
 
 def test_rotations(lib):

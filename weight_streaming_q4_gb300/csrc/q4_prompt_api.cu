@@ -25,6 +25,11 @@ int check_rows(const void* p, int type, int64_t ld, int64_t row) {
   return aligned(p, type == Q4_TYPE_F32 ? 4 : 2) ? Q4_OK : Q4_ERR_ALIGN;
 }
 
+// An output that starts where an input does has to have its rows there too.
+bool rows_clash(const q4::RowsOut& out, const q4::RowsIn& in, int rows) {
+  return out.p && out.p == in.p && (out.f32 != in.f32 || (rows > 1 && out.ld != in.ld));
+}
+
 #define Q4_CUDA(call)                                           \
   do {                                                          \
     cudaError_t e_ = (call);                                    \
@@ -60,6 +65,8 @@ int run_gemm(const void* w0, const void* w1, const uint16_t* x, int64_t x_ld, in
   if (rows == 0) return Q4_OK;
   if (!x || !y || x_ld < k || x_ld > (int64_t{1} << 31) || y_ld < n || y_ld > (int64_t{1} << 31)) return Q4_ERR_ARG;
   if (!aligned(x, 16) || x_ld % 8 || !aligned(y, 2)) return Q4_ERR_ALIGN;
+  const void* const out = y;
+  if (out == x || out == w0 || out == w1 || rows_clash({y, y_ld, 0}, residual, rows)) return Q4_ERR_ARG;
   q4::GemmArgs a;
   a.w[0] = static_cast<const uint8_t*>(w0), a.w[1] = static_cast<const uint8_t*>(w1);
   a.x = reinterpret_cast<const __half*>(x), a.x_ld = x_ld;
@@ -119,6 +126,9 @@ extern "C" int q4_block_norm(const q4_norms* norms, int rows, int n, const void*
   a.residual = {residual, residual_ld, residual_type == Q4_TYPE_F32};
   a.t = {t, t_ld, t_type == Q4_TYPE_F32};
   a.z = {z, z_ld, z_type == Q4_TYPE_F32};
+  if (t == z) return Q4_ERR_ARG;
+  for (const q4::RowsIn& in : {a.block, a.residual})
+    if (rows_clash(a.t, in, rows) || rows_clash(a.z, in, rows)) return Q4_ERR_ARG;
   const q4::PromptDevice* d = nullptr;
   if ((st = device_of(&d)) != Q4_OK) return st;
   Q4_CUDA(q4::block_norm_launch(a, d->sms, static_cast<cudaStream_t>(stream)));
