@@ -20,7 +20,7 @@
 // is why tiles are as wide as tensor memory lets them be and the plan weighs
 // both times.
 //
-// With few tiles, a cluster of 4 or 8 CTAs shares one tile: each pair takes a part
+// With few tiles, a cluster of 4, 8 or 16 CTAs shares one tile: each pair takes a part
 // of k and the parts are added, in a fixed order, over distributed shared memory.
 //
 // The tensor cores cut the fp32 sums at every step instead of rounding them:
@@ -46,6 +46,7 @@ __device__ int g_status_gm;
 
 constexpr int kGmThreads = 768;
 constexpr int kGmConvert = 4, kGmEpilogue = 20;     // first warps of these roles
+constexpr int kGmSplits = 4;                        // 1, 2, 4 or 8 pairs share a tile
 constexpr int kGmTeams = 5;                         // of four warps, that finish the last tile
 constexpr int kGmMaxX = 16, kGmMaxW = 8;            // stages of the rings at most
 constexpr int kGmSmem = 232448 - 1024;              // dynamic shared memory at most
@@ -536,7 +537,9 @@ __global__ void __launch_bounds__(kGmThreads, 1)
 // Time of a plan in cycles, roughly: rounds of tiles, each as long as the slower of its products and its conversion, and
 // its epilogue where nothing is formed meanwhile.  The conversion's 370 (two matrices 600) cycles a step decide between
 // narrow and wide tiles: 500 rows of 4096 x 14336 46.3 us with 370 and 49.2 with 300, 500 rows of the gated 28672 x 8192
-// 344 us with 740 and 326 with 600; 300 rows of that 262 us with tiles of at most 128 rows of x, 184 with up to 192.
+// 344 us with 740 and 326 with 600; 300 rows of that 262 us with tiles of at most 128 rows of x, 184 with up to 192.  Eight pairs to a
+// tile (7 such clusters fit the GPU): 44 rows of the gated 277 x 27648 38 us, with four 60; 33 rows of 1024 x 8192 11.9 and
+// 13.3, of 1024 x 4096 the same; 200 rows of 1024 x 8192 17.2 as one tile of 8 pairs and 15.4 as three of four.
 GmPlan plan(const GemmArgs& a, const PromptDevice& d, int mats, int w_stage) {
   const int units = (a.k + 255) / 256, most = mats == 2 ? 192 : 256;
   const double convert = (mats == 2 ? 600. : 370.) * (a.k % 256 ? 1.2 : 1.);
@@ -547,12 +550,12 @@ GmPlan plan(const GemmArgs& a, const PromptDevice& d, int mats, int w_stage) {
     const int tok = (a.rows + bn - 1) / bn;
     if (bn > 32 && (a.rows + bn - 33) / (bn - 32) == tok) continue;      // (a narrower tile does as well)
     const int64_t tiles = static_cast<int64_t>(tok) * best.row_tiles;
-    for (int log = 0; log < 3; ++log) {
+    for (int log = 0; log < kGmSplits; ++log) {
       const int split = 1 << log;
       if (log > 0 && (tiles > d.clusters[log] || units < 2 * split)) break;
       const int64_t waves = (tiles + d.clusters[log] - 1) / d.clusters[log];
       const double step = 2. * bn * mats > convert ? 2. * bn * mats : convert;
-      const double time = waves * ((units + split - 1) / split * 4 * step + (bn * mats > 128 ? 12. * bn * mats : 0)) + (log ? 3000 + 4. * bn * mats : 0);
+      const double time = waves * ((units + split - 1) / split * 4 * step + (bn * mats > 128 ? 12. * bn * mats : 0)) + (log ? (3000 + 4. * bn * mats) * (log == 3 ? 1.5 : 1.) : 0);
       if (least == 0 || time < least) least = time, best.bn = bn, best.split = split, best.tok_tiles = tok;
     }
   }
@@ -608,11 +611,13 @@ cudaError_t launch(const GemmArgs& a, const PromptDevice& d, cudaStream_t s) {
 template <int MATS, bool RAGGED, bool WIDE>
 cudaError_t prepare(PromptDevice* d) {
   cudaError_t e = cudaFuncSetAttribute(gemm_kernel<MATS, RAGGED, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGmSmem);
-  for (int log = 0; e == cudaSuccess && log < 3; ++log) {
+  // (clusters of 16 CTAs are no portable size)
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(gemm_kernel<MATS, RAGGED, WIDE>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  for (int log = 0; e == cudaSuccess && log < kGmSplits; ++log) {
     cudaLaunchAttribute at;
     const cudaLaunchConfig_t cfg = config(1, 1 << log, &at);
     e = cudaOccupancyMaxActiveClusters(&d->clusters[log], gemm_kernel<MATS, RAGGED, WIDE>, &cfg);
-    if (e == cudaSuccess && d->clusters[log] < 1) e = cudaErrorInvalidConfiguration;
+    if (e == cudaSuccess && d->clusters[log] < 1 && log < 3) e = cudaErrorInvalidConfiguration;
   }
   return e;
 }

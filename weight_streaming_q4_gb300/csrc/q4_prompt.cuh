@@ -39,7 +39,7 @@ struct GemmArgs {
 // What the kernels need to know of the device they run on.
 struct PromptDevice {
   int sms;
-  int clusters[3];          // of 2, 4 and 8 CTAs of the product's kernel that run at once
+  int clusters[4];          // of 2, 4, 8 and 16 CTAs of the product's kernel that run at once
 };
 cudaError_t gemm_prepare(PromptDevice* d);
 cudaError_t gemm_launch(const GemmArgs& a, const PromptDevice& d, cudaStream_t s);
