@@ -39,6 +39,7 @@ ODD = [(1, 1, 32), (1, 64, 256), (2, 5, 64), (3, 130, 96), (7, 128, 512), (16, 1
        (257, 260, 2304), (300, 1030, 512), (520, 700, 320), (1000, 257, 128), (1500, 5200, 96), (2100, 4100, 512), (37, 4099, 4128), (1, 4096, 4096), (4, 6144, 4096),
        # few tiles and a long k, shared by up to 8 pairs
        (40, 300, 8192), (33, 1024, 8192), (200, 1000, 4096), (17, 256, 11008), (60, 520, 8224), (96, 1500, 4352), (12, 100, 28672),
+       (5, 300, 11008), (8, 1030, 8224), (1, 1024, 4096), (3, 2000, 6176), (7, 40, 28672), (2, 5000, 4128), (1, 100, 3200), (6, 2500, 2304),
        # more tiles than run at once, by the rows of x that a tile takes
        (30, 20000, 288), (64, 20000, 256), (100, 20000, 256), (150, 500, 320), (190, 700, 512), (384, 10300, 256), (8, 12000, 256), (9, 5000, 96)]
 

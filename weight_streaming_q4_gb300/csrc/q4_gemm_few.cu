@@ -11,7 +11,10 @@
 // is free, so a thread takes 36 bytes of its two rows of W, two whole
 // blocks, and the same 64 columns of x, and nothing is exchanged.  9 words
 // apart, the four threads of a row and the eight rows of a load fall in 32
-// different banks.  The warps' sums meet in shared memory, in a fixed order.
+// different banks.  The warps' sums meet in shared memory, in a fixed order; few
+// tiles are shared by clusters of 2, 4 or 8 CTAs, each with a part of k, whose
+// sums meet over distributed shared memory (1024 x 4096, one row: 5.7 -> 4.4 us;
+// 6176 x 17824, five: 39 -> 31; the gated 328 x 15616, two: 18.7 -> 7.0).
 //
 // Measured in a graph: one row, 4096 x 4096 with a residual 5.5 us (the kernel of many rows 14.4); gated 14336 x 4096
 // 21.7 us, 3.0 TB/s, with 8 rows 27 (the other kernel 27 for any number up to 32).  What bounds it is the arithmetic from
@@ -22,6 +25,7 @@
 
 #include "q4_frag.cuh"
 #include "q4_gemm.cuh"
+#include "q4_tensor.cuh"
 
 namespace q4 {
 
@@ -42,8 +46,14 @@ struct Fw {
   static constexpr int W_BYTES = kFwRowsW * PITCH;
 };
 
-template <int MATS, bool RAGGED>
-__global__ void __launch_bounds__(kFwThreads, kFwCtas) few_kernel(const __grid_constant__ GemmArgs a, int stages, int stage_bytes) {
+__device__ __forceinline__ float cluster_load(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+template <int MATS, bool RAGGED, bool SHARED>
+__global__ void __launch_bounds__(kFwThreads, kFwCtas) few_kernel(const __grid_constant__ GemmArgs a, int stages, int stage_bytes, int members) {
   using F = Fw<RAGGED>;
   constexpr int ROWS = kFwRowsW / MATS, COLS = kFewRows + 4;   // rows of each matrix; floats between the rows of the sums
   extern __shared__ __align__(128) char smem[];
@@ -51,6 +61,10 @@ __global__ void __launch_bounds__(kFwThreads, kFwCtas) few_kernel(const __grid_c
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int nb = a.k / kQK, units = (nb + 7) / 8, count = (units + kFwSlices - 1) / kFwSlices;
   const int tiles = (a.n + ROWS - 1) / ROWS;
+  // SHARED: the CTAs of a cluster, `split` of them, share a tile, and this one takes these stages of it
+  const int split = SHARED ? members : 1;
+  const int part = SHARED ? static_cast<int>(cluster_rank()) : 0, s0 = count * part / split, s1 = count * (part + 1) / split;
+  const int first = blockIdx.x / split, stride = gridDim.x / split;
   const int64_t row_bytes = static_cast<int64_t>(nb) * kBlockBytes, end = row_bytes * a.n;
 
   // The copies, a stage ahead of another: tile c_tile, columns 1024 c_s ...  Row r of a tile is its row r % ROWS of matrix
@@ -59,7 +73,7 @@ __global__ void __launch_bounds__(kFwThreads, kFwCtas) few_kernel(const __grid_c
   const uint8_t* const w = a.w[MATS == 2 ? r >> 4 : 0];
   auto start = [&](int64_t row) { return RAGGED ? (row * row_bytes) & ~int64_t{15} : row * row_bytes; };
   const uint32_t base = smem_u32(smem);
-  int c_tile = blockIdx.x, c_s = 0, c_slot = 0;
+  int c_tile = first, c_s = s0, c_slot = 0;
   int64_t from = start(c_tile * ROWS + (MATS == 2 ? r & 15 : r));
   auto copy = [&]() {
     if (c_tile < tiles) {
@@ -94,8 +108,8 @@ __global__ void __launch_bounds__(kFwThreads, kFwCtas) few_kernel(const __grid_c
         cp16_part(to + F::W_BYTES + rr * kFwXRow + (p >> 3) * kFwChunk + (p & 7) * 16, a.x + (bytes ? rr * a.x_ld + col : 0), bytes);
       }
       if (++c_slot == stages) c_slot = 0;
-      if (++c_s == count) {
-        c_s = 0, c_tile += gridDim.x;
+      if (++c_s == s1) {
+        c_s = s0, c_tile += stride;
         from = start(static_cast<int64_t>(c_tile) * ROWS + (MATS == 2 ? r & 15 : r));
       }
     }
@@ -108,13 +122,13 @@ __global__ void __launch_bounds__(kFwThreads, kFwCtas) few_kernel(const __grid_c
   const int x_at = F::W_BYTES + (there ? g : 0) * kFwXRow + (slice * 4 + t) * kFwChunk;
   const int w_at = r0 * F::PITCH + slice * 144 + 36 * t;
   int slot = 0;
-  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+  for (int tile = first; tile < tiles; tile += stride) {
     const int w0 = tile * ROWS;
     float acc[2][4] = {};                                     // two sums that do not wait for one another
     int shift[2] = {0, 0};
     if (RAGGED)
       for (int h = 0; h < 2; ++h) shift[h] = static_cast<int>(((w0 + (MATS == 2 ? (r0 + 8 * h) & 15 : r0 + 8 * h)) * row_bytes) & 15);
-    for (int s = 0; s < count; ++s) {
+    for (int s = s0; s < s1; ++s) {
       // (the group of this stage is done when at most stages - 2 later ones are not)
       switch (stages) {
         case 2: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
@@ -174,16 +188,34 @@ __global__ void __launch_bounds__(kFwThreads, kFwCtas) few_kernel(const __grid_c
 #pragma unroll
     for (int e = 0; e < 4; ++e) sums[slice][r0 + (e >> 1) * 8][2 * t + (e & 1)] = acc[0][e] + acc[1][e];
     __syncthreads();
+    if (SHARED) {
+      // (a CTA's slices are added up before the others read them)
+      for (int i = tid; i < kFwRowsW * a.rows; i += kFwThreads) {
+        const int rr = i % kFwRowsW, c = i / kFwRowsW;
+        float f = sums[0][rr][c];
+#pragma unroll
+        for (int j = 1; j < kFwSlices; ++j) f += sums[j][rr][c];
+        sums[0][rr][c] = f;
+      }
+      __syncwarp();
+      cluster_sync();
+    }
     // (the next sums are stored behind another barrier)
-    for (int i = tid; i < ROWS * a.rows; i += kFwThreads) {
+    for (int i = part * kFwThreads + tid; i < ROWS * a.rows; i += split * kFwThreads) {
       const int rr = i % ROWS, c = i / ROWS, n = w0 + rr;
       if (n >= a.n) continue;
       float f[MATS];
 #pragma unroll
       for (int m = 0; m < MATS; ++m) {
         f[m] = 0.f;
+        if (SHARED) {
 #pragma unroll
-        for (int j = 0; j < kFwSlices; ++j) f[m] += sums[j][m * 16 + rr][c];
+          for (int q = 0; q < 8; ++q)
+            if (q < split) f[m] += cluster_load(cluster_addr(&sums[0][m * 16 + rr][c], q));
+        } else {
+#pragma unroll
+          for (int j = 0; j < kFwSlices; ++j) f[m] += sums[j][m * 16 + rr][c];
+        }
         if (a.bias[m]) f[m] += __ldg(a.bias[m] + n);
       }
       activate<1>(f, a.act);
@@ -198,30 +230,51 @@ __global__ void __launch_bounds__(kFwThreads, kFwCtas) few_kernel(const __grid_c
       }
       a.y[c * a.y_ld + n] = __float2half_rn(f[0]);
     }
+    if (SHARED) {
+      __syncwarp();
+      cluster_sync();                // (the sums have been read)
+    }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ host
 
-constexpr int kFwSmemMost = 200 * 1024;
+constexpr int kFwSmemMost = 204 * 1024;          // of an SM
 
 template <int MATS, bool RAGGED>
 cudaError_t launch(const GemmArgs& a, const PromptDevice& d, cudaStream_t s) {
   const int stage = Fw<RAGGED>::W_BYTES + a.rows * kFwXRow;
   const int64_t tiles = (static_cast<int64_t>(a.n) + kFwRowsW / MATS - 1) / (kFwRowsW / MATS);
-  // one CTA of an SM may fill its memory, else several share it
-  const int ctas = tiles <= d.sms ? 1 : kFwCtas;
-  int stages = (ctas == 1 ? kFwSmemMost : 68 * 1024) / stage;
+  // Few tiles: clusters share them, while all their CTAs run at once, if the SM with most to do then has fewer stages, by more
+  // than what the meeting of a cluster takes (about one stage with one row of x, two with eight).
+  const int count = (a.k + 1023) / 1024;
+  auto most = [&](int split) { return (tiles * split + d.sms - 1) / d.sms * ((count + split - 1) / split); };
+  int split = 1;
+  for (int other = 2; other <= 8 && other * tiles <= d.sms * kFwCtas && other <= count; other *= 2)
+    if (most(other) + (split == 1) * (1 + a.rows / 8) < most(split)) split = other;
+  // what runs on an SM shares its memory
+  const int64_t all = tiles * split;
+  const int ctas = all <= d.sms ? 1 : all <= 2 * d.sms ? 2 : kFwCtas;
+  int stages = kFwSmemMost / ctas / stage;
   stages = stages < 2 ? 2 : stages > 5 ? 5 : stages;
-  const int grid = static_cast<int>(tiles < d.sms * ctas ? tiles : d.sms * ctas);
-  few_kernel<MATS, RAGGED><<<grid, kFwThreads, stages * stage, s>>>(a, stages, stage);
-  return cudaGetLastError();
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = split, at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(all < d.sms * ctas ? all : d.sms * ctas));
+  cfg.blockDim = dim3(kFwThreads);
+  cfg.dynamicSmemBytes = stages * stage;
+  cfg.stream = s;
+  cfg.attrs = &at;
+  cfg.numAttrs = split > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, split > 1 ? few_kernel<MATS, RAGGED, true> : few_kernel<MATS, RAGGED, false>, a, stages, stage, split);
 }
 
 template <int MATS, bool RAGGED>
 cudaError_t prepare() {
-  return cudaFuncSetAttribute(few_kernel<MATS, RAGGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFwSmemMost);
+  const cudaError_t e = cudaFuncSetAttribute(few_kernel<MATS, RAGGED, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFwSmemMost);
+  return e != cudaSuccess ? e : cudaFuncSetAttribute(few_kernel<MATS, RAGGED, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFwSmemMost);
 }
 
 }  // namespace
