@@ -397,6 +397,24 @@ def test_rope_far_positions_and_frequencies_beyond_a_turn():
     ref.assert_near(ref.host(y), *ref.rope(v, places, freqs, [0] * 4, 8, True))
 
 
+@pytest.mark.parametrize("heads,hd", [(1, 8), (1, 16), (3, 8)])
+@pytest.mark.parametrize("halves", [True, False])
+@pytest.mark.parametrize("rows", [1, 2500])
+def test_rope_of_the_smallest_heads(heads, hd, halves, rows):
+    """Rows of one or a few 16-byte pieces, where a share of the rows' pieces rounds to none."""
+    rng, pairs = np.random.default_rng(heads * hd), hd // 2
+    freqs = [10000.0 ** (-j / pairs) for j in range(pairs)]
+    places = rng.integers(0, 100000, size=(1, rows))
+    x, v = rows_of(rng, rows, heads * hd, F16)
+    y = torch.full((rows + 1, heads * hd), 7.0, dtype=torch.float16, device="cuda")
+    rot = q4.Rope.of(hd, freqs, None, q4.Q4_ROPE_HALVES if halves else q4.Q4_ROPE_ADJACENT)
+    q4.q4_rope(rot, q4.RopePlaces.of(dev(places.astype(np.int32)), 1, rows), heads, x, F16, heads * hd, y, F16, heads * hd)
+    settled()
+    want, off = ref.rope(v, places, freqs, [0] * pairs, hd, halves)
+    ref.assert_near(ref.host(y[:rows]), want, ref.rounded(want, off))
+    assert torch.all(y[rows:] == 7), "memory behind the rows was written"
+
+
 @pytest.mark.parametrize("new", [[1], [3, 0, 5], [1] * 40, [0, 0, 2], [100, 1, 1, 300]])
 def test_rope_at_a_batchs_positions(new):
     rng, heads, hd = np.random.default_rng(len(new)), 6, 128

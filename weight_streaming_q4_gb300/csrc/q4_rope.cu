@@ -178,7 +178,9 @@ cudaError_t rope_launch(const RopeArgs& a, int sms, cudaStream_t s) {
   const bool wide = a.rot.head_dim % 8 == 0 && (halves ? pairs : a.rot.rot_dim) % 8 == 0 &&
                     rows16(a.x.p, a.x.ld, a.x.f32) && rows16(a.y.p, a.y.ld, a.y.f32);
   // About 8 pieces a thread; with few rows the heads are shared out too, up to two CTAs per SM.
-  const int64_t pieces = static_cast<int64_t>(a.heads) * a.rot.head_dim / (wide ? 16 : 2);
+  // (one head of 8 values is half of two pieces)
+  const int each = wide ? 16 : 2;
+  const int64_t pieces = (static_cast<int64_t>(a.heads) * a.rot.head_dim + each - 1) / each;
   int cta_rows = static_cast<int>(8 * kRopeThreads / pieces);
   cta_rows = cta_rows < 1 ? 1 : cta_rows > kRopeTable / pairs ? kRopeTable / pairs : cta_rows;
   while (cta_rows > 1 && (a.rows + cta_rows - 1) / cta_rows < 2 * sms) cta_rows /= 2;
