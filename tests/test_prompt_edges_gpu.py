@@ -1,0 +1,79 @@
+"""Products, norms and rotations of a prompt's layer where tiles, rings, lengths and values meet their ends, on the GPU, against plain 64-bit forms."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import prompt_ref as ref
+import weight_streaming_q4_gb300 as q4
+
+pytestmark = pytest.mark.gpu
+
+F16, F32 = q4.Q4_TYPE_F16, q4.Q4_TYPE_F32
+
+
+def dev(a, dtype=None):
+    t = torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    return t if dtype is None else t.to(dtype)
+
+
+def settled():
+    torch.cuda.synchronize()
+    assert q4.q4_device_status() == 0, "a kernel's wait ran out"
+
+
+def activated(t, off, gelu):
+    """(the activation of t in 64 bits, how far it may be): as in prompt_ref, GELU by the 64-bit complementary error function."""
+    a = 0.5 * t * torch.erfc(torch.from_numpy(-t / math.sqrt(2))).numpy() if gelu else t
+    return a, ref.SLOPE * off + 2.0 ** -20 * np.abs(a) + 2.0 ** -22 * np.abs(t)
+
+
+# Two and more tiles for each of 76 pairs of CTAs, and rows so short that the operand ring holds more than the steps of the tiles whose
+# sums have a place: the warps that fill it are done while the products of the tile before the last one still wait for an epilogue.
+SHORT = [(300, 28672, 512), (150, 49152, 512), (550, 16384, 288), (280, 28672, 256), (150, 25000, 256), (12, 128256, 256), (64, 128256, 256)]
+
+
+@pytest.mark.parametrize("slow", [False, True], ids=["plain", "slow_epilogue"])
+@pytest.mark.parametrize("rows,n,k", SHORT)
+def test_short_rows_and_many_tiles(rows, n, k, slow):
+    rng = np.random.default_rng(rows + n + k)
+    blocks = ref.q4_bytes(n, k, n)
+    w, x = ref.weights(blocks), rng.normal(size=(rows, k)).astype(np.float16)
+    bias = rng.normal(size=n).astype(np.float32) if slow else None
+    res = dev(rng.normal(size=(rows, n)).astype(np.float32)) if slow else None
+    ep = q4.Epilogue.of(n, rows, q4.Q4_ACT_GELU, 0.5, dev(bias), res, F32) if slow else None
+    wd, xd = dev(blocks), dev(x)
+    ys = [torch.zeros((rows, n), dtype=torch.float16, device="cuda") for _ in range(5)]
+    for y in ys:
+        q4.q4_gemm(wd, xd, k, n, k, rows, ep, y, n)
+    settled()
+    t, off = ref.product(w, x.astype(np.float64), bias)
+    if slow:
+        a, off = activated(t, off, True)
+        t = 0.5 * a + ref.host(res)
+        off = 0.5 * off + 2.0 ** -23 * (np.abs(a) + np.abs(t) + np.abs(ref.host(res)))
+    ref.assert_near(ref.host(ys[0]), t, ref.rounded(t, off), f"{rows} x {n} x {k}")
+    for y in ys[1:]:
+        assert torch.equal(y, ys[0])
+
+
+@pytest.mark.parametrize("gelu", [False, True], ids=["none", "gelu"])
+@pytest.mark.parametrize("rows,n,k", [(80, 49152, 256), (70, 50001, 224)])
+def test_short_rows_and_many_tiles_of_two_matrices(rows, n, k, gelu):
+    rng = np.random.default_rng(rows + n + k)
+    blocks = [ref.q4_bytes(n, k, n + i) for i in range(2)]
+    x = rng.normal(size=(rows, k)).astype(np.float16)
+    bias = [rng.normal(size=n).astype(np.float32) for _ in range(2)]
+    ep = q4.GatedEpilogue.of(n, q4.Q4_ACT_GELU if gelu else q4.Q4_ACT_NONE, *map(dev, bias))
+    wd, xd = [dev(b) for b in blocks], dev(x)
+    ys = [torch.zeros((rows, n), dtype=torch.float16, device="cuda") for _ in range(5)]
+    for y in ys:
+        q4.q4_gemm_gated(*wd, xd, k, n, k, rows, ep, y, n)
+    settled()
+    (g, dg), (u, du) = (ref.product(ref.weights(b), x.astype(np.float64), v) for b, v in zip(blocks, bias))
+    a, da = activated(g, dg, gelu)
+    want = a * u
+    ref.assert_near(ref.host(ys[0]), want, ref.rounded(want, np.abs(a) * du + da * np.abs(u) + da * du + 2.0 ** -23 * np.abs(want)), f"{rows} x {n} x {k}")
+    for y in ys[1:]:
+        assert torch.equal(y, ys[0])

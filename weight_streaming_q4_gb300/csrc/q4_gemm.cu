@@ -79,6 +79,7 @@ struct GmPlan {
 struct GmCtl {
   uint64_t w_full[kGmMaxW], w_empty[kGmMaxW], x_full[kGmMaxX], x_empty[kGmMaxX], a_full[kGmMaxA], a_empty[kGmMaxA];
   uint64_t d_full[2], d_empty[2];
+  uint64_t d_last;     // the last tile's sums are whole
   uint32_t tmem;
   int dead;
 };
@@ -213,6 +214,7 @@ __global__ void __launch_bounds__(kGmThreads, 1)
     for (int i = 0; i < kGmMaxX; ++i) mbar_init(&c->x_full[i], 1), mbar_init(&c->x_empty[i], 1);
     for (int i = 0; i < kGmMaxA; ++i) mbar_init(&c->a_full[i], 8 * G::AS * MATS), mbar_init(&c->a_empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&c->d_full[i], 1), mbar_init(&c->d_empty[i], 8);
+    mbar_init(&c->d_last, 1);
     c->dead = 0;
     fence_mbar_init();
   }
@@ -328,7 +330,9 @@ __global__ void __launch_bounds__(kGmThreads, 1)
             }
           }
         }
-        tm2_commit(&c->d_full[rd.slot], pair_mask);
+        // (the last tile has a barrier of its own: the converting warps, which finish it too, have waited for no turn of d_full
+        // before, and a parity alone does not tell its last turn from the one two before)
+        tm2_commit(t + stride < tiles ? &c->d_full[rd.slot] : &c->d_last, pair_mask);
         rd.step(p.sums);
       }
     }
@@ -464,7 +468,7 @@ __global__ void __launch_bounds__(kGmThreads, 1)
   if (warp >= kGmConvert) {
     if (a.bias[0] && i < a.n) bg = __ldg(a.bias[0] + i);
     if (MATS == 2 && a.bias[1] && i < a.n) bu = __ldg(a.bias[1] + i);
-    gm_wait(c, &c->d_full[before % p.sums], static_cast<uint32_t>(before / p.sums) & 1);
+    gm_wait(c, &c->d_last, 0);
     tm_after();
   }
   if (p.split == 1) {
