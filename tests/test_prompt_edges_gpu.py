@@ -77,3 +77,25 @@ def test_short_rows_and_many_tiles_of_two_matrices(rows, n, k, gelu):
     ref.assert_near(ref.host(ys[0]), want, ref.rounded(want, np.abs(a) * du + da * np.abs(u) + da * du + 2.0 ** -23 * np.abs(want)), f"{rows} x {n} x {k}")
     for y in ys[1:]:
         assert torch.equal(y, ys[0])
+
+
+@pytest.mark.parametrize("k", [256, 512, 768, 1280, 1792, 2304, 2560])
+@pytest.mark.parametrize("rows,n", [(9, 20000), (70, 20000), (130, 20000), (250, 20000), (250, 300)])
+def test_rings_that_end_in_any_place(rows, n, k):
+    """Steps of k that fill the rings once, in part or several times, over the same buffers again and again: what one launch leaves open the next would meet."""
+    rng = np.random.default_rng(rows + n + k)
+    blocks = [dev(ref.q4_bytes(n, k, n + i)) for i in range(2)]
+    w = [torch.from_numpy(ref.weights(ref.q4_bytes(n, k, n + i))).cuda().float() for i in range(2)]
+    x = dev(rng.normal(size=(rows, k)).astype(np.float16))
+    first = None
+    for _ in range(8):
+        y = torch.zeros((2, rows, n), dtype=torch.float16, device="cuda")
+        q4.q4_gemm(blocks[0], x, k, n, k, rows, None, y[0], n)
+        q4.q4_gemm_gated(*blocks, x, k, n, k, rows, q4.GatedEpilogue.of(n, q4.Q4_ACT_NONE), y[1], n)
+        first = y if first is None else first
+        assert torch.equal(y, first)
+    settled()
+    t = [x.double() @ v.double().T for v in w]
+    s = [k * 2.0 ** -23 * (x.double().abs() @ v.double().abs().T) for v in w]
+    for got, want, off in ((first[0], t[0], s[0]), (first[1], t[0] * t[1], t[0].abs() * s[1] + s[0] * t[1].abs() + s[0] * s[1] + 2.0 ** -23 * (t[0] * t[1]).abs())):
+        assert torch.all((got.double() - want).abs() <= off + 2.0 ** -11 * (want.abs() + off) + 2.0 ** -25)

@@ -447,10 +447,11 @@ __global__ void __launch_bounds__(kGmThreads, 1)
     }
   }
   __syncwarp();
-  // The barriers that the last products' ends are told to are not gone before they are.
+  // The barriers that the last products' ends are told to are not gone before they are.  (Behind d_last every turn of theirs but
+  // the last has ended, or its stage could not have been filled again: a parity then tells the last one.)
   if (warp == 3) {
-    int64_t mine = 0;
-    for (int64_t t = first; t < tiles; t += stride) mine += (u1 - u0) * 4;
+    gm_wait(c, &c->d_last, 0);
+    const int64_t mine = ((tiles - 1 - first) / stride + 1) * (u1 - u0) * 4;
     for (int64_t s = max(mine / G::AS - p.na, int64_t{0}); s < mine / G::AS; ++s)
       gm_drain(&c->a_empty[s % p.na], static_cast<uint32_t>(s / p.na) & 1);
     for (int64_t s = max(mine / G::XS - p.nx, int64_t{0}); s < mine / G::XS; ++s)
