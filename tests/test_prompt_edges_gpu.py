@@ -99,3 +99,18 @@ def test_rings_that_end_in_any_place(rows, n, k):
     s = [k * 2.0 ** -23 * (x.double().abs() @ v.double().abs().T) for v in w]
     for got, want, off in ((first[0], t[0], s[0]), (first[1], t[0] * t[1], t[0].abs() * s[1] + s[0] * t[1].abs() + s[0] * s[1] + 2.0 ** -23 * (t[0] * t[1]).abs())):
         assert torch.all((got.double() - want).abs() <= off + 2.0 ** -11 * (want.abs() + off) + 2.0 ** -25)
+
+
+@pytest.mark.parametrize("kind", [F16, F32])
+@pytest.mark.parametrize("rows,n,k", [(20, 33, 256), (100, 20001, 320), (250, 20031, 256), (40, 289, 8192), (200, 1055, 4096), (256, 14337, 1024), (65, 31, 96)])
+def test_warps_whose_last_rows_of_w_are_not_there(rows, n, k, kind):
+    """A residual, and a matrix whose last warp has rows of W in some lanes only, in the first, middle, last and shared tiles of a pair."""
+    rng = np.random.default_rng(rows + n + k)
+    blocks = ref.q4_bytes(n, k, n)
+    x = dev(rng.normal(size=(rows, k)).astype(np.float16))
+    res = dev(rng.normal(size=(rows, n))).to(torch.float32 if kind == F32 else torch.float16)
+    y = torch.full((rows + 1, n), 7.0, dtype=torch.float16, device="cuda")
+    q4.q4_gemm(dev(blocks), x, k, n, k, rows, q4.Epilogue.of(n, rows, residual=res, residual_type=kind), y, n)
+    settled()
+    ref.assert_near(ref.host(y[:rows]), *ref.gemm(ref.weights(blocks), ref.host(x), residual=ref.host(res)))
+    assert torch.all(y[rows:] == 7)

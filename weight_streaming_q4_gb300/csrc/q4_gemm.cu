@@ -147,25 +147,28 @@ __device__ __forceinline__ void staged_words(const char* row, uint32_t* w) {
   for (int i = 0; i < 9; ++i) w[i] = v[J + i];
 }
 
-// The residual of N rows of x from row0 on (`rows` of them there), at this thread's row i of W.
+// The residual of N rows of x from row0 on (`rows` of them there), at this thread's row i of W.  The whole warp calls it, and
+// has come together again behind it: instructions on tensor memory follow, which want every lane.
 template <int N>
 __device__ __forceinline__ void load_residual(const GemmArgs& a, int i, int row0, int rows, float* r) {
-  if (i >= a.n) return;
-  const int64_t at = row0 * a.residual.ld + i;
-  if (a.residual.f32) {
-    const float* p = static_cast<const float*>(a.residual.p) + at;
+  if (i < a.n) {
+    const int64_t at = row0 * a.residual.ld + i;
+    if (a.residual.f32) {
+      const float* p = static_cast<const float*>(a.residual.p) + at;
 #pragma unroll
-    for (int c = 0; c < N; ++c)
-      if (c < rows) r[c] = p[c * a.residual.ld];
-  } else {
-    const __half* p = static_cast<const __half*>(a.residual.p) + at;
+      for (int c = 0; c < N; ++c)
+        if (c < rows) r[c] = p[c * a.residual.ld];
+    } else {
+      const __half* p = static_cast<const __half*>(a.residual.p) + at;
 #pragma unroll
-    for (int c = 0; c < N; ++c)
-      if (c < rows) r[c] = __half2float(p[c * a.residual.ld]);
+      for (int c = 0; c < N; ++c)
+        if (c < rows) r[c] = __half2float(p[c * a.residual.ld]);
+    }
   }
+  __syncwarp();
 }
 
-// N columns of sums of this thread's row i of W, of x's rows row0 .. : epilogue and store.
+// N columns of sums of this thread's row i of W, of x's rows row0 .. : epilogue and store.  The whole warp, as load_residual.
 template <int MATS, int N>
 __device__ __forceinline__ void finish(const GemmArgs& a, int i, int row0, int rows, float* g, float* u, const float* r, float bg, float bu) {
 #pragma unroll
@@ -173,19 +176,21 @@ __device__ __forceinline__ void finish(const GemmArgs& a, int i, int row0, int r
   activate<N>(g, a.act);
 #pragma unroll
   for (int c = 0; c < N; ++c) g[c] = MATS == 2 ? g[c] * (u[c] + bu) : a.residual.p ? fmaf(g[c], a.scale, r[c]) : g[c] * a.scale;
-  if (i >= a.n) return;
-  __half* y = a.y + row0 * a.y_ld + i;
-  if (rows >= N) {
+  if (i < a.n) {
+    __half* y = a.y + row0 * a.y_ld + i;
+    if (rows >= N) {
 #pragma unroll
-    for (int c = 0; c < N; ++c) {
-      *y = __float2half_rn(g[c]);
-      y += a.y_ld;
+      for (int c = 0; c < N; ++c) {
+        *y = __float2half_rn(g[c]);
+        y += a.y_ld;
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < N; ++c)
+        if (c < rows) y[c * a.y_ld] = __float2half_rn(g[c]);
     }
-  } else {
-#pragma unroll
-    for (int c = 0; c < N; ++c)
-      if (c < rows) y[c * a.y_ld] = __float2half_rn(g[c]);
   }
+  __syncwarp();
 }
 
 template <int MATS, bool RAGGED, bool WIDE>
