@@ -732,7 +732,7 @@ typedef struct q4_rotation {
 } q4_rotation;
 
 /*
- *   freqs      host, rot_dim / 2 finite values: radians per position
+ *   freqs      host, rot_dim / 2 values within +-2^60: radians per position
  *   axes       host, rot_dim / 2 values 0 .. 3, or null: all 0
  *   head_dim   2 .. 1024;  rot_dim even, 2 .. 256, at most head_dim
  * Errors: Q4_ERR_ARG.
@@ -754,8 +754,9 @@ typedef struct q4_places {
  * Turns every head of the rows of x into y: pair (a, b) becomes
  * (a cos - b sin, a sin + b cos), or with `inverse` turns back (keys that move
  * to another position; the gradient of the turn).  Queries and keys that lie
- * side by side are one call.  The angle is reduced in 64 bits, so a far
- * position costs no accuracy: cos and sin are within 2^-22.
+ * side by side are one call.  The turns of a position are exact to 2^-64 and
+ * multiplied in 64 bits, so a far position costs no accuracy: cos and sin of
+ * position * frequency are within 2^-22 at any position.
  *   x      device, n_tokens rows of n_heads * head_dim values of x_type, x_ld apart
  *   y      device, rows laid out likewise of y_type, written; x itself (same
  *          type and ld) or memory that does not overlap x

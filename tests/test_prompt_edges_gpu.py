@@ -1,11 +1,13 @@
 """Products, norms and rotations of a prompt's layer where tiles, rings, lengths and values meet their ends, on the GPU, against plain 64-bit forms."""
 import math
+from fractions import Fraction
 
 import numpy as np
 import pytest
 import torch
 
 import prompt_ref as ref
+from exact_circle import circle
 import weight_streaming_q4_gb300 as q4
 
 pytestmark = pytest.mark.gpu
@@ -114,3 +116,24 @@ def test_warps_whose_last_rows_of_w_are_not_there(rows, n, k, kind):
     settled()
     ref.assert_near(ref.host(y[:rows]), *ref.gemm(ref.weights(blocks), ref.host(x), residual=ref.host(res)))
     assert torch.all(y[rows:] == 7)
+
+
+@pytest.mark.parametrize("halves", [True, False])
+def test_far_positions_against_exact_angles(halves):
+    """Cosines and sines of angles reduced in exact arithmetic: within 2^-22 whatever the position and the frequency."""
+    freqs = [1.0, 0.794, 2.0, 3.7, 30.0, 100.0, -3.0, 0.25, 1e-4, 12345.678, -1e9, 2.0 ** 60]
+    places = [2 ** 31 - 1, -2 ** 31, 2 ** 30 + 1, 123456789, 100003, 1, 0, -77]
+    two_pi, pairs = circle(), len(freqs)
+    turns = np.array([[float(Fraction(f) * p / two_pi % 1) for f in freqs] for p in places])
+    x = torch.zeros((len(places), 2 * pairs), device="cuda")
+    first = np.arange(pairs) if halves else 2 * np.arange(pairs)
+    second = first + (pairs if halves else 1)
+    x[:, dev(first)] = 1                          # (1, 0) turns into (cos, sin)
+    y = torch.zeros_like(x)
+    rot = q4.Rope.of(2 * pairs, freqs, None, q4.Q4_ROPE_HALVES if halves else q4.Q4_ROPE_ADJACENT)
+    at = q4.RopePlaces.of(dev(np.array(places, dtype=np.int32)), 1, len(places))
+    q4.q4_rope(rot, at, 1, x, F32, 2 * pairs, y, F32, 2 * pairs)
+    settled()
+    got = ref.host(y)
+    ref.assert_near(got[:, first], np.cos(2 * math.pi * turns), 2.0 ** -22, "cosines")
+    ref.assert_near(got[:, second], np.sin(2 * math.pi * turns), 2.0 ** -22, "sines")

@@ -83,6 +83,28 @@ int run_gemm(const void* w0, const void* w1, const uint16_t* x, int64_t x_ld, in
   return Q4_OK;
 }
 
+// 1 / (2 pi), the turns of a radian, in 2^-128.
+constexpr uint64_t kTurnHigh = 0x28be60db9391054a, kTurnLow = 0x7f09d5f47d4d3770;
+constexpr double kMostFreq = 1152921504606846976.;      // 2^60: the constant's last bit is 2^-5 of a unit of turns_of there
+
+// The turns of freq radians in 2^-64, whole ones left out, rounded: freq is m 2^(e - 53) with a whole number m, and the product
+// of m and the constant's 126 bits is whole too.  (A division in 64-bit floating point is off by 2^-53 of the turns, whole ones
+// among them, which 2^31 positions make 2^-22.)
+uint64_t turns_of(double freq) {
+  int e;
+  const uint64_t m = static_cast<uint64_t>(ldexp(frexp(fabs(freq), &e), 53));
+  const unsigned __int128 low = static_cast<unsigned __int128>(m) * kTurnLow;
+  const unsigned __int128 high = static_cast<unsigned __int128>(m) * kTurnHigh + static_cast<uint64_t>(low >> 64);
+  // in 2^(e - 53 - 128), 181 bits at most
+  const uint64_t word[4] = {static_cast<uint64_t>(low), static_cast<uint64_t>(high), static_cast<uint64_t>(high >> 64), 0};
+  const int shift = 53 + 128 - 64 - e;      // (56 or more, as freq is 2^60 at most)
+  if (shift >= 192) return 0;
+  const int w = shift / 64, b = shift % 64;
+  uint64_t turns = word[w] >> b | (b ? word[w + 1] << (64 - b) : 0);
+  turns += word[(shift - 1) / 64] >> (shift - 1) % 64 & 1;
+  return freq < 0 ? 0 - turns : turns;
+}
+
 }  // namespace
 
 extern "C" int q4_gemm(const void* w, const uint16_t* x, int64_t x_ld, int n, int k, int rows, const q4_epilogue* ep,
@@ -143,12 +165,8 @@ extern "C" int q4_rotation_init(q4_rotation* rot, int head_dim, int rot_dim, con
   memset(&r, 0, sizeof(r));
   r.head_dim = head_dim, r.rot_dim = rot_dim, r.style = style, r.n_axes = 1;
   for (int i = 0; i < rot_dim / 2; ++i) {
-    if (!isfinite(freqs[i]) || (axes && (axes[i] < 0 || axes[i] >= Q4_ROPE_AXES))) return Q4_ERR_ARG;
-    // what is over a whole number of turns, from -1/2 to below 1/2 (small frequencies keep all their bits), in 2^-64
-    const double turns = freqs[i] / 6.283185307179586476925286766559;
-    double part = turns - rint(turns);
-    if (part >= 0.5) part -= 1.;
-    r.turn[i] = static_cast<uint64_t>(static_cast<int64_t>(part * 18446744073709551616.));
+    if (!(fabs(freqs[i]) <= kMostFreq) || (axes && (axes[i] < 0 || axes[i] >= Q4_ROPE_AXES))) return Q4_ERR_ARG;
+    r.turn[i] = turns_of(freqs[i]);
     r.axis[i] = static_cast<uint8_t>(axes ? axes[i] : 0);
     if (r.axis[i] >= r.n_axes) r.n_axes = r.axis[i] + 1;
   }
