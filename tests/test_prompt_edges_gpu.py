@@ -137,3 +137,27 @@ def test_far_positions_against_exact_angles(halves):
     got = ref.host(y)
     ref.assert_near(got[:, first], np.cos(2 * math.pi * turns), 2.0 ** -22, "cosines")
     ref.assert_near(got[:, second], np.sin(2 * math.pi * turns), 2.0 ** -22, "sines")
+
+
+@pytest.mark.parametrize("rows,k", [(1, 2 ** 30 + 4096), (9, 2 ** 30 + 4096), (2, 2 ** 30 + 4096 + 32), (1, 2 ** 31 - 32)])
+def test_rows_of_a_billion_values(rows, k):
+    """One row of W whose bytes, and whose x's, are no longer counted in 31 bits; x is zero but for some runs of it."""
+    gen = torch.Generator(device="cuda").manual_seed(k % 1000 + rows)
+    w = torch.randint(0, 256, (k // 32, 18), generator=gen, dtype=torch.uint8, device="cuda")
+    w[:, 1] = (w[:, 1] & 0x83) | 0x24              # scales of both signs, 2^-6 to 2^-5
+    x = torch.zeros((rows, k), dtype=torch.float16, device="cuda")
+    runs = [0, 4096, 2 ** 29 - 64, 2 ** 30 - 64, 2 ** 30 + 2048, k - 2048, k - 96]
+    runs = [(a, min(a + 2048, k)) for a in runs]
+    for a, b in runs:
+        x[:, a:b] = torch.randn((rows, b - a), generator=gen, device="cuda").half()
+    there = torch.cat([torch.arange(a // 32, b // 32) for a, b in runs]).unique()
+    ws = ref.weights(w[there.cuda()].cpu().numpy()[None])                 # [1][values there]
+    xs = ref.host(x.view(rows, -1, 32)[:, there.cuda()].reshape(rows, -1))
+    y, z = (torch.zeros((rows, 1), dtype=torch.float16, device="cuda") for _ in range(2))
+    q4.q4_gemm(w, x, k, 1, k, rows, None, y, 1)
+    q4.q4_gemm_gated(w, w, x, k, 1, k, rows, q4.GatedEpilogue.of(1, q4.Q4_ACT_NONE), z, 1)
+    settled()
+    # (sums of zeros are exact: prompt_ref's bound with the number of values that are there for k)
+    t, off = ref.product(ws, xs)
+    ref.assert_near(ref.host(y), t, ref.rounded(t, off), "product")
+    ref.assert_near(ref.host(z), t * t, ref.rounded(t * t, 2 * np.abs(t) * off + off * off + 2.0 ** -23 * t * t), "gated product")

@@ -103,8 +103,8 @@ __global__ void __launch_bounds__(kFwThreads, kFwCtas) few_kernel(const __grid_c
       }
       // x: 128 pieces of a row, what lies behind the row's end as zeros
       for (int i = tid; i < a.rows * 128; i += kFwThreads) {
-        const int rr = i >> 7, p = i & 127, col = c_s * 1024 + p * 8, left = (a.k - col) * 2;
-        const int bytes = left < 0 ? 0 : left > 16 ? 16 : left;
+        const int rr = i >> 7, p = i & 127, col = c_s * 1024 + p * 8, left = a.k - col;
+        const int bytes = left < 0 ? 0 : left > 8 ? 16 : left * 2;
         cp16_part(to + F::W_BYTES + rr * kFwXRow + (p >> 3) * kFwChunk + (p & 7) * 16, a.x + (bytes ? rr * a.x_ld + col : 0), bytes);
       }
       if (++c_slot == stages) c_slot = 0;
