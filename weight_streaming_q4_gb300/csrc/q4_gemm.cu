@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(kGmThreads, 1)
 // tile (7 such clusters fit the GPU): 44 rows of the gated 277 x 27648 38 us, with four 60; 33 rows of 1024 x 8192 11.9 and
 // 13.3, of 1024 x 4096 the same; 200 rows of 1024 x 8192 17.2 as one tile of 8 pairs and 15.4 as three of four.
 GmPlan plan(const GemmArgs& a, const PromptDevice& d, int mats, int w_stage) {
-  const int units = (a.k + 255) / 256, most = mats == 2 ? 192 : 256;
+  const int units = (a.k - 1) / 256 + 1, most = mats == 2 ? 192 : 256;
   const double convert = (mats == 2 ? 600. : 370.) * (a.k % 256 ? 1.2 : 1.);
   GmPlan best = {};
   best.row_tiles = (a.n + 255) / 256;

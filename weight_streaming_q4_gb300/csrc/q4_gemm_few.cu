@@ -248,7 +248,7 @@ cudaError_t launch(const GemmArgs& a, const PromptDevice& d, cudaStream_t s) {
   const int64_t tiles = (static_cast<int64_t>(a.n) + kFwRowsW / MATS - 1) / (kFwRowsW / MATS);
   // Few tiles: clusters share them, while all their CTAs run at once, if the SM with most to do then has fewer stages, by more
   // than what the meeting of a cluster takes (about one stage with one row of x, two with eight).
-  const int count = (a.k + 1023) / 1024;
+  const int count = (a.k - 1) / 1024 + 1;
   auto most = [&](int split) { return (tiles * split + d.sms - 1) / d.sms * ((count + split - 1) / split); };
   int split = 1;
   for (int other = 2; other <= 8 && other * tiles <= d.sms * kFwCtas && other <= count; other *= 2)
