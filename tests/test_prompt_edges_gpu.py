@@ -161,3 +161,38 @@ def test_rows_of_a_billion_values(rows, k):
     t, off = ref.product(ws, xs)
     ref.assert_near(ref.host(y), t, ref.rounded(t, off), "product")
     ref.assert_near(ref.host(z), t * t, ref.rounded(t * t, 2 * np.abs(t) * off + off * off + 2.0 ** -23 * t * t), "gated product")
+
+
+# The size of a relative error of an activation, in 2^-23, beside its rounding to binary16, for an argument t that is exact.
+#   gelu       t / sqrt 2 is off by 2^-23 of itself, which (t^2 + 2) times over is erfc's error; erfcf itself 4, three products 3
+#   silu       __expf 2 + 1.173 |t|, half as much again for the sum and the quotient's own 2, a product
+#   gelu_tanh  the exponent z is off by 2^-21 of itself (five roundings), which is e^z's error |z| times over; the rest as for silu
+TAILS = dict(gelu=lambda t: t * t + 9, silu=lambda t: 1.173 * np.abs(t) + 9,
+             gelu_tanh=lambda t: (4 + 1.173) * np.abs(math.sqrt(8 / math.pi) * (t + 0.044715 * t ** 3)) + 9)
+
+
+@pytest.mark.parametrize("name", list(TAILS))
+@pytest.mark.parametrize("rows", [8, 40])
+def test_the_tails_of_activations_keep_their_digits(rows, name):
+    """Small values of an activation, multiplied by a large second product or scale: what is left of them is right relative to itself."""
+    n, k = 37, 32
+    d = np.linspace(0.25, 1.0, n).astype(np.float16)
+    blocks = [np.full((n, 1, 18), 0x88, dtype=np.uint8) for _ in range(2)]
+    for b, scale, at in ((blocks[0], d, 0), (blocks[1], np.full(n, 1000, dtype=np.float16), 1)):
+        b[:, 0, :2] = scale[:, None].view(np.uint8)
+        b[:, 0, 2 + at] = 0x89                    # one weight of 1, the others 0
+    x = np.zeros((rows, k), dtype=np.float16)
+    x[:, 0], x[:, 1] = np.linspace(-12, 9, rows), np.linspace(1000, 60000, rows)
+    g = x[:, :1].astype(np.float64) * d.astype(np.float64)
+    u = x[:, 1:2].astype(np.float64) * 1000
+    a = {"gelu": lambda t: 0.5 * t * torch.erfc(torch.from_numpy(-t / math.sqrt(2))).numpy(), "silu": lambda t: t / (1 + np.exp(-t)),
+         "gelu_tanh": lambda t: t / (1 + np.exp(-math.sqrt(8 / math.pi) * (t + 0.044715 * t ** 3)))}[name](g)
+    y = torch.zeros((2, rows, n), dtype=torch.float16, device="cuda")
+    act = dict(gelu=q4.Q4_ACT_GELU, silu=q4.Q4_ACT_SILU, gelu_tanh=q4.Q4_ACT_GELU_TANH)[name]
+    q4.q4_gemm_gated(*map(dev, blocks), dev(x), k, n, k, rows, q4.GatedEpilogue.of(n, act), y[0], n)
+    q4.q4_gemm(dev(blocks[0]), dev(x), k, n, k, rows, q4.Epilogue.of(n, rows, act, 2.0 ** 20), y[1], n)
+    settled()
+    for got, want in ((y[0], a * u), (y[1], a * 2.0 ** 20)):
+        there = np.abs(want) < 65000              # (beyond that binary16 has only infinity)
+        off = np.abs(want) * (2.0 ** -11 + 2.0 ** -23 * TAILS[name](g)) + 2.0 ** -25
+        ref.assert_near(ref.host(got)[there], want[there], off[there], name)

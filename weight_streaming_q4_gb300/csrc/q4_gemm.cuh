@@ -70,8 +70,9 @@ __device__ __forceinline__ void activate(float* t, int act) {
       for (int i = 0; i < N; ++i) t[i] = over_1_and_exp(t[i], -t[i]);
       break;
     case Q4_ACT_GELU:
+      // (1 + erf would cancel for negative t: a last bit where t stands alone, all of it times a large second product)
 #pragma unroll
-      for (int i = 0; i < N; ++i) t[i] = 0.5f * t[i] * (1.f + erff(t[i] * 0.70710678f));
+      for (int i = 0; i < N; ++i) t[i] = 0.5f * t[i] * erfcf(t[i] * -0.70710678f);
       break;
     case Q4_ACT_GELU_TANH:
 #pragma unroll
