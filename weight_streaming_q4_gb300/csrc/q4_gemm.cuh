@@ -57,6 +57,27 @@ __device__ __forceinline__ void q4_second_block(const uint32_t* w, uint32_t* o) 
 // overflows leaves 0 for every finite t.
 __device__ __forceinline__ float over_1_and_exp(float t, float z) { return __fdividef(t, 1.f + __expf(z)); }
 
+// t times the normal distribution's share below t.  The share below -|t| is r 2^(P(r) - t^2 log2(e) / 2) with r = 1 / (1 + 0.4 |t|) and
+// a polynomial P that was fitted for the least relative error at all |t| <= 14 (8.6e-8): small values keep their digits, where 1 + erf
+// cancels (4 % of the value at -5, all of it at -6, and a large second product brings that up).  Off by (t^2 + 9) 2^-23 of the value
+// at most.  (erfcf does as well, but its registers spilled: 4000 rows of 4099 x 4128 took 185 us, with 1 + erf 138, with this 120.)
+__device__ __forceinline__ float gelu(float t) {
+  float r, e;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(fabsf(t), 0.4f, 1.f)));
+  float p = 0.273944438f;
+  p = fmaf(p, r, -1.40286124f);
+  p = fmaf(p, r, 2.8012476f);
+  p = fmaf(p, r, -2.51524973f);
+  p = fmaf(p, r, 0.774264574f);
+  p = fmaf(p, r, -0.258475393f);
+  p = fmaf(p, r, 0.536042273f);
+  p = fmaf(p, r, 1.4386102f);
+  p = fmaf(p, r, -2.64752269f);
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(t * -0.72134752f, t, p)));
+  const float below = r * e;
+  return t * (t < 0.f ? below : 1.f - below);
+}
+
 // The activation of N values; the choice is the same for all.
 template <int N>
 __device__ __forceinline__ void activate(float* t, int act) {
@@ -70,9 +91,8 @@ __device__ __forceinline__ void activate(float* t, int act) {
       for (int i = 0; i < N; ++i) t[i] = over_1_and_exp(t[i], -t[i]);
       break;
     case Q4_ACT_GELU:
-      // (1 + erf would cancel for negative t: a last bit where t stands alone, all of it times a large second product)
 #pragma unroll
-      for (int i = 0; i < N; ++i) t[i] = 0.5f * t[i] * erfcf(t[i] * -0.70710678f);
+      for (int i = 0; i < N; ++i) t[i] = gelu(t[i]);
       break;
     case Q4_ACT_GELU_TANH:
 #pragma unroll
