@@ -453,14 +453,16 @@ __global__ void __launch_bounds__(kGmThreads, 1)
   }
   __syncwarp();
   // The barriers that the last products' ends are told to are not gone before they are.  (Behind d_last every turn of theirs but
-  // the last has ended, or its stage could not have been filled again: a parity then tells the last one.)
+  // the last has ended, or its stage could not have been filled again: a parity then tells the last one.)  A lane to a barrier:
+  // one after the other they took 0.7 to 1.2 us.
   if (warp == 3) {
+    const bool of_x = lane < kGmMaxX;
+    const int slot = lane % kGmMaxX, ring = of_x ? p.nx : p.na;
+    const int64_t turns = ((tiles - 1 - first) / stride + 1) * (u1 - u0) * (4 / (of_x ? G::XS : G::AS)) - slot;
+    const uint32_t parity = static_cast<uint32_t>((turns - 1) / ring) & 1;
     gm_wait(c, &c->d_last, 0);
-    const int64_t mine = ((tiles - 1 - first) / stride + 1) * (u1 - u0) * 4;
-    for (int64_t s = max(mine / G::AS - p.na, int64_t{0}); s < mine / G::AS; ++s)
-      gm_drain(&c->a_empty[s % p.na], static_cast<uint32_t>(s / p.na) & 1);
-    for (int64_t s = max(mine / G::XS - p.nx, int64_t{0}); s < mine / G::XS; ++s)
-      gm_drain(&c->x_empty[s % p.nx], static_cast<uint32_t>(s / p.nx) & 1);
+    if (slot < ring && turns > 0 && !mbar_wait_bounded(of_x ? &c->x_empty[slot] : &c->a_empty[slot], parity, kGmWaitLimit))
+      atomicOr(&g_status_gm, ST_DRAIN_TIMEOUT);
   }
   __syncwarp();
 
