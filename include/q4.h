@@ -611,8 +611,10 @@ size_t q4_attn_paged_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim
  * batch, a single token) around the paged cache and q4_attn_paged: products
  * with an epilogue, the gated product, the norms around a block and rotary
  * positions.  Rows are binary16 or fp32 (Q4_TYPE_*), `ld` values from row to
- * row (ld >= the row); row r of an output depends on row r of the inputs
- * alone, whatever the number of rows.  With no row a call does nothing.
+ * row (ld >= the row).  Row r of an output depends on row r of the inputs
+ * alone, and on the number of rows: products and norms share out their sums by
+ * it, so that last bits may differ (within the bounds below) from one number to
+ * another.  With no row a call does nothing.
  */
 
 /* Activations. */

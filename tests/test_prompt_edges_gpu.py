@@ -196,3 +196,29 @@ def test_the_tails_of_activations_keep_their_digits(rows, name):
         there = np.abs(want) < 65000              # (beyond that binary16 has only infinity)
         off = np.abs(want) * (2.0 ** -11 + 2.0 ** -23 * TAILS[name](g)) + 2.0 ** -25
         ref.assert_near(ref.host(got)[there], want[there], off[there], name)
+
+
+@pytest.mark.parametrize("rows", [2, 8, 9, 40, 300])
+def test_a_row_depends_on_its_own_inputs_and_the_number_of_rows(rows):
+    """Other values in the other rows leave a row's bits as they were; other numbers of rows its values within the bound (the sums' order may be another)."""
+    n, k, rng = 700, 4096, np.random.default_rng(rows)
+    blocks = ref.q4_bytes(n, k, 3)
+    w, x = dev(blocks), dev(rng.normal(size=(2, rows, k)).astype(np.float16))
+    x[1, rows // 2] = x[0, rows // 2]
+    y, z = (torch.zeros((2, rows, n), dtype=torch.float16, device="cuda") for _ in range(2))
+    wide = dev(rng.normal(size=(2, 200 * (rows > 8) + rows, 5001)).astype(np.float16))        # more and fewer rows than SMs
+    wide[1, rows // 2] = wide[0, rows // 2]
+    v = torch.zeros_like(wide)
+    for i in range(2):
+        q4.q4_gemm(w, x[i], k, n, k, rows, None, y[i], n)
+        q4.q4_gemm_gated(w, w, x[i], k, n, k, rows, None, z[i], n)
+        q4.q4_block_norm(q4.BlockNorm.of(5001), wide.size(1), wide[i], F16, 5001, None, F16, 5001, None, F16, 5001, v[i], F16, 5001)
+    one = torch.zeros((3, n), dtype=torch.float16, device="cuda")
+    q4.q4_gemm(w, x[0, rows // 2:], k, n, k, 1, None, one, n)
+    settled()
+    for got in (y, z, v):
+        assert torch.equal(got[0, rows // 2], got[1, rows // 2])
+    want, off = ref.gemm(ref.weights(blocks), ref.host(x[0, rows // 2:rows // 2 + 1]))
+    for got in (one[0], y[0, rows // 2]):
+        ref.assert_near(ref.host(got)[None], want, off)
+    assert torch.all(one[1:] == 0)
