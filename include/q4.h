@@ -708,8 +708,12 @@ typedef struct q4_norms {
  *              (not both null)
  *   n          1 .. 32768;  rows 0 .. 2^24
  * t and z may each be the block or the residual itself (of the same type and
- * ld, else Q4_ERR_ARG), but not overlap one another or them in another way.  A value that is not finite
- * leaves its own row not finite.  Squares are fp32: values within +-2^56.
+ * ld, else Q4_ERR_ARG), but not overlap one another or them in another way.
+ * A value that is not finite spoils its own row alone, as the formulas have it:
+ * every value of a norm is NaN with a NaN in it, and with an infinity under
+ * Q4_NORM_LAYER; under Q4_NORM_RMS an infinity is NaN in its place and makes the
+ * others 0.  Squares are fp32: values within +-2^56, and with an eps of 0 a root
+ * mean square of 2^-56 or more.
  * Errors: Q4_ERR_ARG, Q4_ERR_ALIGN, Q4_ERR_CUDA.
  */
 int q4_block_norm(const q4_norms *norms, int rows, int n, const void *block, int block_type, int64_t block_ld,

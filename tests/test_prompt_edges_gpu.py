@@ -222,3 +222,32 @@ def test_a_row_depends_on_its_own_inputs_and_the_number_of_rows(rows):
     for got in (one[0], y[0, rows // 2]):
         ref.assert_near(ref.host(got)[None], want, off)
     assert torch.all(one[1:] == 0)
+
+
+@pytest.mark.parametrize("n", [64, 300, 4096, 5001, 8200, 20001])
+@pytest.mark.parametrize("kind", [q4.Q4_NORM_RMS, q4.Q4_NORM_LAYER])
+@pytest.mark.parametrize("typ", [F16, F32])
+def test_norms_of_infinities_and_nan_in_every_place(n, kind, typ):
+    """Every value of a row with something that is not finite: NaN, or of a root mean square with an infinity 0 times the weight and the bias."""
+    rows, rng = 6, np.random.default_rng(n)
+    x = dev(rng.normal(size=(rows, n))).to(torch.float16 if typ == F16 else torch.float32)
+    x[1, 5], x[2, n - 1], x[4, 9], x[4, 30] = math.nan, math.inf, -math.inf, math.inf
+    clean = ref.host(x)[[0, 3, 5]]
+    weight, bias, post = rng.normal(size=n).astype(np.float32), rng.integers(-4, 5, size=n).astype(np.float32), rng.integers(-4, 5, size=n).astype(np.float32)
+    res = dev(rng.integers(-8, 9, size=(rows, n)).astype(np.float32))
+    t, z = (torch.zeros((rows, n), device="cuda") for _ in range(2))
+    # one norm, then one around the block that has a clean residual and a scale of 2
+    q4.q4_block_norm(q4.BlockNorm.of(n, kind, weight=dev(weight), bias=dev(bias)), rows, x, typ, n, None, F32, n, None, F32, n, z, F32, n)
+    q4.q4_block_norm(q4.BlockNorm.of(n, kind, post_bias=dev(post), scale=2.0), rows, x, typ, n, res, F32, n, t, F32, n, None, F32, n)
+    settled()
+    gone = {1: list(range(n)), 2: [n - 1], 4: [9, 30]} if kind == q4.Q4_NORM_RMS else {r: list(range(n)) for r in (1, 2, 4)}
+    for r, places in gone.items():
+        for got, rest in ((z[r], bias), (t[r], ref.host(res[r]) + 2 * post)):
+            want = rest.astype(np.float64)
+            want[places] = math.nan
+            np.testing.assert_array_equal(ref.host(got), want)
+    name, eps = "rms" if kind == q4.Q4_NORM_RMS else "layer", float(np.float32(1e-5))
+    v, off = ref.block_norm(clean, None, name, eps, weight=weight, bias=bias)[1]
+    ref.assert_near(ref.host(z)[[0, 3, 5]], v, off + 2.0 ** -23 * np.abs(v))
+    v, off = ref.block_norm(clean, ref.host(res)[[0, 3, 5]], name, eps, post=True, post_bias=post, scale=2.0)[0]
+    ref.assert_near(ref.host(t)[[0, 3, 5]], v, off + 2.0 ** -23 * np.abs(v))
