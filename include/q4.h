@@ -646,9 +646,9 @@ typedef struct q4_epilogue {
  *          aligned, read only
  *   y      device, binary16 [rows] rows of n values, y_ld apart, written; it
  *          must not overlap w or x
- *   n, k   n 1 .. 2^30; k a multiple of 32.  k that is no multiple of 256 (rows
- *          that do not start 16-byte aligned) is fetched row by row, and
- *          q4_matrix_bytes(n, k) must then stay below 2^32
+ *   n, k   n 1 .. 2^30; k a multiple of 32.  With k that is no multiple of 256
+ *          (rows that do not start 16-byte aligned) q4_matrix_bytes(n, k) has to
+ *          stay below 2^32: larger ones are untested, and refused
  *   rows   0 .. 2^24
  *   ep     null: y = f16(W x)
  * The first call on a device makes the kernels ready (before any stream

@@ -59,7 +59,7 @@ int run_gemm(const void* w0, const void* w1, const uint16_t* x, int64_t x_ld, in
              const float* bias1, int act, float scale, q4::RowsIn residual, uint16_t* y, int64_t y_ld, void* stream) {
   if (!w0 || n < 1 || n > kMostOutputs || k < q4::kQK || k % q4::kQK || rows < 0 || rows > kMostRows) return Q4_ERR_ARG;
   if (act < Q4_ACT_NONE || act > Q4_ACT_GELU_TANH) return Q4_ERR_ARG;
-  // (rows that do not start 16-byte aligned are addressed by 16-bit elements in 31 bits)
+  // (no address of the kernels needs this: matrices of 4 GB and more with such rows are untested)
   if (k % 256 && static_cast<int64_t>(n) * (k / q4::kQK) > ((int64_t{1} << 32) - 1) / q4::kBlockBytes) return Q4_ERR_ARG;
   if (!aligned(w0, 16) || (w1 && !aligned(w1, 16)) || !aligned(bias0, 4) || !aligned(bias1, 4)) return Q4_ERR_ALIGN;
   if (rows == 0) return Q4_OK;
