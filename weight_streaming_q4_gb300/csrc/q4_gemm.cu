@@ -28,7 +28,7 @@
 //
 // Measured in a graph, other inputs every time: 2048 rows, gated 14336 x 4096 289 us, 1666 TFLOP/s (88 % of a library
 // matrix product's rate); 4096 x 14336 with a residual 154 us, 1557 (two rounds of tiles where 1.68 would do); 300 rows, gated
-// 28672 x 8192 171 us, 1646.  16 rows, gated 14336 x 4096 27 us, 2.5 TB/s of W: the conversion bounds it, and 56 of
+// 28672 x 8192 171 us, 1646.  16 rows, gated 14336 x 4096 25 to 28 us, 2.4 to 2.7 TB/s of W: the conversion bounds it, and 56 of
 // the 76 pairs have a tile.
 #include <cuda_fp16.h>
 #include <stdint.h>

@@ -104,7 +104,8 @@ __device__ __forceinline__ void activate(float* t, int act) {
 
 // The kernel of few rows (q4_gemm_few.cu).  At 8 rows it takes 6.2 us for 4096 x 4096 where that of many takes 14.4, and
 // 27 us for the gated 14336 x 4096 where that takes 27; a second set of 8 columns took 44 us at 16 rows, for x is staged
-// again for every tile.
+// again for every tile.  (The rule goes by rows alone, although the sides' times depend on the number of tiles too: from 9 rows
+// on small matrices pay for it.)
 constexpr int kFewRows = 8;
 cudaError_t gemm_few_prepare();
 cudaError_t gemm_few_launch(const GemmArgs& a, const PromptDevice& d, cudaStream_t s);

@@ -17,9 +17,10 @@
 // 6176 x 17824, five: 39 -> 31; the gated 328 x 15616, two: 18.7 -> 7.0).
 //
 // Measured in a graph: one row, 4096 x 4096 with a residual 5.5 us (the kernel of many rows 14.4); gated 14336 x 4096
-// 21.7 us, 3.0 TB/s, with 8 rows 27 (the other kernel 27 for any number up to 32).  What bounds it is the arithmetic from
-// nibbles to binary16: integer and binary16 pipes 45 and 41 % busy, each instruction two cycles; two, three
-// or four CTAs of an SM, and two or four chains of sums, measure the same.
+// 21.7 us, 3.0 TB/s, with 8 rows 27 (the other kernel 25 to 27 for any number up to 32).  No pipe bounds it: issue slots 57 %,
+// integer and binary16 pipes 40 and 38 % busy; what is seen is a barrier of the whole CTA per 1024 columns and instructions
+// from nibbles to binary16 that take two cycles each.  Two, three or four CTAs of an SM, and two or four chains of sums, measure
+// the same.  With 7 and 8 rows only two of the CTAs fit an SM's memory, and the rest of the grid runs behind them.
 #include <cuda_fp16.h>
 #include <stdint.h>
 
@@ -32,7 +33,7 @@ namespace q4 {
 namespace {
 
 constexpr int kFwThreads = 256;
-constexpr int kFwCtas = 3;                // of an SM
+constexpr int kFwCtas = 3;                // of an SM (with 7 and 8 rows two fit)
 constexpr int kFwRowsW = 32;              // rows of W of a CTA
 constexpr int kFwSlices = 4;              // warps along k
 constexpr int kFwChunk = 144;             // bytes between 64 columns of a staged row of x (128 and a shift of the banks)
